@@ -371,6 +371,143 @@ int pkv_paged_attn_noalloc(void *out, const void *query, int64_t query_token_str
                            int32_t block_size, float scale, int32_t num_splits,
                            int32_t *device_status, void *stream);
 
+/*
+ * The step before the cache write, in the same pass as the write: the norm of
+ * each query and key head, and their rotation to the tokens' positions.
+ *
+ * pkv_qk_norm_rope_kv_write — for every token t with position p = positions[t]
+ * and slot s = slot_mapping[t] (block b = s / 16, offset o = s % 16):
+ *     query_out[t][h]         = R_p(norm(query[t][h], q_weight))
+ *     kv_cache[b][h][0][o][:] = R_p(norm(key[t][h], k_weight))
+ *     kv_cache[b][h][1][o][:] = value[t][h]                        (bit copy)
+ * with, per head of d = head_size dims, in fp32 and rounded once at the end
+ * (to nearest even):
+ *     norm(x, w)_i = x_i / sqrt(sum_j x_j^2 / d + eps) * w_i       (x itself if w is NULL)
+ *     R_p          turns plane f = 0 .. rotary_dim / 2 - 1, the dims
+ *                  (f, rotary_dim / 2 + f), or (2 f, 2 f + 1) if interleaved != 0,
+ *                  from (x, y) to (x c - y s, y c + x s) with
+ *                  c = cos_sin[p][f], s = cos_sin[p][rotary_dim / 2 + f];
+ *                  dims from rotary_dim on stay as they are.
+ * It replaces pkv_kv_write in a step; pkv_paged_attn follows on query_out.
+ *
+ *  query_out         bf16; token t, head h at ptr + t*token_stride + h*head_size.  May be
+ *                    query itself (same pointer and stride); must not overlap the
+ *                    inputs in any other way.
+ *  query, key, value bf16, token strides as in pkv_kv_write (views of a fused QKV).
+ *  kv_cache, slot_mapping, num_blocks, device_status
+ *                    as pkv_kv_write.  A token with a negative slot is padding: its
+ *                    query row is still written if its position is in the table.
+ *                    Two tokens with one slot leave no defined K/V there.
+ *  q_weight, k_weight bf16 [head_size], or NULL for no norm.
+ *  eps               >= 0.
+ *  cos_sin           fp32 [max_position][rotary_dim]: rotary_dim / 2 cosines, then as
+ *                    many sines.  rotary_dim is a multiple of 16 in [16, head_size].
+ *  positions         int64 [num_tokens].  A token whose position is outside
+ *                    [0, max_position) is skipped, query row and slot, and
+ *                    PKV_ERR_DEVICE_INDEX stored in device_status unless its slot is
+ *                    negative; one with a slot past the cache has its query row
+ *                    written, its K/V skipped and the same code stored.
+ * Pointers are 16-byte aligned (positions, slot_mapping 8), strides multiples
+ * of 8.  num_tokens == 0 enqueues nothing.
+ */
+int pkv_qk_norm_rope_kv_write(void *query_out, int64_t query_out_token_stride,
+                              void *kv_cache, int64_t num_blocks,
+                              int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_size, int32_t block_size,
+                              const void *query, int64_t query_token_stride,
+                              const void *key, int64_t key_token_stride,
+                              const void *value, int64_t value_token_stride,
+                              const void *q_weight, const void *k_weight, float eps,
+                              const float *cos_sin, int64_t max_position,
+                              int32_t rotary_dim, int32_t interleaved,
+                              const int64_t *positions, const int64_t *slot_mapping,
+                              int32_t num_tokens, int32_t *device_status, void *stream);
+
+/*
+ * pkv_qk_norm_rope_kv_write_fp8 — the same into an E4M3 cache: the K row's fp32
+ * values and the V row are stored as the codes of their quotients by k_scale
+ * and v_scale (rounding as pkv_kv_write_fp8; K is not rounded to bf16 on the way).
+ */
+int pkv_qk_norm_rope_kv_write_fp8(void *query_out, int64_t query_out_token_stride,
+                                  void *kv_cache, int64_t num_blocks,
+                                  int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_size, int32_t block_size,
+                                  const void *query, int64_t query_token_stride,
+                                  const void *key, int64_t key_token_stride,
+                                  const void *value, int64_t value_token_stride,
+                                  const void *q_weight, const void *k_weight, float eps,
+                                  const float *cos_sin, int64_t max_position,
+                                  int32_t rotary_dim, int32_t interleaved,
+                                  const int64_t *positions, const int64_t *slot_mapping,
+                                  int32_t num_tokens, float k_scale, float v_scale,
+                                  int32_t *device_status, void *stream);
+
+/*
+ * The latent cache (latent attention): one row a token instead of keys and
+ * values per head,
+ *     bf16 latent_cache[num_blocks][16][576]
+ * of 512 latent dims (keys and values of every head are made from them) and 64
+ * rotated key dims that all heads share.  Blocks, slots and block tables as
+ * for the K/V cache; pkv_copy_blocks does not apply to it.
+ */
+#define PKV_LATENT_DIM 512
+#define PKV_LATENT_ROPE_DIM 64
+
+/*
+ * pkv_latent_kv_write — for every token t with position p and slot s:
+ *     latent_cache[s][0 .. 511]   = norm(latent[t], weight)
+ *     latent_cache[s][512 .. 575] = R_p(key_rope[t])
+ *     query_rope_out[t][h]        = R_p(query_rope[t][h])   for h < num_heads
+ * with norm (over 512 dims) and R_p (rotary_dim 64) as in
+ * pkv_qk_norm_rope_kv_write: fp32, rounded once.
+ *
+ *  latent            bf16, 512 dims at ptr + t*token_stride.
+ *  key_rope          bf16, 64 dims at ptr + t*token_stride (both may be views of one
+ *                    projection's output).
+ *  weight            bf16 [512], or NULL for no norm.
+ *  cos_sin           fp32 [max_position][64].
+ *  query_rope(_out)  bf16, 64 dims at ptr + t*token_stride + h*head_stride; the output
+ *                    may be the input itself, or the last 64 dims of the 576-wide rows
+ *                    that pkv_latent_paged_attn takes.  num_heads == 0: no query.
+ *  slot_mapping, positions, device_status
+ *                    as pkv_qk_norm_rope_kv_write; padding tokens' query rows are
+ *                    written if their positions are in the table.
+ * Pointers are 16-byte aligned (positions, slot_mapping 8), strides multiples of 8.
+ */
+int pkv_latent_kv_write(void *latent_cache, int64_t num_blocks, int32_t block_size,
+                        const void *latent, int64_t latent_token_stride,
+                        const void *key_rope, int64_t key_rope_token_stride,
+                        const void *weight, float eps,
+                        const float *cos_sin, int64_t max_position, int32_t interleaved,
+                        const int64_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
+                        void *query_rope_out, int64_t query_rope_out_token_stride,
+                        int64_t query_rope_out_head_stride,
+                        const void *query_rope, int64_t query_rope_token_stride,
+                        int64_t query_rope_head_stride, int32_t num_heads,
+                        int32_t *device_status, void *stream);
+
+/*
+ * pkv_latent_gather — the cached rows of every request, in order, into one
+ * contiguous array: out[key_start_loc[r] + j] = row j of request r (bit copy),
+ * j < seq_lens[r].  The per-head keys and values of the expanded form
+ * (pkv_latent_attn_expanded) are a linear map of these rows.
+ *
+ *  out             bf16 [out_rows][576]; rows no request covers are left as they were.
+ *  block_tables    int32 [num_seqs][max_blocks_per_seq].
+ *  seq_lens, key_start_loc
+ *                  int32 [num_seqs] (key_start_loc may be longer).
+ *  max_seq_len     host-side bound of seq_lens; at most 16 * max_blocks_per_seq.
+ *  device_status   optional int32 device word, never cleared by the library.  A
+ *                  request with a negative length, one past max_seq_len, or rows
+ *                  outside `out` is skipped (PKV_ERR_DEVICE_METADATA); the rows of a
+ *                  block id outside the cache are skipped (PKV_ERR_DEVICE_INDEX).
+ * num_seqs is at most 65535.
+ */
+int pkv_latent_gather(void *out, int64_t out_rows, const void *latent_cache, int64_t num_blocks,
+                      int32_t block_size, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *seq_lens, const int32_t *key_start_loc, int32_t num_seqs,
+                      int32_t max_seq_len, int32_t *device_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,6 +17,9 @@ Calls (same names as the C ABI without the ``pkv_`` prefix):
   a batch sharing a table prefix reads the shared blocks once)
 * ``kv_write_fp8`` / ``paged_attn_fp8`` / ``paged_attn_shared_prefix_fp8`` (E4M3 cache with per-tensor
   K and V scales)
+* ``qk_norm_rope_kv_write`` / ``qk_norm_rope_kv_write_fp8`` (norm and rotation of query and key heads with the
+  cache write, in one pass)
+* ``latent_kv_write`` / ``latent_gather`` (a cache of one latent row a token)
 
 plus ``paged_attn_workspace_size(...)`` (the C call's size query) and
 ``workspace_status(workspace)`` (reads the device status word).
@@ -38,9 +41,12 @@ __all__ = [
     "paged_attn_workspace_size", "workspace_status", "STATUS_NAMES", "library_path", "copy_blocks",
     "paged_attn_noalloc", "paged_attn_shared_prefix", "paged_attn_shared_prefix_workspace_size",
     "kv_write_fp8", "paged_attn_fp8", "paged_attn_shared_prefix_fp8", "workspace_schedule",
+    "qk_norm_rope_kv_write", "qk_norm_rope_kv_write_fp8", "LATENT_DIM", "LATENT_ROPE_DIM", "latent_kv_write",
+    "latent_gather",
 ]
 
 BLOCK_SIZE = 16
+LATENT_DIM, LATENT_ROPE_DIM = 512, 64        # dims of a latent cache row: latent, then rotated key
 STATUS_NAMES = {
     0: "PKV_OK", 1: "PKV_ERR_NULL", 2: "PKV_ERR_SHAPE", 3: "PKV_ERR_UNSUPPORTED", 4: "PKV_ERR_ALIGNMENT",
     5: "PKV_ERR_WORKSPACE", 6: "PKV_ERR_CUDA", 7: "PKV_ERR_DEVICE_INDEX", 8: "PKV_ERR_DEVICE_METADATA",
@@ -97,6 +103,17 @@ def load():
                                                          ctypes.c_float, i32, i32, P, ctypes.c_size_t,
                                                          ctypes.POINTER(ctypes.c_size_t), P]
         lib.pkv_paged_attn_shared_prefix_fp8.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        qk = [P, i64, P, i64, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, f32, P, i64, i32, i32, P, P, i32]
+        lib.pkv_qk_norm_rope_kv_write.argtypes = qk + [P, P]
+        lib.pkv_qk_norm_rope_kv_write.restype = ctypes.c_int
+        lib.pkv_qk_norm_rope_kv_write_fp8.argtypes = qk + [f32, f32, P, P]
+        lib.pkv_qk_norm_rope_kv_write_fp8.restype = ctypes.c_int
+        lib.pkv_latent_kv_write.argtypes = [P, i64, i32, P, i64, P, i64, P, f32, P, i64, i32, P, P, i32, P, i64, i64,
+                                            P, i64, i64, i32, P, P]
+        lib.pkv_latent_kv_write.restype = ctypes.c_int
+        lib.pkv_latent_gather.argtypes = [P, i64, P, i64, i32, P, i32, P, P, i32, i32, P, P]
+        lib.pkv_latent_gather.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -348,3 +365,180 @@ def paged_attn_noalloc(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.T
             int(max_query_len), int(max_seq_len), H, hkv, d, bs, ctypes.c_float(scale), int(num_splits),
             _ptr(device_status), _stream(out, stream))
     _check(rc, "pkv_paged_attn_noalloc")
+
+
+# ---- norm, rotation and the latent cache: calls that check types and devices too -------------------------------
+
+def _expect(what: str, t: Optional[torch.Tensor], dtype, ndim: int, device) -> None:
+    """One tensor argument: a CUDA tensor of this type and rank on the call's device."""
+    if t is None:
+        return
+    if not t.is_cuda:
+        raise ValueError("paged KV-cache calls take CUDA tensors only")
+    if t.dtype != dtype or t.dim() != ndim:
+        raise ValueError(f"{what} must be a {ndim}-dimensional {dtype} tensor, not {t.dim()}-dimensional {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
+
+
+def _contiguous(what: str, t: Optional[torch.Tensor], shape=None) -> None:
+    if t is None:
+        return
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _step(x: torch.Tensor, dim: int, least: int) -> int:
+    """The stride of a dim in elements; of a dim of one entry (where it means nothing), the least that the call takes."""
+    return x.stride(dim) if x.shape[dim] > 1 else least
+
+
+def _call(device, stream, fn, *args) -> None:
+    """Enqueue on `stream` (default: the current one of the tensors' device), with that device current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    handle = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    _check(rc, fn.__name__)
+
+
+def _qk_norm_rope(fp8: bool, query_out, kv_cache, query, key, value, q_weight, k_weight, eps, cos_sin, positions,
+                  slot_mapping, scales, interleaved, device_status, stream) -> None:
+    dev, bf = kv_cache.device, torch.bfloat16
+    if kv_cache.dim() != 5 or kv_cache.element_size() != (1 if fp8 else 2) or (not fp8 and kv_cache.dtype != bf):
+        raise ValueError("kv_cache must be [NB, Hkv, 2, 16, d], bf16 (one byte per element for an FP8 cache)")
+    _expect("kv_cache", kv_cache, kv_cache.dtype, 5, dev)
+    _contiguous("kv_cache", kv_cache)
+    nb, hkv, _, bs, d = kv_cache.shape
+    for what, x in (("query_out", query_out), ("query", query), ("key", key), ("value", value)):
+        _expect(what, x, bf, 3, dev)
+        if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d) or x.shape[2] != d:
+            raise ValueError(f"{what} must be [T, heads, {d}] with contiguous heads")
+    T, H = int(query.shape[0]), int(query.shape[1])
+    if tuple(query_out.shape) != (T, H, d) or tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
+        raise ValueError("query_out must be [T, H, d], key and value [T, Hkv, d]")
+    for what, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _expect(what, x, bf, 1, dev)
+        _contiguous(what, x, (d,))
+    _expect("cos_sin", cos_sin, torch.float32, 2, dev)
+    _contiguous("cos_sin", cos_sin)
+    for what, x in (("positions", positions), ("slot_mapping", slot_mapping)):
+        _expect(what, x, torch.int64, 1, dev)
+        _contiguous(what, x, (T,))
+    _expect("device_status", device_status, torch.int32, 1, dev)
+    lib = load()
+    _call(dev, stream, lib.pkv_qk_norm_rope_kv_write_fp8 if fp8 else lib.pkv_qk_norm_rope_kv_write,
+          _ptr(query_out), _step(query_out, 0, H * d), _ptr(kv_cache), nb, H, hkv, d, bs,
+          _ptr(query), _step(query, 0, H * d), _ptr(key), _step(key, 0, hkv * d), _ptr(value),
+          _step(value, 0, hkv * d), _ptr(q_weight), _ptr(k_weight),
+          float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
+          1 if interleaved else 0, _ptr(positions), _ptr(slot_mapping), T, *scales, _ptr(device_status))
+
+
+def qk_norm_rope_kv_write(query_out: torch.Tensor, kv_cache: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                          value: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                          eps: float, cos_sin: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                          interleaved: bool = False, device_status: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    """Norm and rotate query [T, H, d] into query_out and key [T, Hkv, d] into the cache, and write value there.
+
+    Weights are bf16 [d] (None: no norm); cos_sin is fp32 [max_position, rotary_dim] (cosines, then sines);
+    positions and slot_mapping are int64 [T].  Takes the place of kv_write; query_out may be query."""
+    _qk_norm_rope(False, query_out, kv_cache, query, key, value, q_weight, k_weight, eps, cos_sin, positions,
+                  slot_mapping, (), interleaved, device_status, stream)
+
+
+def qk_norm_rope_kv_write_fp8(query_out: torch.Tensor, kv_cache: torch.Tensor, query: torch.Tensor,
+                              key: torch.Tensor, value: torch.Tensor, q_weight: Optional[torch.Tensor],
+                              k_weight: Optional[torch.Tensor], eps: float, cos_sin: torch.Tensor,
+                              positions: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float, v_scale: float,
+                              interleaved: bool = False, device_status: Optional[torch.Tensor] = None,
+                              stream=None) -> None:
+    """qk_norm_rope_kv_write into an E4M3 cache (uint8 or float8_e4m3fn [NB, Hkv, 2, 16, d])."""
+    _qk_norm_rope(True, query_out, kv_cache, query, key, value, q_weight, k_weight, eps, cos_sin, positions,
+                  slot_mapping, (float(k_scale), float(v_scale)), interleaved, device_status, stream)
+
+
+def _latent_cache(latent_cache: torch.Tensor):
+    _expect("latent_cache", latent_cache, torch.bfloat16, 3, latent_cache.device)
+    _contiguous("latent_cache", latent_cache)
+    if latent_cache.shape[2] != LATENT_DIM + LATENT_ROPE_DIM:
+        raise ValueError(f"latent_cache must be [NB, 16, {LATENT_DIM + LATENT_ROPE_DIM}]")
+    return latent_cache.device, int(latent_cache.shape[0]), int(latent_cache.shape[1])
+
+
+def latent_kv_write(latent_cache: torch.Tensor, latent: torch.Tensor, key_rope: torch.Tensor,
+                    weight: Optional[torch.Tensor], eps: float, cos_sin: torch.Tensor, positions: torch.Tensor,
+                    slot_mapping: torch.Tensor, query_rope_out: Optional[torch.Tensor] = None,
+                    query_rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+                    device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Norm latent [T, 512], rotate key_rope [T, 64] and store both in latent_cache [NB, 16, 576]; rotate
+    query_rope [T, H, 64] into query_rope_out (which may be query_rope, or a view of the attention's query rows).
+    weight is bf16 [512] (None: no norm), cos_sin fp32 [max_position, 64]."""
+    dev, nb, bs = _latent_cache(latent_cache)
+    bf = torch.bfloat16
+    T = int(slot_mapping.shape[0])
+    for what, x, width in (("latent", latent, LATENT_DIM), ("key_rope", key_rope, LATENT_ROPE_DIM)):
+        _expect(what, x, bf, 2, dev)
+        if tuple(x.shape) != (T, width) or x.stride(1) != 1:
+            raise ValueError(f"{what} must be [{T}, {width}] with contiguous rows")
+    _expect("weight", weight, bf, 1, dev)
+    _contiguous("weight", weight, (LATENT_DIM,))
+    _expect("cos_sin", cos_sin, torch.float32, 2, dev)
+    _contiguous("cos_sin", cos_sin, (cos_sin.shape[0], LATENT_ROPE_DIM))
+    for what, x in (("positions", positions), ("slot_mapping", slot_mapping)):
+        _expect(what, x, torch.int64, 1, dev)
+        _contiguous(what, x, (T,))
+    _expect("device_status", device_status, torch.int32, 1, dev)
+    if (query_rope is None) != (query_rope_out is None):
+        raise ValueError("query_rope and query_rope_out go together")
+    H = 0
+    q = [None, 0, 0, None, 0, 0]
+    if query_rope is not None:
+        H = int(query_rope.shape[1])
+        for what, x in (("query_rope_out", query_rope_out), ("query_rope", query_rope)):
+            _expect(what, x, bf, 3, dev)
+            if tuple(x.shape) != (T, H, LATENT_ROPE_DIM) or x.stride(2) != 1:
+                raise ValueError(f"{what} must be [{T}, H, {LATENT_ROPE_DIM}] with contiguous rows")
+        q = []
+        for x in (query_rope_out, query_rope):
+            head = _step(x, 1, LATENT_ROPE_DIM)
+            q += [_ptr(x), _step(x, 0, max(H - 1, 0) * head + LATENT_ROPE_DIM), head]
+    _call(dev, stream, load().pkv_latent_kv_write, _ptr(latent_cache), nb, bs, _ptr(latent),
+          _step(latent, 0, LATENT_DIM), _ptr(key_rope), _step(key_rope, 0, LATENT_ROPE_DIM), _ptr(weight),
+          float(eps), _ptr(cos_sin),
+          int(cos_sin.shape[0]), 1 if interleaved else 0, _ptr(positions), _ptr(slot_mapping), T, *q, H,
+          _ptr(device_status))
+
+
+def _tables(dev, block_tables, S, **lists) -> None:
+    _expect("block_tables", block_tables, torch.int32, 2, dev)
+    _contiguous("block_tables", block_tables)
+    if block_tables.shape[0] != S:
+        raise ValueError("block_tables must have a row per request")
+    for what, x in lists.items():
+        _expect(what, x, torch.int32, 1, dev)
+        _contiguous(what, x)
+
+
+def latent_gather(out: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  key_start_loc: torch.Tensor, max_seq_len: int, device_status: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Copy the cached rows of request r into out[key_start_loc[r]:][:seq_lens[r]] (bf16 [rows, 576])."""
+    dev, nb, bs = _latent_cache(latent_cache)
+    S = int(seq_lens.shape[0])
+    _tables(dev, block_tables, S, seq_lens=seq_lens, key_start_loc=key_start_loc)
+    if key_start_loc.shape[0] < S:
+        raise ValueError("key_start_loc must have an entry per request")
+    _expect("out", out, torch.bfloat16, 2, dev)
+    _contiguous("out", out, (out.shape[0], LATENT_DIM + LATENT_ROPE_DIM))
+    _expect("device_status", device_status, torch.int32, 1, dev)
+    _call(dev, stream, load().pkv_latent_gather, _ptr(out), int(out.shape[0]), _ptr(latent_cache), nb, bs,
+          _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), _ptr(key_start_loc), S, int(max_seq_len),
+          _ptr(device_status))

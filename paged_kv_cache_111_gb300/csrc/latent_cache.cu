@@ -1,0 +1,256 @@
+// The latent cache's write and its gather.
+//
+// Write, for token t with position p and slot s (norm and rotation as in
+// norm_rope.cuh):
+//     cache[s][0 .. 511]   = norm(latent[t]; weight)
+//     cache[s][512 .. 575] = R_p(key_rope[t])
+//     query_rope_out[t][h] = R_p(query_rope[t][h])        (when a query is given)
+// Rounded once, from fp32.  A warp takes a token's latent and key part (512
+// dims in two 16-byte vectors a lane, the 64 rotated dims on 8 lanes), or 16 of
+// its query heads (four heads side by side, four loads a lane in flight).
+//
+// Gather: the cached rows of every request, in order, into one contiguous
+// array (the input of the up-projection to per-head keys and values).  A page
+// is one run of 18432 bytes in both, so this is a copy of runs.
+//
+// Both move bytes and compute next to nothing: HBM-bound at size, bound by
+// launch and memory latency on small batches.
+#include "latent_common.cuh"
+#include "norm_rope.cuh"
+
+namespace pkv {
+
+struct LatentWriteParams {
+    uint4 *cache;                                  // rows of 72 16-byte vectors
+    int64_t num_slots;
+    const __nv_bfloat16 *latent, *key_rope, *weight;   // weight NULL: no norm
+    int64_t latent_stride, key_stride;             // elements, as all strides
+    float eps;
+    const float *cos_sin;
+    int64_t max_position;
+    const int64_t *positions, *slots;
+    __nv_bfloat16 *q_out;
+    int64_t qo_token, qo_head;
+    const __nv_bfloat16 *q;
+    int64_t q_token, q_head;
+    int32_t num_tokens, heads, warps_per_token;
+    int32_t *status;
+};
+
+constexpr int kRopeRows = 16;                      // query heads per warp
+
+template <bool INTER>
+__global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteParams p) {
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t = item / p.warps_per_token;
+    if (t >= p.num_tokens) return;                 // whole warps
+    const int part = static_cast<int>(item - t * p.warps_per_token);
+    const int e0 = (lane & 7) * 8;
+    const int64_t pos = __ldg(p.positions + t);
+    const bool bad_pos = pos < 0 || pos >= p.max_position;
+    if (part == 0) {
+        const int64_t slot = __ldg(p.slots + t);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + t * p.latent_stride);
+        const uint4 raw0 = __ldg(src + lane), raw1 = __ldg(src + 32 + lane);
+        const uint4 rawk = __ldg(reinterpret_cast<const uint4 *>(p.key_rope + t * p.key_stride + e0));
+        if (slot < 0) return;                      // padding
+        if (bad_pos || slot >= p.num_slots) {
+            if (lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
+            return;
+        }
+        LaneAngles<INTER> ang;
+        ang.load(p.cos_sin + pos * kLatRope, e0, kLatRope);
+        float x[8], y[8], k[8];
+        bf16x8_to_f32(raw0, x);
+        bf16x8_to_f32(raw1, y);
+        bf16x8_to_f32(rawk, k);
+        uint4 *dst = p.cache + slot * (kLatRow / 8);
+        if (p.weight) {
+            float w0[8], w1[8];
+            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.weight) + lane), w0);
+            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p.weight) + 32 + lane), w1);
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], fmaf(y[i], y[i], sq));
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+            const float inv = rsqrtf(sq * (1.f / kLatent) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = x[i] * inv * w0[i];
+                y[i] = y[i] * inv * w1[i];
+            }
+        }
+        rotate8<INTER>(k, ang, e0, kLatRope);      // four copies side by side, one stored
+        dst[lane] = f32_to_bf16x8(x);
+        dst[32 + lane] = f32_to_bf16x8(y);
+        if (lane < 8) dst[64 + lane] = f32_to_bf16x8(k);
+    } else {
+        const int h0 = (part - 1) * kRopeRows + (lane >> 3);
+        uint4 raw[kRopeRows / 4];
+#pragma unroll
+        for (int u = 0; u < kRopeRows / 4; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (h0 + 4 * u < p.heads)              // (not __ldg: q_out may be q)
+                raw[u] = *reinterpret_cast<const uint4 *>(p.q + t * p.q_token + (h0 + 4 * u) * p.q_head + e0);
+        }
+        if (bad_pos) {
+            if (lane == 0 && __ldg(p.slots + t) >= 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
+            return;
+        }
+        LaneAngles<INTER> ang;
+        ang.load(p.cos_sin + pos * kLatRope, e0, kLatRope);
+#pragma unroll
+        for (int u = 0; u < kRopeRows / 4; ++u) {
+            float x[8];
+            bf16x8_to_f32(raw[u], x);
+            rotate8<INTER>(x, ang, e0, kLatRope);
+            if (h0 + 4 * u < p.heads)
+                *reinterpret_cast<uint4 *>(p.q_out + t * p.qo_token + (h0 + 4 * u) * p.qo_head + e0) =
+                    f32_to_bf16x8(x);
+        }
+    }
+}
+
+// One CTA copies up to kGatherPages pages of one request.
+constexpr int kGatherPages = 2;
+constexpr int kGatherThreads = 256;
+constexpr int kGatherVecs = kGatherPages * kLatPageBytes / 16;                        // 2304
+constexpr int kGatherPerThread = kGatherVecs / kGatherThreads;                        // 9
+static_assert(kGatherVecs % kGatherThreads == 0, "whole rounds");
+
+__global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(
+    uint4 *out, int64_t out_rows, const uint4 *cache, int64_t num_blocks, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *key_start_loc, int32_t max_seq_len,
+    int32_t *status) {
+    const int r = blockIdx.y;
+    const int page0 = blockIdx.x * kGatherPages;
+    const int L = __ldg(seq_lens + r);
+    const int64_t base = __ldg(key_start_loc + r);
+    // (the first pages' ids are read beside the lengths, before anything is known of them)
+    const int32_t *table = block_tables + static_cast<int64_t>(r) * max_blocks_per_seq;
+    int id[kGatherPages];
+#pragma unroll
+    for (int i = 0; i < kGatherPages; ++i) id[i] = page0 + i < max_blocks_per_seq ? __ldg(table + page0 + i) : -1;
+    if (L < 0 || L > max_seq_len || L > static_cast<int64_t>(max_blocks_per_seq) * kBlock || base < 0 ||
+        base + L > out_rows) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) set_status(status, PKV_ERR_DEVICE_METADATA);
+        return;
+    }
+    const int rows = min(L - page0 * kBlock, kGatherPages * kBlock);   // rows of this CTA
+    if (rows <= 0) return;
+    const int vecs = rows * (kLatRowBytes / 16);
+    uint4 *dst = out + (base + static_cast<int64_t>(page0) * kBlock) * (kLatRowBytes / 16);
+    bool bad = false;
+    const uint4 *src[kGatherPages];
+#pragma unroll
+    for (int i = 0; i < kGatherPages; ++i) {
+        const bool inside = id[i] >= 0 && id[i] < num_blocks;
+        bad |= !inside && i * kBlock < rows;
+        src[i] = inside ? cache + static_cast<int64_t>(id[i]) * (kLatPageBytes / 16) : nullptr;
+    }
+    if (bad && threadIdx.x == 0) set_status(status, PKV_ERR_DEVICE_INDEX);
+    uint4 val[kGatherPerThread];
+#pragma unroll
+    for (int u = 0; u < kGatherPerThread; ++u) {
+        const int v = u * kGatherThreads + threadIdx.x;
+        const int page = v >= kLatPageBytes / 16;
+        const uint4 *s = page ? src[1] : src[0];
+        if (v < vecs && s) val[u] = __ldg(s + v - page * (kLatPageBytes / 16));
+    }
+#pragma unroll
+    for (int u = 0; u < kGatherPerThread; ++u) {
+        const int v = u * kGatherThreads + threadIdx.x;
+        if (v < vecs && (v >= kLatPageBytes / 16 ? src[1] : src[0])) dst[v] = val[u];
+    }
+}
+static_assert(kGatherPages == 2, "the copy picks one of two pages");
+
+}  // namespace pkv
+
+extern "C" int pkv_latent_kv_write(void *latent_cache, int64_t num_blocks, int32_t block_size, const void *latent,
+                                   int64_t latent_token_stride, const void *key_rope, int64_t key_rope_token_stride,
+                                   const void *weight, float eps, const float *cos_sin, int64_t max_position,
+                                   int32_t interleaved, const int64_t *positions, const int64_t *slot_mapping,
+                                   int32_t num_tokens, void *query_rope_out, int64_t query_rope_out_token_stride,
+                                   int64_t query_rope_out_head_stride, const void *query_rope,
+                                   int64_t query_rope_token_stride, int64_t query_rope_head_stride, int32_t num_heads,
+                                   int32_t *device_status, void *stream) {
+    using namespace pkv;
+    if (num_tokens < 0 || num_blocks <= 0 || max_position <= 0 || num_heads < 0 || num_heads > (1 << 20))
+        return PKV_ERR_SHAPE;
+    if (block_size != kBlock) return PKV_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return PKV_ERR_SHAPE;
+    if (num_blocks > INT64_MAX / kLatPageBytes || max_position > INT64_MAX / kLatRope / 4) return PKV_ERR_SHAPE;
+    if (num_tokens == 0) return PKV_OK;
+    if (!latent_cache || !latent || !key_rope || !cos_sin || !positions || !slot_mapping) return PKV_ERR_NULL;
+    if (latent_token_stride < kLatent || key_rope_token_stride < kLatRope) return PKV_ERR_SHAPE;
+    if ((latent_token_stride % 8) || (key_rope_token_stride % 8)) return PKV_ERR_ALIGNMENT;
+    uintptr_t all = reinterpret_cast<uintptr_t>(latent_cache) | reinterpret_cast<uintptr_t>(latent) |
+                    reinterpret_cast<uintptr_t>(key_rope) | reinterpret_cast<uintptr_t>(weight) |
+                    reinterpret_cast<uintptr_t>(cos_sin);
+    if (num_heads > 0) {
+        if (!query_rope_out || !query_rope) return PKV_ERR_NULL;
+        if (query_rope_out_head_stride < kLatRope || query_rope_head_stride < kLatRope ||
+            query_rope_out_token_stride < (num_heads - 1) * query_rope_out_head_stride + kLatRope ||
+            query_rope_token_stride < (num_heads - 1) * query_rope_head_stride + kLatRope)
+            return PKV_ERR_SHAPE;
+        if ((query_rope_out_head_stride % 8) || (query_rope_head_stride % 8) || (query_rope_out_token_stride % 8) ||
+            (query_rope_token_stride % 8))
+            return PKV_ERR_ALIGNMENT;
+        all |= reinterpret_cast<uintptr_t>(query_rope_out) | reinterpret_cast<uintptr_t>(query_rope);
+    }
+    if (all & 15u) return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slot_mapping)) & 7u)
+        return PKV_ERR_ALIGNMENT;
+    LatentWriteParams p;
+    p.cache = static_cast<uint4 *>(latent_cache);
+    p.num_slots = num_blocks * kBlock;
+    p.latent = static_cast<const __nv_bfloat16 *>(latent);
+    p.key_rope = static_cast<const __nv_bfloat16 *>(key_rope);
+    p.weight = static_cast<const __nv_bfloat16 *>(weight);
+    p.latent_stride = latent_token_stride, p.key_stride = key_rope_token_stride;
+    p.eps = eps;
+    p.cos_sin = cos_sin, p.max_position = max_position;
+    p.positions = positions, p.slots = slot_mapping;
+    p.q_out = static_cast<__nv_bfloat16 *>(query_rope_out);
+    p.qo_token = query_rope_out_token_stride, p.qo_head = query_rope_out_head_stride;
+    p.q = static_cast<const __nv_bfloat16 *>(query_rope);
+    p.q_token = query_rope_token_stride, p.q_head = query_rope_head_stride;
+    p.num_tokens = num_tokens, p.heads = num_heads;
+    p.warps_per_token = 1 + (num_heads + kRopeRows - 1) / kRopeRows;
+    p.status = device_status;
+    const int64_t blocks = (static_cast<int64_t>(num_tokens) * p.warps_per_token + 7) / 8;
+    if (blocks > INT32_MAX) return PKV_ERR_SHAPE;
+    (interleaved ? latent_write_kernel<true> : latent_write_kernel<false>)<<<
+        static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" int pkv_latent_gather(void *out, int64_t out_rows, const void *latent_cache, int64_t num_blocks,
+                                 int32_t block_size, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t *seq_lens, const int32_t *key_start_loc, int32_t num_seqs,
+                                 int32_t max_seq_len, int32_t *device_status, void *stream) {
+    using namespace pkv;
+    if (num_seqs < 0 || out_rows < 0 || num_blocks <= 0 || max_seq_len < 0 || max_blocks_per_seq < 0)
+        return PKV_ERR_SHAPE;
+    if (block_size != kBlock) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535) return PKV_ERR_SHAPE;
+    if (num_blocks > INT64_MAX / kLatPageBytes) return PKV_ERR_SHAPE;
+    if (num_seqs == 0 || max_seq_len == 0) return PKV_OK;
+    if ((static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock > max_blocks_per_seq) return PKV_ERR_SHAPE;
+    if (!out || !latent_cache || !block_tables || !seq_lens || !key_start_loc) return PKV_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(latent_cache)) & 15u) return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
+         reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)
+        return PKV_ERR_ALIGNMENT;
+    const int per = kGatherPages * kBlock;
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_seq_len) + per - 1) / per),
+                    static_cast<unsigned>(num_seqs));
+    latent_gather_kernel<<<grid, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<uint4 *>(out), out_rows, static_cast<const uint4 *>(latent_cache), num_blocks, block_tables,
+        max_blocks_per_seq, seq_lens, key_start_loc, max_seq_len, device_status);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
