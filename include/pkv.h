@@ -508,6 +508,53 @@ int pkv_latent_gather(void *out, int64_t out_rows, const void *latent_cache, int
                       const int32_t *seq_lens, const int32_t *key_start_loc, int32_t num_seqs,
                       int32_t max_seq_len, int32_t *device_status, void *stream);
 
+/*
+ * pkv_latent_paged_attn — causal attention over a latent cache, in the latent
+ * space (the absorbed form of latent attention).  Requests, lengths and tables
+ * as pkv_paged_attn; every head reads the same cached rows C_j of 576 dims:
+ *     out[t][h][:] = sum_j softmax_j(scale * <query[t][h], C_j>) * C_j[0 .. 511],
+ *     j = 0 .. c_r + i.
+ * A query row holds the head's query in the latent space (its 128 or so plain
+ * dims times the key up-projection: 512) and its rotated part (64, as
+ * pkv_latent_kv_write leaves it); `out` times the value up-projection is the
+ * head's output.  The request's new rows must already be in the cache.  Scores,
+ * softmax and sums are fp32; the weights enter the product with the values as
+ * bf16 (an error of at most 2^-8 of each weight); out is bf16, nearest even.
+ * One call: no combine follows it.
+ *
+ *  out               bf16 [num_tokens][num_heads][512], contiguous.  Rows that no
+ *                    request owns are left as they were.
+ *  query             bf16; token t, head h at query + t*query_token_stride + h*576.
+ *  latent_cache      bf16 [num_blocks][16][576]; num_blocks < 2^31.  A key row's values
+ *                    must be finite (an infinity or NaN in a row may reach the earlier
+ *                    tokens of its own chunk); unwritten slots may hold anything.
+ *  num_heads         1 .. 1024; num_tokens * num_heads < 2^31.
+ *  max_query_len, max_seq_len, block_tables, seq_lens, query_start_loc
+ *                    as pkv_paged_attn (a request whose values break them is left
+ *                    unwritten, PKV_ERR_DEVICE_METADATA).  A block id outside the cache
+ *                    reads as zeros (PKV_ERR_DEVICE_INDEX).
+ *  workspace         device scratch, 256-byte aligned, of a fixed size (40 MB) whatever
+ *                    the batch.  Its first int32 is the device status word: the call
+ *                    stores PKV_OK or an error code there.  One workspace serves any
+ *                    number of calls in stream order; calls that may overlap (other
+ *                    streams, graphs replayed side by side) need one each.
+ *  workspace_needed  if not NULL, receives that size; with workspace == NULL or
+ *                    workspace_bytes too small nothing is enqueued and
+ *                    PKV_ERR_WORKSPACE is returned (the size query).
+ * Like the attention calls above, the first kernel may start while the kernel
+ * before it (normally pkv_latent_kv_write) still runs, and reads the lengths
+ * (seq_lens, query_start_loc) at once.
+ */
+int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stride,
+                          const void *latent_cache, int64_t num_blocks,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *seq_lens, const int32_t *query_start_loc,
+                          int32_t num_seqs, int32_t num_tokens,
+                          int32_t max_query_len, int32_t max_seq_len,
+                          int32_t num_heads, int32_t block_size, float scale,
+                          void *workspace, size_t workspace_bytes, size_t *workspace_needed,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,7 +19,8 @@ Calls (same names as the C ABI without the ``pkv_`` prefix):
   K and V scales)
 * ``qk_norm_rope_kv_write`` / ``qk_norm_rope_kv_write_fp8`` (norm and rotation of query and key heads with the
   cache write, in one pass)
-* ``latent_kv_write`` / ``latent_gather`` (a cache of one latent row a token)
+* ``latent_kv_write`` / ``latent_paged_attn`` / ``latent_gather`` (a cache of one latent row a token, and attention
+  over it in the latent space)
 
 plus ``paged_attn_workspace_size(...)`` (the C call's size query) and
 ``workspace_status(workspace)`` (reads the device status word).
@@ -42,7 +43,7 @@ __all__ = [
     "paged_attn_noalloc", "paged_attn_shared_prefix", "paged_attn_shared_prefix_workspace_size",
     "kv_write_fp8", "paged_attn_fp8", "paged_attn_shared_prefix_fp8", "workspace_schedule",
     "qk_norm_rope_kv_write", "qk_norm_rope_kv_write_fp8", "LATENT_DIM", "LATENT_ROPE_DIM", "latent_kv_write",
-    "latent_gather",
+    "latent_gather", "latent_paged_attn", "latent_paged_attn_workspace_size",
 ]
 
 BLOCK_SIZE = 16
@@ -114,6 +115,9 @@ def load():
         lib.pkv_latent_kv_write.restype = ctypes.c_int
         lib.pkv_latent_gather.argtypes = [P, i64, P, i64, i32, P, i32, P, P, i32, i32, P, P]
         lib.pkv_latent_gather.restype = ctypes.c_int
+        lib.pkv_latent_paged_attn.argtypes = [P, P, i64, P, i64, P, i32, P, P, i32, i32, i32, i32, i32, i32, f32, P,
+                                              ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), P]
+        lib.pkv_latent_paged_attn.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -542,3 +546,41 @@ def latent_gather(out: torch.Tensor, latent_cache: torch.Tensor, block_tables: t
     _call(dev, stream, load().pkv_latent_gather, _ptr(out), int(out.shape[0]), _ptr(latent_cache), nb, bs,
           _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), _ptr(key_start_loc), S, int(max_seq_len),
           _ptr(device_status))
+
+
+def latent_paged_attn_workspace_size(num_seqs: int, num_tokens: int, max_query_len: int, max_seq_len: int,
+                                     num_heads: int) -> int:
+    """Bytes of workspace pkv_latent_paged_attn needs for these sizes (no GPU work)."""
+    need = ctypes.c_size_t(0)
+    rc = load().pkv_latent_paged_attn(None, None, num_heads * (LATENT_DIM + LATENT_ROPE_DIM), None, 1, None,
+                                      (max_seq_len + BLOCK_SIZE - 1) // BLOCK_SIZE, None, None, num_seqs, num_tokens,
+                                      max_query_len, max_seq_len, num_heads, BLOCK_SIZE, 1.0, None, 0,
+                                      ctypes.byref(need), None)
+    if rc not in (0, 5):
+        _check(rc, "pkv_latent_paged_attn (size query)")
+    return int(need.value)
+
+
+def latent_paged_attn(out: torch.Tensor, query: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor,
+                      seq_lens: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int, max_seq_len: int,
+                      scale: float, workspace: torch.Tensor, stream=None) -> None:
+    """Causal attention of query [T, H, 576] over the latent cache [NB, 16, 576]; out [T, H, 512] bf16.
+
+    One call (no combine after it); workspace_status(workspace) reads its device status."""
+    dev, nb, bs = _latent_cache(latent_cache)
+    S = int(seq_lens.shape[0])
+    _tables(dev, block_tables, S, seq_lens=seq_lens, query_start_loc=query_start_loc)
+    if query_start_loc.shape[0] != S + 1:
+        raise ValueError("query_start_loc must have an entry per request and one more")
+    _expect("query", query, torch.bfloat16, 3, dev)
+    T, H, D = query.shape
+    if D != LATENT_DIM + LATENT_ROPE_DIM or query.stride(2) != 1 or (H > 1 and query.stride(1) != D):
+        raise ValueError(f"query must be [T, H, {LATENT_DIM + LATENT_ROPE_DIM}] with contiguous heads")
+    _expect("out", out, torch.bfloat16, 3, dev)
+    _contiguous("out", out, (T, H, LATENT_DIM))
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    _call(dev, stream, load().pkv_latent_paged_attn, _ptr(out), _ptr(query), _step(query, 0, H * D),
+          _ptr(latent_cache), nb, _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens),
+          _ptr(query_start_loc), S, T, int(max_query_len), int(max_seq_len), H, bs, float(scale), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), None)

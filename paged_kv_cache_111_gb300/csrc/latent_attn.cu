@@ -1,0 +1,903 @@
+// Paged attention over a latent cache, in the latent space (the absorbed form
+// of latent attention), on the 5th-generation tensor cores.
+//
+// Request r's i-th query token sits at position c + i (c keys before the
+// step's tokens).  For every head h, with rows C_j of 576 dims read through the
+// block table,
+//     out[t][h][:] = sum_j softmax_j(scale <query[t][h], C_j>) C_j[0 .. 511],
+//     j = 0 .. c + i:
+// one row serves every head as key (576 dims) and value (its first 512), so a
+// cached row is read once for up to 64 rows of queries.
+//
+// Work item: one row tile, (up to 64 heads) x (tokens that fit, a power of
+// two), against the 64-key tiles that its last token sees.  Rows of a tile are
+// token * heads + head.  Per key tile, in shared memory once:
+//   S  = Q C^T    tcgen05.mma 64 x 64 x 16, 36 of them: both operands K-major
+//   softmax       each of four warps reads 16 rows of S (four threads a row, 16
+//                 keys each), keeps the rows' running max and sum in fp32, and
+//                 writes the weights as bf16 into shared memory
+//   O' += C'P'    the products transposed: tcgen05.mma 128 x rows x 16 with A =
+//                 the same tile's latent dims read MN-major, B = the weights; 16
+//                 of them, O' as four blocks of 128 dims (lanes) x rows (columns)
+// Transposed, the 64 x 512 outputs take 256 tensor-memory columns and leave
+// room for two S buffers; the straight form (rows on lanes) would leave half of
+// the lanes empty and fill all 512 columns.  Heads beyond 64 are split into
+// groups, and CTAs of one lane (below) read the same keys at the same time, one
+// from memory and the others through L2.
+//
+// Split: the batch is one line of (row tile, key tile) units, request after
+// request; it is cut into equal runs, one per CTA lane, so that every SM gets
+// the same number of key tiles whatever the lengths (a decode of one long
+// request and a batch of short ones alike).  Every CTA finds its run from the
+// lengths itself; there is no plan kernel.  A row tile that falls into one run
+// is written at once; one that runs across lanes leaves unnormalised partial
+// sums with their maxima, merged by a second kernel.  A run holds at most two
+// such partial tiles, its first and its last, so the workspace has a fixed size.
+//
+// The weights enter the second product as bf16: an error of at most 2^-8 of
+// each weight, about that of the output's own rounding.  Sums, maxima and
+// outputs are fp32.
+//
+// Warp roles (256 threads): warp 0 walks the run, publishes items and loads
+// pages by TMA (one 18 KiB box a page); warp 1 issues the MMAs; warp 2 loads Q
+// (TMA) and owns tensor memory; warps 4-7 are the softmax and epilogue warps.
+// Rows past a tile's last visible key are zeroed in shared memory, so that what
+// an unwritten slot holds never meets a zero weight.  Every wait is bounded.
+#include <mutex>
+
+#include "latent_common.cuh"
+#include "prefill_common.cuh"
+
+namespace pkv {
+
+constexpr int kLaRows = 64;                                  // rows of a tile (M of the S product)
+constexpr int kLaKeys = 64;                                  // keys of a tile
+constexpr int kLaPages = kLaKeys / kBlock;                   // 4
+constexpr int kLaStage = kLaPages * kLatPageBytes;           // 73728
+constexpr int kLaStages = 2;
+constexpr int kLaChunks = kLatRow / 64;                      // 9 chunks of 64 dims
+constexpr int kLaQChunk = kLaRows * 128;                     // 8192: 64 dims of 64 rows
+constexpr int kLaMaxCtas = 152;
+constexpr int kLaMaxHeads = 1024;
+constexpr int kLaThreads = 256;
+constexpr int kLaItemSlots = 4;
+
+// A page in shared memory as its box lands: [token half][chunk][token % 8][64
+// dims], 128-byte swizzle.  The 8-row groups of a tile's 64 keys then sit at one
+// stride (9216) across pages, for both products.
+constexpr int kLaGroup = kLaChunks * 1024;                   // 9216
+
+// shared memory (from a 1 KiB boundary)
+constexpr int kLaOffQ = 0;
+constexpr int kLaOffKV = kLaOffQ + kLaChunks * kLaQChunk;                 // 73728
+constexpr int kLaOffP = kLaOffKV + kLaStages * kLaStage;                  // 221184
+constexpr int kLaOffBar = kLaOffP + kLaRows * 128;                        // 229376
+constexpr int kLaOffAlpha = kLaOffBar + 256;                              // float [2][64]
+constexpr int kLaOffRow = kLaOffAlpha + 512;                              // float [64], int [64]
+constexpr int kLaOffItems = kLaOffRow + 512;
+constexpr int kLaSmem = kLaOffItems + 256 + 1024;                         // with alignment slack
+static_assert(kLaSmem <= 227 * 1024, "shared memory of one CTA");
+
+// tensor memory: O' block m at columns 64 m, S buffer b at 256 + 64 b
+constexpr uint32_t kLaTmemCols = 512;
+__device__ __forceinline__ constexpr uint32_t la_col_s(int b) { return 256u + 64u * b; }
+
+// workspace
+constexpr int64_t kLaWsStatus = 256;                                      // int32 per CTA
+constexpr int64_t kLaWsDesc = 1280;                                       // int4 per CTA
+constexpr int64_t kLaWsMl = 4096;                                         // float [CTA][2][max, sum][64]
+constexpr int64_t kLaWsO = kLaWsMl + kLaMaxCtas * 2 * 2 * kLaRows * 4;    // float [CTA][2][64 x 512]
+constexpr int64_t kLaPartFloats = kLaRows * kLatent;
+constexpr int64_t kLaWsBytes = kLaWsO + static_cast<int64_t>(kLaMaxCtas) * 2 * kLaPartFloats * 4;
+static_assert(kLaWsStatus + kLaMaxCtas * 4 <= kLaWsDesc && kLaWsDesc + kLaMaxCtas * 16 <= kLaWsMl, "workspace");
+
+struct LaParams {
+    __nv_bfloat16 *out;
+    const int32_t *block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t *seq_lens, *qsl;
+    int32_t num_seqs, num_tokens, max_query_len, max_seq_len;
+    int32_t heads;            // query heads
+    int32_t groups;           // head groups: CTAs of a lane
+    int32_t hpt, tpt;         // heads and tokens of a row tile
+    int32_t lanes;
+    int64_t num_blocks;
+    float scale_log2;
+    uint8_t *ws;
+};
+
+// One item of a CTA's run: key tiles [kv0, kv1) of a row tile.
+struct LaItem {
+    int32_t valid;
+    int32_t tok0, ntok;       // its tokens in the batch
+    int32_t lim0;             // keys its first token sees (each later one sees one more)
+    int32_t kv0, kv1;
+    int32_t n_kv;             // key tiles of the whole row tile
+    int32_t slot;             // -1: complete, written to out; else the partial slot of this CTA
+};
+static_assert(kLaItemSlots * sizeof(LaItem) <= 256, "item ring");
+
+enum LaBar {
+    kLaQFull = 0, kLaQEmpty = 1,
+    kLaSFull = 2,             // S buffer b written (+ b)
+    kLaPFull = 4,             // weights of a tile written (and O' rescaled where needed)
+    kLaODone = 5,             // the tile's second products completed
+    kLaOFree = 6,             // O' read out by the epilogue
+    kLaVote = 7,              // the four softmax warps meet (every tile)
+    kLaMeet = 8,              // the same, at the end of an item
+    kLaKVFull = 9,            // (+ stage)
+    kLaKVEmpty = 11,          // (+ stage)
+    kLaFix = 13,              // rows past the last visible key zeroed (+ stage)
+    kLaItemFull = 15, kLaItemEmpty = 19,
+    kLaNumBars = 23
+};
+static_assert(kLaNumBars * 8 + 48 <= 256, "barriers, tensor-memory address, status, votes");
+
+// Request r's share of the line of units.
+struct LaReq {
+    int32_t q, L, ctx, qs;
+    int32_t n_full;           // row tiles whose tokens are all there
+    int64_t units;            // key tiles of all its row tiles
+};
+
+// sum of floor(x / u) over x < m
+__device__ __forceinline__ int64_t la_floor_sum(int64_t m, int u) {
+    const int64_t d = m / u;
+    return u * (d * (d - 1) / 2) + d * (m - d * u);
+}
+
+// Key tiles of the row tiles before tile j of a request (j <= n_full): tile i
+// sees ctx + (i + 1) tpt keys, and tpt divides 64.
+__device__ __forceinline__ int64_t la_units_before(int32_t ctx, int tpt, int64_t j) {
+    const int u = kLaKeys / tpt;
+    const int64_t b = (ctx + kLaKeys - 1) / tpt;
+    return la_floor_sum(b + j + 1, u) - la_floor_sum(b + 1, u);
+}
+
+__device__ __forceinline__ LaReq la_request(const LaParams &p, int r, bool &bad) {
+    LaReq a;
+    a.qs = __ldg(p.qsl + r);
+    const int q1 = __ldg(p.qsl + r + 1);
+    a.L = __ldg(p.seq_lens + r);
+    a.q = q1 - a.qs;
+    a.ctx = a.L - a.q;
+    a.n_full = 0;
+    a.units = 0;
+    const bool ok = !(a.qs < 0 || a.q < 0 || q1 > p.num_tokens || a.L < a.q || a.L > p.max_seq_len ||
+                      a.q > p.max_query_len || (a.L + kBlock - 1) / kBlock > p.max_blocks_per_seq);
+    bad |= !ok;
+    if (ok && a.q > 0) {
+        a.n_full = a.q / p.tpt;
+        a.units = la_units_before(a.ctx, p.tpt, a.n_full);
+        if (a.q % p.tpt) a.units += (a.L + kLaKeys - 1) / kLaKeys;
+    }
+    return a;
+}
+
+// 16 lanes x 64 columns of tensor memory: thread t gets rows t / 4 (registers
+// 4 k, 4 k + 1) and t / 4 + 8 (4 k + 2, 4 k + 3), columns 8 k + 2 (t % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_16x64f(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+
+__global__ void __launch_bounds__(kLaThreads, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+                       const LaParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kLaOffBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kLaNumBars);
+    int32_t *status = reinterpret_cast<int32_t *>(tmem_slot + 1);       // of this CTA, in shared memory
+    volatile uint8_t *votes = reinterpret_cast<volatile uint8_t *>(tmem_slot + 2);    // [tile & 1][warp]
+    int64_t *scan = reinterpret_cast<int64_t *>(smem + kLaOffAlpha);    // before the roles start only
+    volatile LaItem *items = reinterpret_cast<volatile LaItem *>(smem + kLaOffItems);
+    const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sP = smem_u32(smem + kLaOffP);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int my_lane = blockIdx.x / p.groups;               // run
+    const int group = blockIdx.x - my_lane * p.groups;       // head group
+
+    if (threadIdx.x < kLaNumBars) {
+        const int b = threadIdx.x;
+        int count = 1;
+        if (b == kLaPFull || b == kLaOFree || b == kLaVote || b == kLaMeet) count = 4;
+        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 6;   // MMA, Q, 4 softmax warps
+        mbar_init(&bars[b], count);
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&kv_map);
+        tma_prefetch_desc(&q_map);
+        *status = PKV_OK;
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, kLaTmemCols);
+        tmem_relinquish();
+    }
+    fence_barrier_init();
+
+    // this CTA's run [lo, hi) of the line of units, and the request that holds lo
+    bool bad = false;
+    int64_t units = 0;
+    const LaReq first_req = threadIdx.x < p.num_seqs ? la_request(p, threadIdx.x, bad) : LaReq{};
+    units = first_req.units;
+    for (int r = threadIdx.x + kLaThreads; r < p.num_seqs; r += kLaThreads) units += la_request(p, r, bad).units;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) units += __shfl_xor_sync(0xffffffffu, units, m);
+    if (lane == 0) scan[warp] = units;
+    const bool any_bad = __syncthreads_or(bad);
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kLaThreads / 32; ++w) total += scan[w];
+    const int64_t per = max(static_cast<int64_t>(1), (total + p.lanes - 1) / p.lanes);
+    const int64_t lo = min(total, my_lane * per), hi = min(total, lo + per);
+    __syncthreads();
+    if (threadIdx.x == 0) scan[8] = -1;
+    int64_t base = 0;
+    for (int r0 = 0; r0 < p.num_seqs && lo < hi; r0 += kLaThreads) {
+        const int r = r0 + threadIdx.x;
+        int64_t mine = first_req.units;
+        bool unused = false;
+        if (r0 > 0) mine = r < p.num_seqs ? la_request(p, r, unused).units : 0;
+        int64_t inc = mine;                                   // inclusive scan in the warp, then over the warps
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += y;
+        }
+        if (lane == 31) scan[warp] = inc;
+        __syncthreads();
+        int64_t before = base + inc - mine, all = base;
+#pragma unroll
+        for (int w = 0; w < kLaThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+        }
+        if (lo >= before && lo < before + mine) {
+            scan[8] = r;
+            scan[9] = lo - before;
+        }
+        base = all;
+        __syncthreads();
+        if (all > lo) break;                                  // uniform
+    }
+    int start_req = 0;
+    int64_t start_off = 0;
+    if (lo < hi) {
+        start_req = static_cast<int>(scan[8]);
+        start_off = scan[9];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // everything before this call is complete from here on: the cache write, the
+    // query, and the previous use of the workspace
+    pdl_wait();
+    const bool work = lo < hi;
+    int4 *desc = reinterpret_cast<int4 *>(p.ws + kLaWsDesc) + blockIdx.x;
+
+    if (warp == 0) {
+        // ---------------- walk of the run; pages through the block table ----------------
+        bool ok = true;
+        int r = start_req;
+        int64_t off = start_off, left = hi - lo, at = lo;     // at: position in the line
+        int gt = 0;                                           // key tiles of this CTA so far
+        int issued = 0;                                       // stages of copies issued
+        int4 split = make_int4(0, 0, 0, 0);                   // the row tile that starts here and ends in another lane
+        bool unused = false;
+        LaReq req = work ? la_request(p, r, unused) : LaReq{};
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kLaItemSlots;
+            if (k >= kLaItemSlots)
+                ok = __all_sync(0xffffffffu,
+                                pf_wait(&bars[kLaItemEmpty + slot], (k / kLaItemSlots - 1) & 1, status));
+            if (!ok) break;
+            LaItem it{};
+            if (left > 0) {
+                while (req.units == off) {                    // the next request with rows (there is one: left > 0)
+                    ++r;
+                    req = la_request(p, r, unused);
+                    off = 0;
+                }
+                // the row tile that holds `off`: largest j with units_before(j) <= off
+                int lo_j = 0, hi_j = req.n_full;
+                while (lo_j < hi_j) {
+                    const int mid = (lo_j + hi_j + 1) >> 1;
+                    if (la_units_before(req.ctx, p.tpt, mid) <= off) lo_j = mid;
+                    else hi_j = mid - 1;
+                }
+                const int64_t before = la_units_before(req.ctx, p.tpt, lo_j);
+                it.valid = 1;
+                it.tok0 = req.qs + lo_j * p.tpt;
+                it.ntok = min(p.tpt, req.q - lo_j * p.tpt);
+                it.lim0 = req.ctx + lo_j * p.tpt + 1;
+                it.n_kv = (it.lim0 + it.ntok - 1 + kLaKeys - 1) / kLaKeys;
+                it.kv0 = static_cast<int32_t>(off - before);
+                it.kv1 = static_cast<int32_t>(min(static_cast<int64_t>(it.n_kv), it.kv0 + left));
+                it.slot = it.kv0 > 0 ? 0 : (it.kv1 < it.n_kv ? 1 : -1);
+                if (it.slot == 1) {
+                    const int64_t last = (at + it.n_kv - 1) / per;       // lane of its last key tile
+                    split = make_int4(it.tok0, it.ntok, static_cast<int>(last - my_lane) + 1, 0);
+                }
+                const int n = it.kv1 - it.kv0;
+                off += n, at += n, left -= n;
+            }
+            if (lane == 0) {
+                volatile int32_t *dst = reinterpret_cast<volatile int32_t *>(items + slot);
+                const int32_t *src = reinterpret_cast<const int32_t *>(&it);
+#pragma unroll
+                for (int e = 0; e < static_cast<int>(sizeof(LaItem) / 4); ++e) dst[e] = src[e];
+                mbar_arrive(&bars[kLaItemFull + slot]);
+            }
+            if (!it.valid) break;
+            const int end = it.lim0 + it.ntok - 1;            // keys the tile's last token sees
+            const int n_pages = (end + kBlock - 1) / kBlock;
+            const int32_t *bt = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq;
+            // block ids in windows of 32 pages (8 key tiles), a lane each, the next
+            // window a window ahead; pages past the end, and ids outside the cache
+            // (reported), become -1 and load as zeros
+            auto load_window = [&](int w) -> int {
+                const int page = it.kv0 * kLaPages + w * 32 + lane;
+                if (page >= n_pages) return -1;
+                const int b = __ldg(bt + page);
+                if (b < 0 || b >= p.num_blocks) {
+                    set_status(status, PKV_ERR_DEVICE_INDEX);
+                    return -1;
+                }
+                return b;
+            };
+            int win_cur = load_window(0), win_next = load_window(1);
+            for (int j = it.kv0; j < it.kv1 && ok; ++j, ++gt) {
+                const int st = gt % kLaStages;
+                const int wofs = ((j - it.kv0) * kLaPages) % 32;
+                if (j > it.kv0 && wofs == 0) {
+                    win_cur = win_next;
+                    win_next = load_window((j - it.kv0) * kLaPages / 32 + 1);
+                }
+                const int page = __shfl_sync(0xffffffffu, win_cur, wofs + (lane & (kLaPages - 1)));
+                if (gt >= kLaStages)
+                    ok = __all_sync(0xffffffffu,
+                                    pf_wait(&bars[kLaKVEmpty + st], (gt / kLaStages - 1) & 1, status));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + st], kLaStage);
+                __syncwarp();
+                if (lane < kLaPages)
+                    tma_load_5d(smem + kLaOffKV + st * kLaStage + lane * kLatPageBytes, &kv_map,
+                                &bars[kLaKVFull + st], 0, 0, 0, 0, page);
+                issued = gt + 1;
+                if (j == it.n_kv - 1 && end % kBlock) {
+                    // zero the rows past the last visible key in its page
+                    ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaKVFull + st], (gt / kLaStages) & 1, status));
+                    if (!ok) break;
+                    const int first = end % kBlock, rows = kBlock - first;
+                    const uint32_t pg = sKV + st * kLaStage + ((end - 1) / kBlock - j * kLaPages) * kLatPageBytes;
+                    for (int e = lane; e < rows * kLaChunks * 8; e += 32) {
+                        const int t = first + e / (kLaChunks * 8), v = e % (kLaChunks * 8);
+                        const uint32_t a = pg + (t >> 3) * kLaGroup + (v >> 3) * 1024 + (t & 7) * 128 + (v & 7) * 16;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kLaFix + st]);
+                }
+            }
+        }
+        // (after a failed wait: the copies in flight land before the CTA ends)
+        for (int g = max(0, issued - kLaStages); g < issued && !ok; ++g)
+            mbar_wait_bounded(&bars[kLaKVFull + g % kLaStages], (g / kLaStages) & 1);
+        if (lane == 0) *desc = split;
+    } else if (warp == 1) {
+        // ---------------- MMA issue ----------------
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_bf16_f32(kLaRows, kLaKeys, 0, 0);
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(sKV, 16, kLaGroup);          // K-major, 8-key groups 9216 apart
+            const uint64_t dv = smem_desc_sw128(sKV, 1024, kLaGroup);        // MN-major, 64-dim chunks 1024 apart
+            const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
+            bool ok = true;
+            int gt0 = 0;
+            uint32_t fix_par = 0;
+            for (int k = 0; ok; ++k) {
+                const int slot = k % kLaItemSlots;
+                ok = pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status);
+                if (!ok) break;
+                const bool valid = items[slot].valid != 0;
+                const int n = items[slot].kv1 - items[slot].kv0;
+                const int rows = items[slot].ntok * p.hpt;
+                const int end = items[slot].lim0 + items[slot].ntok - 1;
+                const int fix_tile = (items[slot].kv1 == items[slot].n_kv && end % kBlock) ? n - 1 : -1;
+                mbar_arrive(&bars[kLaItemEmpty + slot]);
+                if (!valid) break;
+                // the second products' N: the tile's rows, in sixteens
+                const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 0);
+                ok = pf_wait(&bars[kLaQFull], k & 1, status);
+                int js = 0, jp = 0;
+                uint64_t t_idle = 0;
+                // S(j) once its stage has landed (S buffer j & 1 was read before the
+                // weights of tile j - 2 were written, and those products are issued
+                // before); the second products of j once its weights are written, the
+                // end tile is fixed and the previous item's O' has been read out.
+                while (ok && jp < n) {
+                    const bool s_can = js < n && js <= jp + 1;
+                    const bool p_can = jp < js;
+                    const int gs = gt0 + js, gp = gt0 + jp;
+                    if (s_can && mbar_test_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1)) {
+                        tc_fence_after();
+                        const uint64_t b0 = dk + ((gs % kLaStages) * (kLaStage >> 4));
+                        const uint32_t d = tmem + la_col_s(gs & 1);
+#pragma unroll
+                        for (int c = 0; c < kLaChunks; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_f16_ss(d, dq + c * (kLaQChunk >> 4) + kk * 2, b0 + c * (1024 >> 4) + kk * 2, kIdescS,
+                                            (c | kk) ? 1u : 0u);
+                        umma_commit(&bars[kLaSFull + (gs & 1)]);
+                        if (++js == n) umma_commit(&bars[kLaQEmpty]);
+                        t_idle = 0;
+                        continue;
+                    }
+                    if (p_can) {
+                        const int st = gp % kLaStages;
+                        bool ready = mbar_test_wait(&bars[kLaPFull], gp & 1);
+                        if (ready && jp == fix_tile) ready = mbar_test_wait(&bars[kLaFix + st], (fix_par >> st) & 1u);
+                        if (ready && jp == 0 && k > 0) ready = mbar_test_wait(&bars[kLaOFree], (k - 1) & 1);
+                        if (ready) {
+                            if (jp == fix_tile) fix_par ^= 1u << st;
+                            tc_fence_after();
+                            const uint64_t a0 = dv + st * (kLaStage >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < kLaPages; ++kk)
+#pragma unroll
+                                for (int m = 0; m < kLatent / 128; ++m)
+                                    umma_f16_ss(tmem + 64u * m, a0 + kk * (kLatPageBytes >> 4) + m * (2048 >> 4), dp + kk * 2,
+                                                idesc_o, (jp > 0 || kk > 0) ? 1u : 0u);
+                            umma_commit(&bars[kLaODone]);
+                            umma_commit(&bars[kLaKVEmpty + st]);
+                            ++jp;
+                            t_idle = 0;
+                            continue;
+                        }
+                    }
+                    if (p_can)
+                        mbar_try_wait_for(&bars[kLaPFull], gp & 1, 200);
+                    else
+                        mbar_try_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1);
+                    const uint64_t now = global_ns();
+                    if (t_idle == 0) {
+                        t_idle = now;
+                    } else if (now - t_idle > kWaitLimitNs) {
+                        set_status(status, PKV_ERR_DEVICE_TIMEOUT);
+                        ok = false;
+                    }
+                }
+                gt0 += n;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---------------- Q of each item, once the previous item's last S has read it ----------------
+        bool ok = true;
+        int loaded = 0;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kLaItemSlots;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            if (!ok) break;
+            const bool valid = items[slot].valid != 0;
+            const int tok0 = items[slot].tok0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+            if (!valid) break;
+            if (k > 0) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaQEmpty], (k - 1) & 1, status));
+            if (!ok) break;
+            // a box is 64 dims of the group's heads of tpt tokens; tokens past the batch
+            // and heads past the last load as zeros, rows that no item holds are masked
+            if (lane == 0) mbar_arrive_expect_tx(&bars[kLaQFull], kLaChunks * 128 * p.hpt * p.tpt);
+            __syncwarp();
+            if (lane < kLaChunks)
+                tma_load_3d(smem + kLaOffQ + lane * kLaQChunk, &q_map, &bars[kLaQFull], lane * 64, group * p.hpt, tok0);
+            loaded = k + 1;
+        }
+        if (loaded > 0) mbar_wait_bounded(&bars[kLaQFull], (loaded - 1) & 1);    // landed before the CTA ends
+    } else if (warp >= 4) {
+        // ---------------- softmax and epilogue ----------------
+        const int quad = warp - 4;
+        const float NEG_INF = -__int_as_float(0x7f800000);
+        float *alphas = reinterpret_cast<float *>(smem + kLaOffAlpha);
+        float *row_inv = reinterpret_cast<float *>(smem + kLaOffRow);
+        int *row_dst = reinterpret_cast<int *>(row_inv + kLaRows);
+        const int rA = quad * 16 + (lane >> 2);              // this thread's rows: rA and rA + 8
+        const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const float sl2 = p.scale_log2;
+        const int heads_here = min(p.hpt, p.heads - group * p.hpt);
+        bool ok = true;
+        int gt = 0, k = 0;
+        for (;; ++k) {
+            const int slot = k % kLaItemSlots;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            if (!ok) break;
+            const volatile LaItem *cur = items + slot;
+            if (!cur->valid) break;
+            const int kv0 = cur->kv0, kv1 = cur->kv1, ntok = cur->ntok, lim0 = cur->lim0, tok0 = cur->tok0;
+            const int part = cur->slot;
+            const int rows = ntok * p.hpt;
+            int lim[2], dst[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = rA + 8 * i, tok = row / p.hpt, h = row - tok * p.hpt;
+                const bool in = row < rows && h < heads_here;
+                lim[i] = in ? lim0 + tok : 0;
+                dst[i] = in ? (tok0 + tok) * p.heads + group * p.hpt + h : -1;
+            }
+            float m_ref[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};
+            for (int j = kv0; j < kv1 && ok; ++j, ++gt) {
+                const int sb = gt & 1;
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaSFull + sb], (gt >> 1) & 1, status));
+                if (!ok) break;
+                tc_fence_after();
+                float s[32];
+                tmem_ld_16x64f(tlane + la_col_s(sb), s);
+                tmem_ld_wait();
+                const int key0 = j * kLaKeys + 2 * (lane & 3);
+                const bool masked = __any_sync(0xffffffffu, (j + 1) * kLaKeys > min(lim[0], lim[1]));
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] *= sl2;
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (key0 + (e >> 2) * 8 + (e & 1) >= lim[(e >> 1) & 1]) s[e] = NEG_INF;
+                }
+                float mx[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float a = fmaxf(s[2 * i], s[2 * i + 1]), b = fmaxf(s[4 + 2 * i], s[4 + 2 * i + 1]);
+#pragma unroll
+                    for (int c = 8; c < 32; c += 8) {
+                        a = fmax3(a, s[c + 2 * i], s[c + 2 * i + 1]);
+                        b = fmax3(b, s[c + 4 + 2 * i], s[c + 4 + 2 * i + 1]);
+                    }
+                    mx[i] = fmaxf(a, b);
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                }
+                // The reference moves on a row's first visible key, and then only when the
+                // tile's max exceeds it by 2^40: fp32 sums and bf16 weights keep their
+                // relative accuracy at any common scale, and 2^40 leaves 2^87 of range.
+                bool grow = false;
+                float alpha[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool first = m_ref[i] == NEG_INF;
+                    const bool g = !first && mx[i] > m_ref[i] + 40.f;
+                    alpha[i] = g ? fast_exp2(m_ref[i] - mx[i]) : 1.f;
+                    if (first || g) m_ref[i] = mx[i];
+                    l[i] *= alpha[i];
+                    grow |= g;
+                }
+                // the warps' votes on a rescale of O' (its columns are rows of every warp)
+                if ((lane & 3) == 0) {
+                    alphas[sb * kLaRows + rA] = alpha[0];
+                    alphas[sb * kLaRows + rA + 8] = alpha[1];
+                }
+                grow = __any_sync(0xffffffffu, grow);
+                if (lane == 0) {
+                    votes[4 * sb + quad] = grow ? 1 : 0;
+                    mbar_arrive(&bars[kLaVote]);
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float ref = m_ref[i] == NEG_INF ? 0.f : m_ref[i];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float a = fast_exp2(s[4 * c + 2 * i] - ref), b = fast_exp2(s[4 * c + 2 * i + 1] - ref);
+                        sum += a + b;
+                        w[2 * c + i] = pack_bf16x2(a, b);
+                    }
+                    l[i] += sum;
+                }
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaVote], gt & 1, status));
+                // the weights' buffer and O' are free once the previous tile's products completed
+                if (ok && gt > 0) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
+                if (!ok) break;
+                if (*reinterpret_cast<volatile const uint32_t *>(votes + 4 * sb) && j > kv0) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {             // 32 rows of one 128-dim block at a time
+                        uint32_t v[32];
+                        const uint32_t a = tlane + 64u * (c >> 1) + 32u * (c & 1);
+                        tmem_ld32(a, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * alphas[sb * kLaRows + 32 * (c & 1) + e]);
+                        tmem_st32(a, v);
+                    }
+                    tmem_st_wait();
+                }
+                // weights of row rA (+ 8), keys 8 c + 2 (lane % 4) + {0, 1}: K-major rows of 64 keys
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t a = sP + rA * 128 + ((c ^ (rA & 7)) << 4) + (lane & 3) * 4;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[2 * c]) : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a + 1024), "r"(w[2 * c + 1]) : "memory");
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaPFull]);
+            }
+            // epilogue
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                }
+                if ((lane & 3) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = rA + 8 * i;
+                        row_inv[row] = l[i] > 0.f ? 1.f / l[i] : 0.f;
+                        row_dst[row] = dst[i];
+                        if (part >= 0) {
+                            float *ml = reinterpret_cast<float *>(p.ws + kLaWsMl) +
+                                        (static_cast<int64_t>(blockIdx.x) * 2 + part) * 2 * kLaRows;
+                            ml[row] = m_ref[i];
+                            ml[kLaRows + row] = l[i];
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaMeet]);
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaMeet], k & 1, status));
+            }
+            if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
+            if (ok) {
+                tc_fence_after();
+                float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
+                            (static_cast<int64_t>(blockIdx.x) * 2 + max(part, 0)) * kLaPartFloats;
+                const int dim = quad * 32 + lane;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const int m = c >> 1, r0 = 32 * (c & 1);
+                    if (r0 >= rows) continue;
+                    float v[32];
+                    tmem_ld32f(tlane + 64u * m + r0, v);
+                    tmem_ld_wait();
+                    if (part >= 0) {
+                        // [128-dim block][row / 4][dim][row % 4]
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (r0 + e < rows)
+                                *reinterpret_cast<float4 *>(po + ((m * 16 + (r0 + e) / 4) * 128 + dim) * 4) =
+                                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    } else {
+                        // neighbouring lanes exchange a row each: 4-byte stores, 64 bytes a row
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float a = v[e] * row_inv[r0 + e], b = v[e + 1] * row_inv[r0 + e + 1];
+                            const bool odd = lane & 1;
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                            const int row = row_dst[r0 + e + (odd ? 1 : 0)];
+                            if (row >= 0)
+                                *reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(row) * kLatent + m * 128 +
+                                                              (dim & ~1)) =
+                                    odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaOFree]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+            if (!ok) break;
+        }
+    }
+
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kLaTmemCols);
+    }
+    if (threadIdx.x == 0) {
+        int32_t s = *reinterpret_cast<volatile int32_t *>(status);
+        if (s == PKV_OK && any_bad) s = PKV_ERR_DEVICE_METADATA;
+        reinterpret_cast<int32_t *>(p.ws + kLaWsStatus)[blockIdx.x] = s;
+    }
+}
+
+// Merge of the row tiles that run across lanes, and the call's status word.
+// Piece i of the tile that starts in CTA c lies in CTA c + i * groups, slot 1
+// for the first and 0 for the others:
+//     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
+// blockIdx.y: 128 dims x 16 rows; a thread takes four rows of one dim at a time.
+__global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, int ctas) {
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+        int32_t s = 0;
+        for (int c = threadIdx.x; c < ctas; c += 32) {
+            const int32_t x = reinterpret_cast<const int32_t *>(p.ws + kLaWsStatus)[c];
+            s = s ? s : x;
+        }
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int32_t y = __shfl_down_sync(0xffffffffu, s, m);
+            s = s ? s : y;
+        }
+        if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = s;
+    }
+    const int cta = blockIdx.x;
+    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
+    const int pieces = d.z;
+    if (pieces == 0) return;
+    const int group = cta % p.groups;
+    const int rows = d.y * p.hpt, heads_here = min(p.hpt, p.heads - group * p.hpt);
+    const int m = blockIdx.y >> 2, dim = threadIdx.x & 127;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl);
+    const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO);
+    auto part_of = [&](int i) { return static_cast<int64_t>(cta + i * p.groups) * 2 + (i == 0 ? 1 : 0); };
+#pragma unroll 1
+    for (int q = threadIdx.x >> 7; q < 4; q += 2) {
+        const int r4 = (blockIdx.y & 3) * 4 + q;
+        if (r4 * 4 >= rows) return;
+        float M[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll 4
+        for (int i = 0; i < pieces; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(ml + part_of(i) * 2 * kLaRows + r4 * 4);
+            M[0] = fmaxf(M[0], x.x), M[1] = fmaxf(M[1], x.y), M[2] = fmaxf(M[2], x.z), M[3] = fmaxf(M[3], x.w);
+        }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f}, L[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = 0; i < pieces; ++i) {
+            const int64_t part = part_of(i);
+            const float4 x = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + r4 * 4);
+            const float4 y = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + kLaRows + r4 * 4);
+            const float4 v = *reinterpret_cast<const float4 *>(o + part * kLaPartFloats + ((m * 16 + r4) * 128 + dim) * 4);
+            const float mx[4] = {x.x, x.y, x.z, x.w}, ls[4] = {y.x, y.y, y.z, y.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float w = mx[e] == NEG_INF ? 0.f : fast_exp2(mx[e] - M[e]);
+                L[e] = fmaf(w, ls[e], L[e]);
+                acc[e] = fmaf(w, w == 0.f ? 0.f : vs[e], acc[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = r4 * 4 + e, tok = row / p.hpt, h = row - tok * p.hpt;
+            if (row < rows && h < heads_here)
+                p.out[(static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent + m * 128 + dim] =
+                    __float2bfloat16_rn(L[e] > 0.f ? acc[e] / L[e] : 0.f);
+        }
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+// {64 dims, 8 tokens, 9 chunks, 2 halves, blocks}: a box {64, 8, 9, 2, 1} is one page.
+static int make_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t dims[5] = {64, 8, kLaChunks, 2, static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t strides[4] = {kLatRowBytes, 128, 8 * kLatRowBytes, kLatPageBytes};
+    const cuuint32_t box[5] = {64, 8, kLaChunks, 2, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+// {576 dims, heads, tokens}: a box is 64 dims of hpt heads of tpt tokens.
+static int make_latent_query_map(CUtensorMap *map, const void *query, int64_t q_stride, const LaParams &p) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t dims[3] = {kLatRow, static_cast<cuuint64_t>(p.heads), static_cast<cuuint64_t>(p.num_tokens)};
+    const cuuint64_t strides[2] = {kLatRowBytes, static_cast<cuuint64_t>(q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.hpt), static_cast<cuuint32_t>(p.tpt)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(query), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stride,
+                                     const void *latent_cache, int64_t num_blocks, const int32_t *block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                     const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t max_query_len, int32_t max_seq_len, int32_t num_heads,
+                                     int32_t block_size, float scale, void *workspace, size_t workspace_bytes,
+                                     size_t *workspace_needed, void *stream) {
+    using namespace pkv;
+    if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || max_seq_len < 0 || max_blocks_per_seq < 0 ||
+        num_heads <= 0 || num_blocks <= 0)
+        return PKV_ERR_SHAPE;
+    if (block_size != kBlock || num_heads > kLaMaxHeads) return PKV_ERR_UNSUPPORTED;
+    if (num_blocks > INT32_MAX || static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX) return PKV_ERR_SHAPE;
+    if (!(scale > -3.0e38f && scale < 3.0e38f)) return PKV_ERR_SHAPE;
+    if (num_seqs == 0) return num_tokens ? PKV_ERR_SHAPE : PKV_OK;
+    if (max_query_len > max_seq_len || max_seq_len > INT32_MAX - 128) return PKV_ERR_SHAPE;
+    if ((static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock > max_blocks_per_seq) return PKV_ERR_SHAPE;
+    if (workspace_needed) *workspace_needed = kLaWsBytes;
+    if (!workspace || workspace_bytes < static_cast<size_t>(kLaWsBytes)) return PKV_ERR_WORKSPACE;
+    if (!block_tables || !seq_lens || !query_start_loc || !latent_cache) return PKV_ERR_NULL;
+    if (num_tokens > 0 && (!out || !query)) return PKV_ERR_NULL;
+    if (query_token_stride < static_cast<int64_t>(num_heads) * kLatRow) return PKV_ERR_SHAPE;
+    if (query_token_stride >= (int64_t(1) << 38)) return PKV_ERR_SHAPE;
+    if (query_token_stride % 8) return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(query) |
+         reinterpret_cast<uintptr_t>(latent_cache)) & 15u)
+        return PKV_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
+         reinterpret_cast<uintptr_t>(query_start_loc)) & 3u)
+        return PKV_ERR_ALIGNMENT;
+
+    LaParams p;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.seq_lens = seq_lens, p.qsl = query_start_loc;
+    p.num_seqs = num_seqs, p.num_tokens = num_tokens;
+    p.max_query_len = max_query_len, p.max_seq_len = max_seq_len;
+    p.heads = num_heads;
+    p.groups = (num_heads + kLaRows - 1) / kLaRows;
+    p.hpt = (num_heads + p.groups - 1) / p.groups;
+    p.tpt = 1;
+    if (p.groups == 1)
+        while (2 * p.tpt * p.hpt <= kLaRows && p.tpt < max_query_len) p.tpt *= 2;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.ws = static_cast<uint8_t *>(workspace);
+
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
+    p.lanes = (sms < kLaMaxCtas ? sms : kLaMaxCtas) / p.groups;
+    const int ctas = p.lanes * p.groups;
+    CUtensorMap kvm, qm;
+    int rc = make_latent_map(&kvm, latent_cache, num_blocks);
+    if (rc) return rc;
+    if (num_tokens > 0) {
+        rc = make_latent_query_map(&qm, query, query_token_stride, p);
+        if (rc) return rc;
+    } else {
+        qm = kvm;                                  // no rows: not read
+    }
+    static std::mutex mu;
+    static uint64_t done_mask = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+        if (!bit || !(done_mask & bit)) {
+            if (cudaFuncSetAttribute(latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaSmem) !=
+                cudaSuccess)
+                return PKV_ERR_CUDA;
+            done_mask |= bit;
+        }
+    }
+    if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
+                   static_cast<cudaStream_t>(stream), kvm, qm, p) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    if (launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(ctas), 16), dim3(256), 0,
+                   static_cast<cudaStream_t>(stream), p, ctas) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    return PKV_OK;
+}
