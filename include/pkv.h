@@ -555,6 +555,47 @@ int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stri
                           void *workspace, size_t workspace_bytes, size_t *workspace_needed,
                           void *stream);
 
+/*
+ * pkv_latent_attn_expanded — causal attention over per-head keys and values
+ * made of latent rows (the expanded form of latent attention), for long
+ * chunks.  Request r owns query tokens [query_start_loc[r], query_start_loc[r+1])
+ * (q_r of them) and keys [key_start_loc[r], key_start_loc[r+1]) (L_r >= q_r: its
+ * cached context, then the chunk); its i-th query sees the keys j <= L_r - q_r + i:
+ *     s_j          = scale * (<query[t][h][0 .. 127], key[j][h]>
+ *                             + <query[t][h][128 .. 191], key_rope[j]>)
+ *     out[t][h][:] = sum_j softmax_j(s_j) * value[j][h][:]
+ * pkv_latent_gather gives the rows of cached requests in this order: key and
+ * value are their first 512 dims times the up-projection, key_rope is the last
+ * 64 (a view of the gathered rows).  Arithmetic as pkv_latent_paged_attn.
+ *
+ *  out               bf16 [num_tokens][num_heads][128], contiguous; rows that no request
+ *                    owns are left as they were.
+ *  query             bf16; token t, head h at ptr + t*token_stride + h*192 (128 plain
+ *                    dims, then 64 rotated ones).
+ *  key, value        bf16; key row j, head h at ptr + j*token_stride + h*head_stride, 128
+ *                    dims (views of one projection's output, or head-major).
+ *  key_rope          bf16; 64 dims at ptr + j*token_stride, shared by the heads.
+ *  query_start_loc, key_start_loc
+ *                    int32 [num_seqs + 1], non-decreasing, the last at most num_tokens
+ *                    and num_keys.
+ *  max_query_len, max_key_len
+ *                    host-side bounds of q_r and L_r.  A request that breaks them, or
+ *                    has fewer keys than queries, is left unwritten.
+ *  device_status     optional int32 device word, never cleared by the library:
+ *                    PKV_ERR_DEVICE_METADATA for such a request.
+ * Values of a request's keys must be finite; what lies between or behind the
+ * requests' rows may be anything.  Pointers are 16-byte aligned, strides
+ * multiples of 8.  No workspace.
+ */
+int pkv_latent_attn_expanded(void *out, const void *query, int64_t query_token_stride,
+                             const void *key, int64_t key_token_stride, int64_t key_head_stride,
+                             const void *key_rope, int64_t key_rope_token_stride,
+                             const void *value, int64_t value_token_stride, int64_t value_head_stride,
+                             const int32_t *query_start_loc, const int32_t *key_start_loc,
+                             int32_t num_seqs, int32_t num_tokens, int32_t num_keys,
+                             int32_t max_query_len, int32_t max_key_len,
+                             int32_t num_heads, float scale, int32_t *device_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ Calls (same names as the C ABI without the ``pkv_`` prefix):
   cache write, in one pass)
 * ``latent_kv_write`` / ``latent_paged_attn`` / ``latent_gather`` (a cache of one latent row a token, and attention
   over it in the latent space)
+* ``latent_attn_expanded`` (attention over the per-head keys and values that gathered latent rows expand to)
 
 plus ``paged_attn_workspace_size(...)`` (the C call's size query) and
 ``workspace_status(workspace)`` (reads the device status word).
@@ -43,7 +44,7 @@ __all__ = [
     "paged_attn_noalloc", "paged_attn_shared_prefix", "paged_attn_shared_prefix_workspace_size",
     "kv_write_fp8", "paged_attn_fp8", "paged_attn_shared_prefix_fp8", "workspace_schedule",
     "qk_norm_rope_kv_write", "qk_norm_rope_kv_write_fp8", "LATENT_DIM", "LATENT_ROPE_DIM", "latent_kv_write",
-    "latent_gather", "latent_paged_attn", "latent_paged_attn_workspace_size",
+    "latent_gather", "latent_paged_attn", "latent_paged_attn_workspace_size", "latent_attn_expanded",
 ]
 
 BLOCK_SIZE = 16
@@ -118,6 +119,9 @@ def load():
         lib.pkv_latent_paged_attn.argtypes = [P, P, i64, P, i64, P, i32, P, P, i32, i32, i32, i32, i32, i32, f32, P,
                                               ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), P]
         lib.pkv_latent_paged_attn.restype = ctypes.c_int
+        lib.pkv_latent_attn_expanded.argtypes = [P, P, i64, P, i64, i64, P, i64, P, i64, i64, P, P, i32, i32, i32, i32,
+                                                 i32, i32, f32, P, P]
+        lib.pkv_latent_attn_expanded.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -584,3 +588,39 @@ def latent_paged_attn(out: torch.Tensor, query: torch.Tensor, latent_cache: torc
           _ptr(latent_cache), nb, _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens),
           _ptr(query_start_loc), S, T, int(max_query_len), int(max_seq_len), H, bs, float(scale), _ptr(workspace),
           workspace.numel() * workspace.element_size(), None)
+
+
+_NOPE, _VALUE = 128, 128        # plain key dims and value dims of a head in the expanded form
+
+
+def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, key_rope: torch.Tensor,
+                         value: torch.Tensor, query_start_loc: torch.Tensor, key_start_loc: torch.Tensor,
+                         max_query_len: int, max_key_len: int, scale: float,
+                         device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Causal attention of query [T, H, 192] over key [K, H, 128], key_rope [K, 64] (shared by the heads) and
+    value [K, H, 128], requests side by side; out [T, H, 128] bf16."""
+    dev, bf = query.device, torch.bfloat16
+    _expect("query", query, bf, 3, dev)
+    T, H, D = query.shape
+    if D != _NOPE + LATENT_ROPE_DIM or query.stride(2) != 1 or (H > 1 and query.stride(1) != D):
+        raise ValueError(f"query must be [T, H, {_NOPE + LATENT_ROPE_DIM}] with contiguous heads")
+    _expect("key_rope", key_rope, bf, 2, dev)
+    K = int(key_rope.shape[0])
+    for what, x, width in (("key", key, _NOPE), ("value", value, _VALUE)):
+        _expect(what, x, bf, 3, dev)
+        if tuple(x.shape) != (K, H, width) or x.stride(2) != 1:
+            raise ValueError(f"{what} must be [{K}, {H}, {width}] with contiguous rows")
+    if key_rope.shape[1] != LATENT_ROPE_DIM or key_rope.stride(1) != 1:
+        raise ValueError(f"key_rope must be [K, {LATENT_ROPE_DIM}] with contiguous rows")
+    _expect("out", out, bf, 3, dev)
+    _contiguous("out", out, (T, H, _VALUE))
+    S = int(query_start_loc.shape[0]) - 1
+    for what, x in (("query_start_loc", query_start_loc), ("key_start_loc", key_start_loc)):
+        _expect(what, x, torch.int32, 1, dev)
+        _contiguous(what, x, (S + 1,))
+    _expect("device_status", device_status, torch.int32, 1, dev)
+    kh, vh = _step(key, 1, _NOPE), _step(value, 1, _VALUE)
+    _call(dev, stream, load().pkv_latent_attn_expanded, _ptr(out), _ptr(query), _step(query, 0, H * D),
+          _ptr(key), _step(key, 0, _NOPE), kh, _ptr(key_rope), _step(key_rope, 0, LATENT_ROPE_DIM), _ptr(value),
+          _step(value, 0, _VALUE), vh, _ptr(query_start_loc), _ptr(key_start_loc), S, T, K, int(max_query_len),
+          int(max_key_len), H, float(scale), _ptr(device_status))

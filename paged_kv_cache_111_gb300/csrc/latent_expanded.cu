@@ -1,0 +1,484 @@
+// Causal attention over per-head keys and values that were expanded from latent
+// rows (the expanded form of latent attention), on the 5th-generation tensor
+// cores.
+//
+// Request r owns query tokens [query_start_loc[r], [r + 1]) (q of them) and keys
+// [key_start_loc[r], [r + 1]) (L >= q); its i-th query sees keys 0 .. L - q + i.
+// For head h, with query rows of 128 plain and 64 rotated dims,
+//     s_j       = scale (<query[t][h][0 .. 127], key[j][h]> + <query[t][h][128 ..], key_rope[j]>)
+//     out[t][h] = sum_j softmax_j(s_j) value[j][h]
+// The rotated part of a key is one row for all heads and is read as such: the
+// 192-wide keys of each head are put together in shared memory only.
+//
+// A CTA takes 256 tokens of one head of one request as two 128-row tiles that
+// share every key tile.  Per 128-key tile and row tile: S = Q K^T (12
+// tcgen05.mma 128 x 128 x 16, shared memory), softmax by four warps (a row per
+// thread), P as bf16 over S in tensor memory, O += P V (8 tcgen05.mma 128 x 128
+// x 16, P from tensor memory).  The two row tiles take turns: while one's
+// softmax works, the tensor cores have the other's products.  Tensor memory: S
+// of both tiles, O of both tiles (512 columns).  Shared memory: Q of both (96
+// KiB), two stages of K (96 KiB), one of V (32 KiB).
+//
+// Against the latent-space form this does (128 + 64 + 128) / (576 + 512) = 0.29
+// of the products per visible pair, and reads keys per head: the form for long
+// chunks, where a key is used by many rows.
+//
+// Warp roles (384 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warp 2
+// owns tensor memory, warps 4-7 and 8-11 are the softmax and epilogue of the
+// two row tiles.  V rows past the last visible key are zeroed in shared memory
+// (they belong to other requests, or to nobody).  Every wait is bounded.
+#include <mutex>
+
+#include "latent_common.cuh"
+#include "prefill_common.cuh"
+
+namespace pkv {
+
+constexpr int kExNope = 128, kExDim = kExNope + kLatRope, kExV = 128;
+constexpr int kExRows = 128, kExKeys = 128;             // of a row tile, of a key tile
+constexpr int kExTokens = 2 * kExRows;                  // of a CTA
+constexpr int kExChunk = 128 * 128;                     // 64 dims of 128 rows: 16 KiB
+constexpr int kExQ = 3 * kExChunk, kExK = 3 * kExChunk, kExVTile = 2 * kExChunk;
+constexpr int kExThreads = 384;
+
+constexpr int kExOffQ = 0;
+constexpr int kExOffK = kExOffQ + 2 * kExQ;
+constexpr int kExOffV = kExOffK + 2 * kExK;
+constexpr int kExOffBar = kExOffV + kExVTile;           // 229376
+constexpr int kExSmem = kExOffBar + 512 + 1024;         // with alignment slack
+static_assert(kExSmem <= 227 * 1024, "shared memory of one CTA");
+
+enum ExBar {
+    kExQFull = 0,        // (+ row tile)
+    kExKFull = 2,        // (+ stage)
+    kExKEmpty = 4,       // (+ stage)
+    kExVFull = 6, kExVEmpty = 7, kExFix = 8,
+    kExSFull = 9,        // (+ row tile)
+    kExPFull = 11,       // (+ row tile)
+    kExODone = 13,       // (+ row tile)
+    kExNumBars = 15
+};
+
+struct ExParams {
+    __nv_bfloat16 *out;
+    const int32_t *qsl, *ksl;
+    int32_t num_seqs, num_tokens, num_keys, max_query_len, max_key_len, heads;
+    int32_t tiles;            // upper bound of the CTAs' token tiles over all requests
+    float scale_log2;
+    int32_t *status;
+};
+
+struct ExReq {
+    int32_t qs, q, ks, L;
+    bool ok;
+};
+__device__ __forceinline__ ExReq ex_request(const ExParams &p, int r) {
+    ExReq a;
+    a.qs = __ldg(p.qsl + r);
+    a.q = __ldg(p.qsl + r + 1) - a.qs;
+    a.ks = __ldg(p.ksl + r);
+    a.L = __ldg(p.ksl + r + 1) - a.ks;
+    a.ok = a.qs >= 0 && a.q >= 0 && a.qs + a.q <= p.num_tokens && a.ks >= 0 && a.L >= a.q &&
+           a.ks + a.L <= p.num_keys && a.q <= p.max_query_len && a.L <= p.max_key_len;
+    return a;
+}
+
+__global__ void __launch_bounds__(kExThreads, 1)
+    latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                           const __grid_constant__ CUtensorMap r_map, const __grid_constant__ CUtensorMap v_map,
+                           const ExParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kExOffBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kExNumBars);
+    int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
+    const uint32_t sQ = smem_u32(smem + kExOffQ), sK = smem_u32(smem + kExOffK), sV = smem_u32(smem + kExOffV);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the last tiles of a request see the most keys: they go first
+    const int head = blockIdx.x % p.heads;
+    const int tile = p.tiles - 1 - blockIdx.x / p.heads;
+    int32_t *status = p.status;
+
+    pdl_trigger();
+    // the request whose token tile this is (tiles of 256 tokens, request after request)
+    int base = 0;
+    if (threadIdx.x == 0) scan[16] = -1;
+    for (int r0 = 0; r0 < p.num_seqs; r0 += kExThreads) {
+        const int r = r0 + threadIdx.x;
+        int mine = 0;
+        if (r < p.num_seqs) {
+            const ExReq a = ex_request(p, r);
+            mine = a.ok ? (a.q + kExTokens - 1) / kExTokens : 0;
+            if (!a.ok && blockIdx.x == 0) set_status(status, PKV_ERR_DEVICE_METADATA);
+        }
+        int inc = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += y;
+        }
+        if (lane == 31) scan[warp] = inc;
+        __syncthreads();
+        int before = base + inc - mine, all = base;
+#pragma unroll
+        for (int w = 0; w < kExThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+        }
+        if (tile >= before && tile < before + mine) {
+            scan[16] = r;
+            scan[17] = tile - before;
+        }
+        base = all;
+        __syncthreads();
+        // (the first CTA looks at every request, to report the bad ones)
+        if (all > tile && blockIdx.x != 0) break;
+    }
+    __syncthreads();
+    const int r = scan[16];
+    if (r < 0) return;                                  // the bound was not reached: uniform
+    const ExReq req = ex_request(p, r);
+    const int t0 = scan[17] * kExTokens;                // first token, within the request
+    const int ctx = req.L - req.q;
+    // rows and key tiles of the two row tiles
+    const int rows[2] = {min(kExRows, req.q - t0), max(0, min(kExRows, req.q - t0 - kExRows))};
+    const int n[2] = {(ctx + t0 + rows[0] + kExKeys - 1) / kExKeys,
+                      rows[1] ? (ctx + t0 + kExRows + rows[1] + kExKeys - 1) / kExKeys : 0};
+    const int n_all = max(n[0], n[1]);
+    const int end = ctx + t0 + rows[0] + rows[1];       // keys the last row sees
+    const bool fix = end % kExKeys != 0;
+
+    if (threadIdx.x < kExNumBars)
+        mbar_init(&bars[threadIdx.x], threadIdx.x >= kExPFull && threadIdx.x < kExPFull + 2 ? 4 : 1);
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    fence_barrier_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();                                         // the inputs are complete
+
+    if (warp == 0) {
+        // ---------------- loads ----------------
+        bool ok = true;
+        int k_issued = 0, v_issued = 0;
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (rows[i]) {
+                    mbar_arrive_expect_tx(&bars[kExQFull + i], kExQ);
+                    for (int c = 0; c < 3; ++c)
+                        tma_load_3d(smem + kExOffQ + i * kExQ + c * kExChunk, &q_map, &bars[kExQFull + i], c * 64, head,
+                                    req.qs + t0 + i * kExRows);
+                }
+        }
+        for (int j = 0; j < n_all && ok; ++j) {
+            const int st = j & 1, key0 = req.ks + j * kExKeys;
+            if (j >= 2) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExKEmpty + st], (j / 2 - 1) & 1, status));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[kExKFull + st], kExK);
+                uint8_t *dst = smem + kExOffK + st * kExK;
+                tma_load_3d(dst, &k_map, &bars[kExKFull + st], 0, head, key0);
+                tma_load_3d(dst + kExChunk, &k_map, &bars[kExKFull + st], 64, head, key0);
+                tma_load_3d(dst + 2 * kExChunk, &r_map, &bars[kExKFull + st], 0, 0, key0);
+            }
+            k_issued = j + 1;
+            if (j >= 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVEmpty], (j - 1) & 1, status));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[kExVFull], kExVTile);
+                tma_load_3d(smem + kExOffV, &v_map, &bars[kExVFull], 0, head, key0);
+                tma_load_3d(smem + kExOffV + kExChunk, &v_map, &bars[kExVFull], 64, head, key0);
+            }
+            v_issued = j + 1;
+            if (fix && j == n_all - 1) {
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVFull], j & 1, status));
+                if (!ok) break;
+                const int first = end - j * kExKeys;
+                for (int e = lane; e < (kExKeys - first) * 16; e += 32) {
+                    const uint32_t a = sV + ((e & 15) >> 3) * kExChunk + (first + (e >> 4)) * 128 + (e & 7) * 16;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kExFix]);
+            }
+        }
+        if (!ok) {                                      // the copies in flight land before the CTA ends
+            for (int i = 0; i < 2; ++i)
+                if (rows[i]) mbar_wait_bounded(&bars[kExQFull + i], 0);
+            for (int j = max(0, k_issued - 2); j < k_issued; ++j) mbar_wait_bounded(&bars[kExKFull + (j & 1)], (j / 2) & 1);
+            if (v_issued) mbar_wait_bounded(&bars[kExVFull], (v_issued - 1) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issue ----------------
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
+            constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
+            bool ok = true;
+            auto issue_s = [&](int i, int j) {
+                const uint64_t a = dq + i * (kExQ >> 4), b = dk + (j & 1) * (kExK >> 4);
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ss(tmem + 128u * i, a + c * (kExChunk >> 4) + kk * 2, b + c * (kExChunk >> 4) + kk * 2,
+                                    kIdescS, (c | kk) ? 1u : 0u);
+                umma_commit(&bars[kExSFull + i]);
+            };
+            auto issue_pv = [&](int i, int j) {
+#pragma unroll
+                for (int kk = 0; kk < kExKeys / 16; ++kk)
+                    umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, dv + kk * (2048 >> 4), kIdescO,
+                                (j > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(&bars[kExODone + i]);
+            };
+            ok = pf_wait(&bars[kExKFull], 0, status);
+            for (int i = 0; i < 2 && ok; ++i)
+                if (n[i]) {
+                    ok = pf_wait(&bars[kExQFull + i], 0, status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(i, 0);
+                }
+            umma_commit(&bars[kExKEmpty]);
+            // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
+            for (int j = 0; j < n_all && ok; ++j) {
+                ok = pf_wait(&bars[kExVFull], j & 1, status);
+                if (ok && fix && j == n_all - 1) ok = pf_wait(&bars[kExFix], 0, status);
+                if (ok && j + 1 < n_all) ok = pf_wait(&bars[kExKFull + ((j + 1) & 1)], ((j + 1) / 2) & 1, status);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok || j >= n[i]) continue;
+                    ok = pf_wait(&bars[kExPFull + i], j & 1, status);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_pv(i, j);
+                    if (j + 1 < n[i]) issue_s(i, j + 1);
+                }
+                umma_commit(&bars[kExVEmpty]);
+                if (j + 1 < n_all) umma_commit(&bars[kExKEmpty + ((j + 1) & 1)]);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---------------- softmax (a row per thread) and epilogue ----------------
+        const int i = (warp - 4) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const bool mine = row < rows[i];
+        const int lim = mine ? ctx + t0 + i * kExRows + row + 1 : 0;      // keys this row sees
+        const float NEG_INF = -__int_as_float(0x7f800000);
+        const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * i;
+        const uint32_t tO = tS + 256u;
+        // |scale| and a flip of the scores, so that the largest score has the largest
+        // weight; not quite 0, so that masked scores stay -inf
+        const float sl2 = fmaxf(fabsf(p.scale_log2), 1.2e-38f);
+        float m_ref = NEG_INF, l = 0.f;
+        bool ok = true;
+        const int n_mine = n[i];
+        for (int j = 0; j < n_mine && ok; ++j) {
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kExSFull + i], j & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+            float s[kExKeys];
+#pragma unroll
+            for (int c = 0; c < kExKeys / 32; ++c) tmem_ld32f(tS + 32 * c, s + 32 * c);
+            tmem_ld_wait();
+            if (p.scale_log2 < 0.f) {
+#pragma unroll
+                for (int c = 0; c < kExKeys; ++c) s[c] = -s[c];
+            }
+            const int key0 = j * kExKeys;
+            if (__any_sync(0xffffffffu, key0 + kExKeys > lim)) {
+#pragma unroll
+                for (int c = 0; c < kExKeys; ++c) s[c] = key0 + c < lim ? s[c] : NEG_INF;
+            }
+            float mx4[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
+#pragma unroll
+            for (int c = 8; c < kExKeys; c += 8) {
+                mx4[0] = fmax3(mx4[0], s[c], s[c + 1]);
+                mx4[1] = fmax3(mx4[1], s[c + 2], s[c + 3]);
+                mx4[2] = fmax3(mx4[2], s[c + 4], s[c + 5]);
+                mx4[3] = fmax3(mx4[3], s[c + 6], s[c + 7]);
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+            // the reference moves on the first visible key, and then only when the max
+            // exceeds it by 2^40 (fp32 sums and bf16 weights keep their relative
+            // accuracy at any common scale)
+            const bool first = m_ref == NEG_INF;
+            const bool grow = !first && mx > m_ref + 40.f;
+            const float alpha = grow ? fast_exp2(m_ref - mx) : 1.f;
+            if (first || grow) m_ref = mx;
+            if (__any_sync(0xffffffffu, grow)) {
+                // rare: O rescaled once the previous tile's product has completed
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kExODone + i], (j - 1) & 1, status));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kExV / 16; ++c) {
+                    float v[16];
+                    uint32_t w[16];
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+                          "=f"(v[15])
+                        : "r"(tO + 16 * c));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * alpha);
+                    tmem_st16(tO + 16 * c, w);
+                }
+                l *= alpha;
+            }
+            const float ref = m_ref == NEG_INF ? 0.f : m_ref;
+            const uint64_t sc2 = f2_pack(sl2, sl2), nref2 = f2_pack(-ref, -ref);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < kExKeys / 32; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float y0, y1;
+                    f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, nref2), y0, y1);
+                    const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                    sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
+                    w[e] = pack_bf16x2(p0, p1);
+                }
+                tmem_st16(tS + 16 * c, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kExPFull + i]);
+            float a, b;
+            f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+            l += a + b;
+        }
+        if (ok && n_mine) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExODone + i], (n_mine - 1) & 1, status));
+        if (ok && n_mine) {
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            __nv_bfloat16 *o = p.out + (static_cast<int64_t>(req.qs + t0 + i * kExRows + row) * p.heads + head) * kExV;
+#pragma unroll
+            for (int c = 0; c < kExV / 32; ++c) {
+                float v[32];
+                tmem_ld32f(tO + 32 * c, v);
+                tmem_ld_wait();
+                if (mine) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(o + 32 * c + e) =
+                            make_uint4(pack_bf16x2(v[e] * inv, v[e + 1] * inv), pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
+                                       pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv),
+                                       pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// {dims, heads, tokens} of 16-bit elements: a box is 64 dims of one head of 128 tokens.
+static int make_rows_map(CUtensorMap *map, const void *base, int dims_in, int64_t heads, int64_t head_stride,
+                         int64_t tokens, int64_t token_stride) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dims_in), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
+    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t query_token_stride, const void *key,
+                                        int64_t key_token_stride, int64_t key_head_stride, const void *key_rope,
+                                        int64_t key_rope_token_stride, const void *value, int64_t value_token_stride,
+                                        int64_t value_head_stride, const int32_t *query_start_loc,
+                                        const int32_t *key_start_loc, int32_t num_seqs, int32_t num_tokens,
+                                        int32_t num_keys, int32_t max_query_len, int32_t max_key_len,
+                                        int32_t num_heads, float scale, int32_t *device_status, void *stream) {
+    using namespace pkv;
+    if (num_seqs < 0 || num_tokens < 0 || num_keys < 0 || max_query_len < 0 || max_key_len < 0 || num_heads <= 0)
+        return PKV_ERR_SHAPE;
+    if (num_heads > (1 << 16) || max_key_len > INT32_MAX - 256 || max_query_len > max_key_len) return PKV_ERR_SHAPE;
+    if (num_keys > INT32_MAX - 256 || num_tokens > INT32_MAX - 256) return PKV_ERR_SHAPE;
+    if (!(scale > -3.0e38f && scale < 3.0e38f)) return PKV_ERR_SHAPE;
+    if (num_seqs == 0) return num_tokens ? PKV_ERR_SHAPE : PKV_OK;
+    if (num_tokens == 0 || num_keys == 0 || max_query_len == 0) return PKV_OK;
+    if (!out || !query || !key || !key_rope || !value || !query_start_loc || !key_start_loc) return PKV_ERR_NULL;
+    constexpr int64_t kMost = int64_t(1) << 38;          // of a tensor map's strides, in elements
+    if (key_head_stride < kExNope || value_head_stride < kExV || key_head_stride > kMost || value_head_stride > kMost)
+        return PKV_ERR_SHAPE;
+    const int64_t h = num_heads;
+    if (query_token_stride < h * kExDim || query_token_stride > kMost ||
+        key_token_stride < kExNope || key_token_stride > kMost || key_rope_token_stride < kLatRope ||
+        key_rope_token_stride > kMost || value_token_stride < kExV || value_token_stride > kMost)
+        return PKV_ERR_SHAPE;
+    if ((query_token_stride % 8) || (key_token_stride % 8) || (key_head_stride % 8) || (key_rope_token_stride % 8) ||
+        (value_token_stride % 8) || (value_head_stride % 8))
+        return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(query) | reinterpret_cast<uintptr_t>(key) |
+         reinterpret_cast<uintptr_t>(key_rope) | reinterpret_cast<uintptr_t>(value)) & 15u)
+        return PKV_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(query_start_loc) | reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)
+        return PKV_ERR_ALIGNMENT;
+
+    ExParams p;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.qsl = query_start_loc, p.ksl = key_start_loc;
+    p.num_seqs = num_seqs, p.num_tokens = num_tokens, p.num_keys = num_keys;
+    p.max_query_len = max_query_len, p.max_key_len = max_key_len;
+    p.heads = num_heads;
+    // sum of ceil(q_r / 256), at most one tile a request beyond the whole ones
+    const int64_t bound = num_tokens / kExTokens + static_cast<int64_t>(num_seqs);
+    const int64_t tiles = bound < num_tokens ? bound : num_tokens;
+    if (tiles * num_heads > INT32_MAX) return PKV_ERR_SHAPE;
+    p.tiles = static_cast<int32_t>(tiles);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = device_status;
+    CUtensorMap qm, km, rm, vm;
+    int rc = make_rows_map(&qm, query, kExDim, h, kExDim, num_tokens, query_token_stride);
+    if (!rc) rc = make_rows_map(&km, key, kExNope, h, key_head_stride, num_keys, key_token_stride);
+    if (!rc) rc = make_rows_map(&rm, key_rope, kLatRope, 1, kLatRope, num_keys, key_rope_token_stride);
+    if (!rc) rc = make_rows_map(&vm, value, kExV, h, value_head_stride, num_keys, value_token_stride);
+    if (rc) return rc;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    static std::mutex mu;
+    static uint64_t done_mask = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+        if (!bit || !(done_mask & bit)) {
+            if (cudaFuncSetAttribute(latent_expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem) !=
+                cudaSuccess)
+                return PKV_ERR_CUDA;
+            done_mask |= bit;
+        }
+    }
+    if (launch_pdl(latent_expanded_kernel, dim3(static_cast<unsigned>(tiles * num_heads)), dim3(kExThreads), kExSmem,
+                   static_cast<cudaStream_t>(stream), qm, km, rm, vm, p) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    return PKV_OK;
+}
