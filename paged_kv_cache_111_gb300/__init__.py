@@ -376,77 +376,117 @@ def paged_attn_noalloc(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.T
 
 
 # ---- norm, rotation and the latent cache: calls that check types and devices too -------------------------------
+#
+# These calls stand in a decode step of some microseconds, so their checks read each property of a tensor once and
+# pass plain integers on: the device index (-1 on the CPU, so one comparison also refuses CPU tensors), the type, the
+# shape and the strides.
 
-def _expect(what: str, t: Optional[torch.Tensor], dtype, ndim: int, device) -> None:
-    """One tensor argument: a CUDA tensor of this type and rank on the call's device."""
-    if t is None:
-        return
-    if not t.is_cuda:
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_ROW = LATENT_DIM + LATENT_ROPE_DIM
+_NOPE, _VALUE = 128, 128        # plain key dims and value dims of a head in the expanded form
+_QK = _NOPE + LATENT_ROPE_DIM
+
+
+def _refuse(what: str, x: torch.Tensor, dtype, dev: int, form: str) -> None:
+    """The reason why a tensor argument does not do."""
+    if not x.is_cuda:
         raise ValueError("paged KV-cache calls take CUDA tensors only")
-    if t.dtype != dtype or t.dim() != ndim:
-        raise ValueError(f"{what} must be a {ndim}-dimensional {dtype} tensor, not {t.dim()}-dimensional {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    if x.get_device() != dev:
+        raise ValueError(f"{what} is on {x.device}, the call's other tensors on cuda:{dev}")
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
+    raise ValueError(f"{what} must be {form}, not {list(x.shape)} with strides {list(x.stride())}")
 
 
-def _contiguous(what: str, t: Optional[torch.Tensor], shape=None) -> None:
-    if t is None:
-        return
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {tuple(shape)}, not {tuple(t.shape)}")
+def _full(what: str, x: Optional[torch.Tensor], dtype, dev: int, shape: tuple, form: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of this type and shape (-1: any size), or None."""
+    if x is None:
+        return None
+    if x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous():
+        _refuse(what, x, dtype, dev, form)
+    have = x.shape
+    if have != shape and (len(have) != len(shape) or any(b not in (a, -1) for a, b in zip(have, shape))):
+        _refuse(what, x, dtype, dev, form)
+    return x.data_ptr()
 
 
-def _step(x: torch.Tensor, dim: int, least: int) -> int:
-    """The stride of a dim in elements; of a dim of one entry (where it means nothing), the least that the call takes."""
-    return x.stride(dim) if x.shape[dim] > 1 else least
+def _heads(what: str, x: torch.Tensor, dev: int, T: int, H: int, width: int, packed: bool):
+    """(pointer, token stride, head stride) of bf16 [T, H, width] with contiguous rows; packed: heads side by side.
+
+    The stride of a dim of one entry, which means nothing, is given as the least that the call takes."""
+    if x.get_device() != dev or x.dtype is not _BF16 or x.shape != (T, H, width):
+        _refuse(what, x, _BF16, dev, f"[{T}, {H}, {width}]")
+    token, head, one = x.stride()
+    if H <= 1:
+        head = width
+    if one != 1 or (packed and head != width):
+        _refuse(what, x, _BF16, dev, f"[{T}, {H}, {width}] with contiguous " + ("heads" if packed else "rows"))
+    if T <= 1:
+        token = max((H - 1) * head + width, 0)
+    return x.data_ptr(), token, head
 
 
-def _call(device, stream, fn, *args) -> None:
-    """Enqueue on `stream` (default: the current one of the tensors' device), with that device current."""
+def _tokens(what: str, x: torch.Tensor, dev: int, T: int, width: int):
+    """(pointer, token stride) of bf16 [T, width] with contiguous rows."""
+    if x.get_device() != dev or x.dtype is not _BF16 or x.shape != (T, width):
+        _refuse(what, x, _BF16, dev, f"[{T}, {width}]")
+    token, one = x.stride()
+    if one != 1:
+        _refuse(what, x, _BF16, dev, f"[{T}, {width}] with contiguous rows")
+    return x.data_ptr(), (token if T > 1 else width)
+
+
+def _latent_cache(x: torch.Tensor):
+    """(pointer, device, blocks, block size) of a latent cache."""
+    dev = x.get_device()
+    if dev < 0 or x.dtype is not _BF16 or x.dim() != 3 or not x.is_contiguous() or x.shape[2] != _ROW:
+        _refuse("latent_cache", x, _BF16, dev, f"a contiguous [NB, 16, {_ROW}]")
+    nb, bs, _ = x.shape
+    return x.data_ptr(), dev, nb, bs
+
+
+def _raw_stream(dev: int, stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, handle)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(dev: int, name: str, fn, *args) -> None:
+    """The C call, with the tensors' device current."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle)
-    _check(rc, fn.__name__)
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != 0:
+        raise PagedKVError(rc, name)
 
 
 def _qk_norm_rope(fp8: bool, query_out, kv_cache, query, key, value, q_weight, k_weight, eps, cos_sin, positions,
                   slot_mapping, scales, interleaved, device_status, stream) -> None:
-    dev, bf = kv_cache.device, torch.bfloat16
-    if kv_cache.dim() != 5 or kv_cache.element_size() != (1 if fp8 else 2) or (not fp8 and kv_cache.dtype != bf):
-        raise ValueError("kv_cache must be [NB, Hkv, 2, 16, d], bf16 (one byte per element for an FP8 cache)")
-    _expect("kv_cache", kv_cache, kv_cache.dtype, 5, dev)
-    _contiguous("kv_cache", kv_cache)
-    nb, hkv, _, bs, d = kv_cache.shape
-    for what, x in (("query_out", query_out), ("query", query), ("key", key), ("value", value)):
-        _expect(what, x, bf, 3, dev)
-        if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d) or x.shape[2] != d:
-            raise ValueError(f"{what} must be [T, heads, {d}] with contiguous heads")
-    T, H = int(query.shape[0]), int(query.shape[1])
-    if tuple(query_out.shape) != (T, H, d) or tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
-        raise ValueError("query_out must be [T, H, d], key and value [T, Hkv, d]")
-    for what, x in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _expect(what, x, bf, 1, dev)
-        _contiguous(what, x, (d,))
-    _expect("cos_sin", cos_sin, torch.float32, 2, dev)
-    _contiguous("cos_sin", cos_sin)
-    for what, x in (("positions", positions), ("slot_mapping", slot_mapping)):
-        _expect(what, x, torch.int64, 1, dev)
-        _contiguous(what, x, (T,))
-    _expect("device_status", device_status, torch.int32, 1, dev)
+    dev = kv_cache.get_device()
+    if (dev < 0 or kv_cache.dim() != 5 or not kv_cache.is_contiguous()
+            or (kv_cache.element_size() != 1 if fp8 else kv_cache.dtype is not _BF16)):
+        _refuse("kv_cache", kv_cache, None if fp8 else _BF16, dev, "a contiguous [NB, Hkv, 2, 16, d], "
+                + ("one byte per element" if fp8 else "bf16"))
+    nb, hkv, two, bs, d = kv_cache.shape
+    if two != 2 or query.dim() != 3:
+        raise ValueError("kv_cache must be [NB, Hkv, 2, 16, d] and query [T, H, d]")
+    T, H, _ = query.shape
+    qo, qo_step, _ = _heads("query_out", query_out, dev, T, H, d, True)
+    q, q_step, _ = _heads("query", query, dev, T, H, d, True)
+    k, k_step, _ = _heads("key", key, dev, T, hkv, d, True)
+    v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
+    table = _full("cos_sin", cos_sin, _F32, dev, (-1, -1), "a contiguous [max_position, rotary_dim]")
+    max_position, rot = cos_sin.shape
     lib = load()
-    _call(dev, stream, lib.pkv_qk_norm_rope_kv_write_fp8 if fp8 else lib.pkv_qk_norm_rope_kv_write,
-          _ptr(query_out), _step(query_out, 0, H * d), _ptr(kv_cache), nb, H, hkv, d, bs,
-          _ptr(query), _step(query, 0, H * d), _ptr(key), _step(key, 0, hkv * d), _ptr(value),
-          _step(value, 0, hkv * d), _ptr(q_weight), _ptr(k_weight),
-          float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
-          1 if interleaved else 0, _ptr(positions), _ptr(slot_mapping), T, *scales, _ptr(device_status))
+    _call(dev, "pkv_qk_norm_rope_kv_write", lib.pkv_qk_norm_rope_kv_write_fp8 if fp8 else lib.pkv_qk_norm_rope_kv_write,
+          qo, qo_step, kv_cache.data_ptr(), nb, H, hkv, d, bs, q, q_step, k, k_step, v, v_step,
+          _full("q_weight", q_weight, _BF16, dev, (d,), "[d]"), _full("k_weight", k_weight, _BF16, dev, (d,), "[d]"),
+          eps, table, max_position, rot, 1 if interleaved else 0,
+          _full("positions", positions, _I64, dev, (T,), "a contiguous [T]"),
+          _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T, *scales,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
 
 
 def qk_norm_rope_kv_write(query_out: torch.Tensor, kv_cache: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -470,15 +510,7 @@ def qk_norm_rope_kv_write_fp8(query_out: torch.Tensor, kv_cache: torch.Tensor, q
                               stream=None) -> None:
     """qk_norm_rope_kv_write into an E4M3 cache (uint8 or float8_e4m3fn [NB, Hkv, 2, 16, d])."""
     _qk_norm_rope(True, query_out, kv_cache, query, key, value, q_weight, k_weight, eps, cos_sin, positions,
-                  slot_mapping, (float(k_scale), float(v_scale)), interleaved, device_status, stream)
-
-
-def _latent_cache(latent_cache: torch.Tensor):
-    _expect("latent_cache", latent_cache, torch.bfloat16, 3, latent_cache.device)
-    _contiguous("latent_cache", latent_cache)
-    if latent_cache.shape[2] != LATENT_DIM + LATENT_ROPE_DIM:
-        raise ValueError(f"latent_cache must be [NB, 16, {LATENT_DIM + LATENT_ROPE_DIM}]")
-    return latent_cache.device, int(latent_cache.shape[0]), int(latent_cache.shape[1])
+                  slot_mapping, (k_scale, v_scale), interleaved, device_status, stream)
 
 
 def latent_kv_write(latent_cache: torch.Tensor, latent: torch.Tensor, key_rope: torch.Tensor,
@@ -489,74 +521,48 @@ def latent_kv_write(latent_cache: torch.Tensor, latent: torch.Tensor, key_rope: 
     """Norm latent [T, 512], rotate key_rope [T, 64] and store both in latent_cache [NB, 16, 576]; rotate
     query_rope [T, H, 64] into query_rope_out (which may be query_rope, or a view of the attention's query rows).
     weight is bf16 [512] (None: no norm), cos_sin fp32 [max_position, 64]."""
-    dev, nb, bs = _latent_cache(latent_cache)
-    bf = torch.bfloat16
-    T = int(slot_mapping.shape[0])
-    for what, x, width in (("latent", latent, LATENT_DIM), ("key_rope", key_rope, LATENT_ROPE_DIM)):
-        _expect(what, x, bf, 2, dev)
-        if tuple(x.shape) != (T, width) or x.stride(1) != 1:
-            raise ValueError(f"{what} must be [{T}, {width}] with contiguous rows")
-    _expect("weight", weight, bf, 1, dev)
-    _contiguous("weight", weight, (LATENT_DIM,))
-    _expect("cos_sin", cos_sin, torch.float32, 2, dev)
-    _contiguous("cos_sin", cos_sin, (cos_sin.shape[0], LATENT_ROPE_DIM))
-    for what, x in (("positions", positions), ("slot_mapping", slot_mapping)):
-        _expect(what, x, torch.int64, 1, dev)
-        _contiguous(what, x, (T,))
-    _expect("device_status", device_status, torch.int32, 1, dev)
-    if (query_rope is None) != (query_rope_out is None):
-        raise ValueError("query_rope and query_rope_out go together")
-    H = 0
-    q = [None, 0, 0, None, 0, 0]
-    if query_rope is not None:
-        H = int(query_rope.shape[1])
-        for what, x in (("query_rope_out", query_rope_out), ("query_rope", query_rope)):
-            _expect(what, x, bf, 3, dev)
-            if tuple(x.shape) != (T, H, LATENT_ROPE_DIM) or x.stride(2) != 1:
-                raise ValueError(f"{what} must be [{T}, H, {LATENT_ROPE_DIM}] with contiguous rows")
-        q = []
-        for x in (query_rope_out, query_rope):
-            head = _step(x, 1, LATENT_ROPE_DIM)
-            q += [_ptr(x), _step(x, 0, max(H - 1, 0) * head + LATENT_ROPE_DIM), head]
-    _call(dev, stream, load().pkv_latent_kv_write, _ptr(latent_cache), nb, bs, _ptr(latent),
-          _step(latent, 0, LATENT_DIM), _ptr(key_rope), _step(key_rope, 0, LATENT_ROPE_DIM), _ptr(weight),
-          float(eps), _ptr(cos_sin),
-          int(cos_sin.shape[0]), 1 if interleaved else 0, _ptr(positions), _ptr(slot_mapping), T, *q, H,
-          _ptr(device_status))
-
-
-def _tables(dev, block_tables, S, **lists) -> None:
-    _expect("block_tables", block_tables, torch.int32, 2, dev)
-    _contiguous("block_tables", block_tables)
-    if block_tables.shape[0] != S:
-        raise ValueError("block_tables must have a row per request")
-    for what, x in lists.items():
-        _expect(what, x, torch.int32, 1, dev)
-        _contiguous(what, x)
+    cache, dev, nb, bs = _latent_cache(latent_cache)
+    T = slot_mapping.numel()
+    lat, lat_step = _tokens("latent", latent, dev, T, LATENT_DIM)
+    kr, kr_step = _tokens("key_rope", key_rope, dev, T, LATENT_ROPE_DIM)
+    if query_rope is None and query_rope_out is None:
+        H, q = 0, (None, 0, 0, None, 0, 0)
+    elif query_rope is None or query_rope_out is None or query_rope.dim() != 3:
+        raise ValueError(f"query_rope and query_rope_out go together, [T, H, {LATENT_ROPE_DIM}] both")
+    else:
+        H = query_rope.shape[1]
+        q = (_heads("query_rope_out", query_rope_out, dev, T, H, LATENT_ROPE_DIM, False)
+             + _heads("query_rope", query_rope, dev, T, H, LATENT_ROPE_DIM, False))
+    _call(dev, "pkv_latent_kv_write", load().pkv_latent_kv_write, cache, nb, bs, lat, lat_step, kr, kr_step,
+          _full("weight", weight, _BF16, dev, (LATENT_DIM,), f"[{LATENT_DIM}]"), eps,
+          _full("cos_sin", cos_sin, _F32, dev, (-1, LATENT_ROPE_DIM),
+                f"a contiguous [max_position, {LATENT_ROPE_DIM}]"), cos_sin.shape[0],
+          1 if interleaved else 0, _full("positions", positions, _I64, dev, (T,), "a contiguous [T]"),
+          _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T, *q, H,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
 
 
 def latent_gather(out: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
                   key_start_loc: torch.Tensor, max_seq_len: int, device_status: Optional[torch.Tensor] = None,
                   stream=None) -> None:
     """Copy the cached rows of request r into out[key_start_loc[r]:][:seq_lens[r]] (bf16 [rows, 576])."""
-    dev, nb, bs = _latent_cache(latent_cache)
-    S = int(seq_lens.shape[0])
-    _tables(dev, block_tables, S, seq_lens=seq_lens, key_start_loc=key_start_loc)
-    if key_start_loc.shape[0] < S:
+    cache, dev, nb, bs = _latent_cache(latent_cache)
+    S = seq_lens.numel()
+    if key_start_loc.numel() < S:
         raise ValueError("key_start_loc must have an entry per request")
-    _expect("out", out, torch.bfloat16, 2, dev)
-    _contiguous("out", out, (out.shape[0], LATENT_DIM + LATENT_ROPE_DIM))
-    _expect("device_status", device_status, torch.int32, 1, dev)
-    _call(dev, stream, load().pkv_latent_gather, _ptr(out), int(out.shape[0]), _ptr(latent_cache), nb, bs,
-          _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), _ptr(key_start_loc), S, int(max_seq_len),
-          _ptr(device_status))
+    _call(dev, "pkv_latent_gather", load().pkv_latent_gather,
+          _full("out", out, _BF16, dev, (-1, _ROW), f"a contiguous [rows, {_ROW}]"), out.shape[0], cache, nb, bs,
+          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
+          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
+          _full("key_start_loc", key_start_loc, _I32, dev, (-1,), "a contiguous vector"), S, max_seq_len,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
 
 
 def latent_paged_attn_workspace_size(num_seqs: int, num_tokens: int, max_query_len: int, max_seq_len: int,
                                      num_heads: int) -> int:
     """Bytes of workspace pkv_latent_paged_attn needs for these sizes (no GPU work)."""
     need = ctypes.c_size_t(0)
-    rc = load().pkv_latent_paged_attn(None, None, num_heads * (LATENT_DIM + LATENT_ROPE_DIM), None, 1, None,
+    rc = load().pkv_latent_paged_attn(None, None, num_heads * _ROW, None, 1, None,
                                       (max_seq_len + BLOCK_SIZE - 1) // BLOCK_SIZE, None, None, num_seqs, num_tokens,
                                       max_query_len, max_seq_len, num_heads, BLOCK_SIZE, 1.0, None, 0,
                                       ctypes.byref(need), None)
@@ -571,26 +577,21 @@ def latent_paged_attn(out: torch.Tensor, query: torch.Tensor, latent_cache: torc
     """Causal attention of query [T, H, 576] over the latent cache [NB, 16, 576]; out [T, H, 512] bf16.
 
     One call (no combine after it); workspace_status(workspace) reads its device status."""
-    dev, nb, bs = _latent_cache(latent_cache)
-    S = int(seq_lens.shape[0])
-    _tables(dev, block_tables, S, seq_lens=seq_lens, query_start_loc=query_start_loc)
-    if query_start_loc.shape[0] != S + 1:
-        raise ValueError("query_start_loc must have an entry per request and one more")
-    _expect("query", query, torch.bfloat16, 3, dev)
-    T, H, D = query.shape
-    if D != LATENT_DIM + LATENT_ROPE_DIM or query.stride(2) != 1 or (H > 1 and query.stride(1) != D):
-        raise ValueError(f"query must be [T, H, {LATENT_DIM + LATENT_ROPE_DIM}] with contiguous heads")
-    _expect("out", out, torch.bfloat16, 3, dev)
-    _contiguous("out", out, (T, H, LATENT_DIM))
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    _call(dev, stream, load().pkv_latent_paged_attn, _ptr(out), _ptr(query), _step(query, 0, H * D),
-          _ptr(latent_cache), nb, _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens),
-          _ptr(query_start_loc), S, T, int(max_query_len), int(max_seq_len), H, bs, float(scale), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), None)
-
-
-_NOPE, _VALUE = 128, 128        # plain key dims and value dims of a head in the expanded form
+    cache, dev, nb, bs = _latent_cache(latent_cache)
+    S = seq_lens.numel()
+    if query.dim() != 3:
+        raise ValueError(f"query must be [T, H, {_ROW}]")
+    T, H, _ = query.shape
+    q, q_step, _ = _heads("query", query, dev, T, H, _ROW, True)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("workspace", workspace, None, dev, "contiguous")
+    _call(dev, "pkv_latent_paged_attn", load().pkv_latent_paged_attn,
+          _full("out", out, _BF16, dev, (T, H, LATENT_DIM), f"a contiguous [T, H, {LATENT_DIM}]"), q, q_step, cache, nb,
+          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
+          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
+          _full("query_start_loc", query_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"), S, T,
+          max_query_len, max_seq_len, H, bs, scale, workspace.data_ptr(), workspace.nbytes, None,
+          _raw_stream(dev, stream))
 
 
 def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, key_rope: torch.Tensor,
@@ -599,28 +600,18 @@ def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tens
                          device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Causal attention of query [T, H, 192] over key [K, H, 128], key_rope [K, 64] (shared by the heads) and
     value [K, H, 128], requests side by side; out [T, H, 128] bf16."""
-    dev, bf = query.device, torch.bfloat16
-    _expect("query", query, bf, 3, dev)
-    T, H, D = query.shape
-    if D != _NOPE + LATENT_ROPE_DIM or query.stride(2) != 1 or (H > 1 and query.stride(1) != D):
-        raise ValueError(f"query must be [T, H, {_NOPE + LATENT_ROPE_DIM}] with contiguous heads")
-    _expect("key_rope", key_rope, bf, 2, dev)
-    K = int(key_rope.shape[0])
-    for what, x, width in (("key", key, _NOPE), ("value", value, _VALUE)):
-        _expect(what, x, bf, 3, dev)
-        if tuple(x.shape) != (K, H, width) or x.stride(2) != 1:
-            raise ValueError(f"{what} must be [{K}, {H}, {width}] with contiguous rows")
-    if key_rope.shape[1] != LATENT_ROPE_DIM or key_rope.stride(1) != 1:
-        raise ValueError(f"key_rope must be [K, {LATENT_ROPE_DIM}] with contiguous rows")
-    _expect("out", out, bf, 3, dev)
-    _contiguous("out", out, (T, H, _VALUE))
-    S = int(query_start_loc.shape[0]) - 1
-    for what, x in (("query_start_loc", query_start_loc), ("key_start_loc", key_start_loc)):
-        _expect(what, x, torch.int32, 1, dev)
-        _contiguous(what, x, (S + 1,))
-    _expect("device_status", device_status, torch.int32, 1, dev)
-    kh, vh = _step(key, 1, _NOPE), _step(value, 1, _VALUE)
-    _call(dev, stream, load().pkv_latent_attn_expanded, _ptr(out), _ptr(query), _step(query, 0, H * D),
-          _ptr(key), _step(key, 0, _NOPE), kh, _ptr(key_rope), _step(key_rope, 0, LATENT_ROPE_DIM), _ptr(value),
-          _step(value, 0, _VALUE), vh, _ptr(query_start_loc), _ptr(key_start_loc), S, T, K, int(max_query_len),
-          int(max_key_len), H, float(scale), _ptr(device_status))
+    dev = query.get_device()
+    if dev < 0 or query.dim() != 3:
+        _refuse("query", query, _BF16, dev, f"[T, H, {_QK}]")
+    T, H, _ = query.shape
+    K = key_rope.shape[0]
+    S = query_start_loc.numel() - 1
+    q, q_step, _ = _heads("query", query, dev, T, H, _QK, True)
+    _call(dev, "pkv_latent_attn_expanded", load().pkv_latent_attn_expanded,
+          _full("out", out, _BF16, dev, (T, H, _VALUE), f"a contiguous [T, H, {_VALUE}]"), q, q_step,
+          *_heads("key", key, dev, K, H, _NOPE, False), *_tokens("key_rope", key_rope, dev, K, LATENT_ROPE_DIM),
+          *_heads("value", value, dev, K, H, _VALUE, False),
+          _full("query_start_loc", query_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"),
+          _full("key_start_loc", key_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"), S, T, K,
+          max_query_len, max_key_len, H, scale,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))

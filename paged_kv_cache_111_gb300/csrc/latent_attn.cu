@@ -126,12 +126,12 @@ enum LaBar {
     kLaVote = 7,              // the four softmax warps meet (every tile)
     kLaMeet = 8,              // the same, at the end of an item
     kLaKVFull = 9,            // (+ stage)
-    kLaKVEmpty = 11,          // (+ stage)
-    kLaFix = 13,              // rows past the last visible key zeroed (+ stage)
-    kLaItemFull = 15, kLaItemEmpty = 19,
-    kLaNumBars = 23
+    kLaFix = 11,              // rows past the last visible key zeroed (+ stage)
+    kLaItemFull = 13, kLaItemEmpty = 17,
+    kLaKVEmpty = 21,          // a page read by its last product (+ 4 stage + page)
+    kLaNumBars = 29
 };
-static_assert(kLaNumBars * 8 + 48 <= 256, "barriers, tensor-memory address, status, votes");
+static_assert(kLaNumBars * 8 + 24 <= 256, "barriers, tensor-memory address, status, votes");
 
 // Request r's share of the line of units.
 struct LaReq {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     int64_t *scan = reinterpret_cast<int64_t *>(smem + kLaOffAlpha);    // before the roles start only
     volatile LaItem *items = reinterpret_cast<volatile LaItem *>(smem + kLaOffItems);
     const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sP = smem_u32(smem + kLaOffP);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     const int my_lane = blockIdx.x / p.groups;               // run
     const int group = blockIdx.x - my_lane * p.groups;       // head group
 
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     // everything before this call is complete from here on: the cache write, the
     // query, and the previous use of the workspace
     pdl_wait();
@@ -362,16 +362,22 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     win_next = load_window((j - it.kv0) * kLaPages / 32 + 1);
                 }
                 const int page = __shfl_sync(0xffffffffu, win_cur, wofs + (lane & (kLaPages - 1)));
-                if (gt >= kLaStages)
-                    ok = __all_sync(0xffffffffu,
-                                    pf_wait(&bars[kLaKVEmpty + st], (gt / kLaStages - 1) & 1, status));
+                // each page as soon as the products of the tile two before have read it
+#pragma unroll 1
+                for (int i = 0; i < kLaPages && ok; ++i) {
+                    if (gt >= kLaStages)
+                        ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaKVEmpty + st * kLaPages + i],
+                                                             (gt / kLaStages - 1) & 1, status));
+                    if (!ok) break;
+                    if (lane == 0 && i == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + st], kLaStage);
+                    __syncwarp();
+                    if (lane == i)
+                        tma_load_5d(smem + kLaOffKV + st * kLaStage + i * kLatPageBytes, &kv_map,
+                                    &bars[kLaKVFull + st], 0, 0, 0, 0, page);
+                    // (a stage of which some pages were not asked for never completes: not waited for)
+                    if (i == kLaPages - 1) issued = gt + 1;
+                }
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + st], kLaStage);
-                __syncwarp();
-                if (lane < kLaPages)
-                    tma_load_5d(smem + kLaOffKV + st * kLaStage + lane * kLatPageBytes, &kv_map,
-                                &bars[kLaKVFull + st], 0, 0, 0, 0, page);
-                issued = gt + 1;
                 if (j == it.n_kv - 1 && end % kBlock) {
                     // zero the rows past the last visible key in its page
                     ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaKVFull + st], (gt / kLaStages) & 1, status));
@@ -394,44 +400,46 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             mbar_wait_bounded(&bars[kLaKVFull + g % kLaStages], (g / kLaStages) & 1);
         if (lane == 0) *desc = split;
     } else if (warp == 1) {
-        // ---------------- MMA issue ----------------
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_bf16_f32(kLaRows, kLaKeys, 0, 0);
-            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
-            const uint64_t dk = smem_desc_sw128(sKV, 16, kLaGroup);          // K-major, 8-key groups 9216 apart
-            const uint64_t dv = smem_desc_sw128(sKV, 1024, kLaGroup);        // MN-major, 64-dim chunks 1024 apart
-            const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
-            bool ok = true;
-            int gt0 = 0;
-            uint32_t fix_par = 0;
-            for (int k = 0; ok; ++k) {
-                const int slot = k % kLaItemSlots;
-                ok = pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status);
-                if (!ok) break;
-                const bool valid = items[slot].valid != 0;
-                const int n = items[slot].kv1 - items[slot].kv0;
-                const int rows = items[slot].ntok * p.hpt;
-                const int end = items[slot].lim0 + items[slot].ntok - 1;
-                const int fix_tile = (items[slot].kv1 == items[slot].n_kv && end % kBlock) ? n - 1 : -1;
-                mbar_arrive(&bars[kLaItemEmpty + slot]);
-                if (!valid) break;
-                // the second products' N: the tile's rows, in sixteens
-                const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 0);
-                ok = pf_wait(&bars[kLaQFull], k & 1, status);
-                int js = 0, jp = 0;
-                uint64_t t_idle = 0;
-                // S(j) once its stage has landed (S buffer j & 1 was read before the
-                // weights of tile j - 2 were written, and those products are issued
-                // before); the second products of j once its weights are written, the
-                // end tile is fixed and the previous item's O' has been read out.
-                while (ok && jp < n) {
-                    const bool s_can = js < n && js <= jp + 1;
-                    const bool p_can = jp < js;
-                    const int gs = gt0 + js, gp = gt0 + jp;
-                    if (s_can && mbar_test_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1)) {
-                        tc_fence_after();
-                        const uint64_t b0 = dk + ((gs % kLaStages) * (kLaStage >> 4));
-                        const uint32_t d = tmem + la_col_s(gs & 1);
+        // ---------------- MMA issue (the warp stays converged) ----------------
+        constexpr uint32_t kIdescS = idesc_bf16_f32(kLaRows, kLaKeys, 0, 0);
+        const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
+        const uint64_t dk = smem_desc_sw128(sKV, 16, kLaGroup);          // K-major, 8-key groups 9216 apart
+        const uint64_t dv = smem_desc_sw128(sKV, 1024, kLaGroup);        // MN-major, 64-dim chunks 1024 apart
+        const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
+        bool ok = true;
+        int gt0 = 0;
+        uint32_t fix_par = 0;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kLaItemSlots;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            if (!ok) break;
+            const volatile LaItem *cur = items + slot;
+            const bool valid = uniform(static_cast<int>(cur->valid)) != 0;
+            const int n = uniform(cur->kv1 - cur->kv0);
+            const int rows = uniform(cur->ntok * p.hpt);
+            const int end = uniform(cur->lim0 + cur->ntok - 1);
+            const int fix_tile = uniform(cur->kv1 == cur->n_kv && end % kBlock ? n - 1 : -1);
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+            if (!valid) break;
+            // the second products' N: the tile's rows, in sixteens
+            const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 0);
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaQFull], k & 1, status));
+            int js = 0, jp = 0;
+            uint64_t t_idle = 0;
+            // S(j) once its stage has landed (S buffer j & 1 was read before the
+            // weights of tile j - 2 were written, and those products are issued
+            // before); the second products of j once its weights are written, the
+            // end tile is fixed and the previous item's O' has been read out.
+            while (ok && jp < n) {
+                const bool s_can = js < n && js <= jp + 1;
+                const bool p_can = jp < js;
+                const int gs = gt0 + js, gp = gt0 + jp;
+                if (s_can && warp_test(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1)) {
+                    tc_fence_after();
+                    const uint64_t b0 = dk + static_cast<uint32_t>((gs % kLaStages) * (kLaStage >> 4));
+                    const uint32_t d = tmem + la_col_s(gs & 1);
+                    ++js;
+                    if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < kLaChunks; ++c)
 #pragma unroll
@@ -439,48 +447,54 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                 umma_f16_ss(d, dq + c * (kLaQChunk >> 4) + kk * 2, b0 + c * (1024 >> 4) + kk * 2, kIdescS,
                                             (c | kk) ? 1u : 0u);
                         umma_commit(&bars[kLaSFull + (gs & 1)]);
-                        if (++js == n) umma_commit(&bars[kLaQEmpty]);
+                        if (js == n) umma_commit(&bars[kLaQEmpty]);
+                    }
+                    __syncwarp();
+                    t_idle = 0;
+                    continue;
+                }
+                if (p_can) {
+                    const int st = gp % kLaStages;
+                    bool ready = warp_test(&bars[kLaPFull], gp & 1);
+                    if (ready && jp == fix_tile) ready = warp_test(&bars[kLaFix + st], (fix_par >> st) & 1u);
+                    if (ready && jp == 0 && k > 0) ready = warp_test(&bars[kLaOFree], (k - 1) & 1);
+                    if (ready) {
+                        if (jp == fix_tile) fix_par ^= 1u << st;
+                        tc_fence_after();
+                        const uint64_t a0 = dv + static_cast<uint32_t>(st * (kLaStage >> 4));
+                        const uint32_t more = jp > 0 ? 1u : 0u;
+                        if (elect_one()) {
+                            // a page (16 keys) at a time, each free for the next load on its own
+#pragma unroll
+                            for (int kk = 0; kk < kLaPages; ++kk) {
+#pragma unroll
+                                for (int m = 0; m < kLatent / 128; ++m)
+                                    umma_f16_ss(tmem + 64u * m, a0 + kk * (kLatPageBytes >> 4) + m * (2048 >> 4),
+                                                dp + kk * 2, idesc_o, kk > 0 ? 1u : more);
+                                umma_commit(&bars[kLaKVEmpty + st * kLaPages + kk]);
+                            }
+                            umma_commit(&bars[kLaODone]);
+                        }
+                        __syncwarp();
+                        ++jp;
                         t_idle = 0;
                         continue;
                     }
-                    if (p_can) {
-                        const int st = gp % kLaStages;
-                        bool ready = mbar_test_wait(&bars[kLaPFull], gp & 1);
-                        if (ready && jp == fix_tile) ready = mbar_test_wait(&bars[kLaFix + st], (fix_par >> st) & 1u);
-                        if (ready && jp == 0 && k > 0) ready = mbar_test_wait(&bars[kLaOFree], (k - 1) & 1);
-                        if (ready) {
-                            if (jp == fix_tile) fix_par ^= 1u << st;
-                            tc_fence_after();
-                            const uint64_t a0 = dv + st * (kLaStage >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < kLaPages; ++kk)
-#pragma unroll
-                                for (int m = 0; m < kLatent / 128; ++m)
-                                    umma_f16_ss(tmem + 64u * m, a0 + kk * (kLatPageBytes >> 4) + m * (2048 >> 4), dp + kk * 2,
-                                                idesc_o, (jp > 0 || kk > 0) ? 1u : 0u);
-                            umma_commit(&bars[kLaODone]);
-                            umma_commit(&bars[kLaKVEmpty + st]);
-                            ++jp;
-                            t_idle = 0;
-                            continue;
-                        }
-                    }
-                    if (p_can)
-                        mbar_try_wait_for(&bars[kLaPFull], gp & 1, 200);
-                    else
-                        mbar_try_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1);
-                    const uint64_t now = global_ns();
-                    if (t_idle == 0) {
-                        t_idle = now;
-                    } else if (now - t_idle > kWaitLimitNs) {
-                        set_status(status, PKV_ERR_DEVICE_TIMEOUT);
-                        ok = false;
-                    }
                 }
-                gt0 += n;
+                if (p_can)
+                    mbar_try_wait_for(&bars[kLaPFull], gp & 1, 200);
+                else
+                    mbar_try_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1);
+                const uint64_t now = uniform(global_ns());
+                if (t_idle == 0) {
+                    t_idle = now;
+                } else if (now - t_idle > kWaitLimitNs) {
+                    set_status(status, PKV_ERR_DEVICE_TIMEOUT);
+                    ok = false;
+                }
             }
+            gt0 += n;
         }
-        __syncwarp();
     } else if (warp == 2) {
         // ---------------- Q of each item, once the previous item's last S has read it ----------------
         bool ok = true;

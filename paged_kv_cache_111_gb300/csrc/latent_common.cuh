@@ -2,7 +2,7 @@
 // (keys and values both) followed by 64 rotated key dims.
 #pragma once
 
-#include "pkv_common.cuh"
+#include "tc_common.cuh"
 
 namespace pkv {
 
@@ -11,5 +11,29 @@ constexpr int kLatRope = PKV_LATENT_ROPE_DIM;        // 64: rotated key dims
 constexpr int kLatRow = kLatent + kLatRope;          // 576: a cached row, the keys' width
 constexpr int kLatRowBytes = kLatRow * 2;            // 1152
 constexpr int kLatPageBytes = kBlock * kLatRowBytes; // 18432
+
+// ---- issuing MMAs from a converged warp -----------------------------------------
+//
+// tcgen05.mma takes its descriptors from uniform registers.  When one lane
+// issues inside `if (lane == 0)`, the compiler moves every operand of every
+// product there from per-lane registers, and a product costs at least 45 cycles
+// of issue whatever its shape (measured alone on an SM: 64 x 64 x 16 at 50
+// cycles).  A warp that stays converged, with the lane chosen by elect.sync only
+// around the products, keeps the operands uniform: 64 x 64 x 16 at 33 cycles, 128 x
+// 64 x 16 at 50, 128 x 128 x 16 at 65, which is what their shared-memory reads
+// (128 bytes a cycle) and arithmetic take.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// A value that is the same in every lane, in a form the compiler knows to be.
+template <typename T> __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// One converged poll of a barrier's phase.
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+}
 
 }  // namespace pkv

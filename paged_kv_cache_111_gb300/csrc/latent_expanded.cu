@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kExNumBars);
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
     const uint32_t sQ = smem_u32(smem + kExOffQ), sK = smem_u32(smem + kExOffK), sV = smem_u32(smem + kExOffV);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     // the last tiles of a request see the most keys: they go first
     const int head = blockIdx.x % p.heads;
     const int tile = p.tiles - 1 - blockIdx.x / p.heads;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     pdl_wait();                                         // the inputs are complete
 
     if (warp == 0) {
@@ -215,15 +215,18 @@ __global__ void __launch_bounds__(kExThreads, 1)
             if (v_issued) mbar_wait_bounded(&bars[kExVFull], (v_issued - 1) & 1);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issue ----------------
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
-            constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
-            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
-            const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
-            bool ok = true;
-            auto issue_s = [&](int i, int j) {
-                const uint64_t a = dq + i * (kExQ >> 4), b = dk + (j & 1) * (kExK >> 4);
+        // ---------------- MMA issue (the warp stays converged) ----------------
+        constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
+        constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
+        const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
+        const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
+        const int n0 = uniform(n[0]), n1 = uniform(n[1]), n_max = max(n0, n1);
+        auto wait = [&](int b, uint32_t parity) {
+            return __all_sync(0xffffffffu, pf_wait(&bars[b], parity, status));
+        };
+        auto issue_s = [&](int i, int j) {
+            const uint64_t a = dq + i * (kExQ >> 4), b = dk + static_cast<uint32_t>((j & 1) * (kExK >> 4));
+            if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -231,42 +234,54 @@ __global__ void __launch_bounds__(kExThreads, 1)
                         umma_f16_ss(tmem + 128u * i, a + c * (kExChunk >> 4) + kk * 2, b + c * (kExChunk >> 4) + kk * 2,
                                     kIdescS, (c | kk) ? 1u : 0u);
                 umma_commit(&bars[kExSFull + i]);
-            };
-            auto issue_pv = [&](int i, int j) {
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int i, int j) {
+            const uint32_t more = j > 0 ? 1u : 0u;
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kExKeys / 16; ++kk)
                     umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, dv + kk * (2048 >> 4), kIdescO,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                                kk > 0 ? 1u : more);
                 umma_commit(&bars[kExODone + i]);
-            };
-            ok = pf_wait(&bars[kExKFull], 0, status);
-            for (int i = 0; i < 2 && ok; ++i)
-                if (n[i]) {
-                    ok = pf_wait(&bars[kExQFull + i], 0, status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_s(i, 0);
-                }
-            umma_commit(&bars[kExKEmpty]);
-            // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
-            for (int j = 0; j < n_all && ok; ++j) {
-                ok = pf_wait(&bars[kExVFull], j & 1, status);
-                if (ok && fix && j == n_all - 1) ok = pf_wait(&bars[kExFix], 0, status);
-                if (ok && j + 1 < n_all) ok = pf_wait(&bars[kExKFull + ((j + 1) & 1)], ((j + 1) / 2) & 1, status);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (!ok || j >= n[i]) continue;
-                    ok = pf_wait(&bars[kExPFull + i], j & 1, status);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    issue_pv(i, j);
-                    if (j + 1 < n[i]) issue_s(i, j + 1);
-                }
-                umma_commit(&bars[kExVEmpty]);
-                if (j + 1 < n_all) umma_commit(&bars[kExKEmpty + ((j + 1) & 1)]);
             }
+            __syncwarp();
+        };
+        auto commit = [&](int b) {
+            if (elect_one()) umma_commit(&bars[b]);
+            __syncwarp();
+        };
+        bool ok = wait(kExKFull, 0);
+        if (ok && n0) {
+            ok = wait(kExQFull, 0);
+            tc_fence_after();
+            if (ok) issue_s(0, 0);
         }
-        __syncwarp();
+        if (ok && n1) {
+            ok = wait(kExQFull + 1, 0);
+            tc_fence_after();
+            if (ok) issue_s(1, 0);
+        }
+        commit(kExKEmpty);
+        // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
+        for (int j = 0; j < n_max && ok; ++j) {
+            ok = wait(kExVFull, j & 1);
+            if (ok && fix && j == n_max - 1) ok = wait(kExFix, 0);
+            if (ok && j + 1 < n_max) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n_i = i ? n1 : n0;
+                if (ok && j < n_i) {
+                    ok = wait(kExPFull + i, j & 1);
+                    tc_fence_after();
+                    if (ok) issue_pv(i, j);
+                    if (ok && j + 1 < n_i) issue_s(i, j + 1);
+                }
+            }
+            commit(kExVEmpty);
+            if (j + 1 < n_max) commit(kExKEmpty + ((j + 1) & 1));
+        }
     } else if (warp >= 4) {
         // ---------------- softmax (a row per thread) and epilogue ----------------
         const int i = (warp - 4) >> 2, quad = warp & 3;
