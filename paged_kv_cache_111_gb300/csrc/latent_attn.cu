@@ -38,11 +38,12 @@
 // each weight, about that of the output's own rounding.  Sums, maxima and
 // outputs are fp32.
 //
-// Warp roles (256 threads): warp 0 walks the run, publishes items and loads
-// pages by TMA (one 18 KiB box a page); warp 1 issues the MMAs; warp 2 loads Q
-// (TMA) and owns tensor memory; warps 4-7 are the softmax and epilogue warps.
-// Rows past a tile's last visible key are zeroed in shared memory, so that what
-// an unwritten slot holds never meets a zero weight.  Every wait is bounded.
+// Warp roles (256 threads): warp 3 walks the run and publishes items ahead of
+// the others; warp 0 loads pages by TMA (one 18 KiB box a page); warp 1 issues
+// the MMAs; warp 2 loads Q (TMA), zeroes the rows past a tile's last visible key
+// (so that what an unwritten slot holds never meets a zero weight) and owns
+// tensor memory; warps 4-7 are the softmax and epilogue warps.  Every wait is
+// bounded.
 #include <mutex>
 
 #include "latent_common.cuh"
@@ -100,6 +101,7 @@ struct LaParams {
     int32_t heads;            // query heads
     int32_t groups;           // head groups: CTAs of a lane
     int32_t hpt, tpt;         // heads and tokens of a row tile
+    int32_t tpt_shift;        // log2(tpt)
     int32_t lanes;
     int64_t num_blocks;
     float scale_log2;
@@ -114,6 +116,7 @@ struct LaItem {
     int32_t kv0, kv1;
     int32_t n_kv;             // key tiles of the whole row tile
     int32_t slot;             // -1: complete, written to out; else the partial slot of this CTA
+    int32_t r;                // request
 };
 static_assert(kLaItemSlots * sizeof(LaItem) <= 256, "item ring");
 
@@ -140,19 +143,19 @@ struct LaReq {
     int64_t units;            // key tiles of all its row tiles
 };
 
-// sum of floor(x / u) over x < m
-__device__ __forceinline__ int64_t la_floor_sum(int64_t m, int u) {
-    const int64_t d = m / u;
-    return u * (d * (d - 1) / 2) + d * (m - d * u);
+// sum of floor(x / 2^s) over x < m
+__device__ __forceinline__ int64_t la_floor_sum(int64_t m, int s) {
+    const int64_t d = m >> s;
+    return ((d * (d - 1) / 2) << s) + d * (m - (d << s));
 }
 
 // Key tiles of the row tiles before tile j of a request (j <= n_full): tile i
-// sees ctx + (i + 1) tpt keys, and tpt divides 64.
-__device__ __forceinline__ int64_t la_units_before(int32_t ctx, int tpt, int64_t j) {
-    const int u = kLaKeys / tpt;
-    const int64_t b = (ctx + kLaKeys - 1) / tpt;
-    return la_floor_sum(b + j + 1, u) - la_floor_sum(b + 1, u);
+// sees ctx + (i + 1) tpt keys, and tpt = 2^shift divides 64.
+__device__ __forceinline__ int64_t la_units_before(int32_t ctx, int shift, int64_t j) {
+    const int64_t b = (ctx + kLaKeys - 1) >> shift;
+    return la_floor_sum(b + j + 1, 6 - shift) - la_floor_sum(b + 1, 6 - shift);
 }
+static_assert(kLaKeys == 64, "2^6 keys a tile");
 
 __device__ __forceinline__ LaReq la_request(const LaParams &p, int r, bool &bad) {
     LaReq a;
@@ -167,9 +170,9 @@ __device__ __forceinline__ LaReq la_request(const LaParams &p, int r, bool &bad)
                       a.q > p.max_query_len || (a.L + kBlock - 1) / kBlock > p.max_blocks_per_seq);
     bad |= !ok;
     if (ok && a.q > 0) {
-        a.n_full = a.q / p.tpt;
-        a.units = la_units_before(a.ctx, p.tpt, a.n_full);
-        if (a.q % p.tpt) a.units += (a.L + kLaKeys - 1) / kLaKeys;
+        a.n_full = a.q >> p.tpt_shift;
+        a.units = la_units_before(a.ctx, p.tpt_shift, a.n_full);
+        if (a.q & (p.tpt - 1)) a.units += (a.L + kLaKeys - 1) / kLaKeys;
     }
     return a;
 }
@@ -186,6 +189,25 @@ __device__ __forceinline__ void tmem_ld_16x64f(uint32_t taddr, float (&r)[32]) {
           "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
           "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr));
+}
+
+// The same of 32 columns.
+__device__ __forceinline__ void tmem_ld_16x32f(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 tiles of 16-bit values to shared memory, transposed: thread t holds
+// elements (t / 4, 2 (t % 4) + {0, 1}) of each, and gives the address of column
+// t % 8 of tile t / 8.
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kLaThreads, 1)
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         const int b = threadIdx.x;
         int count = 1;
         if (b == kLaPFull || b == kLaOFree || b == kLaVote || b == kLaMeet) count = 4;
-        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 6;   // MMA, Q, 4 softmax warps
+        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 7;   // loads, MMA, Q, 4 softmax warps
         mbar_init(&bars[b], count);
     }
     if (threadIdx.x == 0) {
@@ -283,13 +305,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const bool work = lo < hi;
     int4 *desc = reinterpret_cast<int4 *>(p.ws + kLaWsDesc) + blockIdx.x;
 
-    if (warp == 0) {
-        // ---------------- walk of the run; pages through the block table ----------------
+    if (warp == 3) {
+        // ---------------- walk of the run: items, ahead of the other warps ----------------
         bool ok = true;
         int r = start_req;
         int64_t off = start_off, left = hi - lo, at = lo;     // at: position in the line
-        int gt = 0;                                           // key tiles of this CTA so far
-        int issued = 0;                                       // stages of copies issued
         int4 split = make_int4(0, 0, 0, 0);                   // the row tile that starts here and ends in another lane
         bool unused = false;
         LaReq req = work ? la_request(p, r, unused) : LaReq{};
@@ -310,11 +330,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 int lo_j = 0, hi_j = req.n_full;
                 while (lo_j < hi_j) {
                     const int mid = (lo_j + hi_j + 1) >> 1;
-                    if (la_units_before(req.ctx, p.tpt, mid) <= off) lo_j = mid;
+                    if (la_units_before(req.ctx, p.tpt_shift, mid) <= off) lo_j = mid;
                     else hi_j = mid - 1;
                 }
-                const int64_t before = la_units_before(req.ctx, p.tpt, lo_j);
+                const int64_t before = la_units_before(req.ctx, p.tpt_shift, lo_j);
                 it.valid = 1;
+                it.r = r;
                 it.tok0 = req.qs + lo_j * p.tpt;
                 it.ntok = min(p.tpt, req.q - lo_j * p.tpt);
                 it.lim0 = req.ctx + lo_j * p.tpt + 1;
@@ -337,31 +358,59 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 mbar_arrive(&bars[kLaItemFull + slot]);
             }
             if (!it.valid) break;
-            const int end = it.lim0 + it.ntok - 1;            // keys the tile's last token sees
-            const int n_pages = (end + kBlock - 1) / kBlock;
-            const int32_t *bt = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq;
-            // block ids in windows of 32 pages (8 key tiles), a lane each, the next
-            // window a window ahead; pages past the end, and ids outside the cache
-            // (reported), become -1 and load as zeros
-            auto load_window = [&](int w) -> int {
-                const int page = it.kv0 * kLaPages + w * 32 + lane;
-                if (page >= n_pages) return -1;
-                const int b = __ldg(bt + page);
-                if (b < 0 || b >= p.num_blocks) {
-                    set_status(status, PKV_ERR_DEVICE_INDEX);
-                    return -1;
-                }
-                return b;
-            };
-            int win_cur = load_window(0), win_next = load_window(1);
-            for (int j = it.kv0; j < it.kv1 && ok; ++j, ++gt) {
+        }
+        if (lane == 0) *desc = split;
+    } else if (warp == 0) {
+        // ---------------- pages through the block table ----------------
+        bool ok = true;
+        int gt = 0;                                           // key tiles of this CTA so far
+        int issued = 0;                                       // stages of copies issued
+        struct {
+            bool valid;
+            int kv0, kv1, n_pages;
+            const int32_t *table;
+        } cur, next{};
+        // block ids in windows of 32 pages (8 key tiles), a lane each, loaded a window
+        // ahead, and for the next item while the current one ends
+        auto window = [&](int w) -> int {
+            const int page = next.kv0 * kLaPages + w * 32 + lane;
+            return next.valid && page < next.n_pages ? __ldg(next.table + page) : -1;
+        };
+        auto fetch = [&](int k) {
+            const int slot = k % kLaItemSlots;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            const volatile LaItem *it = items + slot;
+            next.valid = ok && it->valid;
+            next.kv0 = it->kv0, next.kv1 = it->kv1;
+            next.n_pages = (it->lim0 + it->ntok - 1 + kBlock - 1) / kBlock;    // with a key that the last token sees
+            next.table = p.block_tables + static_cast<int64_t>(it->r) * p.max_blocks_per_seq;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+        };
+        fetch(0);
+        int win_cur = window(0), win_next = window(1);
+        for (int k = 0; ok && next.valid; ++k) {
+            cur = next;
+            int ahead0 = -1, ahead1 = -1;                     // the next item's first windows
+            for (int j = cur.kv0; j < cur.kv1 && ok; ++j, ++gt) {
                 const int st = gt % kLaStages;
-                const int wofs = ((j - it.kv0) * kLaPages) % 32;
-                if (j > it.kv0 && wofs == 0) {
+                const int wofs = ((j - cur.kv0) * kLaPages) % 32;
+                if (j > cur.kv0 && wofs == 0) {
                     win_cur = win_next;
-                    win_next = load_window((j - it.kv0) * kLaPages / 32 + 1);
+                    win_next = window((j - cur.kv0) * kLaPages / 32 + 1);
                 }
-                const int page = __shfl_sync(0xffffffffu, win_cur, wofs + (lane & (kLaPages - 1)));
+                // pages past the end, and ids outside the cache (reported), become -1: they
+                // load as zeros
+                int id = __shfl_sync(0xffffffffu, win_cur, wofs + (lane & (kLaPages - 1)));
+                if (id < 0 || id >= p.num_blocks) {
+                    if (j * kLaPages + (lane & (kLaPages - 1)) < cur.n_pages) set_status(status, PKV_ERR_DEVICE_INDEX);
+                    id = -1;
+                }
+                if (j == cur.kv1 - 1) {
+                    fetch(k + 1);
+                    if (!ok) break;
+                    ahead0 = window(0), ahead1 = window(1);
+                }
                 // each page as soon as the products of the tile two before have read it
 #pragma unroll 1
                 for (int i = 0; i < kLaPages && ok; ++i) {
@@ -373,32 +422,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     __syncwarp();
                     if (lane == i)
                         tma_load_5d(smem + kLaOffKV + st * kLaStage + i * kLatPageBytes, &kv_map,
-                                    &bars[kLaKVFull + st], 0, 0, 0, 0, page);
+                                    &bars[kLaKVFull + st], 0, 0, 0, 0, id);
                     // (a stage of which some pages were not asked for never completes: not waited for)
                     if (i == kLaPages - 1) issued = gt + 1;
                 }
-                if (!ok) break;
-                if (j == it.n_kv - 1 && end % kBlock) {
-                    // zero the rows past the last visible key in its page
-                    ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaKVFull + st], (gt / kLaStages) & 1, status));
-                    if (!ok) break;
-                    const int first = end % kBlock, rows = kBlock - first;
-                    const uint32_t pg = sKV + st * kLaStage + ((end - 1) / kBlock - j * kLaPages) * kLatPageBytes;
-                    for (int e = lane; e < rows * kLaChunks * 8; e += 32) {
-                        const int t = first + e / (kLaChunks * 8), v = e % (kLaChunks * 8);
-                        const uint32_t a = pg + (t >> 3) * kLaGroup + (v >> 3) * 1024 + (t & 7) * 128 + (v & 7) * 16;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[kLaFix + st]);
-                }
             }
+            win_cur = ahead0, win_next = ahead1;
         }
         // (after a failed wait: the copies in flight land before the CTA ends)
         for (int g = max(0, issued - kLaStages); g < issued && !ok; ++g)
             mbar_wait_bounded(&bars[kLaKVFull + g % kLaStages], (g / kLaStages) & 1);
-        if (lane == 0) *desc = split;
     } else if (warp == 1) {
         // ---------------- MMA issue (the warp stays converged) ----------------
         constexpr uint32_t kIdescS = idesc_bf16_f32(kLaRows, kLaKeys, 0, 0);
@@ -496,27 +529,53 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             gt0 += n;
         }
     } else if (warp == 2) {
-        // ---------------- Q of each item, once the previous item's last S has read it ----------------
+        // ---------------- Q of each item; rows past its last visible key ----------------
         bool ok = true;
-        int loaded = 0;
+        int loaded = 0, gt = 0;
+        int kv1 = 0, end = 0;                                 // of the item before
+        bool fix = false;
         for (int k = 0; ok; ++k) {
             const int slot = k % kLaItemSlots;
             ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
             if (!ok) break;
-            const bool valid = items[slot].valid != 0;
-            const int tok0 = items[slot].tok0;
+            const volatile LaItem *it = items + slot;
+            const bool valid = it->valid != 0;
+            const int tok0 = it->tok0, n = it->kv1 - it->kv0;
+            const int next_end = it->lim0 + it->ntok - 1, next_kv1 = it->kv1;
+            const bool next_fix = valid && next_kv1 == it->n_kv && next_end % kBlock;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
-            if (!valid) break;
+            // the previous item's last S has read its Q (and that tile's keys)
             if (k > 0) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaQEmpty], (k - 1) & 1, status));
             if (!ok) break;
-            // a box is 64 dims of the group's heads of tpt tokens; tokens past the batch
-            // and heads past the last load as zeros, rows that no item holds are masked
-            if (lane == 0) mbar_arrive_expect_tx(&bars[kLaQFull], kLaChunks * 128 * p.hpt * p.tpt);
-            __syncwarp();
-            if (lane < kLaChunks)
-                tma_load_3d(smem + kLaOffQ + lane * kLaQChunk, &q_map, &bars[kLaQFull], lane * 64, group * p.hpt, tok0);
-            loaded = k + 1;
+            if (valid) {
+                // a box is 64 dims of the group's heads of tpt tokens; tokens past the batch
+                // and heads past the last load as zeros, rows that no item holds are masked
+                if (lane == 0) mbar_arrive_expect_tx(&bars[kLaQFull], kLaChunks * 128 * p.hpt * p.tpt);
+                __syncwarp();
+                if (lane < kLaChunks)
+                    tma_load_3d(smem + kLaOffQ + lane * kLaQChunk, &q_map, &bars[kLaQFull], lane * 64, group * p.hpt,
+                                tok0);
+                loaded = k + 1;
+            }
+            if (fix) {
+                // zero the rows past the previous item's last visible key, in its page, while
+                // the softmax works on that tile
+                const int st = (gt - 1) % kLaStages;
+                const int first = end % kBlock, rows = kBlock - first;
+                const uint32_t pg = sKV + st * kLaStage + ((end - 1) / kBlock - (kv1 - 1) * kLaPages) * kLatPageBytes;
+                for (int e = lane; e < rows * kLaChunks * 8; e += 32) {
+                    const int t = first + e / (kLaChunks * 8), v = e % (kLaChunks * 8);
+                    const uint32_t a = pg + (t >> 3) * kLaGroup + (v >> 3) * 1024 + (t & 7) * 128 + (v & 7) * 16;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaFix + st]);
+            }
+            if (!valid) break;
+            gt += n;
+            fix = next_fix, end = next_end, kv1 = next_kv1;
         }
         if (loaded > 0) mbar_wait_bounded(&bars[kLaQFull], (loaded - 1) & 1);    // landed before the CTA ends
     } else if (warp >= 4) {
@@ -617,9 +676,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     }
                     l[i] += sum;
                 }
-                ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaVote], gt & 1, status));
-                // the weights' buffer and O' are free once the previous tile's products completed
-                if (ok && gt > 0) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
+                // the votes are in; and the weights' buffer and O' are free once the previous
+                // tile's products completed (odd lanes wait for that, even ones for the votes)
+                const bool odd = lane & 1;
+                ok = __all_sync(0xffffffffu, (odd && gt == 0) || pf_wait(&bars[odd ? kLaODone : kLaVote],
+                                                                         (odd ? gt - 1 : gt) & 1, status));
                 if (!ok) break;
                 if (*reinterpret_cast<volatile const uint32_t *>(votes + 4 * sb) && j > kv0) {
                     tc_fence_after();
@@ -678,33 +739,66 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 tc_fence_after();
                 float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
                             (static_cast<int64_t>(blockIdx.x) * 2 + max(part, 0)) * kLaPartFloats;
-                const int dim = quad * 32 + lane;
+                if (part >= 0) {
+                    // [128-dim block][row / 4][dim][row % 4]
+                    const int dim = quad * 32 + lane;
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const int m = c >> 1, r0 = 32 * (c & 1);
-                    if (r0 >= rows) continue;
-                    float v[32];
-                    tmem_ld32f(tlane + 64u * m + r0, v);
-                    tmem_ld_wait();
-                    if (part >= 0) {
-                        // [128-dim block][row / 4][dim][row % 4]
+                    for (int c = 0; c < 8; ++c) {
+                        const int m = c >> 1, r0 = 32 * (c & 1);
+                        if (r0 >= rows) continue;
+                        float v[32];
+                        tmem_ld32f(tlane + 64u * m + r0, v);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             if (r0 + e < rows)
                                 *reinterpret_cast<float4 *>(po + ((m * 16 + (r0 + e) / 4) * 128 + dim) * 4) =
                                     make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    } else {
-                        // neighbouring lanes exchange a row each: 4-byte stores, 64 bytes a row
+                    }
+                } else {
+                    // 32 dims x 32 rows at a time through this warp's 2 KiB of the weights'
+                    // buffer, transposed by stmatrix: rows of 64 bytes, 16 a lane
+                    const uint32_t stage = sP + quad * 2048;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < rows; r0 += 32) {
+                        float inv[8];
+                        int64_t to[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float a = v[e] * row_inv[r0 + e], b = v[e + 1] * row_inv[r0 + e + 1];
-                            const bool odd = lane & 1;
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                            const int row = row_dst[r0 + e + (odd ? 1 : 0)];
-                            if (row >= 0)
-                                *reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(row) * kLatent + m * 128 +
-                                                              (dim & ~1)) =
-                                    odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                        for (int e = 0; e < 4; ++e) {
+                            inv[2 * e] = row_inv[r0 + 8 * e + 2 * (lane & 3)];
+                            inv[2 * e + 1] = row_inv[r0 + 8 * e + 2 * (lane & 3) + 1];
+                            to[e] = row_dst[r0 + 8 * e + (lane >> 2)];
+                        }
+#pragma unroll 1
+                        for (int m = 0; m < kLatent / 128; ++m) {
+                            float a[16], b[16];                 // dims t / 4 (+ 8), and 16 further
+                            tmem_ld_16x32f(tlane + 64u * m + r0, a);
+                            tmem_ld_16x32f(tlane + (16u << 16) + 64u * m + r0, b);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {       // rows r0 + 8 e ..
+                                const int row = 8 * e + (lane & 7);
+                                const float x = inv[2 * e], y = inv[2 * e + 1];
+                                stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
+                                              pack_bf16x2(a[4 * e] * x, a[4 * e + 1] * y),
+                                              pack_bf16x2(a[4 * e + 2] * x, a[4 * e + 3] * y),
+                                              pack_bf16x2(b[4 * e] * x, b[4 * e + 1] * y),
+                                              pack_bf16x2(b[4 * e + 2] * x, b[4 * e + 3] * y));
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int row = 8 * e + (lane >> 2);
+                                uint4 w;
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                             : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
+                                             : "memory");
+                                if (to[e] >= 0)
+                                    *reinterpret_cast<uint4 *>(p.out + to[e] * kLatent + m * 128 + quad * 32 +
+                                                               (lane & 3) * 8) = w;
+                            }
+                            __syncwarp();
                         }
                     }
                 }
@@ -877,6 +971,8 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     p.tpt = 1;
     if (p.groups == 1)
         while (2 * p.tpt * p.hpt <= kLaRows && p.tpt < max_query_len) p.tpt *= 2;
+    p.tpt_shift = 0;
+    while ((1 << p.tpt_shift) < p.tpt) ++p.tpt_shift;
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.ws = static_cast<uint8_t *>(workspace);
