@@ -38,9 +38,11 @@
 // each weight, about that of the output's own rounding.  Sums, maxima and
 // outputs are fp32.
 //
-// Warp roles (256 threads): warp 3 walks the run and publishes items ahead of
-// the others; warp 0 loads pages by TMA (one 18 KiB box a page); warp 1 issues
-// the MMAs; warp 2 loads Q (TMA), zeroes the rows past a tile's last visible key
+// Warp roles (288 threads): warp 3 walks the run and publishes items ahead of
+// the others; warp 0 loads pages by TMA (two boxes a page); warp 1 issues the S
+// products and warp 8 the second ones, each as soon as its operands are there (one
+// warp for both had to look for two events in turn, about 600 cycles a tile);
+// warp 2 loads Q (TMA), zeroes the rows past a tile's last visible key
 // (so that what an unwritten slot holds never meets a zero weight) and owns
 // tensor memory; warps 4-7 are the softmax and epilogue warps.  Every wait is
 // bounded.
@@ -60,19 +62,29 @@ constexpr int kLaChunks = kLatRow / 64;                      // 9 chunks of 64 d
 constexpr int kLaQChunk = kLaRows * 128;                     // 8192: 64 dims of 64 rows
 constexpr int kLaMaxCtas = 152;
 constexpr int kLaMaxHeads = 1024;
-constexpr int kLaThreads = 256;
+constexpr int kLaThreads = 288;
 constexpr int kLaItemSlots = 4;
 
-// A page in shared memory as its box lands: [token half][chunk][token % 8][64
-// dims], 128-byte swizzle.  The 8-row groups of a tile's 64 keys then sit at one
-// stride (9216) across pages, for both products.
-constexpr int kLaGroup = kLaChunks * 1024;                   // 9216
+// A stage holds a tile's 64 keys in two parts, each [page][token half][chunk]
+// [token % 8][64 dims] with 128-byte swizzle: part A has chunks 0-3 (dims 0 .. 255),
+// part B chunks 4-8 (dims 256 .. 511 and the rotated 64).  In each part the 8-key
+// groups of the tile sit at one stride, for both products.  The parts are loaded,
+// waited for and released on their own: S starts on A while B is on its way, and
+// A's next load starts while the products with B's dims still run.  The rotated
+// chunk is not needed once S is computed: the tile's weights are written over it
+// (rows of 64 query rows per key, MN-major).
+constexpr int kLaChunksA = 4, kLaChunksB = kLaChunks - kLaChunksA;        // 4, 5
+constexpr int kLaGroupA = kLaChunksA * 1024, kLaGroupB = kLaChunksB * 1024;
+constexpr int kLaPageA = 2 * kLaGroupA, kLaPageB = 2 * kLaGroupB;         // 8192, 10240
+constexpr int kLaPartA = kLaPages * kLaPageA, kLaPartB = kLaPages * kLaPageB;
+static_assert(kLaPartA + kLaPartB == kLaStage, "a stage's parts");
+constexpr int kLaOffW = kLaPartA + (kLaChunksB - 1) * 1024;               // weights of key group 0 in a stage
 
 // shared memory (from a 1 KiB boundary)
 constexpr int kLaOffQ = 0;
 constexpr int kLaOffKV = kLaOffQ + kLaChunks * kLaQChunk;                 // 73728
-constexpr int kLaOffP = kLaOffKV + kLaStages * kLaStage;                  // 221184
-constexpr int kLaOffBar = kLaOffP + kLaRows * 128;                        // 229376
+constexpr int kLaOffOut = kLaOffKV + kLaStages * kLaStage;                // rows on their way out, 2 KiB a warp
+constexpr int kLaOffBar = kLaOffOut + 4 * 2048;                           // 229376
 constexpr int kLaOffAlpha = kLaOffBar + 256;                              // float [2][64]
 constexpr int kLaOffRow = kLaOffAlpha + 512;                              // float [64], int [64]
 constexpr int kLaOffItems = kLaOffRow + 512;
@@ -123,15 +135,16 @@ static_assert(kLaItemSlots * sizeof(LaItem) <= 256, "item ring");
 enum LaBar {
     kLaQFull = 0, kLaQEmpty = 1,
     kLaSFull = 2,             // S buffer b written (+ b)
-    kLaPFull = 4,             // weights of a tile written (and O' rescaled where needed)
+    kLaSFree = 27,            // S buffer b read (+ b)
+    kLaPFull = 4,             // weights and votes of a tile written
     kLaODone = 5,             // the tile's second products completed
     kLaOFree = 6,             // O' read out by the epilogue
-    kLaVote = 7,              // the four softmax warps meet (every tile)
-    kLaMeet = 8,              // the same, at the end of an item
-    kLaKVFull = 9,            // (+ stage)
-    kLaFix = 11,              // rows past the last visible key zeroed (+ stage)
-    kLaItemFull = 13, kLaItemEmpty = 17,
-    kLaKVEmpty = 21,          // a page read by its last product (+ 4 stage + page)
+    kLaRescaled = 7,          // O' rescaled (only in tiles where some warp voted for it)
+    kLaMeet = 8,              // the four softmax warps meet at the end of an item
+    kLaFix = 9,               // rows past the last visible key zeroed (+ stage)
+    kLaItemFull = 11, kLaItemEmpty = 15,
+    kLaKVFull = 19,           // a part landed (+ 2 stage + part)
+    kLaKVEmpty = 23,          // a part read by its last product (+ 2 stage + part)
     kLaNumBars = 29
 };
 static_assert(kLaNumBars * 8 + 24 <= 256, "barriers, tensor-memory address, status, votes");
@@ -211,8 +224,8 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32
 }
 
 __global__ void __launch_bounds__(kLaThreads, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
-                       const LaParams p) {
+    latent_attn_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                       const __grid_constant__ CUtensorMap q_map, const LaParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kLaOffBar);
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     volatile uint8_t *votes = reinterpret_cast<volatile uint8_t *>(tmem_slot + 2);    // [tile & 1][warp]
     int64_t *scan = reinterpret_cast<int64_t *>(smem + kLaOffAlpha);    // before the roles start only
     volatile LaItem *items = reinterpret_cast<volatile LaItem *>(smem + kLaOffItems);
-    const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sP = smem_u32(smem + kLaOffP);
+    const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sOut = smem_u32(smem + kLaOffOut);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     const int my_lane = blockIdx.x / p.groups;               // run
     const int group = blockIdx.x - my_lane * p.groups;       // head group
@@ -229,12 +242,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (threadIdx.x < kLaNumBars) {
         const int b = threadIdx.x;
         int count = 1;
-        if (b == kLaPFull || b == kLaOFree || b == kLaVote || b == kLaMeet) count = 4;
-        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 7;   // loads, MMA, Q, 4 softmax warps
+        if (b == kLaPFull || b == kLaOFree || b == kLaRescaled || b == kLaMeet || b == kLaSFree ||
+            b == kLaSFree + 1)
+            count = 4;
+        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 8;   // loads, 2 MMA warps, Q, 4 softmax warps
         mbar_init(&bars[b], count);
     }
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&kv_map);
+        tma_prefetch_desc(&a_map);
+        tma_prefetch_desc(&b_map);
         tma_prefetch_desc(&q_map);
         *status = PKV_OK;
     }
@@ -260,7 +276,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int64_t per = max(static_cast<int64_t>(1), (total + p.lanes - 1) / p.lanes);
     const int64_t lo = min(total, my_lane * per), hi = min(total, lo + per);
     __syncthreads();
-    if (threadIdx.x == 0) scan[8] = -1;
+    if (threadIdx.x == 0) scan[10] = -1;
     int64_t base = 0;
     for (int r0 = 0; r0 < p.num_seqs && lo < hi; r0 += kLaThreads) {
         const int r = r0 + threadIdx.x;
@@ -282,8 +298,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             all += scan[w];
         }
         if (lo >= before && lo < before + mine) {
-            scan[8] = r;
-            scan[9] = lo - before;
+            scan[10] = r;
+            scan[11] = lo - before;
         }
         base = all;
         __syncthreads();
@@ -292,8 +308,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     int start_req = 0;
     int64_t start_off = 0;
     if (lo < hi) {
-        start_req = static_cast<int>(scan[8]);
-        start_off = scan[9];
+        start_req = static_cast<int>(scan[10]);
+        start_off = scan[11];
     }
     tc_fence_before();
     __syncthreads();
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // ---------------- pages through the block table ----------------
         bool ok = true;
         int gt = 0;                                           // key tiles of this CTA so far
-        int issued = 0;                                       // stages of copies issued
+        int issued = 0;                                       // parts whose copies were issued
         struct {
             bool valid;
             int kv0, kv1, n_pages;
@@ -411,122 +427,141 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     if (!ok) break;
                     ahead0 = window(0), ahead1 = window(1);
                 }
-                // each page as soon as the products of the tile two before have read it
+                // each part as soon as the products of the tile two before have read it
 #pragma unroll 1
-                for (int i = 0; i < kLaPages && ok; ++i) {
+                for (int part = 0; part < 2 && ok; ++part) {
+                    const int b = 2 * st + part;
                     if (gt >= kLaStages)
-                        ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaKVEmpty + st * kLaPages + i],
-                                                             (gt / kLaStages - 1) & 1, status));
+                        ok = __all_sync(0xffffffffu,
+                                        pf_wait(&bars[kLaKVEmpty + b], (gt / kLaStages - 1) & 1, status));
                     if (!ok) break;
-                    if (lane == 0 && i == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + st], kLaStage);
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + b], part ? kLaPartB : kLaPartA);
                     __syncwarp();
-                    if (lane == i)
-                        tma_load_5d(smem + kLaOffKV + st * kLaStage + i * kLatPageBytes, &kv_map,
-                                    &bars[kLaKVFull + st], 0, 0, 0, 0, id);
-                    // (a stage of which some pages were not asked for never completes: not waited for)
-                    if (i == kLaPages - 1) issued = gt + 1;
+                    if (lane < kLaPages)
+                        tma_load_5d(smem + kLaOffKV + st * kLaStage + (part ? kLaPartA + lane * kLaPageB : lane * kLaPageA),
+                                    part ? &b_map : &a_map, &bars[kLaKVFull + b], 0, 0, part ? kLaChunksA : 0, 0, id);
+                    issued = 2 * gt + part + 1;
                 }
             }
             win_cur = ahead0, win_next = ahead1;
         }
         // (after a failed wait: the copies in flight land before the CTA ends)
-        for (int g = max(0, issued - kLaStages); g < issued && !ok; ++g)
-            mbar_wait_bounded(&bars[kLaKVFull + g % kLaStages], (g / kLaStages) & 1);
+        for (int g = max(0, issued - 2 * kLaStages); g < issued && !ok; ++g)
+            mbar_wait_bounded(&bars[kLaKVFull + g % (2 * kLaStages)], (g / (2 * kLaStages)) & 1);
     } else if (warp == 1) {
-        // ---------------- MMA issue (the warp stays converged) ----------------
+        // ---------------- S products (the warp stays converged) ----------------
         constexpr uint32_t kIdescS = idesc_bf16_f32(kLaRows, kLaKeys, 0, 0);
+        // queries and keys K-major (8-key groups one stride apart)
         const uint64_t dq = smem_desc_sw128(sQ, 16, 1024);
-        const uint64_t dk = smem_desc_sw128(sKV, 16, kLaGroup);          // K-major, 8-key groups 9216 apart
-        const uint64_t dv = smem_desc_sw128(sKV, 1024, kLaGroup);        // MN-major, 64-dim chunks 1024 apart
-        const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
+        const uint64_t dka = smem_desc_sw128(sKV, 16, kLaGroupA), dkb = smem_desc_sw128(sKV + kLaPartA, 16, kLaGroupB);
         bool ok = true;
-        int gt0 = 0;
-        uint32_t fix_par = 0;
+        int gt = 0;
         for (int k = 0; ok; ++k) {
             const int slot = k % kLaItemSlots;
-            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            ok = warp_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status);
+            if (!ok) break;
+            const bool valid = uniform(static_cast<int>(items[slot].valid)) != 0;
+            const int n = uniform(items[slot].kv1 - items[slot].kv0);
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+            if (!valid) break;
+            ok = warp_wait(&bars[kLaQFull], k & 1, status);
+            for (int j = 0; j < n && ok; ++j, ++gt) {
+                const int st = gt % kLaStages, sb = gt & 1;
+                const uint32_t par = (gt / kLaStages) & 1;
+                // the buffer's scores of the tile two before have been read
+                if (gt >= 2) ok = warp_wait(&bars[kLaSFree + sb], ((gt >> 1) - 1) & 1, status);
+                if (ok) ok = warp_wait(&bars[kLaKVFull + 2 * st], par, status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t so = static_cast<uint32_t>(st * (kLaStage >> 4));
+                const uint32_t d = tmem + la_col_s(sb);
+                const uint64_t ba = dka + so, bb = dkb + so;
+                if (elect_one()) {
+#pragma unroll
+                    for (int c = 0; c < kLaChunksA; ++c)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16_ss(d, dq + c * (kLaQChunk >> 4) + kk * 2, ba + c * (1024 >> 4) + kk * 2, kIdescS,
+                                        (c | kk) ? 1u : 0u);
+                }
+                __syncwarp();
+                ok = warp_wait(&bars[kLaKVFull + 2 * st + 1], par, status);
+                if (!ok) break;
+                tc_fence_after();
+                const bool last = j == n - 1;
+                if (elect_one()) {
+#pragma unroll
+                    for (int c = 0; c < kLaChunksB; ++c)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16_ss(d, dq + (kLaChunksA + c) * (kLaQChunk >> 4) + kk * 2, bb + c * (1024 >> 4) + kk * 2,
+                                        kIdescS, 1u);
+                    umma_commit(&bars[kLaSFull + sb]);
+                    if (last) umma_commit(&bars[kLaQEmpty]);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == 8) {
+        // ---------------- second products (the warp stays converged) ----------------
+        // values MN-major (64-dim chunks 1024 apart), weights MN-major
+        const uint64_t dva = smem_desc_sw128(sKV, 1024, kLaGroupA), dvb = smem_desc_sw128(sKV + kLaPartA, 1024, kLaGroupB);
+        const uint64_t dw = smem_desc_sw128(sKV + kLaOffW, 16, kLaGroupB);
+        bool ok = true;
+        int gt = 0;
+        uint32_t fix_par = 0, rescales = 0;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kLaItemSlots;
+            ok = warp_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status);
             if (!ok) break;
             const volatile LaItem *cur = items + slot;
             const bool valid = uniform(static_cast<int>(cur->valid)) != 0;
             const int n = uniform(cur->kv1 - cur->kv0);
             const int rows = uniform(cur->ntok * p.hpt);
             const int end = uniform(cur->lim0 + cur->ntok - 1);
-            const int fix_tile = uniform(cur->kv1 == cur->n_kv && end % kBlock ? n - 1 : -1);
+            const bool fix = uniform(static_cast<int>(cur->kv1 == cur->n_kv && end % kBlock)) != 0;
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
             if (!valid) break;
-            // the second products' N: the tile's rows, in sixteens
-            const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 0);
-            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaQFull], k & 1, status));
-            int js = 0, jp = 0;
-            uint64_t t_idle = 0;
-            // S(j) once its stage has landed (S buffer j & 1 was read before the
-            // weights of tile j - 2 were written, and those products are issued
-            // before); the second products of j once its weights are written, the
-            // end tile is fixed and the previous item's O' has been read out.
-            while (ok && jp < n) {
-                const bool s_can = js < n && js <= jp + 1;
-                const bool p_can = jp < js;
-                const int gs = gt0 + js, gp = gt0 + jp;
-                if (s_can && warp_test(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1)) {
-                    tc_fence_after();
-                    const uint64_t b0 = dk + static_cast<uint32_t>((gs % kLaStages) * (kLaStage >> 4));
-                    const uint32_t d = tmem + la_col_s(gs & 1);
-                    ++js;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int c = 0; c < kLaChunks; ++c)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_f16_ss(d, dq + c * (kLaQChunk >> 4) + kk * 2, b0 + c * (1024 >> 4) + kk * 2, kIdescS,
-                                            (c | kk) ? 1u : 0u);
-                        umma_commit(&bars[kLaSFull + (gs & 1)]);
-                        if (js == n) umma_commit(&bars[kLaQEmpty]);
-                    }
-                    __syncwarp();
-                    t_idle = 0;
-                    continue;
+            // N: the tile's rows, in sixteens
+            const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 1);
+            // O' has been read out by the previous item's epilogue
+            if (k > 0) ok = warp_wait(&bars[kLaOFree], (k - 1) & 1, status);
+            for (int j = 0; j < n && ok; ++j, ++gt) {
+                const int st = gt % kLaStages;
+                ok = warp_wait(&bars[kLaPFull], gt & 1, status);
+                if (!ok) break;
+                if (fix && j == n - 1) {
+                    ok = warp_wait(&bars[kLaFix + st], (fix_par >> st) & 1u, status);
+                    fix_par ^= 1u << st;
                 }
-                if (p_can) {
-                    const int st = gp % kLaStages;
-                    bool ready = warp_test(&bars[kLaPFull], gp & 1);
-                    if (ready && jp == fix_tile) ready = warp_test(&bars[kLaFix + st], (fix_par >> st) & 1u);
-                    if (ready && jp == 0 && k > 0) ready = warp_test(&bars[kLaOFree], (k - 1) & 1);
-                    if (ready) {
-                        if (jp == fix_tile) fix_par ^= 1u << st;
-                        tc_fence_after();
-                        const uint64_t a0 = dv + static_cast<uint32_t>(st * (kLaStage >> 4));
-                        const uint32_t more = jp > 0 ? 1u : 0u;
-                        if (elect_one()) {
-                            // a page (16 keys) at a time, each free for the next load on its own
-#pragma unroll
-                            for (int kk = 0; kk < kLaPages; ++kk) {
-#pragma unroll
-                                for (int m = 0; m < kLatent / 128; ++m)
-                                    umma_f16_ss(tmem + 64u * m, a0 + kk * (kLatPageBytes >> 4) + m * (2048 >> 4),
-                                                dp + kk * 2, idesc_o, kk > 0 ? 1u : more);
-                                umma_commit(&bars[kLaKVEmpty + st * kLaPages + kk]);
-                            }
-                            umma_commit(&bars[kLaODone]);
-                        }
-                        __syncwarp();
-                        ++jp;
-                        t_idle = 0;
-                        continue;
-                    }
+                if (j > 0 && uniform(*reinterpret_cast<volatile const uint32_t *>(votes + 4 * (gt & 1)))) {
+                    if (ok) ok = warp_wait(&bars[kLaRescaled], rescales & 1, status);
+                    ++rescales;
                 }
-                if (p_can)
-                    mbar_try_wait_for(&bars[kLaPFull], gp & 1, 200);
-                else
-                    mbar_try_wait(&bars[kLaKVFull + gs % kLaStages], (gs / kLaStages) & 1);
-                const uint64_t now = uniform(global_ns());
-                if (t_idle == 0) {
-                    t_idle = now;
-                } else if (now - t_idle > kWaitLimitNs) {
-                    set_status(status, PKV_ERR_DEVICE_TIMEOUT);
-                    ok = false;
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t so = static_cast<uint32_t>(st * (kLaStage >> 4));
+                const uint64_t a0 = dva + so, a1 = dvb + so, w0 = dw + so;
+                const uint32_t more = j > 0 ? 1u : 0u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int kk = 0; kk < kLaPages; ++kk)
+                            umma_f16_ss(tmem + 64u * m, a0 + kk * (kLaPageA >> 4) + m * (2048 >> 4),
+                                        w0 + kk * (kLaPageB >> 4), idesc_o, kk > 0 ? 1u : more);
+                    umma_commit(&bars[kLaKVEmpty + 2 * st]);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int kk = 0; kk < kLaPages; ++kk)
+                            umma_f16_ss(tmem + 128u + 64u * m, a1 + kk * (kLaPageB >> 4) + m * (2048 >> 4),
+                                        w0 + kk * (kLaPageB >> 4), idesc_o, kk > 0 ? 1u : more);
+                    umma_commit(&bars[kLaKVEmpty + 2 * st + 1]);
+                    umma_commit(&bars[kLaODone]);
                 }
+                __syncwarp();
             }
-            gt0 += n;
         }
     } else if (warp == 2) {
         // ---------------- Q of each item; rows past its last visible key ----------------
@@ -563,10 +598,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 // the softmax works on that tile
                 const int st = (gt - 1) % kLaStages;
                 const int first = end % kBlock, rows = kBlock - first;
-                const uint32_t pg = sKV + st * kLaStage + ((end - 1) / kBlock - (kv1 - 1) * kLaPages) * kLatPageBytes;
-                for (int e = lane; e < rows * kLaChunks * 8; e += 32) {
-                    const int t = first + e / (kLaChunks * 8), v = e % (kLaChunks * 8);
-                    const uint32_t a = pg + (t >> 3) * kLaGroup + (v >> 3) * 1024 + (t & 7) * 128 + (v & 7) * 16;
+                const uint32_t base = sKV + st * kLaStage;
+                const int page = (end - 1) / kBlock - (kv1 - 1) * kLaPages;
+                for (int e = lane; e < rows * (kLatent / 8); e += 32) {      // the values' dims only
+                    const int t = first + e / (kLatent / 8), c = (e % (kLatent / 8)) >> 3;
+                    const uint32_t g = c < kLaChunksA ? (2 * page + (t >> 3)) * kLaGroupA + c * 1024
+                                                      : kLaPartA + (2 * page + (t >> 3)) * kLaGroupB + (c - kLaChunksA) * 1024;
+                    const uint32_t a = base + g + (t & 7) * 128 + (e & 7) * 16;
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
                 }
                 fence_proxy_async_smem();
@@ -589,6 +627,34 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float sl2 = p.scale_log2;
         const int heads_here = min(p.hpt, p.heads - group * p.hpt);
+        // After this warp's weights of tile g: if some warp voted for it, O' is rescaled
+        // (its columns are rows of every warp, its lanes the quadrants of every warp),
+        // between the products of tile g - 1 and those of g.
+        auto rescale = [&](int g) -> bool {
+            if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaPFull], g & 1, status))) return false;
+            const uint32_t vote = *reinterpret_cast<volatile const uint32_t *>(votes + 4 * (g & 1));
+            if (!vote) return true;
+            if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (g - 1) & 1, status))) return false;
+            tc_fence_after();
+            const float *al = alphas + (g & 1) * kLaRows;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {                     // 32 rows of one 128-dim block at a time
+                uint32_t v[32];
+                const uint32_t a = tlane + 64u * (c >> 1) + 32u * (c & 1);
+                tmem_ld32(a, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)                  // (a warp that did not vote wrote no factors)
+                    if ((vote >> (8 * (2 * (c & 1) + (e >> 4)))) & 0xffu)
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) * al[32 * (c & 1) + e]);
+                tmem_st32(a, v);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaRescaled]);
+            return true;
+        };
         bool ok = true;
         int gt = 0, k = 0;
         for (;; ++k) {
@@ -617,6 +683,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 float s[32];
                 tmem_ld_16x64f(tlane + la_col_s(sb), s);
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaSFree + sb]);
                 const int key0 = j * kLaKeys + 2 * (lane & 3);
                 const bool masked = __any_sync(0xffffffffu, (j + 1) * kLaKeys > min(lim[0], lim[1]));
 #pragma unroll
@@ -626,6 +695,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (key0 + (e >> 2) * 8 + (e & 1) >= lim[(e >> 1) & 1]) s[e] = NEG_INF;
                 }
+                // The reference moves on a row's first visible key, and then only when some
+                // score exceeds it by 2^40: fp32 sums and bf16 weights keep their relative
+                // accuracy at any common scale, and 2^40 leaves 2^87 of range.  So most tiles
+                // need no row maximum, only each thread's own.
                 float mx[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -636,32 +709,22 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                         b = fmax3(b, s[c + 4 + 2 * i], s[c + 4 + 2 * i + 1]);
                     }
                     mx[i] = fmaxf(a, b);
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                    mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
                 }
-                // The reference moves on a row's first visible key, and then only when the
-                // tile's max exceeds it by 2^40: fp32 sums and bf16 weights keep their
-                // relative accuracy at any common scale, and 2^40 leaves 2^87 of range.
                 bool grow = false;
-                float alpha[2];
+                if (__any_sync(0xffffffffu, mx[0] > m_ref[0] + 40.f || mx[1] > m_ref[1] + 40.f)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool first = m_ref[i] == NEG_INF;
-                    const bool g = !first && mx[i] > m_ref[i] + 40.f;
-                    alpha[i] = g ? fast_exp2(m_ref[i] - mx[i]) : 1.f;
-                    if (first || g) m_ref[i] = mx[i];
-                    l[i] *= alpha[i];
-                    grow |= g;
-                }
-                // the warps' votes on a rescale of O' (its columns are rows of every warp)
-                if ((lane & 3) == 0) {
-                    alphas[sb * kLaRows + rA] = alpha[0];
-                    alphas[sb * kLaRows + rA + 8] = alpha[1];
-                }
-                grow = __any_sync(0xffffffffu, grow);
-                if (lane == 0) {
-                    votes[4 * sb + quad] = grow ? 1 : 0;
-                    mbar_arrive(&bars[kLaVote]);
+                    for (int i = 0; i < 2; ++i) {
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                        const bool first = m_ref[i] == NEG_INF;
+                        const bool g = !first && mx[i] > m_ref[i] + 40.f;
+                        const float alpha = g ? fast_exp2(m_ref[i] - mx[i]) : 1.f;
+                        if (first || g) m_ref[i] = mx[i];
+                        l[i] *= alpha;
+                        if ((lane & 3) == 0) alphas[sb * kLaRows + rA + 8 * i] = alpha;
+                        grow |= g;
+                    }
+                    grow = __any_sync(0xffffffffu, grow);
                 }
                 uint32_t w[16];
 #pragma unroll
@@ -676,40 +739,27 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     }
                     l[i] += sum;
                 }
-                // the votes are in; and the weights' buffer and O' are free once the previous
-                // tile's products completed (odd lanes wait for that, even ones for the votes)
-                const bool odd = lane & 1;
-                ok = __all_sync(0xffffffffu, (odd && gt == 0) || pf_wait(&bars[odd ? kLaODone : kLaVote],
-                                                                         (odd ? gt - 1 : gt) & 1, status));
-                if (!ok) break;
-                if (*reinterpret_cast<volatile const uint32_t *>(votes + 4 * sb) && j > kv0) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {             // 32 rows of one 128-dim block at a time
-                        uint32_t v[32];
-                        const uint32_t a = tlane + 64u * (c >> 1) + 32u * (c & 1);
-                        tmem_ld32(a, v);
-                        tmem_ld_wait();
+                // weights of 16 rows and 64 keys, transposed by stmatrix into rows of a key, over
+                // the stage's rotated chunk (which S has read)
+                const uint32_t sW = sKV + (gt % kLaStages) * kLaStage + kLaOffW;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * alphas[sb * kLaRows + 32 * (c & 1) + e]);
-                        tmem_st32(a, v);
-                    }
-                    tmem_st_wait();
+                for (int c = 0; c < 8; c += 2) {
+                    const int i = lane & 7, m = lane >> 3;    // key in its group; tile: group c + m / 2, rows m % 2
+                    stsm_x4_trans(sW + (c + (m >> 1)) * kLaGroupB + i * 128 + (((2 * quad + (m & 1)) ^ i) << 4),
+                                  w[2 * c], w[2 * c + 1], w[2 * c + 2], w[2 * c + 3]);
                 }
-                // weights of row rA (+ 8), keys 8 c + 2 (lane % 4) + {0, 1}: K-major rows of 64 keys
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t a = sP + rA * 128 + ((c ^ (rA & 7)) << 4) + (lane & 3) * 4;
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[2 * c]) : "memory");
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a + 1024), "r"(w[2 * c + 1]) : "memory");
-                }
+                if (lane == 0) votes[4 * sb + quad] = grow ? 1 : 0;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kLaPFull]);
+                if (j > kv0) ok = rescale(gt);
             }
             // epilogue
+            // (the last two tiles' products may both be still to come: a parity tells phases
+            // apart one at a time)
+            if (ok && gt > 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], gt & 1, status));
+            if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
             if (ok) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -734,7 +784,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 if (lane == 0) mbar_arrive(&bars[kLaMeet]);
                 ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaMeet], k & 1, status));
             }
-            if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
             if (ok) {
                 tc_fence_after();
                 float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
@@ -756,9 +805,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                     make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 } else {
-                    // 32 dims x 32 rows at a time through this warp's 2 KiB of the weights'
-                    // buffer, transposed by stmatrix: rows of 64 bytes, 16 a lane
-                    const uint32_t stage = sP + quad * 2048;
+                    // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
+                    // stmatrix: rows of 64 bytes, 16 a lane
+                    const uint32_t stage = sOut + quad * 2048;
 #pragma unroll 1
                     for (int r0 = 0; r0 < rows; r0 += 32) {
                         float inv[8];
@@ -769,21 +818,26 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                             inv[2 * e + 1] = row_inv[r0 + 8 * e + 2 * (lane & 3) + 1];
                             to[e] = row_dst[r0 + 8 * e + (lane >> 2)];
                         }
-#pragma unroll 1
+                        // the next block's loads run while this one is packed and stored
+                        float a[2][16], b[2][16];               // dims t / 4 (+ 8), and 16 further
+                        tmem_ld_16x32f(tlane + r0, a[0]);
+                        tmem_ld_16x32f(tlane + (16u << 16) + r0, b[0]);
+#pragma unroll
                         for (int m = 0; m < kLatent / 128; ++m) {
-                            float a[16], b[16];                 // dims t / 4 (+ 8), and 16 further
-                            tmem_ld_16x32f(tlane + 64u * m + r0, a);
-                            tmem_ld_16x32f(tlane + (16u << 16) + 64u * m + r0, b);
                             tmem_ld_wait();
+                            if (m + 1 < kLatent / 128) {
+                                tmem_ld_16x32f(tlane + 64u * (m + 1) + r0, a[(m + 1) & 1]);
+                                tmem_ld_16x32f(tlane + (16u << 16) + 64u * (m + 1) + r0, b[(m + 1) & 1]);
+                            }
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {       // rows r0 + 8 e ..
                                 const int row = 8 * e + (lane & 7);
                                 const float x = inv[2 * e], y = inv[2 * e + 1];
                                 stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
-                                              pack_bf16x2(a[4 * e] * x, a[4 * e + 1] * y),
-                                              pack_bf16x2(a[4 * e + 2] * x, a[4 * e + 3] * y),
-                                              pack_bf16x2(b[4 * e] * x, b[4 * e + 1] * y),
-                                              pack_bf16x2(b[4 * e + 2] * x, b[4 * e + 3] * y));
+                                              pack_bf16x2(a[m & 1][4 * e] * x, a[m & 1][4 * e + 1] * y),
+                                              pack_bf16x2(a[m & 1][4 * e + 2] * x, a[m & 1][4 * e + 3] * y),
+                                              pack_bf16x2(b[m & 1][4 * e] * x, b[m & 1][4 * e + 1] * y),
+                                              pack_bf16x2(b[m & 1][4 * e + 2] * x, b[m & 1][4 * e + 3] * y));
                             }
                             __syncwarp();
 #pragma unroll
@@ -894,13 +948,14 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
 
 // ---- host side --------------------------------------------------------------------
 
-// {64 dims, 8 tokens, 9 chunks, 2 halves, blocks}: a box {64, 8, 9, 2, 1} is one page.
-static int make_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks) {
+// {64 dims, 8 tokens, 9 chunks, 2 halves, blocks}: a box {64, 8, chunks, 2, 1} is
+// that many chunks of one page.
+static int make_latent_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int chunks) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return PKV_ERR_CUDA;
     const cuuint64_t dims[5] = {64, 8, kLaChunks, 2, static_cast<cuuint64_t>(num_blocks)};
     const cuuint64_t strides[4] = {kLatRowBytes, 128, 8 * kLatRowBytes, kLatPageBytes};
-    const cuuint32_t box[5] = {64, 8, kLaChunks, 2, 1};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(chunks), 2, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -982,14 +1037,15 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
     p.lanes = (sms < kLaMaxCtas ? sms : kLaMaxCtas) / p.groups;
     const int ctas = p.lanes * p.groups;
-    CUtensorMap kvm, qm;
-    int rc = make_latent_map(&kvm, latent_cache, num_blocks);
+    CUtensorMap am, bm, qm;
+    int rc = make_latent_map(&am, latent_cache, num_blocks, kLaChunksA);
+    if (!rc) rc = make_latent_map(&bm, latent_cache, num_blocks, kLaChunksB);
     if (rc) return rc;
     if (num_tokens > 0) {
         rc = make_latent_query_map(&qm, query, query_token_stride, p);
         if (rc) return rc;
     } else {
-        qm = kvm;                                  // no rows: not read
+        qm = am;                                   // no rows: not read
     }
     static std::mutex mu;
     static uint64_t done_mask = 0;
@@ -1004,7 +1060,7 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
         }
     }
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
-                   static_cast<cudaStream_t>(stream), kvm, qm, p) != cudaSuccess)
+                   static_cast<cudaStream_t>(stream), am, bm, qm, p) != cudaSuccess)
         return PKV_ERR_CUDA;
     if (launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(ctas), 16), dim3(256), 0,
                    static_cast<cudaStream_t>(stream), p, ctas) != cudaSuccess)

@@ -31,9 +31,11 @@ __device__ __forceinline__ bool elect_one() {
 // A value that is the same in every lane, in a form the compiler knows to be.
 template <typename T> __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// One converged poll of a barrier's phase.
-__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+// A converged warp's bounded wait; false (and the error recorded) once it gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+    if (!ok) set_status(status, PKV_ERR_DEVICE_TIMEOUT);
+    return ok;
 }
 
 }  // namespace pkv
