@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // everything before this call is complete from here on: the cache write, the
     // query, and the previous use of the workspace
     pdl_wait();
+    pdl_trigger();                        // the merge's CTAs may take their places (they wait for this grid)
     const bool work = lo < hi;
     int4 *desc = reinterpret_cast<int4 *>(p.ws + kLaWsDesc) + blockIdx.x;
 
@@ -866,7 +867,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
     }
 
-    pdl_trigger();
     tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -884,7 +884,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 // Piece i of the tile that starts in CTA c lies in CTA c + i * groups, slot 1
 // for the first and 0 for the others:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
-// blockIdx.y: 128 dims x 16 rows; a thread takes four rows of one dim at a time.
+// blockIdx.y: 128 dims x 16 rows; a thread takes one dim of eight rows.  The merge
+// is one trip to memory that the first kernel has just written, and nothing else,
+// so nothing is looked up before it starts: the first two pieces of a tile (most
+// have two) are this CTA's own and the next lane's, and are read beside the record
+// that says whether there is a tile to merge.
+constexpr int kLaCombineY = 4 * (kLaRows / 16);
+
 __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, int ctas) {
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
@@ -900,48 +906,65 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
         }
         if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = s;
     }
+    constexpr int kQ = 2;                                             // groups of four rows a thread
     const int cta = blockIdx.x;
-    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
-    const int pieces = d.z;
-    if (pieces == 0) return;
-    const int group = cta % p.groups;
-    const int rows = d.y * p.hpt, heads_here = min(p.hpt, p.heads - group * p.hpt);
     const int m = blockIdx.y >> 2, dim = threadIdx.x & 127;
+    const int r4 = (blockIdx.y & 3) * 4 + (threadIdx.x >> 7) * kQ;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl);
-    const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO);
-    auto part_of = [&](int i) { return static_cast<int64_t>(cta + i * p.groups) * 2 + (i == 0 ? 1 : 0); };
+    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl) + r4 * 4;
+    const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO) + ((m * 16 + r4) * 128 + dim) * 4;
+    float4 mx[kQ], ls[kQ], acc[kQ], m1[kQ], l1[kQ], a1[kQ];
+    auto load = [&](int64_t part, float4 (&a)[kQ], float4 (&b)[kQ], float4 (&c)[kQ]) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            a[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + q * 4);
+            b[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + kLaRows + q * 4);
+            c[q] = *reinterpret_cast<const float4 *>(o + part * kLaPartFloats + q * 512);
+        }
+    };
+    // two softmax states into one; a state that saw no key has m = -inf, and whatever its sums hold is not used
+    auto join = [&](float &m0, float &l0, float &a0, float m1, float l1, float a1) {
+        const float M = fmaxf(m0, m1);
+        const float w0 = m0 == NEG_INF ? 0.f : fast_exp2(m0 - M), w1 = m1 == NEG_INF ? 0.f : fast_exp2(m1 - M);
+        l0 = (w0 == 0.f ? 0.f : w0 * l0) + (w1 == 0.f ? 0.f : w1 * l1);
+        a0 = (w0 == 0.f ? 0.f : w0 * a0) + (w1 == 0.f ? 0.f : w1 * a1);
+        m0 = M;
+    };
+    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
+    load(static_cast<int64_t>(cta) * 2 + 1, mx, ls, acc);
+    load(static_cast<int64_t>(min(cta + p.groups, ctas - 1)) * 2, m1, l1, a1);
+    const int pieces = d.z;
+    const int rows = d.y * p.hpt;
+    if (pieces < 2 || r4 * 4 >= rows) return;                         // (whole warps)
 #pragma unroll 1
-    for (int q = threadIdx.x >> 7; q < 4; q += 2) {
-        const int r4 = (blockIdx.y & 3) * 4 + q;
-        if (r4 * 4 >= rows) return;
-        float M[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-#pragma unroll 4
-        for (int i = 0; i < pieces; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(ml + part_of(i) * 2 * kLaRows + r4 * 4);
-            M[0] = fmaxf(M[0], x.x), M[1] = fmaxf(M[1], x.y), M[2] = fmaxf(M[2], x.z), M[3] = fmaxf(M[3], x.w);
-        }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f}, L[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = 0; i < pieces; ++i) {
-            const int64_t part = part_of(i);
-            const float4 x = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + r4 * 4);
-            const float4 y = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + kLaRows + r4 * 4);
-            const float4 v = *reinterpret_cast<const float4 *>(o + part * kLaPartFloats + ((m * 16 + r4) * 128 + dim) * 4);
-            const float mx[4] = {x.x, x.y, x.z, x.w}, ls[4] = {y.x, y.y, y.z, y.w}, vs[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 1;;) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float w = mx[e] == NEG_INF ? 0.f : fast_exp2(mx[e] - M[e]);
-                L[e] = fmaf(w, ls[e], L[e]);
-                acc[e] = fmaf(w, w == 0.f ? 0.f : vs[e], acc[e]);
-            }
+        for (int q = 0; q < kQ; ++q) {
+            join(mx[q].x, ls[q].x, acc[q].x, m1[q].x, l1[q].x, a1[q].x);
+            join(mx[q].y, ls[q].y, acc[q].y, m1[q].y, l1[q].y, a1[q].y);
+            join(mx[q].z, ls[q].z, acc[q].z, m1[q].z, l1[q].z, a1[q].z);
+            join(mx[q].w, ls[q].w, acc[q].w, m1[q].w, l1[q].w, a1[q].w);
         }
+        if (++i >= pieces) break;
+        load(static_cast<int64_t>(cta + i * p.groups) * 2, m1, l1, a1);
+    }
+    const int group = cta % p.groups, heads_here = min(p.hpt, p.heads - group * p.hpt);
+    const bool odd = threadIdx.x & 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = r4 * 4 + e, tok = row / p.hpt, h = row - tok * p.hpt;
+    for (int q = 0; q < kQ; ++q) {
+        const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w}, l[4] = {ls[q].x, ls[q].y, ls[q].z, ls[q].w};
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = l[e] > 0.f ? v[e] / l[e] : 0.f;
+        // neighbouring lanes exchange a row each: 4-byte stores
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[e] : y[e + 1], 1);
+            const int row = (r4 + q) * 4 + e + (odd ? 1 : 0), tok = row / p.hpt, h = row - tok * p.hpt;
             if (row < rows && h < heads_here)
-                p.out[(static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent + m * 128 + dim] =
-                    __float2bfloat16_rn(L[e] > 0.f ? acc[e] / L[e] : 0.f);
+                *reinterpret_cast<uint32_t *>(
+                    p.out + (static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent + m * 128 +
+                    (dim & ~1)) = odd ? pack_bf16x2(got, y[e + 1]) : pack_bf16x2(y[e], got);
         }
     }
 }
@@ -1062,7 +1085,7 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
                    static_cast<cudaStream_t>(stream), am, bm, qm, p) != cudaSuccess)
         return PKV_ERR_CUDA;
-    if (launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(ctas), 16), dim3(256), 0,
+    if (launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(ctas), kLaCombineY), dim3(256), 0,
                    static_cast<cudaStream_t>(stream), p, ctas) != cudaSuccess)
         return PKV_ERR_CUDA;
     return PKV_OK;
