@@ -38,14 +38,14 @@
 // each weight, about that of the output's own rounding.  Sums, maxima and
 // outputs are fp32.
 //
-// Warp roles (288 threads): warp 3 walks the run and publishes items ahead of
+// Warp roles (416 threads): warp 3 walks the run and publishes items ahead of
 // the others; warp 0 loads pages by TMA (two boxes a page); warp 1 issues the S
 // products and warp 8 the second ones, each as soon as its operands are there (one
 // warp for both had to look for two events in turn, about 600 cycles a tile);
 // warp 2 loads Q (TMA), zeroes the rows past a tile's last visible key
 // (so that what an unwritten slot holds never meets a zero weight) and owns
-// tensor memory; warps 4-7 are the softmax and epilogue warps.  Every wait is
-// bounded.
+// tensor memory; warps 4-7 are the softmax; warps 9-12 write finished tiles out
+// while the softmax is at the next one.  Every wait is bounded.
 #include <mutex>
 
 #include "latent_common.cuh"
@@ -62,8 +62,10 @@ constexpr int kLaChunks = kLatRow / 64;                      // 9 chunks of 64 d
 constexpr int kLaQChunk = kLaRows * 128;                     // 8192: 64 dims of 64 rows
 constexpr int kLaMaxCtas = 152;
 constexpr int kLaMaxHeads = 1024;
-constexpr int kLaThreads = 288;
+constexpr int kLaThreads = 416;
 constexpr int kLaItemSlots = 4;
+constexpr int kLaAhead = 4;                                  // tiles between a page's way into L2 and its load
+static_assert(kLaAhead * kLaPages <= 32, "one page a lane");
 
 // A stage holds a tile's 64 keys in two parts, each [page][token half][chunk]
 // [token % 8][64 dims] with 128-byte swizzle: part A has chunks 0-3 (dims 0 .. 255),
@@ -85,10 +87,11 @@ constexpr int kLaOffQ = 0;
 constexpr int kLaOffKV = kLaOffQ + kLaChunks * kLaQChunk;                 // 73728
 constexpr int kLaOffOut = kLaOffKV + kLaStages * kLaStage;                // rows on their way out, 2 KiB a warp
 constexpr int kLaOffBar = kLaOffOut + 4 * 2048;                           // 229376
-constexpr int kLaOffAlpha = kLaOffBar + 256;                              // float [2][64]
-constexpr int kLaOffRow = kLaOffAlpha + 512;                              // float [64], int [64]
-constexpr int kLaOffItems = kLaOffRow + 512;
-constexpr int kLaSmem = kLaOffItems + 256 + 1024;                         // with alignment slack
+constexpr int kLaOffAlpha = kLaOffBar + 304;                              // float [2][64]
+constexpr int kLaOffRow = kLaOffAlpha + 512;                              // LaRows [2]
+constexpr int kLaRowsBytes = 528;
+constexpr int kLaOffItems = kLaOffRow + 2 * kLaRowsBytes;
+constexpr int kLaSmem = kLaOffItems + 160 + 1024;                         // with alignment slack
 static_assert(kLaSmem <= 227 * 1024, "shared memory of one CTA");
 
 // tensor memory: O' block m at columns 64 m, S buffer b at 256 + 64 b
@@ -115,6 +118,7 @@ struct LaParams {
     int32_t hpt, tpt;         // heads and tokens of a row tile
     int32_t tpt_shift;        // log2(tpt)
     int32_t lanes;
+    const uint8_t *cache;
     int64_t num_blocks;
     float scale_log2;
     uint8_t *ws;
@@ -130,24 +134,34 @@ struct LaItem {
     int32_t slot;             // -1: complete, written to out; else the partial slot of this CTA
     int32_t r;                // request
 };
-static_assert(kLaItemSlots * sizeof(LaItem) <= 256, "item ring");
+static_assert(kLaItemSlots * sizeof(LaItem) <= 160, "item ring");
+
+// What the softmax warps leave for the warps that write a finished item out.
+struct LaRows {
+    float inv[kLaRows];       // one over the row's sum
+    int32_t dst[kLaRows];     // token * heads + head, or -1
+    int32_t rows, slot;       // of the item (slot: LaItem's)
+};
+static_assert(sizeof(LaRows) <= kLaRowsBytes && kLaRowsBytes % 16 == 0, "row records");
 
 enum LaBar {
     kLaQFull = 0, kLaQEmpty = 1,
     kLaSFull = 2,             // S buffer b written (+ b)
     kLaSFree = 27,            // S buffer b read (+ b)
-    kLaPFull = 4,             // weights and votes of a tile written
+    kLaRowFull = 29,          // row record b written (+ b)
+    kLaRowFree = 31,          // row record b read (+ b)
+    kLaPFull = 33,            // weights and votes of a tile written (+ tile & 1)
     kLaODone = 5,             // the tile's second products completed
+    kLaOReady = 8,            // the item's last ones completed
     kLaOFree = 6,             // O' read out by the epilogue
     kLaRescaled = 7,          // O' rescaled (only in tiles where some warp voted for it)
-    kLaMeet = 8,              // the four softmax warps meet at the end of an item
     kLaFix = 9,               // rows past the last visible key zeroed (+ stage)
     kLaItemFull = 11, kLaItemEmpty = 15,
     kLaKVFull = 19,           // a part landed (+ 2 stage + part)
     kLaKVEmpty = 23,          // a part read by its last product (+ 2 stage + part)
-    kLaNumBars = 29
+    kLaNumBars = 35           // (4 is not used)
 };
-static_assert(kLaNumBars * 8 + 24 <= 256, "barriers, tensor-memory address, status, votes");
+static_assert(kLaNumBars * 8 + 24 <= 304, "barriers, tensor-memory address, status, votes");
 
 // Request r's share of the line of units.
 struct LaReq {
@@ -242,10 +256,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (threadIdx.x < kLaNumBars) {
         const int b = threadIdx.x;
         int count = 1;
-        if (b == kLaPFull || b == kLaOFree || b == kLaRescaled || b == kLaMeet || b == kLaSFree ||
-            b == kLaSFree + 1)
-            count = 4;
-        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 8;   // loads, 2 MMA warps, Q, 4 softmax warps
+        if (b == kLaOFree || b == kLaRescaled || b == kLaSFree || b == kLaSFree + 1 || b >= kLaRowFull)
+            count = 4;                                       // four warps
+        else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 12;  // loads, 2 MMA warps, Q, 4 softmax warps, 4 that write out
         mbar_init(&bars[b], count);
     }
     if (threadIdx.x == 0) {
@@ -276,7 +289,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int64_t per = max(static_cast<int64_t>(1), (total + p.lanes - 1) / p.lanes);
     const int64_t lo = min(total, my_lane * per), hi = min(total, lo + per);
     __syncthreads();
-    if (threadIdx.x == 0) scan[10] = -1;
+    if (threadIdx.x == 0) scan[14] = -1;
     int64_t base = 0;
     for (int r0 = 0; r0 < p.num_seqs && lo < hi; r0 += kLaThreads) {
         const int r = r0 + threadIdx.x;
@@ -298,8 +311,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             all += scan[w];
         }
         if (lo >= before && lo < before + mine) {
-            scan[10] = r;
-            scan[11] = lo - before;
+            scan[14] = r;
+            scan[15] = lo - before;
         }
         base = all;
         __syncthreads();
@@ -308,8 +321,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     int start_req = 0;
     int64_t start_off = 0;
     if (lo < hi) {
-        start_req = static_cast<int>(scan[10]);
-        start_off = scan[11];
+        start_req = static_cast<int>(scan[14]);
+        start_off = scan[15];
     }
     tc_fence_before();
     __syncthreads();
@@ -404,8 +417,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
         };
+        // Pages to come are brought into L2 kLaAhead tiles before they are loaded: two
+        // stages of shared memory are too few to cover memory's latency, and L2's is
+        // half of it.  The CTAs of a lane share the pages out.
+        auto prefetch = [&](int id, bool there) {
+            if (there && id >= 0 && id < p.num_blocks && lane % p.groups == group)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + static_cast<int64_t>(id) *
+                                                                                              kLatPageBytes),
+                             "r"(kLatPageBytes)
+                             : "memory");
+        };
         fetch(0);
         int win_cur = window(0), win_next = window(1);
+        prefetch(win_cur, next.valid && lane < min(kLaAhead, next.kv1 - next.kv0) * kLaPages);
         for (int k = 0; ok && next.valid; ++k) {
             cur = next;
             int ahead0 = -1, ahead1 = -1;                     // the next item's first windows
@@ -423,10 +447,17 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     if (j * kLaPages + (lane & (kLaPages - 1)) < cur.n_pages) set_status(status, PKV_ERR_DEVICE_INDEX);
                     id = -1;
                 }
+                {
+                    // tile j + kLaAhead: in this window or the next
+                    const int w = wofs + kLaAhead * kLaPages + (lane & (kLaPages - 1));
+                    const int a = __shfl_sync(0xffffffffu, win_cur, w & 31), b = __shfl_sync(0xffffffffu, win_next, w & 31);
+                    prefetch(w < 32 ? a : b, lane < kLaPages && j + kLaAhead < cur.kv1);
+                }
                 if (j == cur.kv1 - 1) {
                     fetch(k + 1);
                     if (!ok) break;
                     ahead0 = window(0), ahead1 = window(1);
+                    prefetch(ahead0, next.valid && lane < min(kLaAhead, next.kv1 - next.kv0) * kLaPages);
                 }
                 // each part as soon as the products of the tile two before have read it
 #pragma unroll 1
@@ -529,7 +560,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             if (k > 0) ok = warp_wait(&bars[kLaOFree], (k - 1) & 1, status);
             for (int j = 0; j < n && ok; ++j, ++gt) {
                 const int st = gt % kLaStages;
-                ok = warp_wait(&bars[kLaPFull], gt & 1, status);
+                ok = warp_wait(&bars[kLaPFull + (gt & 1)], (gt >> 1) & 1, status);
                 if (!ok) break;
                 if (fix && j == n - 1) {
                     ok = warp_wait(&bars[kLaFix + st], (fix_par >> st) & 1u, status);
@@ -544,6 +575,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 const uint32_t so = static_cast<uint32_t>(st * (kLaStage >> 4));
                 const uint64_t a0 = dva + so, a1 = dvb + so, w0 = dw + so;
                 const uint32_t more = j > 0 ? 1u : 0u;
+                const bool last = j == n - 1;
                 if (elect_one()) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
@@ -560,6 +592,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                         w0 + kk * (kLaPageB >> 4), idesc_o, kk > 0 ? 1u : more);
                     umma_commit(&bars[kLaKVEmpty + 2 * st + 1]);
                     umma_commit(&bars[kLaODone]);
+                    if (last) umma_commit(&bars[kLaOReady]);
                 }
                 __syncwarp();
             }
@@ -598,15 +631,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 // zero the rows past the previous item's last visible key, in its page, while
                 // the softmax works on that tile
                 const int st = (gt - 1) % kLaStages;
-                const int first = end % kBlock, rows = kBlock - first;
-                const uint32_t base = sKV + st * kLaStage;
+                const int first = end % kBlock;
                 const int page = (end - 1) / kBlock - (kv1 - 1) * kLaPages;
-                for (int e = lane; e < rows * (kLatent / 8); e += 32) {      // the values' dims only
-                    const int t = first + e / (kLatent / 8), c = (e % (kLatent / 8)) >> 3;
-                    const uint32_t g = c < kLaChunksA ? (2 * page + (t >> 3)) * kLaGroupA + c * 1024
-                                                      : kLaPartA + (2 * page + (t >> 3)) * kLaGroupB + (c - kLaChunksA) * 1024;
-                    const uint32_t a = base + g + (t & 7) * 128 + (e & 7) * 16;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+                const uint32_t base = sKV + st * kLaStage + (lane >> 3) * 1024 + (lane & 7) * 16;   // a chunk of each part
+                for (int t = first; t < kBlock; ++t) {                       // (the values' dims only)
+                    const uint32_t g = 2 * page + (t >> 3), a = base + (t & 7) * 128;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a + g * kLaGroupA), "r"(0u) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a + kLaPartA + g * kLaGroupB), "r"(0u)
+                                 : "memory");
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -617,13 +649,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             fix = next_fix, end = next_end, kv1 = next_kv1;
         }
         if (loaded > 0) mbar_wait_bounded(&bars[kLaQFull], (loaded - 1) & 1);    // landed before the CTA ends
-    } else if (warp >= 4) {
-        // ---------------- softmax and epilogue ----------------
+    } else if (warp < 8) {
+        // ---------------- softmax ----------------
         const int quad = warp - 4;
         const float NEG_INF = -__int_as_float(0x7f800000);
         float *alphas = reinterpret_cast<float *>(smem + kLaOffAlpha);
-        float *row_inv = reinterpret_cast<float *>(smem + kLaOffRow);
-        int *row_dst = reinterpret_cast<int *>(row_inv + kLaRows);
         const int rA = quad * 16 + (lane >> 2);              // this thread's rows: rA and rA + 8
         const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float sl2 = p.scale_log2;
@@ -632,7 +662,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // (its columns are rows of every warp, its lanes the quadrants of every warp),
         // between the products of tile g - 1 and those of g.
         auto rescale = [&](int g) -> bool {
-            if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaPFull], g & 1, status))) return false;
+            if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaPFull + (g & 1)], (g >> 1) & 1, status))) return false;
             const uint32_t vote = *reinterpret_cast<volatile const uint32_t *>(votes + 4 * (g & 1));
             if (!vote) return true;
             if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (g - 1) & 1, status))) return false;
@@ -656,9 +686,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             if (lane == 0) mbar_arrive(&bars[kLaRescaled]);
             return true;
         };
+        // this thread's two rows of every tile: token, head
+        int row_tok[2], row_head[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            row_tok[i] = (rA + 8 * i) / p.hpt;
+            row_head[i] = rA + 8 * i - row_tok[i] * p.hpt;
+        }
         bool ok = true;
-        int gt = 0, k = 0;
-        for (;; ++k) {
+        int gt = 0;
+        for (int k = 0;; ++k) {
             const int slot = k % kLaItemSlots;
             ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
             if (!ok) break;
@@ -670,11 +707,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             int lim[2], dst[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int row = rA + 8 * i, tok = row / p.hpt, h = row - tok * p.hpt;
-                const bool in = row < rows && h < heads_here;
-                lim[i] = in ? lim0 + tok : 0;
-                dst[i] = in ? (tok0 + tok) * p.heads + group * p.hpt + h : -1;
+                const bool in = row_tok[i] < ntok && row_head[i] < heads_here;
+                lim[i] = in ? lim0 + row_tok[i] : 0;
+                dst[i] = in ? (tok0 + row_tok[i]) * p.heads + group * p.hpt + row_head[i] : -1;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
             float m_ref[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};
             for (int j = kv0; j < kv1 && ok; ++j, ++gt) {
                 const int sb = gt & 1;
@@ -753,117 +791,134 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kLaPFull]);
+                if (lane == 0) mbar_arrive(&bars[kLaPFull + sb]);
                 if (j > kv0) ok = rescale(gt);
             }
-            // epilogue
-            // (the last two tiles' products may both be still to come: a parity tells phases
-            // apart one at a time)
-            if (ok && gt > 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], gt & 1, status));
-            if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (gt - 1) & 1, status));
-            if (ok) {
+            // the rows' sums and places, for the warps that write the item out
+            const int rb = k & 1;
+            if (ok && k >= 2) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaRowFree + rb], ((k >> 1) - 1) & 1, status));
+            if (!ok) break;
+            LaRows *rec = reinterpret_cast<LaRows *>(smem + kLaOffRow + rb * kLaRowsBytes);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            }
+            if ((lane & 3) == 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                }
-                if ((lane & 3) == 0) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = rA + 8 * i;
-                        row_inv[row] = l[i] > 0.f ? 1.f / l[i] : 0.f;
-                        row_dst[row] = dst[i];
-                        if (part >= 0) {
-                            float *ml = reinterpret_cast<float *>(p.ws + kLaWsMl) +
-                                        (static_cast<int64_t>(blockIdx.x) * 2 + part) * 2 * kLaRows;
-                            ml[row] = m_ref[i];
-                            ml[kLaRows + row] = l[i];
-                        }
+                    const int row = rA + 8 * i;
+                    rec->inv[row] = l[i] > 0.f ? 1.f / l[i] : 0.f;
+                    rec->dst[row] = dst[i];
+                    if (part >= 0) {
+                        float *ml = reinterpret_cast<float *>(p.ws + kLaWsMl) +
+                                    (static_cast<int64_t>(blockIdx.x) * 2 + part) * 2 * kLaRows;
+                        ml[row] = m_ref[i];
+                        ml[kLaRows + row] = l[i];
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kLaMeet]);
-                ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaMeet], k & 1, status));
             }
-            if (ok) {
-                tc_fence_after();
+            if (warp == 4 && lane == 0) rec->rows = rows, rec->slot = part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaRowFull + rb]);
+        }
+    } else {
+        // ---------------- finished tiles to memory (warps 9-12) ----------------
+        const int quad = warp & 3;
+        const uint32_t tlane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t stage = sOut + quad * 2048;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kLaItemSlots;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaItemFull + slot], (k / kLaItemSlots) & 1, status));
+            if (!ok) break;
+            const bool valid = items[slot].valid != 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
+            if (!valid) break;
+            const int rb = k & 1;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaRowFull + rb], (k >> 1) & 1, status));
+            if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaOReady], k & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+            const LaRows *rec = reinterpret_cast<const LaRows *>(smem + kLaOffRow + rb * kLaRowsBytes);
+            const int rows = rec->rows, part = rec->slot;
+            if (part >= 0) {
+                // [128-dim block][row / 4][dim][row % 4]
                 float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
-                            (static_cast<int64_t>(blockIdx.x) * 2 + max(part, 0)) * kLaPartFloats;
-                if (part >= 0) {
-                    // [128-dim block][row / 4][dim][row % 4]
-                    const int dim = quad * 32 + lane;
+                            (static_cast<int64_t>(blockIdx.x) * 2 + part) * kLaPartFloats + (quad * 32 + lane) * 4;
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        const int m = c >> 1, r0 = 32 * (c & 1);
-                        if (r0 >= rows) continue;
-                        float v[32];
-                        tmem_ld32f(tlane + 64u * m + r0, v);
+                for (int r0 = 0; r0 < rows; r0 += 32) {
+                    float v[2][32];                             // the next block's loads run beside the stores
+                    tmem_ld32f(tlane + r0, v[0]);
+#pragma unroll
+                    for (int m = 0; m < kLatent / 128; ++m) {
                         tmem_ld_wait();
+                        if (m + 1 < kLatent / 128) tmem_ld32f(tlane + 64u * (m + 1) + r0, v[(m + 1) & 1]);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             if (r0 + e < rows)
-                                *reinterpret_cast<float4 *>(po + ((m * 16 + (r0 + e) / 4) * 128 + dim) * 4) =
-                                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    }
-                } else {
-                    // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
-                    // stmatrix: rows of 64 bytes, 16 a lane
-                    const uint32_t stage = sOut + quad * 2048;
-#pragma unroll 1
-                    for (int r0 = 0; r0 < rows; r0 += 32) {
-                        float inv[8];
-                        int64_t to[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            inv[2 * e] = row_inv[r0 + 8 * e + 2 * (lane & 3)];
-                            inv[2 * e + 1] = row_inv[r0 + 8 * e + 2 * (lane & 3) + 1];
-                            to[e] = row_dst[r0 + 8 * e + (lane >> 2)];
-                        }
-                        // the next block's loads run while this one is packed and stored
-                        float a[2][16], b[2][16];               // dims t / 4 (+ 8), and 16 further
-                        tmem_ld_16x32f(tlane + r0, a[0]);
-                        tmem_ld_16x32f(tlane + (16u << 16) + r0, b[0]);
-#pragma unroll
-                        for (int m = 0; m < kLatent / 128; ++m) {
-                            tmem_ld_wait();
-                            if (m + 1 < kLatent / 128) {
-                                tmem_ld_16x32f(tlane + 64u * (m + 1) + r0, a[(m + 1) & 1]);
-                                tmem_ld_16x32f(tlane + (16u << 16) + 64u * (m + 1) + r0, b[(m + 1) & 1]);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {       // rows r0 + 8 e ..
-                                const int row = 8 * e + (lane & 7);
-                                const float x = inv[2 * e], y = inv[2 * e + 1];
-                                stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
-                                              pack_bf16x2(a[m & 1][4 * e] * x, a[m & 1][4 * e + 1] * y),
-                                              pack_bf16x2(a[m & 1][4 * e + 2] * x, a[m & 1][4 * e + 3] * y),
-                                              pack_bf16x2(b[m & 1][4 * e] * x, b[m & 1][4 * e + 1] * y),
-                                              pack_bf16x2(b[m & 1][4 * e + 2] * x, b[m & 1][4 * e + 3] * y));
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int row = 8 * e + (lane >> 2);
-                                uint4 w;
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                             : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
-                                             : "memory");
-                                if (to[e] >= 0)
-                                    *reinterpret_cast<uint4 *>(p.out + to[e] * kLatent + m * 128 + quad * 32 +
-                                                               (lane & 3) * 8) = w;
-                            }
-                            __syncwarp();
-                        }
+                                *reinterpret_cast<float4 *>(po + (m * 16 + (r0 + e) / 4) * 512) =
+                                    make_float4(v[m & 1][e], v[m & 1][e + 1], v[m & 1][e + 2], v[m & 1][e + 3]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kLaOFree]);
+            } else {
+                // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
+                // stmatrix: rows of 64 bytes, 16 a lane
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += 32) {
+                    float inv[8];
+                    __nv_bfloat16 *to[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        inv[2 * e] = rec->inv[r0 + 8 * e + 2 * (lane & 3)];
+                        inv[2 * e + 1] = rec->inv[r0 + 8 * e + 2 * (lane & 3) + 1];
+                        const int d = rec->dst[r0 + 8 * e + (lane >> 2)];
+                        to[e] = d < 0 ? nullptr
+                                      : p.out + static_cast<int64_t>(d) * kLatent + quad * 32 + (lane & 3) * 8;
+                    }
+                    // the next block's loads run while this one is packed and stored
+                    float a[2][16], b[2][16];                   // dims t / 4 (+ 8), and 16 further
+                    tmem_ld_16x32f(tlane + r0, a[0]);
+                    tmem_ld_16x32f(tlane + (16u << 16) + r0, b[0]);
+#pragma unroll
+                    for (int m = 0; m < kLatent / 128; ++m) {
+                        tmem_ld_wait();
+                        if (m + 1 < kLatent / 128) {
+                            tmem_ld_16x32f(tlane + 64u * (m + 1) + r0, a[(m + 1) & 1]);
+                            tmem_ld_16x32f(tlane + (16u << 16) + 64u * (m + 1) + r0, b[(m + 1) & 1]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {           // rows r0 + 8 e ..
+                            const int row = 8 * e + (lane & 7);
+                            const float x = inv[2 * e], y = inv[2 * e + 1];
+                            stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
+                                          pack_bf16x2(a[m & 1][4 * e] * x, a[m & 1][4 * e + 1] * y),
+                                          pack_bf16x2(a[m & 1][4 * e + 2] * x, a[m & 1][4 * e + 3] * y),
+                                          pack_bf16x2(b[m & 1][4 * e] * x, b[m & 1][4 * e + 1] * y),
+                                          pack_bf16x2(b[m & 1][4 * e + 2] * x, b[m & 1][4 * e + 3] * y));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = 8 * e + (lane >> 2);
+                            uint4 w;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                         : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
+                                         : "memory");
+                            if (to[e]) *reinterpret_cast<uint4 *>(to[e] + m * 128) = w;
+                        }
+                        __syncwarp();
+                    }
+                }
             }
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
-            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive(&bars[kLaOFree]);
+                mbar_arrive(&bars[kLaRowFree + rb]);
+            }
         }
     }
 
@@ -1051,6 +1106,7 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
         while (2 * p.tpt * p.hpt <= kLaRows && p.tpt < max_query_len) p.tpt *= 2;
     p.tpt_shift = 0;
     while ((1 << p.tpt_shift) < p.tpt) ++p.tpt_shift;
+    p.cache = static_cast<const uint8_t *>(latent_cache);
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.ws = static_cast<uint8_t *>(workspace);
