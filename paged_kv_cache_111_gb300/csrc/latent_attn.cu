@@ -167,7 +167,7 @@ static_assert(kLaNumBars * 8 + 24 <= 304, "barriers, tensor-memory address, stat
 struct LaReq {
     int32_t q, L, ctx, qs;
     int32_t n_full;           // row tiles whose tokens are all there
-    int64_t units;            // key tiles of all its row tiles
+    int64_t units;            // length of all its row tiles on the line
 };
 
 // sum of floor(x / 2^s) over x < m
@@ -176,11 +176,16 @@ __device__ __forceinline__ int64_t la_floor_sum(int64_t m, int s) {
     return ((d * (d - 1) / 2) << s) + d * (m - (d << s));
 }
 
-// Key tiles of the row tiles before tile j of a request (j <= n_full): tile i
-// sees ctx + (i + 1) tpt keys, and tpt = 2^shift divides 64.
+// A row tile costs, beside its key tiles, about as much time as two of them (its
+// query's load, the first softmax, the outputs' way out): on the line it is two
+// units longer, so that runs of many short row tiles are not the last to end.
+constexpr int kLaExtra = 2;
+
+// Units of the row tiles before tile j of a request (j <= n_full): tile i sees
+// ctx + (i + 1) tpt keys, and tpt = 2^shift divides 64.
 __device__ __forceinline__ int64_t la_units_before(int32_t ctx, int shift, int64_t j) {
     const int64_t b = (ctx + kLaKeys - 1) >> shift;
-    return la_floor_sum(b + j + 1, 6 - shift) - la_floor_sum(b + 1, 6 - shift);
+    return la_floor_sum(b + j + 1, 6 - shift) - la_floor_sum(b + 1, 6 - shift) + kLaExtra * j;
 }
 static_assert(kLaKeys == 64, "2^6 keys a tile");
 
@@ -199,7 +204,7 @@ __device__ __forceinline__ LaReq la_request(const LaParams &p, int r, bool &bad)
     if (ok && a.q > 0) {
         a.n_full = a.q >> p.tpt_shift;
         a.units = la_units_before(a.ctx, p.tpt_shift, a.n_full);
-        if (a.q & (p.tpt - 1)) a.units += (a.L + kLaKeys - 1) / kLaKeys;
+        if (a.q & (p.tpt - 1)) a.units += (a.L + kLaKeys - 1) / kLaKeys + kLaExtra;
     }
     return a;
 }
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                 pf_wait(&bars[kLaItemEmpty + slot], (k / kLaItemSlots - 1) & 1, status));
             if (!ok) break;
             LaItem it{};
-            if (left > 0) {
+            while (left > 0 && !it.valid) {
                 while (req.units == off) {                    // the next request with rows (there is one: left > 0)
                     ++r;
                     req = la_request(p, r, unused);
@@ -364,20 +369,22 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     else hi_j = mid - 1;
                 }
                 const int64_t before = la_units_before(req.ctx, p.tpt_shift, lo_j);
-                it.valid = 1;
+                // a row tile is kLaExtra units without keys, then its key tiles
+                const int64_t pos = off - before - kLaExtra;
                 it.r = r;
                 it.tok0 = req.qs + lo_j * p.tpt;
                 it.ntok = min(p.tpt, req.q - lo_j * p.tpt);
                 it.lim0 = req.ctx + lo_j * p.tpt + 1;
                 it.n_kv = (it.lim0 + it.ntok - 1 + kLaKeys - 1) / kLaKeys;
-                it.kv0 = static_cast<int32_t>(off - before);
-                it.kv1 = static_cast<int32_t>(min(static_cast<int64_t>(it.n_kv), it.kv0 + left));
+                const int64_t n = min(it.n_kv - pos, left);                  // its units in this run
+                it.kv0 = static_cast<int32_t>(max(static_cast<int64_t>(0), pos));
+                it.kv1 = static_cast<int32_t>(pos + n);
+                it.valid = it.kv1 > it.kv0;                                  // (else it starts in the next lane)
                 it.slot = it.kv0 > 0 ? 0 : (it.kv1 < it.n_kv ? 1 : -1);
-                if (it.slot == 1) {
-                    const int64_t last = (at + it.n_kv - 1) / per;       // lane of its last key tile
+                if (it.valid && it.slot == 1) {
+                    const int64_t last = (at - pos + it.n_kv - 1) / per;     // lane of its last key tile
                     split = make_int4(it.tok0, it.ntok, static_cast<int>(last - my_lane) + 1, 0);
                 }
-                const int n = it.kv1 - it.kv0;
                 off += n, at += n, left -= n;
             }
             if (lane == 0) {
@@ -864,53 +871,60 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 }
             } else {
                 // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
-                // stmatrix: rows of 64 bytes, 16 a lane
-#pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += 32) {
-                    float inv[8];
-                    __nv_bfloat16 *to[4];
+                // stmatrix: rows of 64 bytes, 16 a lane.  Block i + 1 is packed, and block i + 2
+                // on its way from tensor memory, while block i is read back and stored.
+                const int blocks = rows > 32 ? 8 : 4;           // block i: rows 32 (i / 4) .., dims 128 (i % 4) ..
+                float a[16], b[16];                             // dims t / 4 (+ 8), and 16 further
+                uint32_t w[16];
+                uint4 out[4];
+                int dst[4] = {};
+                auto fetch = [&](int i) {
+                    tmem_ld_16x32f(tlane + 64u * (i & 3) + 32u * (i >> 2), a);
+                    tmem_ld_16x32f(tlane + (16u << 16) + 64u * (i & 3) + 32u * (i >> 2), b);
+                };
+                auto pack = [&](int i) {
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {               // rows 8 e ..
+                        const float2 s = *reinterpret_cast<const float2 *>(rec->inv + 32 * (i >> 2) + 8 * e + 2 * (lane & 3));
+                        w[4 * e] = pack_bf16x2(a[4 * e] * s.x, a[4 * e + 1] * s.y);
+                        w[4 * e + 1] = pack_bf16x2(a[4 * e + 2] * s.x, a[4 * e + 3] * s.y);
+                        w[4 * e + 2] = pack_bf16x2(b[4 * e] * s.x, b[4 * e + 1] * s.y);
+                        w[4 * e + 3] = pack_bf16x2(b[4 * e + 2] * s.x, b[4 * e + 3] * s.y);
+                    }
+                };
+                fetch(0);
+                pack(0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (i >= blocks) break;
+                    if (i + 1 < 8 && i + 1 < blocks) fetch(i + 1);
+                    __syncwarp();                               // the block before has been read back
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        inv[2 * e] = rec->inv[r0 + 8 * e + 2 * (lane & 3)];
-                        inv[2 * e + 1] = rec->inv[r0 + 8 * e + 2 * (lane & 3) + 1];
-                        const int d = rec->dst[r0 + 8 * e + (lane >> 2)];
-                        to[e] = d < 0 ? nullptr
-                                      : p.out + static_cast<int64_t>(d) * kLatent + quad * 32 + (lane & 3) * 8;
+                        const int row = 8 * e + (lane & 7);
+                        stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[4 * e], w[4 * e + 1],
+                                      w[4 * e + 2], w[4 * e + 3]);
                     }
-                    // the next block's loads run while this one is packed and stored
-                    float a[2][16], b[2][16];                   // dims t / 4 (+ 8), and 16 further
-                    tmem_ld_16x32f(tlane + r0, a[0]);
-                    tmem_ld_16x32f(tlane + (16u << 16) + r0, b[0]);
+                    __syncwarp();
+                    if ((i & 3) == 0) {
 #pragma unroll
-                    for (int m = 0; m < kLatent / 128; ++m) {
-                        tmem_ld_wait();
-                        if (m + 1 < kLatent / 128) {
-                            tmem_ld_16x32f(tlane + 64u * (m + 1) + r0, a[(m + 1) & 1]);
-                            tmem_ld_16x32f(tlane + (16u << 16) + 64u * (m + 1) + r0, b[(m + 1) & 1]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {           // rows r0 + 8 e ..
-                            const int row = 8 * e + (lane & 7);
-                            const float x = inv[2 * e], y = inv[2 * e + 1];
-                            stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
-                                          pack_bf16x2(a[m & 1][4 * e] * x, a[m & 1][4 * e + 1] * y),
-                                          pack_bf16x2(a[m & 1][4 * e + 2] * x, a[m & 1][4 * e + 3] * y),
-                                          pack_bf16x2(b[m & 1][4 * e] * x, b[m & 1][4 * e + 1] * y),
-                                          pack_bf16x2(b[m & 1][4 * e + 2] * x, b[m & 1][4 * e + 3] * y));
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int row = 8 * e + (lane >> 2);
-                            uint4 w;
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                         : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
-                                         : "memory");
-                            if (to[e]) *reinterpret_cast<uint4 *>(to[e] + m * 128) = w;
-                        }
-                        __syncwarp();
+                        for (int e = 0; e < 4; ++e) dst[e] = rec->dst[32 * (i >> 2) + 8 * e + (lane >> 2)];
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = 8 * e + (lane >> 2);
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(out[e].x), "=r"(out[e].y), "=r"(out[e].z), "=r"(out[e].w)
+                                     : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
+                                     : "memory");
+                    }
+                    if (i + 1 < 8 && i + 1 < blocks) pack(i + 1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (dst[e] >= 0)
+                            *reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(dst[e]) * kLatent + 128 * (i & 3) +
+                                                       quad * 32 + (lane & 3) * 8) = out[e];
                 }
             }
             tc_fence_before();
@@ -947,6 +961,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 constexpr int kLaCombineY = 4 * (kLaRows / 16);
 
 __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, int ctas) {
+    pdl_trigger();                        // a following call may start looking at its lengths
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
         int32_t s = 0;
