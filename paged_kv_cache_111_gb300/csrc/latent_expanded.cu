@@ -17,7 +17,9 @@
 // x 16, P from tensor memory).  The two row tiles take turns: while one's
 // softmax works, the tensor cores have the other's products.  Tensor memory: S
 // of both tiles, O of both tiles (512 columns).  Shared memory: Q of both (96
-// KiB), two stages of K (96 KiB), one of V (32 KiB).
+// KiB), two stages of K (96 KiB), one of V (32 KiB) in two halves of 64 keys, each
+// loaded again as soon as the second row tile's product has read it: between that
+// and the first row tile's next use lies about the time of a load.
 //
 // Against the latent-space form this does (128 + 64 + 128) / (576 + 512) = 0.29
 // of the products per visible pair, and reads keys per head: the form for long
@@ -52,11 +54,13 @@ enum ExBar {
     kExQFull = 0,        // (+ row tile)
     kExKFull = 2,        // (+ stage)
     kExKEmpty = 4,       // (+ stage)
-    kExVFull = 6, kExVEmpty = 7, kExFix = 8,
-    kExSFull = 9,        // (+ row tile)
-    kExPFull = 11,       // (+ row tile)
-    kExODone = 13,       // (+ row tile)
-    kExNumBars = 15
+    kExVFull = 6,        // (+ half: 64 keys)
+    kExVEmpty = 8,       // (+ half)
+    kExFix = 10,
+    kExSFull = 11,       // (+ row tile)
+    kExPFull = 13,       // (+ row tile)
+    kExODone = 15,       // (+ row tile)
+    kExNumBars = 17
 };
 
 struct ExParams {
@@ -175,10 +179,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
                                     req.qs + t0 + i * kExRows);
                 }
         }
-        for (int j = 0; j < n_all && ok; ++j) {
+        auto load_k = [&](int j) {
             const int st = j & 1, key0 = req.ks + j * kExKeys;
             if (j >= 2) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExKEmpty + st], (j / 2 - 1) & 1, status));
-            if (!ok) break;
+            if (!ok) return;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars[kExKFull + st], kExK);
                 uint8_t *dst = smem + kExOffK + st * kExK;
@@ -187,16 +191,25 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 tma_load_3d(dst + 2 * kExChunk, &r_map, &bars[kExKFull + st], 0, 0, key0);
             }
             k_issued = j + 1;
-            if (j >= 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVEmpty], (j - 1) & 1, status));
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars[kExVFull], kExVTile);
-                tma_load_3d(smem + kExOffV, &v_map, &bars[kExVFull], 0, head, key0);
-                tma_load_3d(smem + kExOffV + kExChunk, &v_map, &bars[kExVFull], 64, head, key0);
+        };
+        load_k(0);
+        for (int j = 0; j < n_all && ok; ++j) {
+            // K a tile ahead of V: its stage is free first, and its use comes first
+            if (j + 1 < n_all) load_k(j + 1);
+            for (int h = 0; h < 2 && ok; ++h) {
+                if (j >= 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVEmpty + h], (j - 1) & 1, status));
+                if (!ok) break;
+                if (lane == 0) {
+                    const int key = req.ks + j * kExKeys + 64 * h;
+                    mbar_arrive_expect_tx(&bars[kExVFull + h], kExVTile / 2);
+                    tma_load_3d(smem + kExOffV + h * 8192, &v_map, &bars[kExVFull + h], 0, head, key);
+                    tma_load_3d(smem + kExOffV + kExChunk + h * 8192, &v_map, &bars[kExVFull + h], 64, head, key);
+                }
+                v_issued = 2 * j + h + 1;
             }
-            v_issued = j + 1;
-            if (fix && j == n_all - 1) {
+            if (ok && fix && j == n_all - 1) {
                 ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVFull], j & 1, status));
+                if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVFull + 1], j & 1, status));
                 if (!ok) break;
                 const int first = end - j * kExKeys;
                 for (int e = lane; e < (kExKeys - first) * 16; e += 32) {
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             for (int i = 0; i < 2; ++i)
                 if (rows[i]) mbar_wait_bounded(&bars[kExQFull + i], 0);
             for (int j = max(0, k_issued - 2); j < k_issued; ++j) mbar_wait_bounded(&bars[kExKFull + (j & 1)], (j / 2) & 1);
-            if (v_issued) mbar_wait_bounded(&bars[kExVFull], (v_issued - 1) & 1);
+            for (int v = max(0, v_issued - 2); v < v_issued; ++v) mbar_wait_bounded(&bars[kExVFull + (v & 1)], (v / 2) & 1);
         }
     } else if (warp == 1) {
         // ---------------- MMA issue (the warp stays converged) ----------------
@@ -237,16 +250,27 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
             __syncwarp();
         };
-        auto issue_pv = [&](int i, int j) {
+        // frees: the last product to read V's halves
+        auto issue_pv = [&](int i, int j, bool frees) {
             const uint32_t more = j > 0 ? 1u : 0u;
+            const uint32_t d = tmem + 256u + 128u * i, a = tmem + 128u * i;
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kExKeys / 16; ++kk)
-                    umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, dv + kk * (2048 >> 4), kIdescO,
-                                kk > 0 ? 1u : more);
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f16_ts(d, a + 8u * kk, dv + kk * (2048 >> 4), kIdescO, kk > 0 ? 1u : more);
+                if (frees) umma_commit(&bars[kExVEmpty]);
+            }
+            __syncwarp();
+            if (!wait(kExVFull + 1, j & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk) umma_f16_ts(d, a + 8u * kk, dv + kk * (2048 >> 4), kIdescO, 1u);
+                if (frees) umma_commit(&bars[kExVEmpty + 1]);
                 umma_commit(&bars[kExODone + i]);
             }
             __syncwarp();
+            return true;
         };
         auto commit = [&](int b) {
             if (elect_one()) umma_commit(&bars[b]);
@@ -275,11 +299,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 if (ok && j < n_i) {
                     ok = wait(kExPFull + i, j & 1);
                     tc_fence_after();
-                    if (ok) issue_pv(i, j);
+                    if (ok) ok = issue_pv(i, j, i == 1 || j >= n1);
                     if (ok && j + 1 < n_i) issue_s(i, j + 1);
                 }
             }
-            commit(kExVEmpty);
             if (j + 1 < n_max) commit(kExKEmpty + ((j + 1) & 1));
         }
     } else if (warp >= 4) {
@@ -407,15 +430,15 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
 }
 
-// {dims, heads, tokens} of 16-bit elements: a box is 64 dims of one head of 128 tokens.
+// {dims, heads, tokens} of 16-bit elements: a box is 64 dims of one head of box_rows tokens.
 static int make_rows_map(CUtensorMap *map, const void *base, int dims_in, int64_t heads, int64_t head_stride,
-                         int64_t tokens, int64_t token_stride) {
+                         int64_t tokens, int64_t token_stride, int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return PKV_ERR_CUDA;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dims_in), static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(tokens)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
-    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -473,10 +496,10 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = device_status;
     CUtensorMap qm, km, rm, vm;
-    int rc = make_rows_map(&qm, query, kExDim, h, kExDim, num_tokens, query_token_stride);
-    if (!rc) rc = make_rows_map(&km, key, kExNope, h, key_head_stride, num_keys, key_token_stride);
-    if (!rc) rc = make_rows_map(&rm, key_rope, kLatRope, 1, kLatRope, num_keys, key_rope_token_stride);
-    if (!rc) rc = make_rows_map(&vm, value, kExV, h, value_head_stride, num_keys, value_token_stride);
+    int rc = make_rows_map(&qm, query, kExDim, h, kExDim, num_tokens, query_token_stride, kExRows);
+    if (!rc) rc = make_rows_map(&km, key, kExNope, h, key_head_stride, num_keys, key_token_stride, kExKeys);
+    if (!rc) rc = make_rows_map(&rm, key_rope, kLatRope, 1, kLatRope, num_keys, key_rope_token_stride, kExKeys);
+    if (!rc) rc = make_rows_map(&vm, value, kExV, h, value_head_stride, num_keys, value_token_stride, kExKeys / 2);
     if (rc) return rc;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
