@@ -715,7 +715,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool in = row_tok[i] < ntok && row_head[i] < heads_here;
-                lim[i] = in ? lim0 + row_tok[i] : 0;
+                // (a row that no head owns computes what it finds, for nobody, rather than put
+                // its warp on the masked path)
+                lim[i] = in ? lim0 + row_tok[i] : INT32_MAX;
                 dst[i] = in ? (tok0 + row_tok[i]) * p.heads + group * p.hpt + row_head[i] : -1;
             }
             __syncwarp();

@@ -68,6 +68,7 @@ struct ExParams {
     const int32_t *qsl, *ksl;
     int32_t num_seqs, num_tokens, num_keys, max_query_len, max_key_len, heads;
     int32_t tiles;            // upper bound of the CTAs' token tiles over all requests
+    int32_t by_head;          // order of the CTAs: all token tiles of one head, then the next
     float scale_log2;
     int32_t *status;
 };
@@ -98,9 +99,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
     const uint32_t sQ = smem_u32(smem + kExOffQ), sK = smem_u32(smem + kExOffK), sV = smem_u32(smem + kExOffV);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    // the last tiles of a request see the most keys: they go first
-    const int head = blockIdx.x % p.heads;
-    const int tile = p.tiles - 1 - blockIdx.x / p.heads;
+    // the last tiles of a request see the most keys: they go first, of all heads or of
+    // each head
+    const int head = p.by_head ? blockIdx.x / p.tiles : blockIdx.x % p.heads;
+    const int tile = p.tiles - 1 - (p.by_head ? blockIdx.x % p.tiles : blockIdx.x / p.heads);
     int32_t *status = p.status;
 
     pdl_trigger();
@@ -228,18 +230,15 @@ __global__ void __launch_bounds__(kExThreads, 1)
             for (int v = max(0, v_issued - 2); v < v_issued; ++v) mbar_wait_bounded(&bars[kExVFull + (v & 1)], (v / 2) & 1);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issue (the warp stays converged) ----------------
-        constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
-        constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
-        const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
-        const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
-        const int n0 = uniform(n[0]), n1 = uniform(n[1]), n_max = max(n0, n1);
-        auto wait = [&](int b, uint32_t parity) {
-            return __all_sync(0xffffffffu, pf_wait(&bars[b], parity, status));
-        };
-        auto issue_s = [&](int i, int j) {
-            const uint64_t a = dq + i * (kExQ >> 4), b = dk + static_cast<uint32_t>((j & 1) * (kExK >> 4));
-            if (elect_one()) {
+        // ---------------- MMA issue: one elected thread ----------------
+        if (elect_one()) {
+            constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
+            constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
+            auto wait = [&](int b, uint32_t parity) { return pf_wait(&bars[b], parity, status); };
+            auto issue_s = [&](int i, int j) {
+                const uint64_t a = dq + i * (kExQ >> 4), b = dk + static_cast<uint32_t>((j & 1) * (kExK >> 4));
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -247,70 +246,76 @@ __global__ void __launch_bounds__(kExThreads, 1)
                         umma_f16_ss(tmem + 128u * i, a + c * (kExChunk >> 4) + kk * 2, b + c * (kExChunk >> 4) + kk * 2,
                                     kIdescS, (c | kk) ? 1u : 0u);
                 umma_commit(&bars[kExSFull + i]);
-            }
-            __syncwarp();
-        };
-        // frees: the last product to read V's halves
-        auto issue_pv = [&](int i, int j, bool frees) {
-            const uint32_t more = j > 0 ? 1u : 0u;
-            const uint32_t d = tmem + 256u + 128u * i, a = tmem + 128u * i;
-            if (elect_one()) {
+            };
+            // half h (64 keys) of tile i's P V
+            auto issue_pv = [&](int i, int h, uint32_t more) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_f16_ts(d, a + 8u * kk, dv + kk * (2048 >> 4), kIdescO, kk > 0 ? 1u : more);
-                if (frees) umma_commit(&bars[kExVEmpty]);
-            }
-            __syncwarp();
-            if (!wait(kExVFull + 1, j & 1)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 4; kk < 8; ++kk) umma_f16_ts(d, a + 8u * kk, dv + kk * (2048 >> 4), kIdescO, 1u);
-                if (frees) umma_commit(&bars[kExVEmpty + 1]);
-                umma_commit(&bars[kExODone + i]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto commit = [&](int b) {
-            if (elect_one()) umma_commit(&bars[b]);
-            __syncwarp();
-        };
-        bool ok = wait(kExKFull, 0);
-        if (ok && n0) {
-            ok = wait(kExQFull, 0);
+                    umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * h + 8u * kk,
+                                dv + h * (8192 >> 4) + kk * (2048 >> 4), kIdescO, kk > 0 ? 1u : more);
+            };
+            bool ok = wait(kExKFull, 0);
+            if (ok) ok = wait(kExQFull, 0);
             tc_fence_after();
             if (ok) issue_s(0, 0);
-        }
-        if (ok && n1) {
-            ok = wait(kExQFull + 1, 0);
-            tc_fence_after();
-            if (ok) issue_s(1, 0);
-        }
-        commit(kExKEmpty);
-        // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
-        for (int j = 0; j < n_max && ok; ++j) {
-            ok = wait(kExVFull, j & 1);
-            if (ok && fix && j == n_max - 1) ok = wait(kExFix, 0);
-            if (ok && j + 1 < n_max) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n_i = i ? n1 : n0;
-                if (ok && j < n_i) {
-                    ok = wait(kExPFull + i, j & 1);
+            if (ok && n[1]) {
+                ok = wait(kExQFull + 1, 0);
+                tc_fence_after();
+                if (ok) issue_s(1, 0);
+            }
+            umma_commit(&bars[kExKEmpty]);
+            // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read).
+            // Loads are waited for where the queue of products hides the look at them.
+            const int n0 = n[0], n1 = n[1];
+            if (ok) ok = wait(kExVFull, 0);
+            for (int j = 0; j < n_all && ok; ++j) {
+                const bool last = j == n_all - 1;
+                const uint32_t more = j > 0 ? 1u : 0u;
+                if (fix && last) ok = wait(kExFix, 0);
+                if (j < n0) {
+                    if (ok) ok = wait(kExPFull, j & 1);
+                    if (!ok) break;
                     tc_fence_after();
-                    if (ok) ok = issue_pv(i, j, i == 1 || j >= n1);
-                    if (ok && j + 1 < n_i) issue_s(i, j + 1);
+                    issue_pv(0, 0, more);
+                    if (j >= n1) umma_commit(&bars[kExVEmpty]);
+                    ok = wait(kExVFull + 1, j & 1);
+                    if (!ok) break;
+                    issue_pv(0, 1, 1u);
+                    if (j >= n1) umma_commit(&bars[kExVEmpty + 1]);
+                    umma_commit(&bars[kExODone]);
+                    if (!last) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
+                    if (!ok) break;
+                    if (j + 1 < n0) issue_s(0, j + 1);
+                } else {
+                    ok = ok && wait(kExVFull + 1, j & 1);
+                    if (ok && !last) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
+                }
+                if (j < n1) {
+                    if (ok) ok = wait(kExPFull + 1, j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(1, 0, more);
+                    umma_commit(&bars[kExVEmpty]);
+                    issue_pv(1, 1, 1u);
+                    umma_commit(&bars[kExVEmpty + 1]);
+                    umma_commit(&bars[kExODone + 1]);
+                    if (j + 1 < n1) issue_s(1, j + 1);
+                }
+                if (!last) {
+                    umma_commit(&bars[kExKEmpty + ((j + 1) & 1)]);
+                    ok = wait(kExVFull, (j + 1) & 1);
                 }
             }
-            if (j + 1 < n_max) commit(kExKEmpty + ((j + 1) & 1));
         }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------- softmax (a row per thread) and epilogue ----------------
         const int i = (warp - 4) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
         const bool mine = row < rows[i];
-        const int lim = mine ? ctx + t0 + i * kExRows + row + 1 : 0;      // keys this row sees
+        // keys this row sees (a row that no token owns computes what it finds, for nobody,
+        // rather than put its warp on the masked path)
+        const int lim = mine ? ctx + t0 + i * kExRows + row + 1 : INT32_MAX;
         const float NEG_INF = -__int_as_float(0x7f800000);
         const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * i;
         const uint32_t tO = tS + 256u;
@@ -493,6 +498,10 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     const int64_t tiles = bound < num_tokens ? bound : num_tokens;
     if (tiles * num_heads > INT32_MAX) return PKV_ERR_SHAPE;
     p.tiles = static_cast<int32_t>(tiles);
+    // Keys and values of every head at once outgrow L2 (126 MB) long before one head's
+    // do: then the token tiles of a head run side by side, and its keys and values come
+    // from memory once instead of once a token tile.
+    p.by_head = static_cast<int64_t>(num_keys) * num_heads * (kExNope + kExV) * 2 > (int64_t(64) << 20);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = device_status;
     CUtensorMap qm, km, rm, vm;
