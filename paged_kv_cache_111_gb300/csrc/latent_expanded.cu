@@ -17,9 +17,12 @@
 // x 16, P from tensor memory).  The two row tiles take turns: while one's
 // softmax works, the tensor cores have the other's products.  Tensor memory: S
 // of both tiles, O of both tiles (512 columns).  Shared memory: Q of both (96
-// KiB), two stages of K (96 KiB), one of V (32 KiB) in two halves of 64 keys, each
-// loaded again as soon as the second row tile's product has read it: between that
-// and the first row tile's next use lies about the time of a load.
+// KiB) and a ring of eight 16 KiB slots, filled and released in the order of use,
+// five a key tile: K's three 64-dim chunks, then V's two halves of 64 keys.  Each
+// slot is loaded again when the second row tile's product has read it, a key
+// tile's time or so before it is used again.  (K in two whole stages and V in one
+// left V's load, about 1500 cycles, in the way of every tile: 842 us against 782 us
+// on 2048 tokens at 8192 keys of 128 heads.)
 //
 // Against the latent-space form this does (128 + 64 + 128) / (576 + 512) = 0.29
 // of the products per visible pair, and reads keys per head: the form for long
@@ -40,27 +43,25 @@ constexpr int kExNope = 128, kExDim = kExNope + kLatRope, kExV = 128;
 constexpr int kExRows = 128, kExKeys = 128;             // of a row tile, of a key tile
 constexpr int kExTokens = 2 * kExRows;                  // of a CTA
 constexpr int kExChunk = 128 * 128;                     // 64 dims of 128 rows: 16 KiB
-constexpr int kExQ = 3 * kExChunk, kExK = 3 * kExChunk, kExVTile = 2 * kExChunk;
+constexpr int kExQ = 3 * kExChunk;
+constexpr int kExSlots = 8, kExPerTile = 5;             // ring slots; of a key tile: K chunks 0-2, V halves 0-1
 constexpr int kExThreads = 384;
 
 constexpr int kExOffQ = 0;
-constexpr int kExOffK = kExOffQ + 2 * kExQ;
-constexpr int kExOffV = kExOffK + 2 * kExK;
-constexpr int kExOffBar = kExOffV + kExVTile;           // 229376
+constexpr int kExOffRing = kExOffQ + 2 * kExQ;
+constexpr int kExOffBar = kExOffRing + kExSlots * kExChunk;   // 229376
 constexpr int kExSmem = kExOffBar + 512 + 1024;         // with alignment slack
 static_assert(kExSmem <= 227 * 1024, "shared memory of one CTA");
 
 enum ExBar {
     kExQFull = 0,        // (+ row tile)
-    kExKFull = 2,        // (+ stage)
-    kExKEmpty = 4,       // (+ stage)
-    kExVFull = 6,        // (+ half: 64 keys)
-    kExVEmpty = 8,       // (+ half)
-    kExFix = 10,
-    kExSFull = 11,       // (+ row tile)
-    kExPFull = 13,       // (+ row tile)
-    kExODone = 15,       // (+ row tile)
-    kExNumBars = 17
+    kExFull = 2,         // (+ slot)
+    kExEmpty = 10,       // (+ slot)
+    kExFix = 18,         // V rows past the last visible key zeroed
+    kExSFull = 19,       // (+ row tile)
+    kExPFull = 21,       // (+ row tile)
+    kExODone = 23,       // (+ row tile)
+    kExNumBars = 25
 };
 
 struct ExParams {
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kExOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kExNumBars);
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
-    const uint32_t sQ = smem_u32(smem + kExOffQ), sK = smem_u32(smem + kExOffK), sV = smem_u32(smem + kExOffV);
+    const uint32_t sQ = smem_u32(smem + kExOffQ), sRing = smem_u32(smem + kExOffRing);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     // the last tiles of a request see the most keys: they go first, of all heads or of
     // each head
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     if (warp == 0) {
         // ---------------- loads ----------------
         bool ok = true;
-        int k_issued = 0, v_issued = 0;
+        int issued = 0;                                 // loads of the ring
         if (lane == 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -181,41 +182,41 @@ __global__ void __launch_bounds__(kExThreads, 1)
                                     req.qs + t0 + i * kExRows);
                 }
         }
-        auto load_k = [&](int j) {
-            const int st = j & 1, key0 = req.ks + j * kExKeys;
-            if (j >= 2) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExKEmpty + st], (j / 2 - 1) & 1, status));
-            if (!ok) return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars[kExKFull + st], kExK);
-                uint8_t *dst = smem + kExOffK + st * kExK;
-                tma_load_3d(dst, &k_map, &bars[kExKFull + st], 0, head, key0);
-                tma_load_3d(dst + kExChunk, &k_map, &bars[kExKFull + st], 64, head, key0);
-                tma_load_3d(dst + 2 * kExChunk, &r_map, &bars[kExKFull + st], 0, 0, key0);
-            }
-            k_issued = j + 1;
-        };
-        load_k(0);
         for (int j = 0; j < n_all && ok; ++j) {
-            // K a tile ahead of V: its stage is free first, and its use comes first
-            if (j + 1 < n_all) load_k(j + 1);
-            for (int h = 0; h < 2 && ok; ++h) {
-                if (j >= 1) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVEmpty + h], (j - 1) & 1, status));
+            const int key0 = req.ks + j * kExKeys;
+#pragma unroll 1
+            for (int e = 0; e < kExPerTile && ok; ++e) {
+                const int s = j * kExPerTile + e, slot = s % kExSlots;
+                if (s >= kExSlots)
+                    ok = __all_sync(0xffffffffu, pf_wait(&bars[kExEmpty + slot], (s / kExSlots - 1) & 1, status));
                 if (!ok) break;
                 if (lane == 0) {
-                    const int key = req.ks + j * kExKeys + 64 * h;
-                    mbar_arrive_expect_tx(&bars[kExVFull + h], kExVTile / 2);
-                    tma_load_3d(smem + kExOffV + h * 8192, &v_map, &bars[kExVFull + h], 0, head, key);
-                    tma_load_3d(smem + kExOffV + kExChunk + h * 8192, &v_map, &bars[kExVFull + h], 64, head, key);
+                    uint64_t *bar = &bars[kExFull + slot];
+                    uint8_t *dst = smem + kExOffRing + slot * kExChunk;
+                    mbar_arrive_expect_tx(bar, kExChunk);
+                    if (e < 2) {
+                        tma_load_3d(dst, &k_map, bar, e * 64, head, key0);
+                    } else if (e == 2) {
+                        tma_load_3d(dst, &r_map, bar, 0, 0, key0);
+                    } else {
+                        tma_load_3d(dst, &v_map, bar, 0, head, key0 + (e - 3) * 64);
+                        tma_load_3d(dst + 8192, &v_map, bar, 64, head, key0 + (e - 3) * 64);
+                    }
                 }
-                v_issued = 2 * j + h + 1;
+                issued = s + 1;
             }
-            if (ok && fix && j == n_all - 1) {
-                ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVFull], j & 1, status));
-                if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExVFull + 1], j & 1, status));
-                if (!ok) break;
-                const int first = end - j * kExKeys;
+        }
+        if (ok && fix) {
+            for (int e = 3; e < kExPerTile && ok; ++e) {
+                const int s = (n_all - 1) * kExPerTile + e;
+                ok = __all_sync(0xffffffffu, pf_wait(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1, status));
+            }
+            const int first = end - (n_all - 1) * kExKeys, s = (n_all - 1) * kExPerTile + 3;
+            if (ok) {
                 for (int e = lane; e < (kExKeys - first) * 16; e += 32) {
-                    const uint32_t a = sV + ((e & 15) >> 3) * kExChunk + (first + (e >> 4)) * 128 + (e & 7) * 16;
+                    const int r = first + (e >> 4);
+                    const uint32_t a = sRing + ((s + (r >> 6)) % kExSlots) * kExChunk + ((e & 15) >> 3) * 8192 +
+                                       (r & 63) * 128 + (e & 7) * 16;
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
                 }
                 fence_proxy_async_smem();
@@ -226,84 +227,74 @@ __global__ void __launch_bounds__(kExThreads, 1)
         if (!ok) {                                      // the copies in flight land before the CTA ends
             for (int i = 0; i < 2; ++i)
                 if (rows[i]) mbar_wait_bounded(&bars[kExQFull + i], 0);
-            for (int j = max(0, k_issued - 2); j < k_issued; ++j) mbar_wait_bounded(&bars[kExKFull + (j & 1)], (j / 2) & 1);
-            for (int v = max(0, v_issued - 2); v < v_issued; ++v) mbar_wait_bounded(&bars[kExVFull + (v & 1)], (v / 2) & 1);
+            for (int s = max(0, issued - kExSlots); s < issued; ++s)
+                mbar_wait_bounded(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1);
         }
     } else if (warp == 1) {
         // ---------------- MMA issue: one elected thread ----------------
         if (elect_one()) {
             constexpr uint32_t kIdescS = idesc_bf16_f32(kExRows, kExKeys, 0, 0);
             constexpr uint32_t kIdescO = idesc_bf16_f32(kExRows, kExV, 0, 1);
-            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sK, 16, 1024);
-            const uint64_t dv = smem_desc_sw128(sV, kExChunk, 1024);     // MN-major: 64-dim chunks 16 KiB apart
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(sRing, 8192, 1024);      // MN-major: 64-dim chunks 8 KiB apart
             auto wait = [&](int b, uint32_t parity) { return pf_wait(&bars[b], parity, status); };
+            const int n0 = n[0], n1 = n[1];
+            const int frees = n1 ? 1 : 0;                                // the row tile that reads a slot last
+            int seen = 0;                                                // loads waited for
+            auto need = [&](int s) {
+                if (s < seen) return true;
+                seen = s + 1;
+                const bool there = wait(kExFull + s % kExSlots, (s / kExSlots) & 1);
+                tc_fence_after();
+                return there;
+            };
             auto issue_s = [&](int i, int j) {
-                const uint64_t a = dq + i * (kExQ >> 4), b = dk + static_cast<uint32_t>((j & 1) * (kExK >> 4));
+                const uint64_t a = dq + i * (kExQ >> 4);
 #pragma unroll
-                for (int c = 0; c < 3; ++c)
+                for (int c = 0; c < 3; ++c) {
+                    const int s = j * kExPerTile + c, slot = s % kExSlots;
+                    if (!need(s)) return false;
+                    const uint64_t b = dk + static_cast<uint32_t>(slot * (kExChunk >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ss(tmem + 128u * i, a + c * (kExChunk >> 4) + kk * 2, b + c * (kExChunk >> 4) + kk * 2,
-                                    kIdescS, (c | kk) ? 1u : 0u);
+                        umma_f16_ss(tmem + 128u * i, a + c * (kExChunk >> 4) + kk * 2, b + kk * 2, kIdescS,
+                                    (c | kk) ? 1u : 0u);
+                    if (i == frees) umma_commit(&bars[kExEmpty + slot]);
+                }
                 umma_commit(&bars[kExSFull + i]);
+                return true;
             };
-            // half h (64 keys) of tile i's P V
-            auto issue_pv = [&](int i, int h, uint32_t more) {
+            auto issue_pv = [&](int i, int j) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * h + 8u * kk,
-                                dv + h * (8192 >> 4) + kk * (2048 >> 4), kIdescO, kk > 0 ? 1u : more);
+                for (int h = 0; h < 2; ++h) {
+                    const int s = j * kExPerTile + 3 + h, slot = s % kExSlots;
+                    if (!need(s)) return false;
+                    const uint64_t b = dv + static_cast<uint32_t>(slot * (kExChunk >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * h + 8u * kk, b + kk * (2048 >> 4),
+                                    kIdescO, (h | kk) ? 1u : (j > 0 ? 1u : 0u));
+                    if (i == frees) umma_commit(&bars[kExEmpty + slot]);
+                }
+                umma_commit(&bars[kExODone + i]);
+                return true;
             };
-            bool ok = wait(kExKFull, 0);
-            if (ok) ok = wait(kExQFull, 0);
-            tc_fence_after();
-            if (ok) issue_s(0, 0);
-            if (ok && n[1]) {
-                ok = wait(kExQFull + 1, 0);
-                tc_fence_after();
-                if (ok) issue_s(1, 0);
-            }
-            umma_commit(&bars[kExKEmpty]);
-            // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read).
-            // Loads are waited for where the queue of products hides the look at them.
-            const int n0 = n[0], n1 = n[1];
-            if (ok) ok = wait(kExVFull, 0);
+            bool ok = wait(kExQFull, 0) && issue_s(0, 0);
+            if (ok && n1) ok = wait(kExQFull + 1, 0) && issue_s(1, 0);
+            // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
             for (int j = 0; j < n_all && ok; ++j) {
-                const bool last = j == n_all - 1;
-                const uint32_t more = j > 0 ? 1u : 0u;
-                if (fix && last) ok = wait(kExFix, 0);
-                if (j < n0) {
-                    if (ok) ok = wait(kExPFull, j & 1);
-                    if (!ok) break;
+                if (fix && j == n_all - 1) ok = wait(kExFix, 0);
+                if (ok && j < n0) {
+                    ok = wait(kExPFull, j & 1);
                     tc_fence_after();
-                    issue_pv(0, 0, more);
-                    if (j >= n1) umma_commit(&bars[kExVEmpty]);
-                    ok = wait(kExVFull + 1, j & 1);
-                    if (!ok) break;
-                    issue_pv(0, 1, 1u);
-                    if (j >= n1) umma_commit(&bars[kExVEmpty + 1]);
-                    umma_commit(&bars[kExODone]);
-                    if (!last) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
-                    if (!ok) break;
-                    if (j + 1 < n0) issue_s(0, j + 1);
-                } else {
-                    ok = ok && wait(kExVFull + 1, j & 1);
-                    if (ok && !last) ok = wait(kExKFull + ((j + 1) & 1), ((j + 1) / 2) & 1);
+                    if (ok) ok = issue_pv(0, j);
+                    if (ok && j + 1 < n0) ok = issue_s(0, j + 1);
                 }
-                if (j < n1) {
-                    if (ok) ok = wait(kExPFull + 1, j & 1);
-                    if (!ok) break;
+                if (ok && j < n1) {
+                    ok = wait(kExPFull + 1, j & 1);
                     tc_fence_after();
-                    issue_pv(1, 0, more);
-                    umma_commit(&bars[kExVEmpty]);
-                    issue_pv(1, 1, 1u);
-                    umma_commit(&bars[kExVEmpty + 1]);
-                    umma_commit(&bars[kExODone + 1]);
-                    if (j + 1 < n1) issue_s(1, j + 1);
-                }
-                if (!last) {
-                    umma_commit(&bars[kExKEmpty + ((j + 1) & 1)]);
-                    ok = wait(kExVFull, (j + 1) & 1);
+                    if (ok) ok = issue_pv(1, j);
+                    if (ok && j + 1 < n1) ok = issue_s(1, j + 1);
                 }
             }
         }
