@@ -100,52 +100,97 @@ __global__ void __launch_bounds__(kExThreads, 1)
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
     const uint32_t sQ = smem_u32(smem + kExOffQ), sRing = smem_u32(smem + kExOffRing);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    // the last tiles of a request see the most keys: they go first, of all heads or of
-    // each head
+    // Token tiles (256 tokens of a request) are ranked by the key tiles they see, the
+    // most first, so that the longest are not the last to end; a CTA takes one rank of
+    // one head, all heads of a rank or all ranks of a head after one another.
     const int head = p.by_head ? blockIdx.x / p.tiles : blockIdx.x % p.heads;
-    const int tile = p.tiles - 1 - (p.by_head ? blockIdx.x % p.tiles : blockIdx.x / p.heads);
+    const int rank = p.by_head ? blockIdx.x % p.tiles : blockIdx.x / p.heads;
     int32_t *status = p.status;
 
     pdl_trigger();
-    // the request whose token tile this is (tiles of 256 tokens, request after request)
-    int base = 0;
-    if (threadIdx.x == 0) scan[16] = -1;
-    for (int r0 = 0; r0 < p.num_seqs; r0 += kExThreads) {
-        const int r = r0 + threadIdx.x;
-        int mine = 0;
-        if (r < p.num_seqs) {
-            const ExReq a = ex_request(p, r);
-            mine = a.ok ? (a.q + kExTokens - 1) / kExTokens : 0;
-            if (!a.ok && blockIdx.x == 0) set_status(status, PKV_ERR_DEVICE_METADATA);
-        }
-        int inc = mine;
+    // sum over the block
+    auto block_sum = [&](int v) {
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += y;
-        }
-        if (lane == 31) scan[warp] = inc;
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        if (lane == 0) scan[warp] = v;
         __syncthreads();
-        int before = base + inc - mine, all = base;
+        v = 0;
 #pragma unroll
-        for (int w = 0; w < kExThreads / 32; ++w) {
-            if (w < warp) before += scan[w];
-            all += scan[w];
-        }
-        if (tile >= before && tile < before + mine) {
-            scan[16] = r;
-            scan[17] = tile - before;
-        }
-        base = all;
+        for (int w = 0; w < kExThreads / 32; ++w) v += scan[w];
         __syncthreads();
-        // (the first CTA looks at every request, to report the bad ones)
-        if (all > tile && blockIdx.x != 0) break;
+        return v;
+    };
+    const ExReq mine = threadIdx.x < p.num_seqs ? ex_request(p, threadIdx.x) : ExReq{};
+    auto request = [&](int r) { return r < kExThreads ? mine : ex_request(p, r); };    // (r: one of this thread's)
+    // token tiles of a request that see w key tiles or more
+    auto tiles_from = [&](const ExReq &a, int w) {
+        const int keys = (w - 1) * kExKeys + 1, n = (a.q + kExTokens - 1) / kExTokens;
+        if (!a.ok || a.q == 0 || a.L < keys) return 0;
+        const int first = max(0, (keys - (a.L - a.q) + kExTokens - 1) / kExTokens - 1);    // (but for the last)
+        return max(n - first, 1);
+    };
+    auto count = [&](int w) {
+        int c = 0;
+        for (int r = threadIdx.x; r < p.num_seqs; r += kExThreads) c += tiles_from(request(r), w);
+        return block_sum(c);
+    };
+    if (blockIdx.x == 0)
+        for (int r = threadIdx.x; r < p.num_seqs; r += kExThreads)
+            if (!request(r).ok) set_status(status, PKV_ERR_DEVICE_METADATA);
+    int r = 0, t0 = 0;                                  // request; first token, within it
+    if (p.num_seqs == 1) {
+        const ExReq a = ex_request(p, 0);
+        const int n = a.ok ? (a.q + kExTokens - 1) / kExTokens : 0;
+        if (rank >= n) return;                          // the bound was not reached: uniform
+        t0 = (n - 1 - rank) * kExTokens;
+    } else {
+        const int all = count(1);
+        if (rank >= all) return;
+        // the key tiles of this rank's token tile: the largest w with more than `rank`
+        // tiles from w on
+        int lo = 1, hi = (p.max_key_len + kExKeys - 1) / kExKeys, above = 0;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2, c = count(mid);
+            if (c > rank) lo = mid;
+            else hi = mid - 1, above = c;
+        }
+        if (lo == (p.max_key_len + kExKeys - 1) / kExKeys) above = 0;
+        // the (rank - above)-th of those with exactly lo, in the requests' order
+        int base = above;
+        for (int r0 = 0; r0 < p.num_seqs; r0 += kExThreads) {
+            const int r = r0 + threadIdx.x;
+            int here = 0, from = 0;
+            if (r < p.num_seqs) {
+                const ExReq a = request(r);
+                from = tiles_from(a, lo);
+                here = from - tiles_from(a, lo + 1);
+            }
+            int inc = here;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, m);
+                if (lane >= m) inc += y;
+            }
+            if (lane == 31) scan[warp] = inc;
+            __syncthreads();
+            int before = base + inc - here, total = base;
+#pragma unroll
+            for (int w = 0; w < kExThreads / 32; ++w) {
+                if (w < warp) before += scan[w];
+                total += scan[w];
+            }
+            if (rank >= before && rank < before + here) {
+                scan[16] = r;
+                scan[17] = (request(r).q + kExTokens - 1) / kExTokens - from + rank - before;
+            }
+            base = total;
+            __syncthreads();
+            if (base > rank) break;
+        }
+        r = scan[16];
+        t0 = scan[17] * kExTokens;
     }
-    __syncthreads();
-    const int r = scan[16];
-    if (r < 0) return;                                  // the bound was not reached: uniform
     const ExReq req = ex_request(p, r);
-    const int t0 = scan[17] * kExTokens;                // first token, within the request
     const int ctx = req.L - req.q;
     // rows and key tiles of the two row tiles
     const int rows[2] = {min(kExRows, req.q - t0), max(0, min(kExRows, req.q - t0 - kExRows))};
