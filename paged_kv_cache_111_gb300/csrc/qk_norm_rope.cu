@@ -10,16 +10,22 @@
 // from fp32 straight to the cache's type: one rounding (a bf16 key written by
 // the separate cache write would be rounded twice over an E4M3 cache).
 //
-// What bounds it: memory.  A row is d / 8 lanes of 16 bytes, so a warp holds
-// 2 rows (d = 128) or 4 (d = 64) at a time; it takes kRowsUnroll times that of
-// one token and issues every load (rows, position, slot, then the table row)
-// before any arithmetic, and reads the angles once for all of them.  The rows
-// of a token are its query heads, key heads, then value heads.
+// What bounds it: memory, and close behind it the instructions.  A warp takes one
+// token's query rows, key rows or value rows, 8 rows of 128 dims (16 of 64), d / 8
+// lanes a row, so that what it does with them is the same for all of them: a value
+// row is copied, and of the others each lane has four dims and the four that they
+// turn with (two 8-byte pieces), so that no lane needs another's.  Every load (rows,
+// position, slot, then the table row) is issued before any arithmetic; the
+// arithmetic runs on pairs (f32x2).  Whole rows on 16-byte pieces, with the partner
+// dims fetched from other lanes, took four times the instructions: 60 us on 8192
+// tokens of 32/8 heads of 128 (206 MB), against 36 us.
 #include "norm_rope.cuh"
+#include "prefill_common.cuh"
 
 namespace pkv {
 
-constexpr int kRowsUnroll = 4;
+constexpr int kRowsUnroll = 4;                   // rows a lane
+constexpr int kQkThreads = 128;                  // (256: 41 us where 128 take 39)
 
 struct QkParams {
     __nv_bfloat16 *query_out;
@@ -32,13 +38,14 @@ struct QkParams {
     const int64_t *positions, *slots;
     uint8_t *cache;
     int64_t num_slots;
-    int32_t num_tokens, hq, hkv, rot, chunks;   // chunks: warps per token
+    int32_t num_tokens, hq, hkv, rot;
+    int32_t q_chunks, kv_chunks, chunks;        // warps per token: of the query, of key or value, in all
     float eps, k_scale, v_scale;
     int32_t *status;
 };
 
 template <int HD, bool FP8, bool INTER>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p) {
     pdl_trigger();                            // the attention plan may start (it reads no cache and no query)
     constexpr int kLanes = HD / 8;            // lanes of a row
     constexpr int kGroups = 32 / kLanes;      // rows side by side in a warp
@@ -46,81 +53,145 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int64_t t = item / p.chunks;
     if (t >= p.num_tokens) return;            // whole warps
-    const int chunk = static_cast<int>(item - t * p.chunks);
-    const int group = lane / kLanes, e0 = (lane % kLanes) * 8;
-    const int rows = p.hq + 2 * p.hkv;
-    const int row0 = chunk * kRowsUnroll * kGroups + group;
-
+    int chunk = static_cast<int>(item - t * p.chunks);
     const int64_t pos = __ldg(p.positions + t), slot = __ldg(p.slots + t);
-    uint4 raw[kRowsUnroll];
+    // query, key or value rows
+    const int kind = chunk < p.q_chunks ? 0 : (chunk < p.q_chunks + p.kv_chunks ? 1 : 2);
+    chunk -= kind == 0 ? 0 : (kind == 1 ? p.q_chunks : p.q_chunks + p.kv_chunks);
+    const int rows = kind == 0 ? p.hq : p.hkv;
+    const __nv_bfloat16 *src = kind == 0 ? p.query + t * p.q_stride
+                                         : (kind == 1 ? p.key + t * p.k_stride : p.value + t * p.v_stride);
+    const int l = lane % kLanes;
+    const int row0 = chunk * kRowsUnroll * kGroups + lane / kLanes;
+    // this lane's two pieces of four dims: turned together, or neighbours
+    const bool turns = kind < 2 && l * 8 < p.rot;
+    const bool split = !INTER && turns;
+    const bool whole = INTER || kind == 2;    // 16 bytes in one piece, in every lane
+    const int da = split ? l * 4 : l * 8, db = split ? (p.rot >> 1) + l * 4 : l * 8 + 4;
+    uint2 ra[kRowsUnroll], rb[kRowsUnroll];
 #pragma unroll
     for (int u = 0; u < kRowsUnroll; ++u) {
         const int row = row0 + u * kGroups;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-            const __nv_bfloat16 *src = row < p.hq ? p.query + t * p.q_stride + static_cast<int64_t>(row) * HD
-                                       : row < p.hq + p.hkv
-                                           ? p.key + t * p.k_stride + static_cast<int64_t>(row - p.hq) * HD
-                                           : p.value + t * p.v_stride + static_cast<int64_t>(row - p.hq - p.hkv) * HD;
-            raw[u] = *reinterpret_cast<const uint4 *>(src + e0);   // (not __ldg: query_out may be query)
+        if (row < rows) {                     // (not __ldg: query_out may be query)
+            if (whole) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + row * HD + da);
+                ra[u] = make_uint2(v.x, v.y), rb[u] = make_uint2(v.z, v.w);
+            } else {
+                ra[u] = *reinterpret_cast<const uint2 *>(src + row * HD + da);
+                rb[u] = *reinterpret_cast<const uint2 *>(src + row * HD + db);
+            }
         }
     }
     // a token past the table is skipped; with a negative slot it is padding and no error
-    if (pos < 0 || pos >= p.max_position || slot >= p.num_slots) {
-        if (lane == 0 && (slot >= 0)) set_status(p.status, PKV_ERR_DEVICE_INDEX);
-        if (pos < 0 || pos >= p.max_position) return;
-    }
+    const bool known = pos >= 0 && pos < p.max_position;
+    if (slot >= 0 && (!known || slot >= p.num_slots) && lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
+    if (!known) return;
     const bool stored = slot >= 0 && slot < p.num_slots;
-    LaneAngles<INTER> ang{};
-    if (e0 < p.rot) ang.load(p.cos_sin + pos * p.rot, e0, p.rot);
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (p.q_weight) wq = __ldg(reinterpret_cast<const uint4 *>(p.q_weight + e0));
-    if (p.k_weight) wk = __ldg(reinterpret_cast<const uint4 *>(p.k_weight + e0));
-    const int64_t blk = stored ? slot / kBlock : 0;
-    const int off = static_cast<int>(stored ? slot - blk * kBlock : 0);
+    if (kind > 0 && !stored) return;
 
+    // where a row goes: element offset of its first dim, of row 0 and from row to row
+    const int64_t blk = slot / kBlock;
+    const int64_t dst0 = kind == 0 ? t * p.out_stride
+                                   : ((blk * p.hkv * 2 + (kind - 1)) * kBlock + (slot - blk * kBlock)) * HD;
+    const int step = kind == 0 ? HD : 2 * kBlock * HD;
+    auto store = [&](int row, const uint64_t (&x)[4]) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(x[i], f[2 * i], f[2 * i + 1]);
+        const int64_t dst = dst0 + static_cast<int64_t>(row) * step;
+        if (FP8 && kind > 0) {
+            const uint2 c = f32_to_e4m3x8(f, kind == 1 ? p.k_scale : p.v_scale);
+            if (whole) {
+                *reinterpret_cast<uint2 *>(p.cache + dst + da) = c;
+            } else {
+                *reinterpret_cast<uint32_t *>(p.cache + dst + da) = c.x;
+                *reinterpret_cast<uint32_t *>(p.cache + dst + db) = c.y;
+            }
+        } else {
+            __nv_bfloat16 *out = (kind == 0 ? p.query_out : reinterpret_cast<__nv_bfloat16 *>(p.cache)) + dst;
+            const uint4 v = f32_to_bf16x8(f);
+            if (whole) {
+                *reinterpret_cast<uint4 *>(out + da) = v;
+            } else {
+                *reinterpret_cast<uint2 *>(out + da) = make_uint2(v.x, v.y);
+                *reinterpret_cast<uint2 *>(out + db) = make_uint2(v.z, v.w);
+            }
+        }
+    };
+    auto pair = [](uint32_t w) { return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
+    auto mul = [](uint64_t a, uint64_t b) {
+        uint64_t d;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+        return d;
+    };
+
+    if (kind == 2) {
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u) {
+            const int row = row0 + u * kGroups;
+            if (row >= rows) return;
+            if constexpr (FP8) {
+                const uint64_t x[4] = {pair(ra[u].x), pair(ra[u].y), pair(rb[u].x), pair(rb[u].y)};
+                store(row, x);
+            } else {                          // a bit copy
+                uint8_t *out = p.cache + 2 * (dst0 + static_cast<int64_t>(row) * step);
+                *reinterpret_cast<uint4 *>(out + 2 * da) = make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y);
+            }
+        }
+        return;
+    }
+
+    // cosines and sines of planes 4 l .. 4 l + 3
+    float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (turns) {
+        const float *angles = p.cos_sin + pos * p.rot + l * 4;
+        c4 = __ldg(reinterpret_cast<const float4 *>(angles));
+        s4 = __ldg(reinterpret_cast<const float4 *>(angles + (p.rot >> 1)));
+    }
+    const __nv_bfloat16 *weight = kind == 0 ? p.q_weight : p.k_weight;
+    uint2 wa = make_uint2(0, 0), wb = wa;
+    if (weight) {
+        wa = __ldg(reinterpret_cast<const uint2 *>(weight + da));
+        wb = __ldg(reinterpret_cast<const uint2 *>(weight + db));
+    }
+    const uint64_t w[4] = {pair(wa.x), pair(wa.y), pair(wb.x), pair(wb.y)};
+    const uint64_t c01 = f2_pack(c4.x, c4.y), c23 = f2_pack(c4.z, c4.w);
+    const uint64_t s01 = f2_pack(s4.x, s4.y), s23 = f2_pack(s4.z, s4.w);
+    const uint64_t n01 = f2_pack(-s4.x, -s4.y), n23 = f2_pack(-s4.z, -s4.w);
 #pragma unroll
     for (int u = 0; u < kRowsUnroll; ++u) {
         const int row = row0 + u * kGroups;
-        if (row - group >= rows) break;       // no row of this warp left
-        const bool is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
-        float x[8];
-        bf16x8_to_f32(raw[u], x);
-        float sq = 0.f;
+        if (row - lane / kLanes >= rows) break;               // no row of this warp left
+        uint64_t x[4] = {pair(ra[u].x), pair(ra[u].y), pair(rb[u].x), pair(rb[u].y)};
+        if (weight) {                                         // (rows past the last: of no use, and not stored)
+            float q0, q1;
+            f2_unpack(f2_add(f2_fma(x[0], x[0], mul(x[1], x[1])), f2_fma(x[2], x[2], mul(x[3], x[3]))), q0, q1);
+            float sq = q0 + q1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-#pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-        const bool normed = is_q ? p.q_weight != nullptr : (!is_v && p.k_weight != nullptr);
-        if (normed) {
+            for (int m = kLanes / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
             const float inv = rsqrtf(sq * (1.f / HD) + p.eps);
-            float w[8];
-            bf16x8_to_f32(is_q ? wq : wk, w);
+            const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+            for (int i = 0; i < 4; ++i) x[i] = mul(mul(x[i], inv2), w[i]);
         }
-        if (row - group < p.hq + p.hkv) {     // some row of the warp is a query or key
-            float y[8];
+        if (turns) {
+            if constexpr (INTER) {
+                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i];
-            rotate8<INTER>(y, ang, e0, p.rot);
-            if (!is_v) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = y[i];
+                for (int i = 0; i < 4; ++i) {
+                    float a, b;
+                    f2_unpack(x[i], a, b);
+                    x[i] = f2_pack(a * c[i] - b * s[i], b * c[i] + a * s[i]);
+                }
+            } else {
+                const uint64_t a01 = x[0], a23 = x[1], b01 = x[2], b23 = x[3];
+                x[0] = f2_fma(a01, c01, mul(b01, n01));
+                x[1] = f2_fma(a23, c23, mul(b23, n23));
+                x[2] = f2_fma(b01, c01, mul(a01, s01));
+                x[3] = f2_fma(b23, c23, mul(a23, s23));
             }
         }
-        if (row >= rows) continue;
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(p.query_out + t * p.out_stride + static_cast<int64_t>(row) * HD + e0) =
-                f32_to_bf16x8(x);
-        } else if (stored) {
-            const int h = is_v ? row - p.hq - p.hkv : row - p.hq;
-            const int64_t dst = (((blk * p.hkv + h) * 2 + (is_v ? 1 : 0)) * kBlock + off) * HD + e0;
-            if constexpr (FP8)
-                *reinterpret_cast<uint2 *>(p.cache + dst) = f32_to_e4m3x8(x, is_v ? p.v_scale : p.k_scale);
-            else
-                *reinterpret_cast<uint4 *>(p.cache + dst * 2) = is_v ? raw[u] : f32_to_bf16x8(x);
-        }
+        if (row < rows) store(row, x);
     }
 }
 
@@ -169,11 +240,13 @@ static int qk_norm_rope(bool fp8, void *query_out, int64_t out_stride, void *kv_
     p.num_slots = num_blocks * kBlock;
     p.num_tokens = num_tokens, p.hq = hq, p.hkv = hkv, p.rot = rotary_dim;
     const int per_warp = kRowsUnroll * (32 / (head_size / 8));
-    p.chunks = (hq + 2 * hkv + per_warp - 1) / per_warp;
+    p.q_chunks = (hq + per_warp - 1) / per_warp;
+    p.kv_chunks = (hkv + per_warp - 1) / per_warp;
+    p.chunks = p.q_chunks + 2 * p.kv_chunks;
     p.eps = eps, p.k_scale = k_scale, p.v_scale = v_scale;
     p.status = device_status;
     const int64_t warps = static_cast<int64_t>(num_tokens) * p.chunks;
-    const int64_t blocks = (warps + 7) / 8;
+    const int64_t blocks = (warps + kQkThreads / 32 - 1) / (kQkThreads / 32);
     if (blocks > INT32_MAX) return PKV_ERR_SHAPE;
     void (*kernel)(QkParams);
     const bool it = interleaved != 0;
@@ -183,7 +256,7 @@ static int qk_norm_rope(bool fp8, void *query_out, int64_t out_stride, void *kv_
     else
         kernel = fp8 ? (it ? qk_norm_rope_kernel<64, true, true> : qk_norm_rope_kernel<64, true, false>)
                      : (it ? qk_norm_rope_kernel<64, false, true> : qk_norm_rope_kernel<64, false, false>);
-    kernel<<<static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    kernel<<<static_cast<unsigned>(blocks), kQkThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
