@@ -47,6 +47,7 @@
 // tensor memory; warps 4-7 are the softmax; warps 9-12 write finished tiles out
 // while the softmax is at the next one.  Every wait is bounded.
 #include <mutex>
+#include <type_traits>
 
 #include "latent_common.cuh"
 #include "prefill_common.cuh"
@@ -153,13 +154,14 @@ enum LaBar {
     kLaPFull = 33,            // weights and votes of a tile written (+ tile & 1)
     kLaODone = 5,             // the tile's second products completed
     kLaOReady = 8,            // the item's last ones completed
-    kLaOFree = 6,             // O' read out by the epilogue
+    kLaOFree = 6,             // dims 0 .. 255 of O' read out
+    kLaOFree2 = 4,            // and the others
     kLaRescaled = 7,          // O' rescaled (only in tiles where some warp voted for it)
     kLaFix = 9,               // rows past the last visible key zeroed (+ stage)
     kLaItemFull = 11, kLaItemEmpty = 15,
     kLaKVFull = 19,           // a part landed (+ 2 stage + part)
     kLaKVEmpty = 23,          // a part read by its last product (+ 2 stage + part)
-    kLaNumBars = 35           // (4 is not used)
+    kLaNumBars = 35
 };
 static_assert(kLaNumBars * 8 + 24 <= 304, "barriers, tensor-memory address, status, votes");
 
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (threadIdx.x < kLaNumBars) {
         const int b = threadIdx.x;
         int count = 1;
-        if (b == kLaOFree || b == kLaRescaled || b == kLaSFree || b == kLaSFree + 1 || b >= kLaRowFull)
+        if (b == kLaOFree || b == kLaOFree2 || b == kLaRescaled || b == kLaSFree || b == kLaSFree + 1 || b >= kLaRowFull)
             count = 4;                                       // four warps
         else if (b >= kLaItemEmpty && b < kLaItemEmpty + kLaItemSlots) count = 12;  // loads, 2 MMA warps, Q, 4 softmax warps, 4 that write out
         mbar_init(&bars[b], count);
@@ -563,8 +565,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             if (!valid) break;
             // N: the tile's rows, in sixteens
             const uint32_t idesc_o = idesc_bf16_f32(128, (rows + 15) & ~15, 1, 1);
-            // O' has been read out by the previous item's epilogue
-            if (k > 0) ok = warp_wait(&bars[kLaOFree], (k - 1) & 1, status);
             for (int j = 0; j < n && ok; ++j, ++gt) {
                 const int st = gt % kLaStages;
                 ok = warp_wait(&bars[kLaPFull + (gt & 1)], (gt >> 1) & 1, status);
@@ -577,6 +577,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     if (ok) ok = warp_wait(&bars[kLaRescaled], rescales & 1, status);
                     ++rescales;
                 }
+                // the previous item's O' has been read out, half by half
+                if (ok && k > 0 && j == 0) ok = warp_wait(&bars[kLaOFree], (k - 1) & 1, status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t so = static_cast<uint32_t>(st * (kLaStage >> 4));
@@ -591,6 +593,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                             umma_f16_ss(tmem + 64u * m, a0 + kk * (kLaPageA >> 4) + m * (2048 >> 4),
                                         w0 + kk * (kLaPageB >> 4), idesc_o, kk > 0 ? 1u : more);
                     umma_commit(&bars[kLaKVEmpty + 2 * st]);
+                }
+                __syncwarp();
+                if (k > 0 && j == 0) {
+                    ok = warp_wait(&bars[kLaOFree2], (k - 1) & 1, status);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -852,43 +862,50 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             tc_fence_after();
             const LaRows *rec = reinterpret_cast<const LaRows *>(smem + kLaOffRow + rb * kLaRowsBytes);
             const int rows = rec->rows, part = rec->slot;
-            if (part >= 0) {
-                // [128-dim block][row / 4][dim][row % 4]
-                float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
-                            (static_cast<int64_t>(blockIdx.x) * 2 + part) * kLaPartFloats + (quad * 32 + lane) * 4;
-#pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += 32) {
+            // blocks of 128 dims x 32 rows, dims first
+            auto half_read = [&]() {                          // dims 0 .. 255 of O' have been read out
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kLaOFree]);
+            };
+            auto write = [&](auto two) {                      // rows beyond the first 32, or none
+                constexpr int kH = decltype(two)::value ? 2 : 1, kBlocks = 4 * kH;
+                if (part >= 0) {
+                    // [128-dim block][row / 4][dim][row % 4]
+                    float *po = reinterpret_cast<float *>(p.ws + kLaWsO) +
+                                (static_cast<int64_t>(blockIdx.x) * 2 + part) * kLaPartFloats + (quad * 32 + lane) * 4;
                     float v[2][32];                             // the next block's loads run beside the stores
-                    tmem_ld32f(tlane + r0, v[0]);
+                    tmem_ld32f(tlane, v[0]);
 #pragma unroll
-                    for (int m = 0; m < kLatent / 128; ++m) {
+                    for (int i = 0; i < kBlocks; ++i) {
                         tmem_ld_wait();
-                        if (m + 1 < kLatent / 128) tmem_ld32f(tlane + 64u * (m + 1) + r0, v[(m + 1) & 1]);
+                        if (i == kBlocks / 2 - 1) half_read();
+                        if (i + 1 < kBlocks)
+                            tmem_ld32f(tlane + 64u * ((i + 1) / kH) + 32u * ((i + 1) % kH), v[(i + 1) & 1]);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            if (r0 + e < rows)
-                                *reinterpret_cast<float4 *>(po + (m * 16 + (r0 + e) / 4) * 512) =
-                                    make_float4(v[m & 1][e], v[m & 1][e + 1], v[m & 1][e + 2], v[m & 1][e + 3]);
+                            if (32 * (i % kH) + e < rows)
+                                *reinterpret_cast<float4 *>(po + (i / kH * 16 + 8 * (i % kH) + e / 4) * 512) =
+                                    make_float4(v[i & 1][e], v[i & 1][e + 1], v[i & 1][e + 2], v[i & 1][e + 3]);
                     }
+                    return;
                 }
-            } else {
                 // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
-                // stmatrix: rows of 64 bytes, 16 a lane.  Block i + 1 is packed, and block i + 2
-                // on its way from tensor memory, while block i is read back and stored.
-                const int blocks = rows > 32 ? 8 : 4;           // block i: rows 32 (i / 4) .., dims 128 (i % 4) ..
+                // stmatrix: rows of 64 bytes, 16 a lane.  Block i + 1 is packed while block i is
+                // read back and stored.
                 float a[16], b[16];                             // dims t / 4 (+ 8), and 16 further
                 uint32_t w[16];
                 uint4 out[4];
-                int dst[4] = {};
                 auto fetch = [&](int i) {
-                    tmem_ld_16x32f(tlane + 64u * (i & 3) + 32u * (i >> 2), a);
-                    tmem_ld_16x32f(tlane + (16u << 16) + 64u * (i & 3) + 32u * (i >> 2), b);
+                    tmem_ld_16x32f(tlane + 64u * (i / kH) + 32u * (i % kH), a);
+                    tmem_ld_16x32f(tlane + (16u << 16) + 64u * (i / kH) + 32u * (i % kH), b);
                 };
                 auto pack = [&](int i) {
                     tmem_ld_wait();
+                    if (i == kBlocks / 2 - 1) half_read();
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {               // rows 8 e ..
-                        const float2 s = *reinterpret_cast<const float2 *>(rec->inv + 32 * (i >> 2) + 8 * e + 2 * (lane & 3));
+                        const float2 s = *reinterpret_cast<const float2 *>(rec->inv + 32 * (i % kH) + 8 * e + 2 * (lane & 3));
                         w[4 * e] = pack_bf16x2(a[4 * e] * s.x, a[4 * e + 1] * s.y);
                         w[4 * e + 1] = pack_bf16x2(a[4 * e + 2] * s.x, a[4 * e + 3] * s.y);
                         w[4 * e + 2] = pack_bf16x2(b[4 * e] * s.x, b[4 * e + 1] * s.y);
@@ -898,9 +915,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 fetch(0);
                 pack(0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (i >= blocks) break;
-                    if (i + 1 < 8 && i + 1 < blocks) fetch(i + 1);
+                for (int i = 0; i < kBlocks; ++i) {
+                    if (i + 1 < kBlocks) fetch(i + 1);
                     __syncwarp();                               // the block before has been read back
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -909,30 +925,30 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                       w[4 * e + 2], w[4 * e + 3]);
                     }
                     __syncwarp();
-                    if ((i & 3) == 0) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[e] = rec->dst[32 * (i >> 2) + 8 * e + (lane >> 2)];
-                    }
+                    int dst[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int row = 8 * e + (lane >> 2);
+                        dst[e] = rec->dst[32 * (i % kH) + row];
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(out[e].x), "=r"(out[e].y), "=r"(out[e].z), "=r"(out[e].w)
                                      : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4))
                                      : "memory");
                     }
-                    if (i + 1 < 8 && i + 1 < blocks) pack(i + 1);
+                    if (i + 1 < kBlocks) pack(i + 1);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (dst[e] >= 0)
-                            *reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(dst[e]) * kLatent + 128 * (i & 3) +
+                            *reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(dst[e]) * kLatent + 128 * (i / kH) +
                                                        quad * 32 + (lane & 3) * 8) = out[e];
                 }
-            }
+            };
+            if (rows > 32) write(std::true_type{});
+            else write(std::false_type{});
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bars[kLaOFree]);
+                mbar_arrive(&bars[kLaOFree2]);
                 mbar_arrive(&bars[kLaRowFree + rb]);
             }
         }
