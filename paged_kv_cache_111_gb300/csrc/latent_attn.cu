@@ -102,11 +102,12 @@ __device__ __forceinline__ constexpr uint32_t la_col_s(int b) { return 256u + 64
 // workspace
 constexpr int64_t kLaWsStatus = 256;                                      // int32 per CTA
 constexpr int64_t kLaWsDesc = 1280;                                       // int4 per CTA
-constexpr int64_t kLaWsMl = 4096;                                         // float [CTA][2][max, sum][64]
+constexpr int64_t kLaWsDesc0 = kLaWsDesc + kLaMaxCtas * 16;               // int4 per CTA
+constexpr int64_t kLaWsMl = 8192;                                         // float [CTA][2][max, sum][64]
 constexpr int64_t kLaWsO = kLaWsMl + kLaMaxCtas * 2 * 2 * kLaRows * 4;    // float [CTA][2][64 x 512]
 constexpr int64_t kLaPartFloats = kLaRows * kLatent;
 constexpr int64_t kLaWsBytes = kLaWsO + static_cast<int64_t>(kLaMaxCtas) * 2 * kLaPartFloats * 4;
-static_assert(kLaWsStatus + kLaMaxCtas * 4 <= kLaWsDesc && kLaWsDesc + kLaMaxCtas * 16 <= kLaWsMl, "workspace");
+static_assert(kLaWsStatus + kLaMaxCtas * 4 <= kLaWsDesc && kLaWsDesc0 + kLaMaxCtas * 16 <= kLaWsMl, "workspace");
 
 struct LaParams {
     __nv_bfloat16 *out;
@@ -340,14 +341,17 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     pdl_wait();
     pdl_trigger();                        // the merge's CTAs may take their places (they wait for this grid)
     const bool work = lo < hi;
+    // for the merge kernel, {first token, tokens, lanes that it runs across, this lane among them}: the row tile
+    // that starts here and ends in another lane, and the one that started in an earlier lane
     int4 *desc = reinterpret_cast<int4 *>(p.ws + kLaWsDesc) + blockIdx.x;
+    int4 *desc0 = reinterpret_cast<int4 *>(p.ws + kLaWsDesc0) + blockIdx.x;
 
     if (warp == 3) {
         // ---------------- walk of the run: items, ahead of the other warps ----------------
         bool ok = true;
         int r = start_req;
         int64_t off = start_off, left = hi - lo, at = lo;     // at: position in the line
-        int4 split = make_int4(0, 0, 0, 0);                   // the row tile that starts here and ends in another lane
+        int4 split = make_int4(0, 0, 0, 0), split0 = split;
         bool unused = false;
         LaReq req = work ? la_request(p, r, unused) : LaReq{};
         for (int k = 0; ok; ++k) {
@@ -383,9 +387,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 it.kv1 = static_cast<int32_t>(pos + n);
                 it.valid = it.kv1 > it.kv0;                                  // (else it starts in the next lane)
                 it.slot = it.kv0 > 0 ? 0 : (it.kv1 < it.n_kv ? 1 : -1);
-                if (it.valid && it.slot == 1) {
-                    const int64_t last = (at - pos + it.n_kv - 1) / per;     // lane of its last key tile
-                    split = make_int4(it.tok0, it.ntok, static_cast<int>(last - my_lane) + 1, 0);
+                if (it.valid && it.slot >= 0) {
+                    const int64_t first = (at - pos) / per, last = (at - pos + it.n_kv - 1) / per;   // lanes of its key tiles
+                    const int4 d = make_int4(it.tok0, it.ntok, static_cast<int>(last - first) + 1,
+                                             static_cast<int>(my_lane - first));
+                    if (it.slot == 1) split = d;
+                    else split0 = d;
                 }
                 off += n, at += n, left -= n;
             }
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             }
             if (!it.valid) break;
         }
-        if (lane == 0) *desc = split;
+        if (lane == 0) *desc = split, *desc0 = split0;
     } else if (warp == 0) {
         // ---------------- pages through the block table ----------------
         bool ok = true;
@@ -971,13 +978,21 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 // Piece i of the tile that starts in CTA c lies in CTA c + i * groups, slot 1
 // for the first and 0 for the others:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
-// blockIdx.y: 128 dims x 16 rows; a thread takes one dim of eight rows.  The merge
-// is one trip to memory that the first kernel has just written, and nothing else,
-// so nothing is looked up before it starts: the first two pieces of a tile (most
-// have two) are this CTA's own and the next lane's, and are read beside the record
-// that says whether there is a tile to merge.
+// blockIdx.y: 128 dims x 16 rows.  The merge is one trip to memory that the first
+// kernel has just written, and nothing else, so nothing is looked up before it
+// starts: the first two pieces of a tile (most have two) are this CTA's own and
+// the next lane's, and are read beside the record that says whether there is a
+// tile to merge; a thread takes one dim of eight rows.
+// A tile of many pieces (a long request on an otherwise idle GPU) is shared out
+// instead: over the CTAs of its first four lanes by rows, and in each over two
+// halves of the pieces, with the pieces' factors worked out first.  That code
+// (kShare) takes registers from the other, so a call that can hold many row tiles
+// goes without it: 1000 keys of one request, 16 heads, take 15.4 us without it and
+// 11.6 us with it; 256 requests of 128 heads 101 us and 103 us.
 constexpr int kLaCombineY = 4 * (kLaRows / 16);
+constexpr int kLaMany = 8;                    // pieces from which a tile is shared out
 
+template <bool kShare>
 __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, int ctas) {
     pdl_trigger();                        // a following call may start looking at its lengths
     pdl_wait();
@@ -996,65 +1011,120 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
     }
     constexpr int kQ = 2;                                             // groups of four rows a thread
     const int cta = blockIdx.x;
-    const int m = blockIdx.y >> 2, dim = threadIdx.x & 127;
-    const int r4 = (blockIdx.y & 3) * 4 + (threadIdx.x >> 7) * kQ;
+    const int m = blockIdx.y >> 2, dim = threadIdx.x & 127, half = threadIdx.x >> 7;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl) + r4 * 4;
-    const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO) + ((m * 16 + r4) * 128 + dim) * 4;
-    float4 mx[kQ], ls[kQ], acc[kQ], m1[kQ], l1[kQ], a1[kQ];
-    auto load = [&](int64_t part, float4 (&a)[kQ], float4 (&b)[kQ], float4 (&c)[kQ]) {
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-            a[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + q * 4);
-            b[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + kLaRows + q * 4);
-            c[q] = *reinterpret_cast<const float4 *>(o + part * kLaPartFloats + q * 512);
-        }
-    };
-    // two softmax states into one; a state that saw no key has m = -inf, and whatever its sums hold is not used
-    auto join = [&](float &m0, float &l0, float &a0, float m1, float l1, float a1) {
-        const float M = fmaxf(m0, m1);
-        const float w0 = m0 == NEG_INF ? 0.f : fast_exp2(m0 - M), w1 = m1 == NEG_INF ? 0.f : fast_exp2(m1 - M);
-        l0 = (w0 == 0.f ? 0.f : w0 * l0) + (w1 == 0.f ? 0.f : w1 * l1);
-        a0 = (w0 == 0.f ? 0.f : w0 * a0) + (w1 == 0.f ? 0.f : w1 * a1);
-        m0 = M;
-    };
-    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
-    load(static_cast<int64_t>(cta) * 2 + 1, mx, ls, acc);
-    load(static_cast<int64_t>(min(cta + p.groups, ctas - 1)) * 2, m1, l1, a1);
-    const int pieces = d.z;
-    const int rows = d.y * p.hpt;
-    if (pieces < 2 || r4 * 4 >= rows) return;                         // (whole warps)
-#pragma unroll 1
-    for (int i = 1;;) {
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-            join(mx[q].x, ls[q].x, acc[q].x, m1[q].x, l1[q].x, a1[q].x);
-            join(mx[q].y, ls[q].y, acc[q].y, m1[q].y, l1[q].y, a1[q].y);
-            join(mx[q].z, ls[q].z, acc[q].z, m1[q].z, l1[q].z, a1[q].z);
-            join(mx[q].w, ls[q].w, acc[q].w, m1[q].w, l1[q].w, a1[q].w);
-        }
-        if (++i >= pieces) break;
-        load(static_cast<int64_t>(cta + i * p.groups) * 2, m1, l1, a1);
-    }
+    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl);
+    const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO) + dim * 4;
     const int group = cta % p.groups, heads_here = min(p.hpt, p.heads - group * p.hpt);
     const bool odd = threadIdx.x & 1;
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-        const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w}, l[4] = {ls[q].x, ls[q].y, ls[q].z, ls[q].w};
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = l[e] > 0.f ? v[e] / l[e] : 0.f;
-        // neighbouring lanes exchange a row each: 4-byte stores
+    // four rows (4 r4 ..) of this thread's dim: neighbouring lanes exchange a row each, 4-byte stores
+    auto store = [&](const int4 &d, int r4, const float (&y)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? y[e] : y[e + 1], 1);
-            const int row = (r4 + q) * 4 + e + (odd ? 1 : 0), tok = row / p.hpt, h = row - tok * p.hpt;
-            if (row < rows && h < heads_here)
+            const int row = r4 * 4 + e + (odd ? 1 : 0), tok = row / p.hpt, h = row - tok * p.hpt;
+            if (row < d.y * p.hpt && h < heads_here)
                 *reinterpret_cast<uint32_t *>(
                     p.out + (static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent + m * 128 +
                     (dim & ~1)) = odd ? pack_bf16x2(got, y[e + 1]) : pack_bf16x2(y[e], got);
         }
+    };
+
+    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
+    const int4 d0 = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc0)[cta];
+    {
+        const int r4 = (blockIdx.y & 3) * 4 + half * kQ;
+        float4 mx[kQ], ls[kQ], acc[kQ], m1[kQ], l1[kQ], a1[kQ];
+        auto load = [&](int64_t part, float4 (&a)[kQ], float4 (&b)[kQ], float4 (&c)[kQ]) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                a[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + (r4 + q) * 4);
+                b[q] = *reinterpret_cast<const float4 *>(ml + part * 2 * kLaRows + kLaRows + (r4 + q) * 4);
+                c[q] = *reinterpret_cast<const float4 *>(o + part * kLaPartFloats + (m * 16 + r4 + q) * 512);
+            }
+        };
+        // two softmax states into one; a state that saw no key has m = -inf, and whatever its sums hold is not used
+        auto join = [&](float &m0, float &l0, float &a0, float m1, float l1, float a1) {
+            const float M = fmaxf(m0, m1);
+            const float w0 = m0 == NEG_INF ? 0.f : fast_exp2(m0 - M), w1 = m1 == NEG_INF ? 0.f : fast_exp2(m1 - M);
+            l0 = (w0 == 0.f ? 0.f : w0 * l0) + (w1 == 0.f ? 0.f : w1 * l1);
+            a0 = (w0 == 0.f ? 0.f : w0 * a0) + (w1 == 0.f ? 0.f : w1 * a1);
+            m0 = M;
+        };
+        load(static_cast<int64_t>(cta) * 2 + 1, mx, ls, acc);
+        load(static_cast<int64_t>(min(cta + p.groups, ctas - 1)) * 2, m1, l1, a1);
+        if (d.z >= 2 && (!kShare || d.z < kLaMany) && r4 * 4 < d.y * p.hpt) {      // (whole warps)
+#pragma unroll 1
+            for (int i = 1;;) {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    join(mx[q].x, ls[q].x, acc[q].x, m1[q].x, l1[q].x, a1[q].x);
+                    join(mx[q].y, ls[q].y, acc[q].y, m1[q].y, l1[q].y, a1[q].y);
+                    join(mx[q].z, ls[q].z, acc[q].z, m1[q].z, l1[q].z, a1[q].z);
+                    join(mx[q].w, ls[q].w, acc[q].w, m1[q].w, l1[q].w, a1[q].w);
+                }
+                if (++i >= d.z) break;
+                load(static_cast<int64_t>(cta + i * p.groups) * 2, m1, l1, a1);
+            }
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w}, l[4] = {ls[q].x, ls[q].y, ls[q].z, ls[q].w};
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = l[e] > 0.f ? v[e] / l[e] : 0.f;
+                store(d, r4 + q, y);
+            }
+        }
     }
+
+    if constexpr (!kShare) return;
+    __shared__ float4 factor[kLaMaxCtas];                             // of a piece, for four rows
+    __shared__ float4 other[128];
+    auto many = [&](const int4 &d) {
+        const int first = cta - d.w * p.groups, pieces = d.z;
+        const int r4 = (blockIdx.y & 3) * 4 + d.w;
+        if (d.z < kLaMany || d.w >= 4 || r4 * 4 >= d.y * p.hpt) return;   // (the whole CTA)
+        auto part_of = [&](int i) { return static_cast<int64_t>(first + i * p.groups) * 2 + (i == 0 ? 1 : 0); };
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (warp < 4) {                                               // a row a warp
+            const float *row = ml + r4 * 4 + warp;
+            float M = NEG_INF, L = 0.f;
+            for (int i = lane; i < pieces; i += 32) M = fmaxf(M, row[part_of(i) * 2 * kLaRows]);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+            for (int i = lane; i < pieces; i += 32) {
+                const float mi = row[part_of(i) * 2 * kLaRows];
+                const float w = mi == NEG_INF ? 0.f : fast_exp2(mi - M);
+                if (w > 0.f) L = fmaf(w, row[part_of(i) * 2 * kLaRows + kLaRows], L);
+                reinterpret_cast<float *>(factor + i)[warp] = w;
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            for (int i = lane; i < pieces; i += 32) reinterpret_cast<float *>(factor + i)[warp] *= inv;
+        }
+        __syncthreads();
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = half; i < pieces; i += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(o + part_of(i) * kLaPartFloats + (m * 16 + r4) * 512);
+            const float4 f = factor[i];
+            y[0] = fmaf(f.x, f.x == 0.f ? 0.f : v.x, y[0]);
+            y[1] = fmaf(f.y, f.y == 0.f ? 0.f : v.y, y[1]);
+            y[2] = fmaf(f.z, f.z == 0.f ? 0.f : v.z, y[2]);
+            y[3] = fmaf(f.w, f.w == 0.f ? 0.f : v.w, y[3]);
+        }
+        if (half) other[dim] = make_float4(y[0], y[1], y[2], y[3]);
+        __syncthreads();
+        if (!half) {
+            const float4 v = other[dim];
+            y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+            store(d, r4, y);
+        }
+        __syncthreads();                                              // (the other tile's turn)
+    };
+    many(d);
+    many(d0);
 }
 
 // ---- host side --------------------------------------------------------------------
@@ -1148,6 +1218,10 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
     p.lanes = (sms < kLaMaxCtas ? sms : kLaMaxCtas) / p.groups;
+    // no more lanes than the bounds leave units for
+    const int64_t most = static_cast<int64_t>(num_seqs) * ((max_query_len + p.tpt - 1) / p.tpt);     // row tiles
+    const int64_t units = most * ((max_seq_len + kLaKeys - 1) / kLaKeys + kLaExtra);
+    if (units < p.lanes) p.lanes = units > 1 ? static_cast<int32_t>(units) : 1;
     const int ctas = p.lanes * p.groups;
     CUtensorMap am, bm, qm;
     int rc = make_latent_map(&am, latent_cache, num_blocks, kLaChunksA);
@@ -1174,8 +1248,10 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
                    static_cast<cudaStream_t>(stream), am, bm, qm, p) != cudaSuccess)
         return PKV_ERR_CUDA;
-    if (launch_pdl(latent_combine_kernel, dim3(static_cast<unsigned>(ctas), kLaCombineY), dim3(256), 0,
-                   static_cast<cudaStream_t>(stream), p, ctas) != cudaSuccess)
+    // a tile can have many pieces only where the row tiles are few
+    if (launch_pdl(most <= p.lanes / 4 ? latent_combine_kernel<true> : latent_combine_kernel<false>,
+                   dim3(static_cast<unsigned>(ctas), kLaCombineY), dim3(256), 0, static_cast<cudaStream_t>(stream), p,
+                   ctas) != cudaSuccess)
         return PKV_ERR_CUDA;
     return PKV_OK;
 }
