@@ -65,7 +65,7 @@ constexpr int kLaMaxCtas = 152;
 constexpr int kLaMaxHeads = 1024;
 constexpr int kLaThreads = 416;
 constexpr int kLaItemSlots = 4;
-constexpr int kLaAhead = 4;                                  // tiles between a page's way into L2 and its load
+constexpr int kLaAhead = 1;                                  // tiles between a page's way into L2 and its load
 static_assert(kLaAhead * kLaPages <= 32, "one page a lane");
 
 // A stage holds a tile's 64 keys in two parts, each [page][token half][chunk]
@@ -245,9 +245,22 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t r0, uint32
                  : "memory");
 }
 
+// 2-D tiled store of one box from shared memory, as a bulk group of this thread.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All of this thread's bulk stores have read shared memory (or are complete).
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-                       const __grid_constant__ CUtensorMap q_map, const LaParams p) {
+                       const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap out_map,
+                       const LaParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kLaOffBar);
@@ -433,9 +446,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
         };
-        // Pages to come are brought into L2 kLaAhead tiles before they are loaded: two
-        // stages of shared memory are too few to cover memory's latency, and L2's is
-        // half of it.  The CTAs of a lane share the pages out.
+        // Pages are brought into L2 kLaAhead tiles before they are loaded, the first ones of
+        // an item while the one before ends: two stages of shared memory are too few to
+        // cover memory's latency.  (256 requests of 128 heads: 99 us without, 96 us one tile
+        // ahead, 97 two, 101 four, 109 eight.)  The CTAs of a lane share the pages out.
         auto prefetch = [&](int id, bool there) {
             if (there && id >= 0 && id < p.num_blocks && lane % p.groups == group)
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + static_cast<int64_t>(id) *
@@ -898,8 +912,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     return;
                 }
                 // 32 dims x 32 rows at a time through 2 KiB of shared memory, transposed by
-                // stmatrix: rows of 64 bytes, 16 a lane.  Block i + 1 is packed while block i is
-                // read back and stored.
+                // stmatrix into rows of 64 bytes (64-byte swizzle).  The tile's rows lie one after
+                // another in `out`: 32 of them leave as one TMA store (stores of the lanes would
+                // queue in front of the softmax warps' shuffles), fewer by 16-byte stores.  Block
+                // i + 1 is packed while block i leaves.
                 float a[16], b[16];                             // dims t / 4 (+ 8), and 16 further
                 uint32_t w[16];
                 uint4 out[4];
@@ -921,15 +937,25 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 };
                 fetch(0);
                 pack(0);
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < kBlocks; ++i) {
                     if (i + 1 < kBlocks) fetch(i + 1);
-                    __syncwarp();                               // the block before has been read back
+                    const int first = rec->dst[32 * (i % kH)];
+                    const bool whole = first >= 0 && rec->dst[32 * (i % kH) + 31] >= 0;
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();                               // the block before has been read
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int row = 8 * e + (lane & 7);
                         stsm_x4_trans(stage + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4), w[4 * e], w[4 * e + 1],
                                       w[4 * e + 2], w[4 * e + 3]);
+                    }
+                    if (whole) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store_2d(&out_map, stage, 128 * (i / kH) + 32 * quad, first);
+                        if (i + 1 < kBlocks) pack(i + 1);
+                        continue;
                     }
                     __syncwarp();
                     int dst[4];
@@ -959,6 +985,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                 mbar_arrive(&bars[kLaRowFree + rb]);
             }
         }
+        if (lane == 0) bulk_wait();
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -1145,6 +1173,21 @@ static int make_latent_map(CUtensorMap *map, const void *cache, int64_t num_bloc
                : PKV_ERR_CUDA;
 }
 
+// {512 dims, token x head rows} of the output: a box is 32 dims of 32 rows.
+static int make_latent_out_map(CUtensorMap *map, void *out, int64_t rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t dims[2] = {kLatent, static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {kLatent * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
 // {576 dims, heads, tokens}: a box is 64 dims of hpt heads of tpt tokens.
 static int make_latent_query_map(CUtensorMap *map, const void *query, int64_t q_stride, const LaParams &p) {
     EncodeTiledFn enc = encode_fn();
@@ -1223,15 +1266,16 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     const int64_t units = most * ((max_seq_len + kLaKeys - 1) / kLaKeys + kLaExtra);
     if (units < p.lanes) p.lanes = units > 1 ? static_cast<int32_t>(units) : 1;
     const int ctas = p.lanes * p.groups;
-    CUtensorMap am, bm, qm;
+    CUtensorMap am, bm, qm, om;
     int rc = make_latent_map(&am, latent_cache, num_blocks, kLaChunksA);
     if (!rc) rc = make_latent_map(&bm, latent_cache, num_blocks, kLaChunksB);
     if (rc) return rc;
     if (num_tokens > 0) {
         rc = make_latent_query_map(&qm, query, query_token_stride, p);
+        if (!rc) rc = make_latent_out_map(&om, out, static_cast<int64_t>(num_tokens) * num_heads);
         if (rc) return rc;
     } else {
-        qm = am;                                   // no rows: not read
+        qm = om = am;                              // no rows: not used
     }
     static std::mutex mu;
     static uint64_t done_mask = 0;
@@ -1246,7 +1290,7 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
         }
     }
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
-                   static_cast<cudaStream_t>(stream), am, bm, qm, p) != cudaSuccess)
+                   static_cast<cudaStream_t>(stream), am, bm, qm, om, p) != cudaSuccess)
         return PKV_ERR_CUDA;
     // a tile can have many pieces only where the row tiles are few
     if (launch_pdl(most <= p.lanes / 4 ? latent_combine_kernel<true> : latent_combine_kernel<false>,
