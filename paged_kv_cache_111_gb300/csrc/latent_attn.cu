@@ -1006,58 +1006,173 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 // Piece i of the tile that starts in CTA c lies in CTA c + i * groups, slot 1
 // for the first and 0 for the others:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
-// blockIdx.y: 128 dims x 16 rows.  The merge is one trip to memory that the first
-// kernel has just written, and nothing else, so nothing is looked up before it
-// starts: the first two pieces of a tile (most have two) are this CTA's own and
-// the next lane's, and are read beside the record that says whether there is a
-// tile to merge; a thread takes one dim of eight rows.
-// A tile of many pieces (a long request on an otherwise idle GPU) is shared out
-// instead: over the CTAs of its first four lanes by rows, and in each over two
-// halves of the pieces, with the pieces' factors worked out first.  That code
-// (kShare) takes registers from the other, so a call that can hold many row tiles
-// goes without it: 1000 keys of one request, 16 heads, take 15.4 us without it and
-// 11.6 us with it; 256 requests of 128 heads 101 us and 103 us.
-constexpr int kLaCombineY = 4 * (kLaRows / 16);
+// The merge is one trip to memory that the first kernel has just written, and
+// nothing else.  Two kernels, by what a call can hold:
+//  - many row tiles, so most tiles have two pieces and nearly every lane starts
+//    one: latent_merge_kernel, a CTA for 128 dims of a lane's tile, which takes the
+//    two pieces in bulk into shared memory (64 KiB a CTA, three CTAs an SM: twice
+//    what registers could have in flight; 256 requests of 128 heads, 40 MB: 15 us by
+//    registers) before it knows whether there is a tile to merge;
+//  - few, so a tile can have many pieces (a long request on an otherwise idle GPU):
+//    latent_merge_few_kernel, which shares a tile of many pieces out over the CTAs
+//    of its first four lanes by rows, and in each over two halves of the pieces
+//    (1000 keys of one request, 16 heads: 15.4 us with one after another, 11.6 us).
+
+// The call's status: the first error of its CTAs.
+__device__ __forceinline__ void la_collect_status(const LaParams &p, int ctas) {
+    if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= 32) return;
+    int32_t s = 0;
+    for (int c = threadIdx.x; c < ctas; c += 32) {
+        const int32_t x = reinterpret_cast<const int32_t *>(p.ws + kLaWsStatus)[c];
+        s = s ? s : x;
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int32_t y = __shfl_down_sync(0xffffffffu, s, m);
+        s = s ? s : y;
+    }
+    if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = s;
+}
+
+// Four rows (4 r4 ..) of one dim a thread to `out`: neighbouring lanes exchange a
+// row each, 4-byte stores.  d: {first token, tokens, ..} of the tile.
+__device__ __forceinline__ void la_store_rows(const LaParams &p, const int4 &d, int group, int r4, int m, int dim,
+                                              const float (&y)[4]) {
+    const bool odd = dim & 1;
+    const int heads_here = min(p.hpt, p.heads - group * p.hpt);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? y[e] : y[e + 1], 1);
+        const int row = r4 * 4 + e + (odd ? 1 : 0), tok = row / p.hpt, h = row - tok * p.hpt;
+        if (row < d.y * p.hpt && h < heads_here)
+            *reinterpret_cast<uint32_t *>(p.out +
+                                          (static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent +
+                                          m * 128 + (dim & ~1)) =
+                odd ? pack_bf16x2(got, y[e + 1]) : pack_bf16x2(y[e], got);
+    }
+}
+
+// f v, where a piece's factor is 0 whatever its sums hold is not used
+__device__ __forceinline__ float la_weigh(float f, float v) { return f == 0.f ? 0.f : f * v; }
+
+// 128 dims of a piece of the rows that a tile can have: at most 32 KiB
+__host__ __device__ __forceinline__ uint32_t la_merge_bytes(const LaParams &p) {
+    return static_cast<uint32_t>((p.hpt * p.tpt + 3) / 4) * 2048;
+}
+constexpr uint32_t kLaMergeExtra = 2 * kLaRows * 4 + 16;     // factors, barriers
+constexpr uint32_t kLaMergeMost = 2 * kLaRows * 128 * 4 + kLaMergeExtra;
+
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LaParams p, int ctas) {
+    pdl_trigger();                        // a following call may start looking at its lengths
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t bytes = la_merge_bytes(p);
+    float *factor = reinterpret_cast<float *>(smem_raw + 2 * bytes);                  // [2][64]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(factor + 2 * kLaRows);
+    if (threadIdx.x < 2) mbar_init(&bars[threadIdx.x], 1);
+    fence_barrier_init();
+    __syncthreads();
+    pdl_wait();
+    const int cta = blockIdx.x, m = blockIdx.y, dim = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const int group = cta % p.groups, row = threadIdx.x;     // (of the first 64 threads)
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl);
+    auto part_of = [&](int i) { return static_cast<int64_t>(min(cta + i * p.groups, ctas - 1)) * 2 + (i == 0 ? 1 : 0); };
+    auto load = [&](int i, int b) {                          // (one thread)
+        mbar_arrive_expect_tx(&bars[b], bytes);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(smem_raw + b * bytes)),
+                     "l"(reinterpret_cast<const float *>(p.ws + kLaWsO) + part_of(i) * kLaPartFloats + m * kLaRows * 128),
+                     "r"(bytes), "r"(smem_u32(&bars[b]))
+                     : "memory");
+    };
+    if (threadIdx.x == 0) load(0, 0), load(1, 1);
+    float m0 = NEG_INF, l0 = 0.f, m1 = NEG_INF, l1 = 0.f;
+    if (row < kLaRows) {
+        const float *a = ml + part_of(0) * 2 * kLaRows + row, *b = ml + part_of(1) * 2 * kLaRows + row;
+        m0 = a[0], l0 = a[kLaRows], m1 = b[0], l1 = b[kLaRows];
+    }
+    const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
+    la_collect_status(p, ctas);
+    const int pieces = d.z, rows = d.y * p.hpt;
+    if (pieces < 2) {                                        // the loads land before the CTA ends
+        if (threadIdx.x == 0) mbar_wait_bounded(&bars[0], 0), mbar_wait_bounded(&bars[1], 0);
+        return;
+    }
+    float M = fmaxf(m0, m1), inv = 0.f;
+    if (row < kLaRows) {
+        for (int i = 2; i < pieces; ++i) M = fmaxf(M, ml[part_of(i) * 2 * kLaRows + row]);
+        const float w0 = m0 == NEG_INF ? 0.f : fast_exp2(m0 - M), w1 = m1 == NEG_INF ? 0.f : fast_exp2(m1 - M);
+        float L = la_weigh(w0, l0) + la_weigh(w1, l1);
+        for (int i = 2; i < pieces; ++i) {
+            const float mi = ml[part_of(i) * 2 * kLaRows + row];
+            L += la_weigh(mi == NEG_INF ? 0.f : fast_exp2(mi - M), ml[part_of(i) * 2 * kLaRows + kLaRows + row]);
+        }
+        inv = L > 0.f ? 1.f / L : 0.f;
+        factor[row] = w0 * inv;
+        factor[kLaRows + row] = w1 * inv;
+    }
+    // (the factors are there too; and every thread takes the same way)
+    bool ok = __syncthreads_and(mbar_wait_bounded(&bars[0], 0) && mbar_wait_bounded(&bars[1], 0));
+    float4 acc[8];                                           // rows 32 half + 4 q ..
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int r4 = half * 8 + q;
+        if (r4 * 4 >= rows) break;
+        const float4 a = *reinterpret_cast<const float4 *>(smem_raw + (r4 * 128 + dim) * 16);
+        const float4 b = *reinterpret_cast<const float4 *>(smem_raw + bytes + (r4 * 128 + dim) * 16);
+        const float4 f = *reinterpret_cast<const float4 *>(factor + r4 * 4);
+        const float4 g = *reinterpret_cast<const float4 *>(factor + kLaRows + r4 * 4);
+        acc[q] = make_float4(la_weigh(f.x, a.x) + la_weigh(g.x, b.x), la_weigh(f.y, a.y) + la_weigh(g.y, b.y),
+                             la_weigh(f.z, a.z) + la_weigh(g.z, b.z), la_weigh(f.w, a.w) + la_weigh(g.w, b.w));
+    }
+#pragma unroll 1
+    for (int i = 2; i < pieces && ok; ++i) {                 // further pieces, one after another
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            fence_proxy_async_smem();
+            load(i, 0);
+        }
+        if (row < kLaRows) {
+            const float mi = ml[part_of(i) * 2 * kLaRows + row];
+            factor[row] = mi == NEG_INF ? 0.f : fast_exp2(mi - M) * inv;
+        }
+        ok = __syncthreads_and(mbar_wait_bounded(&bars[0], (i - 1) & 1));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r4 = half * 8 + q;
+            if (r4 * 4 >= rows) break;
+            const float4 a = *reinterpret_cast<const float4 *>(smem_raw + (r4 * 128 + dim) * 16);
+            const float4 f = *reinterpret_cast<const float4 *>(factor + r4 * 4);
+            acc[q].x += la_weigh(f.x, a.x), acc[q].y += la_weigh(f.y, a.y);
+            acc[q].z += la_weigh(f.z, a.z), acc[q].w += la_weigh(f.w, a.w);
+        }
+    }
+    if (!ok) {
+        set_status(reinterpret_cast<int32_t *>(p.ws), PKV_ERR_DEVICE_TIMEOUT);
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int r4 = half * 8 + q;
+        if (r4 * 4 >= rows) break;
+        const float y[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
+        la_store_rows(p, d, group, r4, m, dim, y);
+    }
+}
+
 constexpr int kLaMany = 8;                    // pieces from which a tile is shared out
 
-template <bool kShare>
-__global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, int ctas) {
-    pdl_trigger();                        // a following call may start looking at its lengths
+// blockIdx.y: 128 dims x 16 rows; a thread takes one dim of eight rows.
+__global__ void __launch_bounds__(256) latent_merge_few_kernel(const LaParams p, int ctas) {
+    pdl_trigger();
     pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
-        int32_t s = 0;
-        for (int c = threadIdx.x; c < ctas; c += 32) {
-            const int32_t x = reinterpret_cast<const int32_t *>(p.ws + kLaWsStatus)[c];
-            s = s ? s : x;
-        }
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int32_t y = __shfl_down_sync(0xffffffffu, s, m);
-            s = s ? s : y;
-        }
-        if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = s;
-    }
+    la_collect_status(p, ctas);
     constexpr int kQ = 2;                                             // groups of four rows a thread
-    const int cta = blockIdx.x;
+    const int cta = blockIdx.x, group = cta % p.groups;
     const int m = blockIdx.y >> 2, dim = threadIdx.x & 127, half = threadIdx.x >> 7;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const float *ml = reinterpret_cast<const float *>(p.ws + kLaWsMl);
     const float *o = reinterpret_cast<const float *>(p.ws + kLaWsO) + dim * 4;
-    const int group = cta % p.groups, heads_here = min(p.hpt, p.heads - group * p.hpt);
-    const bool odd = threadIdx.x & 1;
-    // four rows (4 r4 ..) of this thread's dim: neighbouring lanes exchange a row each, 4-byte stores
-    auto store = [&](const int4 &d, int r4, const float (&y)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[e] : y[e + 1], 1);
-            const int row = r4 * 4 + e + (odd ? 1 : 0), tok = row / p.hpt, h = row - tok * p.hpt;
-            if (row < d.y * p.hpt && h < heads_here)
-                *reinterpret_cast<uint32_t *>(
-                    p.out + (static_cast<int64_t>(d.x + tok) * p.heads + group * p.hpt + h) * kLatent + m * 128 +
-                    (dim & ~1)) = odd ? pack_bf16x2(got, y[e + 1]) : pack_bf16x2(y[e], got);
-        }
-    };
-
     const int4 d = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc)[cta];
     const int4 d0 = reinterpret_cast<const int4 *>(p.ws + kLaWsDesc0)[cta];
     {
@@ -1075,13 +1190,13 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
         auto join = [&](float &m0, float &l0, float &a0, float m1, float l1, float a1) {
             const float M = fmaxf(m0, m1);
             const float w0 = m0 == NEG_INF ? 0.f : fast_exp2(m0 - M), w1 = m1 == NEG_INF ? 0.f : fast_exp2(m1 - M);
-            l0 = (w0 == 0.f ? 0.f : w0 * l0) + (w1 == 0.f ? 0.f : w1 * l1);
-            a0 = (w0 == 0.f ? 0.f : w0 * a0) + (w1 == 0.f ? 0.f : w1 * a1);
+            l0 = la_weigh(w0, l0) + la_weigh(w1, l1);
+            a0 = la_weigh(w0, a0) + la_weigh(w1, a1);
             m0 = M;
         };
         load(static_cast<int64_t>(cta) * 2 + 1, mx, ls, acc);
         load(static_cast<int64_t>(min(cta + p.groups, ctas - 1)) * 2, m1, l1, a1);
-        if (d.z >= 2 && (!kShare || d.z < kLaMany) && r4 * 4 < d.y * p.hpt) {      // (whole warps)
+        if (d.z >= 2 && d.z < kLaMany && r4 * 4 < d.y * p.hpt) {      // (whole warps)
 #pragma unroll 1
             for (int i = 1;;) {
 #pragma unroll
@@ -1100,12 +1215,11 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = l[e] > 0.f ? v[e] / l[e] : 0.f;
-                store(d, r4 + q, y);
+                la_store_rows(p, d, group, r4 + q, m, dim, y);
             }
         }
     }
 
-    if constexpr (!kShare) return;
     __shared__ float4 factor[kLaMaxCtas];                             // of a piece, for four rows
     __shared__ float4 other[128];
     auto many = [&](const int4 &d) {
@@ -1137,17 +1251,15 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LaParams p, i
         for (int i = half; i < pieces; i += 2) {
             const float4 v = *reinterpret_cast<const float4 *>(o + part_of(i) * kLaPartFloats + (m * 16 + r4) * 512);
             const float4 f = factor[i];
-            y[0] = fmaf(f.x, f.x == 0.f ? 0.f : v.x, y[0]);
-            y[1] = fmaf(f.y, f.y == 0.f ? 0.f : v.y, y[1]);
-            y[2] = fmaf(f.z, f.z == 0.f ? 0.f : v.z, y[2]);
-            y[3] = fmaf(f.w, f.w == 0.f ? 0.f : v.w, y[3]);
+            y[0] += la_weigh(f.x, v.x), y[1] += la_weigh(f.y, v.y);
+            y[2] += la_weigh(f.z, v.z), y[3] += la_weigh(f.w, v.w);
         }
         if (half) other[dim] = make_float4(y[0], y[1], y[2], y[3]);
         __syncthreads();
         if (!half) {
             const float4 v = other[dim];
             y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
-            store(d, r4, y);
+            la_store_rows(p, d, group, r4, m, dim, y);
         }
         __syncthreads();                                              // (the other tile's turn)
     };
@@ -1284,7 +1396,9 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
         const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
         if (!bit || !(done_mask & bit)) {
             if (cudaFuncSetAttribute(latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaSmem) !=
-                cudaSuccess)
+                    cudaSuccess ||
+                cudaFuncSetAttribute(latent_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaMergeMost) !=
+                    cudaSuccess)
                 return PKV_ERR_CUDA;
             done_mask |= bit;
         }
@@ -1292,10 +1406,14 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
                    static_cast<cudaStream_t>(stream), am, bm, qm, om, p) != cudaSuccess)
         return PKV_ERR_CUDA;
-    // a tile can have many pieces only where the row tiles are few
-    if (launch_pdl(most <= p.lanes / 4 ? latent_combine_kernel<true> : latent_combine_kernel<false>,
-                   dim3(static_cast<unsigned>(ctas), kLaCombineY), dim3(256), 0, static_cast<cudaStream_t>(stream), p,
-                   ctas) != cudaSuccess)
+    // a tile can have many pieces only where the row tiles are few; and of few rows there
+    // is little to bring in in bulk
+    const bool bulk = most > p.lanes / 4 && p.hpt * p.tpt > 32;
+    const dim3 lanes(static_cast<unsigned>(ctas), bulk ? 4 : 16);
+    if ((bulk ? launch_pdl(latent_merge_kernel, lanes, dim3(256), 2 * la_merge_bytes(p) + kLaMergeExtra,
+                           static_cast<cudaStream_t>(stream), p, ctas)
+              : launch_pdl(latent_merge_few_kernel, lanes, dim3(256), 0, static_cast<cudaStream_t>(stream), p, ctas)) !=
+        cudaSuccess)
         return PKV_ERR_CUDA;
     return PKV_OK;
 }
