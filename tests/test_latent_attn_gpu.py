@@ -232,3 +232,69 @@ def test_write_then_attend_captured_in_a_graph():
         torch.cuda.synchronize()
         refresh()
         b.check()
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_batches_twice(seed):
+    """Batches drawn over the range of heads, lengths and chunks: within the bound, and the same bits again from a
+    workspace full of something else."""
+    g = torch.Generator().manual_seed(100 + seed)
+
+    def draw(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+    H = (1, 3, 8, 16, 24, 32, 64, 72, 128)[draw(0, 8)]
+    reqs = []
+    for _ in range(draw(1, 40)):
+        n = draw(1, (80, 700, 2500)[draw(0, 2)])
+        q = min(n, (1, 1, 1, draw(1, 5), draw(1, 90))[draw(0, 4)]) if H <= 32 else min(n, (1, 1, draw(1, 3))[draw(0, 2)])
+        reqs.append((q, n))
+    b = Batch(seed, reqs, H, extra_rows=draw(0, 3))
+    first = b.run().clone()
+    assert pkv.workspace_status(b.ws) == 0
+    b.check()
+    b.ws.random_(0, 256)
+    b.out.fill_(7.0)
+    assert torch.equal(b.run(), first)
+    assert pkv.workspace_status(b.ws) == 0
+
+
+def test_pages_past_four_gigabytes():
+    b = Batch(5, [(1, 300), (1, 17)], 16)
+    nb, used = 260_000, b.cache.shape[0]                       # 4.8 GB
+    far = torch.empty(nb, 16, D, dtype=torch.bfloat16, device="cuda")
+    far[nb - used:] = b.cache
+    b.cache = far
+    b.bt = torch.where(b.bt < used, b.bt + (nb - used), b.bt)
+    b.run()
+    assert pkv.workspace_status(b.ws) == 0
+    b.check()
+    # the same rows gathered
+    starts = torch.tensor([0, 300, 317], dtype=torch.int32, device="cuda")
+    out = torch.empty(317, D, dtype=torch.bfloat16, device="cuda")
+    pkv.latent_gather(out, b.cache, b.bt, b.lens, starts, 300)
+    assert torch.equal(out.double().cpu(), torch.cat(b.rows))
+
+
+def test_no_tokens_at_all():
+    b = Batch(1, [(1, 30)], 4)
+    empty = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pkv.latent_paged_attn(b.out[:0], b.query[:0], b.cache, b.bt, b.lens, empty, 1, 30, 1.0, b.ws)
+    assert pkv.workspace_status(b.ws) == 0
+    assert (b.out == 7.0).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    bs = [Batch(30 + i, [(1, 900), (1, 64), (40, 200)], 16) for i in range(2)]
+    want = []
+    for b in bs:
+        want.append(b.run().clone())
+        b.check()
+        b.out.fill_(7.0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in bs]
+    for _ in range(10):
+        for b, s in zip(bs, streams):
+            b.run(stream=s)
+    torch.cuda.synchronize()
+    for b, w in zip(bs, want):
+        assert torch.equal(b.out, w)

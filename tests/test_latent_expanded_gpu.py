@@ -192,3 +192,31 @@ def test_a_chunk_through_both_forms():
     lat_mag = torch.einsum("hqn,nc->qhc", p, c[:, :512].abs())
     bound_a = torch.einsum("qhc,hcd->qhd", lat_mag * (ds_a.exp() - 1 + 2 * BF16_HALF_STEP * 1.02), up)
     assert ((absorbed - ref).abs() <= bound_a).all()
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_batches_twice(seed):
+    g = torch.Generator().manual_seed(50 + seed)
+
+    def draw(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+    reqs = []
+    for _ in range(draw(1, 12)):
+        q = draw(0, (3, 130, 600)[draw(0, 2)])
+        reqs.append((q, q + draw(0, (1, 140, 900)[draw(0, 2)])))
+    if not any(q for q, _ in reqs):
+        reqs.append((5, 9))
+    b = Ragged(seed, reqs, (1, 2, 7, 16)[draw(0, 3)], head_major=bool(draw(0, 1)))
+    first = b.run().clone()
+    assert int(b.status.item()) == 0
+    b.check()
+    b.out.fill_(7.0)
+    assert torch.equal(b.run(), first)
+
+
+def test_heads_one_after_another():
+    """Keys and values past 64 MB: the token tiles of a head run side by side."""
+    b = Ragged(2, [(600, 4200), (300, 5000)], 16)
+    assert b.K * b.H * 512 > 64 << 20
+    b.run()
+    b.check()

@@ -299,3 +299,60 @@ def test_writes_captured_and_replayed_on_another_stream():
     torch.cuda.synchronize()
     for x, y in zip((out, cache, lat, n["rows"]), want):
         assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def test_slots_past_four_gigabytes():
+    blocks = 140_000                                              # 4.6 GB of K/V, 2.6 GB of latent rows
+    c = qk_case(4, 9, 4, 4, 128, 128)
+    n = latent_case(4, 9, 0)
+    slots = torch.arange(blocks * 16 - 9, blocks * 16, device="cuda")
+    cache = torch.empty(blocks, 4, 2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    out = poisoned(9, 4, 128)
+    pkv.qk_norm_rope_kv_write(out, cache, c["q"], c["k"], c["v"], c["wq"], c["wk"], 1e-6, c["table"], c["pos"], slots)
+    check_rounded(cache[-1, :, 0, 7:].transpose(0, 1), *norm_rotate(c["k"], c["wk"], 1e-6, c["table"], c["pos"], False),
+                  "key")
+    assert torch.equal(cache[-1, :, 1, 7:].transpose(0, 1).contiguous().view(torch.int16),
+                       c["v"].contiguous().view(torch.int16))
+    del cache
+    lat = torch.empty(240_000, 16, 576, dtype=torch.bfloat16, device="cuda")           # 4.4 GB
+    slots = torch.arange(240_000 * 16 - 9, 240_000 * 16, device="cuda")
+    pkv.latent_kv_write(lat, n["c"], n["kr"], None, 0.0, n["table"], n["pos"], slots)
+    assert torch.equal(lat[-1, 7:, :512].view(torch.int16), n["c"].contiguous().view(torch.int16))
+
+
+def test_no_tokens():
+    c = qk_case(4, 3, 4, 4, 64, 64)
+    cache = poisoned(c["blocks"], 4, 2, 16, 64)
+    e = slice(0, 0)
+    pkv.qk_norm_rope_kv_write(c["q"][e], cache, c["q"][e], c["k"][e], c["v"][e], c["wq"], c["wk"], 1e-6, c["table"],
+                              c["pos"][e], c["slots"][e])
+    n = latent_case(4, 3, 2)
+    lat = poisoned(n["blocks"], 16, 576)
+    pkv.latent_kv_write(lat, n["c"][e], n["kr"][e], None, 0.0, n["table"], n["pos"][e], n["slots"][e])
+    assert torch.isnan(cache.float()).all() and torch.isnan(lat.float()).all()
+
+
+def test_refused_forms_on_the_gpu():
+    c = qk_case(4, 3, 4, 4, 64, 64)
+    cache = poisoned(c["blocks"], 4, 2, 16, 64)
+    good = [c["q"].clone(), cache, c["q"], c["k"], c["v"], c["wq"], c["wk"], 1e-6, c["table"], c["pos"], c["slots"]]
+    pkv.qk_norm_rope_kv_write(*good)
+    for i, bad in ((0, good[0].float()), (1, cache.float()), (2, c["q"][:, :, ::2]), (3, c["k"][:2]), (5, c["wq"][:32]),
+                   (8, c["table"].double()), (9, c["pos"].int()), (10, c["slots"].cpu()), (10, c["slots"][:2])):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            pkv.qk_norm_rope_kv_write(*args)
+    with pytest.raises(pkv.PagedKVError):                          # the C call's own refusal: rotary_dim 24
+        args = list(good)
+        args[8] = torch.zeros(8, 24, device="cuda")
+        pkv.qk_norm_rope_kv_write(*args)
+    n = latent_case(4, 3, 2)
+    lat = poisoned(n["blocks"], 16, 576)
+    ok = dict(latent_cache=lat, latent=n["c"], key_rope=n["kr"], weight=n["w"], eps=1e-6, cos_sin=n["table"],
+              positions=n["pos"], slot_mapping=n["slots"])
+    pkv.latent_kv_write(**ok)
+    for k, bad in (("latent", n["c"][:, :500]), ("latent_cache", lat[:, :, :512]), ("weight", n["w"].float()),
+                   ("query_rope", n["q"][:, :, 128:]), ("cos_sin", n["table"][:, :32]), ("key_rope", n["kr"].t())):
+        with pytest.raises(ValueError):
+            pkv.latent_kv_write(**dict(ok, **{k: bad}))
