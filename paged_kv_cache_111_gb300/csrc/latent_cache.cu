@@ -38,15 +38,17 @@ struct LatentWriteParams {
 };
 
 constexpr int kRopeRows = 16;                      // query heads per warp
+constexpr int kWriteThreads = 128;
 
 template <bool INTER>
-__global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const LatentWriteParams p) {
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t = item / p.warps_per_token;
-    if (t >= p.num_tokens) return;                 // whole warps
-    const int part = static_cast<int>(item - t * p.warps_per_token);
+    const uint32_t item = blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5);     // below 2^31
+    const uint32_t token = item / static_cast<uint32_t>(p.warps_per_token);
+    if (token >= static_cast<uint32_t>(p.num_tokens)) return;                         // whole warps
+    const int part = static_cast<int>(item - token * p.warps_per_token);
+    const int64_t t = token;
     const int e0 = (lane & 7) * 8;
     const int64_t pos = __ldg(p.positions + t);
     const bool bad_pos = pos < 0 || pos >= p.max_position;
@@ -222,10 +224,11 @@ extern "C" int pkv_latent_kv_write(void *latent_cache, int64_t num_blocks, int32
     p.num_tokens = num_tokens, p.heads = num_heads;
     p.warps_per_token = 1 + (num_heads + kRopeRows - 1) / kRopeRows;
     p.status = device_status;
-    const int64_t blocks = (static_cast<int64_t>(num_tokens) * p.warps_per_token + 7) / 8;
-    if (blocks > INT32_MAX) return PKV_ERR_SHAPE;
+    const int64_t warps = static_cast<int64_t>(num_tokens) * p.warps_per_token;
+    if (warps > INT32_MAX - kWriteThreads) return PKV_ERR_SHAPE;
+    const int64_t blocks = (warps + kWriteThreads / 32 - 1) / (kWriteThreads / 32);
     (interleaved ? latent_write_kernel<true> : latent_write_kernel<false>)<<<
-        static_cast<unsigned>(blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        static_cast<unsigned>(blocks), kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

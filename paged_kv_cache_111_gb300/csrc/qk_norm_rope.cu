@@ -50,10 +50,11 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams
     constexpr int kLanes = HD / 8;            // lanes of a row
     constexpr int kGroups = 32 / kLanes;      // rows side by side in a warp
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t = item / p.chunks;
-    if (t >= p.num_tokens) return;            // whole warps
-    int chunk = static_cast<int>(item - t * p.chunks);
+    const uint32_t item = blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);     // below 2^31
+    const uint32_t token = item / static_cast<uint32_t>(p.chunks);
+    if (token >= static_cast<uint32_t>(p.num_tokens)) return;                      // whole warps
+    int chunk = static_cast<int>(item - token * p.chunks);
+    const int64_t t = token;
     const int64_t pos = __ldg(p.positions + t), slot = __ldg(p.slots + t);
     // query, key or value rows
     const int kind = chunk < p.q_chunks ? 0 : (chunk < p.q_chunks + p.kv_chunks ? 1 : 2);
@@ -247,7 +248,7 @@ static int qk_norm_rope(bool fp8, void *query_out, int64_t out_stride, void *kv_
     p.status = device_status;
     const int64_t warps = static_cast<int64_t>(num_tokens) * p.chunks;
     const int64_t blocks = (warps + kQkThreads / 32 - 1) / (kQkThreads / 32);
-    if (blocks > INT32_MAX) return PKV_ERR_SHAPE;
+    if (warps > INT32_MAX - kQkThreads) return PKV_ERR_SHAPE;
     void (*kernel)(QkParams);
     const bool it = interleaved != 0;
     if (head_size == 128)
