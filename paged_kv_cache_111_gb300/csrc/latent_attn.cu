@@ -1375,8 +1375,10 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     p.lanes = (sms < kLaMaxCtas ? sms : kLaMaxCtas) / p.groups;
     // no more lanes than the bounds leave units for
     const int64_t most = static_cast<int64_t>(num_seqs) * ((max_query_len + p.tpt - 1) / p.tpt);     // row tiles
-    const int64_t units = most * ((max_seq_len + kLaKeys - 1) / kLaKeys + kLaExtra);
-    if (units < p.lanes) p.lanes = units > 1 ? static_cast<int32_t>(units) : 1;
+    if (most < p.lanes) {                          // (the product of loose bounds can pass 64 bits)
+        const int64_t units = most * ((max_seq_len + kLaKeys - 1) / kLaKeys + kLaExtra);
+        if (units < p.lanes) p.lanes = units > 1 ? static_cast<int32_t>(units) : 1;
+    }
     const int ctas = p.lanes * p.groups;
     CUtensorMap am, bm, qm, om;
     int rc = make_latent_map(&am, latent_cache, num_blocks, kLaChunksA);

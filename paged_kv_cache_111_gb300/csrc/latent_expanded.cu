@@ -137,15 +137,24 @@ __global__ void __launch_bounds__(kExThreads, 1)
     if (blockIdx.x == 0)
         for (int r = threadIdx.x; r < p.num_seqs; r += kExThreads)
             if (!request(r).ok) set_status(status, PKV_ERR_DEVICE_METADATA);
+    // A CTA without a tile waits for the kernel before this one all the same: in a call where
+    // none has one, this grid would otherwise be over before that kernel, and a kernel that
+    // waits for this grid would take that one's writes for complete.
     int r = 0, t0 = 0;                                  // request; first token, within it
     if (p.num_seqs == 1) {
         const ExReq a = ex_request(p, 0);
         const int n = a.ok ? (a.q + kExTokens - 1) / kExTokens : 0;
-        if (rank >= n) return;                          // the bound was not reached: uniform
+        if (rank >= n) {                                // the bound was not reached: uniform
+            pdl_wait();
+            return;
+        }
         t0 = (n - 1 - rank) * kExTokens;
     } else {
         const int all = count(1);
-        if (rank >= all) return;
+        if (rank >= all) {
+            pdl_wait();
+            return;
+        }
         // the key tiles of this rank's token tile: the largest w with more than `rank`
         // tiles from w on
         int lo = 1, hi = (p.max_key_len + kExKeys - 1) / kExKeys, above = 0;

@@ -220,3 +220,41 @@ def test_heads_one_after_another():
     assert b.K * b.H * 512 > 64 << 20
     b.run()
     b.check()
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_a_call_without_a_query_keeps_the_order_around_it(S):
+    """A cache write, then a call in which no request has a query, then attention over what was written: each may
+    start before the one in front has ended, so the call in between has to outlast the write."""
+    g = torch.Generator().manual_seed(3)
+    n, H, Hkv, d = 8192, 8, 8, 128
+    blocks = n // 16
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = randn(n, H, d), randn(n, Hkv, d), randn(n, Hkv, d)
+    table = angles(d, n).cuda()
+    at = torch.arange(n, device="cuda")
+    bt = torch.arange(blocks, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    slots = bt[0].long()[at // 16] * 16 + at % 16
+    lens, qsl = torch.tensor([n], dtype=torch.int32).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda()
+    ws = torch.empty(pkv.paged_attn_workspace_size(1, 1, 1, n, H, Hkv, d), dtype=torch.uint8, device="cuda")
+    c = Ragged(4, [(1, 1)] * S, 2)
+    c.qsl.zero_()
+
+    def step(between):
+        cache = torch.zeros(blocks, Hkv, 2, 16, d, dtype=torch.bfloat16, device="cuda")
+        q_out, out = torch.empty_like(q), torch.empty(1, H, d, dtype=torch.bfloat16, device="cuda")
+        last = q_out[n - 1:]
+        torch.cuda.synchronize()
+        pkv.qk_norm_rope_kv_write(q_out, cache, q, k, v, None, None, 1e-6, table, at, slots)
+        if between:
+            c.run()
+        pkv.paged_attn(out, last, cache, bt, lens, qsl, 1, n, d ** -0.5, ws)
+        pkv.paged_attn_combine(out, ws)
+        torch.cuda.synchronize()
+        return out
+    want = step(False)
+    for _ in range(20):
+        assert torch.equal(step(True), want)
+    assert (c.out == 7.0).all() and int(c.status) == 0
