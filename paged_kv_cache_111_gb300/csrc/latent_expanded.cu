@@ -70,6 +70,7 @@ struct ExParams {
     int32_t num_seqs, num_tokens, num_keys, max_query_len, max_key_len, heads;
     int32_t tiles;            // upper bound of the CTAs' token tiles over all requests
     int32_t by_head;          // order of the CTAs: all token tiles of one head, then the next
+    int32_t split;            // CTAs (a cluster) that share the keys of a token tile: 1, 2 or 4
     float scale_log2;
     int32_t *status;
 };
@@ -89,6 +90,84 @@ __device__ __forceinline__ ExReq ex_request(const ExParams &p, int r) {
     return a;
 }
 
+// Where the keys of a token tile are shared out over a cluster: partial sums on their way
+// between its CTAs, over Q and the ring, as [CTA][group][dim / 4][row][dim % 4] of 32 rows a
+// group, and behind them the rows' {reference, sum}.
+constexpr uint32_t kExGroupBytes = 32 * kExV * 4;
+constexpr uint32_t kExOffState = 8 * kExGroupBytes;
+constexpr uint32_t kExOffStage = kExOffState + 2048;     // finished rows, 32 x 64 dims a warp
+static_assert(8 * 32 * 8 <= 2048 && kExOffStage + 8 * 4096 <= kExOffBar, "the partial sums' place");
+
+// Every thread of the cluster's CTAs comes here.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The address of this CTA's shared memory word `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// A warp's 32 finished rows of P 16-byte pieces on their way out: from the lanes, a row each,
+// into shared memory, and from there in whole rows.  (Stored by the lanes, 16 bytes to 32
+// rows at a time, 8192 keys of 128 heads took 734 us instead of 711.)
+template <int P>
+__device__ __forceinline__ void ex_stage(uint8_t *stage, int lane, int piece, const float (&y)[8], float inv) {
+    *reinterpret_cast<uint4 *>(stage + lane * (16 * P) + ((piece ^ (lane & 7 & (P - 1))) << 4)) =
+        make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv),
+                   pack_bf16x2(y[4] * inv, y[5] * inv), pack_bf16x2(y[6] * inv, y[7] * inv));
+}
+template <int P>
+__device__ __forceinline__ void ex_store(const uint8_t *stage, int lane, int rows, __nv_bfloat16 *out, int64_t stride) {
+    __syncwarp();
+    const int piece = lane % P;
+#pragma unroll 4
+    for (int r = lane / P; r < rows; r += 32 / P)
+        *reinterpret_cast<uint4 *>(out + r * stride + piece * 8) =
+            *reinterpret_cast<const uint4 *>(stage + r * (16 * P) + ((piece ^ (r & 7 & (P - 1))) << 4));
+}
+
+// One row a lane, 128 / C dims a warp (loops kept short: this runs once, from a cold
+// instruction cache): out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the cluster's C
+// CTAs.  A state that saw no key has m = -inf, and whatever its sums hold is not used.
+template <int C>
+__device__ __forceinline__ void ex_join(const uint8_t *smem, int group, int d0, int lane, uint8_t *stage) {
+    constexpr int kPer = 8 / C, kPieces = kExV / C / 8;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    float f[C], M = NEG_INF, L = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        f[c] = *reinterpret_cast<const float *>(smem + kExOffState + ((c * kPer + group) * 32 + lane) * 8);
+        M = fmaxf(M, f[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        f[c] = f[c] == NEG_INF ? 0.f : fast_exp2(f[c] - M);
+        if (f[c] != 0.f)
+            L += f[c] * *reinterpret_cast<const float *>(smem + kExOffState + ((c * kPer + group) * 32 + lane) * 8 + 4);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll 1
+    for (int d = 0; d < kPieces; ++d) {
+        float y[8] = {};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint8_t *at = smem + (c * kPer + group) * kExGroupBytes + (d0 / 4 + 2 * d) * 512 + lane * 16;
+            const float4 a = *reinterpret_cast<const float4 *>(at), b = *reinterpret_cast<const float4 *>(at + 512);
+            if (f[c] != 0.f) {
+                y[0] = fmaf(f[c], a.x, y[0]), y[1] = fmaf(f[c], a.y, y[1]);
+                y[2] = fmaf(f[c], a.z, y[2]), y[3] = fmaf(f[c], a.w, y[3]);
+                y[4] = fmaf(f[c], b.x, y[4]), y[5] = fmaf(f[c], b.y, y[5]);
+                y[6] = fmaf(f[c], b.z, y[6]), y[7] = fmaf(f[c], b.w, y[7]);
+            }
+        }
+        ex_stage<kPieces>(stage, lane, d, y, inv);
+    }
+}
+
 __global__ void __launch_bounds__(kExThreads, 1)
     latent_expanded_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                            const __grid_constant__ CUtensorMap r_map, const __grid_constant__ CUtensorMap v_map,
@@ -103,8 +182,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
     // Token tiles (256 tokens of a request) are ranked by the key tiles they see, the
     // most first, so that the longest are not the last to end; a CTA takes one rank of
     // one head, all heads of a rank or all ranks of a head after one another.
-    const int head = p.by_head ? blockIdx.x / p.tiles : blockIdx.x % p.heads;
-    const int rank = p.by_head ? blockIdx.x % p.tiles : blockIdx.x / p.heads;
+    const int part = blockIdx.x % p.split, item = blockIdx.x / p.split;
+    const int head = p.by_head ? item / p.tiles : item % p.heads;
+    const int rank = p.by_head ? item % p.tiles : item / p.heads;
     int32_t *status = p.status;
 
     pdl_trigger();
@@ -203,11 +283,16 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const int ctx = req.L - req.q;
     // rows and key tiles of the two row tiles
     const int rows[2] = {min(kExRows, req.q - t0), max(0, min(kExRows, req.q - t0 - kExRows))};
-    const int n[2] = {(ctx + t0 + rows[0] + kExKeys - 1) / kExKeys,
-                      rows[1] ? (ctx + t0 + kExRows + rows[1] + kExKeys - 1) / kExKeys : 0};
-    const int n_all = max(n[0], n[1]);
+    const int seen[2] = {(ctx + t0 + rows[0] + kExKeys - 1) / kExKeys,
+                         rows[1] ? (ctx + t0 + kExRows + rows[1] + kExKeys - 1) / kExKeys : 0};
+    const int seen_all = max(seen[0], seen[1]);
+    // of these, [j0, j1) are this CTA's, and counted from j0 from here on
+    const int j0 = static_cast<int>(static_cast<int64_t>(seen_all) * part / p.split);
+    const int j1 = static_cast<int>(static_cast<int64_t>(seen_all) * (part + 1) / p.split);
+    const int n[2] = {max(0, min(seen[0], j1) - j0), max(0, min(seen[1], j1) - j0)};
+    const int n_all = j1 - j0;                          // (the later row tile sees them all)
     const int end = ctx + t0 + rows[0] + rows[1];       // keys the last row sees
-    const bool fix = end % kExKeys != 0;
+    const bool fix = n_all > 0 && j1 == seen_all && end % kExKeys != 0;
 
     if (threadIdx.x < kExNumBars)
         mbar_init(&bars[threadIdx.x], threadIdx.x >= kExPFull && threadIdx.x < kExPFull + 2 ? 4 : 1);
@@ -229,7 +314,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         if (lane == 0) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (rows[i]) {
+                if (n[i]) {
                     mbar_arrive_expect_tx(&bars[kExQFull + i], kExQ);
                     for (int c = 0; c < 3; ++c)
                         tma_load_3d(smem + kExOffQ + i * kExQ + c * kExChunk, &q_map, &bars[kExQFull + i], c * 64, head,
@@ -237,7 +322,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
         }
         for (int j = 0; j < n_all && ok; ++j) {
-            const int key0 = req.ks + j * kExKeys;
+            const int key0 = req.ks + (j0 + j) * kExKeys;
 #pragma unroll 1
             for (int e = 0; e < kExPerTile && ok; ++e) {
                 const int s = j * kExPerTile + e, slot = s % kExSlots;
@@ -265,7 +350,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 const int s = (n_all - 1) * kExPerTile + e;
                 ok = __all_sync(0xffffffffu, pf_wait(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1, status));
             }
-            const int first = end - (n_all - 1) * kExKeys, s = (n_all - 1) * kExPerTile + 3;
+            const int first = end - (seen_all - 1) * kExKeys, s = (n_all - 1) * kExPerTile + 3;
             if (ok) {
                 for (int e = lane; e < (kExKeys - first) * 16; e += 32) {
                     const int r = first + (e >> 4);
@@ -280,7 +365,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         }
         if (!ok) {                                      // the copies in flight land before the CTA ends
             for (int i = 0; i < 2; ++i)
-                if (rows[i]) mbar_wait_bounded(&bars[kExQFull + i], 0);
+                if (n[i]) mbar_wait_bounded(&bars[kExQFull + i], 0);
             for (int s = max(0, issued - kExSlots); s < issued; ++s)
                 mbar_wait_bounded(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1);
         }
@@ -294,10 +379,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
             auto wait = [&](int b, uint32_t parity) { return pf_wait(&bars[b], parity, status); };
             const int n0 = n[0], n1 = n[1];
             const int frees = n1 ? 1 : 0;                                // the row tile that reads a slot last
-            int seen = 0;                                                // loads waited for
+            int landed = 0;                                              // loads waited for
             auto need = [&](int s) {
-                if (s < seen) return true;
-                seen = s + 1;
+                if (s < landed) return true;
+                landed = s + 1;
                 const bool there = wait(kExFull + s % kExSlots, (s / kExSlots) & 1);
                 tc_fence_after();
                 return there;
@@ -333,7 +418,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 umma_commit(&bars[kExODone + i]);
                 return true;
             };
-            bool ok = wait(kExQFull, 0) && issue_s(0, 0);
+            bool ok = true;
+            if (n0) ok = wait(kExQFull, 0) && issue_s(0, 0);
             if (ok && n1) ok = wait(kExQFull + 1, 0) && issue_s(1, 0);
             // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
             for (int j = 0; j < n_all && ok; ++j) {
@@ -382,7 +468,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kExKeys; ++c) s[c] = -s[c];
             }
-            const int key0 = j * kExKeys;
+            const int key0 = (j0 + j) * kExKeys;
             if (__any_sync(0xffffffffu, key0 + kExKeys > lim)) {
 #pragma unroll
                 for (int c = 0; c < kExKeys; ++c) s[c] = key0 + c < lim ? s[c] : NEG_INF;
@@ -451,27 +537,67 @@ __global__ void __launch_bounds__(kExThreads, 1)
             l += a + b;
         }
         if (ok && n_mine) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExODone + i], (n_mine - 1) & 1, status));
-        if (ok && n_mine) {
+        const int64_t stride = static_cast<int64_t>(p.heads) * kExV;
+        __nv_bfloat16 *o = p.out + static_cast<int64_t>(req.qs + t0) * stride + head * kExV;
+        if (p.split > 1) {
+            // 32 rows (a warp's) of the 256 are one of eight groups; 8 / split of them are
+            // finished in each CTA, by split warps a group, from the states and sums that
+            // every CTA leaves there.
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            __nv_bfloat16 *o = p.out + (static_cast<int64_t>(req.qs + t0 + i * kExRows + row) * p.heads + head) * kExV;
-#pragma unroll
+            if (!ok || !n_mine) m_ref = NEG_INF;
+            const int per = 8 / p.split, w = warp - 4;
+            cluster_sync();                             // no CTA's products read shared memory any more
+            const uint32_t to = cluster_address(sQ, w / per);
+            const uint32_t slot = part * per + w % per;
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + kExOffState + (slot * 32 + lane) * 8),
+                         "f"(m_ref), "f"(l)
+                         : "memory");
+            const uint32_t at = to + slot * kExGroupBytes + lane * 16;
+#pragma unroll 1
             for (int c = 0; c < kExV / 32; ++c) {
                 float v[32];
                 tmem_ld32f(tO + 32 * c, v);
                 tmem_ld_wait();
-                if (mine) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>(o + 32 * c + e) =
-                            make_uint4(pack_bf16x2(v[e] * inv, v[e + 1] * inv), pack_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
-                                       pack_bf16x2(v[e + 4] * inv, v[e + 5] * inv),
-                                       pack_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
+                for (int e = 0; e < 32; e += 4)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + (8 * c + e / 4) * 512),
+                                 "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]), "f"(v[e + 3])
+                                 : "memory");
+            }
+            cluster_sync();
+            const int g = w / p.split, dims = kExV / p.split, d0 = w % p.split * dims;
+            const int row0 = (part * per + g) * 32;
+            const int owned = min(32, (row0 < kExRows ? rows[0] : rows[1] + kExRows) - row0);
+            uint8_t *stage = smem + kExOffStage + w * 4096;
+            if (p.split == 2) {
+                ex_join<2>(smem, g, d0, lane, stage);
+                ex_store<8>(stage, lane, owned, o + row0 * stride + d0, stride);
+            } else {
+                ex_join<4>(smem, g, d0, lane, stage);
+                ex_store<4>(stage, lane, owned, o + row0 * stride + d0, stride);
+            }
+        } else if (ok && n_mine) {
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int owned = min(32, (i ? rows[1] : rows[0]) - quad * 32);
+            uint8_t *stage = smem + kExOffQ + i * kExQ + quad * 8192;      // over Q, which the last S has read
+#pragma unroll 1
+            for (int c = 0; c < kExV / 32; ++c) {
+                float v[32];
+                tmem_ld32f(tO + 32 * c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y[8] = {v[8 * e],     v[8 * e + 1], v[8 * e + 2], v[8 * e + 3],
+                                        v[8 * e + 4], v[8 * e + 5], v[8 * e + 6], v[8 * e + 7]};
+                    ex_stage<16>(stage, lane, 4 * c + e, y, inv);
                 }
             }
+            ex_store<16>(stage, lane, owned, o + (i * kExRows + quad * 32) * stride, stride);
         }
     }
 
+    if (p.split > 1 && warp < 4) cluster_sync(), cluster_sync();       // (with the softmax warps')
     tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -538,8 +664,8 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     p.num_seqs = num_seqs, p.num_tokens = num_tokens, p.num_keys = num_keys;
     p.max_query_len = max_query_len, p.max_key_len = max_key_len;
     p.heads = num_heads;
-    // sum of ceil(q_r / 256), at most one tile a request beyond the whole ones
-    const int64_t bound = num_tokens / kExTokens + static_cast<int64_t>(num_seqs);
+    // the most that sum of ceil(q_r / 256) can be
+    const int64_t bound = (num_tokens + static_cast<int64_t>(num_seqs) * (kExTokens - 1)) / kExTokens;
     const int64_t tiles = bound < num_tokens ? bound : num_tokens;
     if (tiles * num_heads > INT32_MAX) return PKV_ERR_SHAPE;
     p.tiles = static_cast<int32_t>(tiles);
@@ -569,8 +695,31 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
             done_mask |= bit;
         }
     }
-    if (launch_pdl(latent_expanded_kernel, dim3(static_cast<unsigned>(tiles * num_heads)), dim3(kExThreads), kExSmem,
-                   static_cast<cudaStream_t>(stream), qm, km, rm, vm, p) != cudaSuccess)
-        return PKV_ERR_CUDA;
+    // Few token tiles of many keys each leave SMs idle and wait for the longest.  Then the
+    // CTAs of a cluster share a tile's keys: as long as the CTAs were at most one an SM before
+    // they are doubled (a causal chunk's tiles see half of the longest's keys on average), and
+    // each keeps a key tile or more.  2048 tokens of 16 heads: SPLITA; 256 tokens at
+    // 8192 keys: SPLITB.  More CTAs than that pay each one's start and end, 6 us, instead
+    // (300 tokens to 2046 in three requests, 240 CTAs: 33 us whole, 51 us by two), and of
+    // clusters of eight only 15 find a place on the 152 SMs.
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
+    const int key_tiles = (max_key_len + kExKeys - 1) / kExKeys;
+    p.split = 1;
+    if (tiles * num_heads <= sms && key_tiles >= 2) p.split = 2;
+    if (tiles * num_heads * 4 <= sms && key_tiles >= 4) p.split = 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * num_heads * p.split));
+    cfg.blockDim = dim3(kExThreads);
+    cfg.dynamicSmemBytes = kExSmem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, latent_expanded_kernel, qm, km, rm, vm, p) != cudaSuccess) return PKV_ERR_CUDA;
     return PKV_OK;
 }

@@ -258,3 +258,43 @@ def test_a_call_without_a_query_keeps_the_order_around_it(S):
     for _ in range(20):
         assert torch.equal(step(True), want)
     assert (c.out == 7.0).all() and int(c.status) == 0
+
+
+@pytest.mark.parametrize("H,reqs,scale", [
+    (1, [(1, 5000)], None),                                 # one row, eight shares
+    (3, [(300, 2001)], None),
+    (2, [(7, 129), (256, 1100), (0, 40), (1, 1), (257, 257)], None),     # shares without a key
+    (16, [(129, 640), (40, 41), (513, 513)], None),
+    (40, [(2, 900), (128, 128)], None),
+    (5, [(33, 1500), (1, 1030)], -0.2),
+])
+def test_keys_shared_out_over_a_cluster(H, reqs, scale):
+    """Few rows and many keys: the shares' sums are joined, and the rows behind and between stay as they were."""
+    c = Ragged(21, reqs, H, gain=2.0)
+    if scale is not None:
+        c.scale = scale
+    first = c.run().clone()
+    c.check(f"{H} heads {reqs}")
+    assert int(c.status) == 0
+    assert torch.equal(c.run(), first)
+
+
+def test_scores_that_grow_from_share_to_share():
+    """The shares' references lie hundreds of powers of two apart; a share whose weights vanish adds nothing."""
+    for sign in (1.0, -1.0):
+        c = Ragged(22, [(5, 2048)], 2)
+        c.query[:5] = 1.0
+        steps = sign * torch.arange(2048, device="cuda") / 2048 * 40
+        c.key[:2048] = steps[:, None, None].to(torch.bfloat16)
+        c.rope[:2048] = 0
+        c.run()
+        c.check(f"sign {sign}")
+
+
+def test_a_bad_request_beside_a_shared_one():
+    c = Ragged(23, [(4, 1600), (9, 700)], 2)
+    c.qsl[1] = 2000                                         # past the bound, and the next one starts there
+    before = c.out.clone()
+    c.run()
+    assert int(c.status) != 0
+    assert torch.equal(c.out, before)
