@@ -31,7 +31,17 @@
 // Warp roles (384 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warp 2
 // owns tensor memory, warps 4-7 and 8-11 are the softmax and epilogue of the
 // two row tiles.  V rows past the last visible key are zeroed in shared memory
-// (they belong to other requests, or to nobody).  Every wait is bounded.
+// (they belong to other requests, or to nobody).  Every mbarrier wait is bounded.
+//
+// Where token tiles are few, the CTAs of a cluster share a tile's keys and join their
+// sums through distributed shared memory (the rule and its figures: at the launch).
+//
+// What bounds it: per key tile and CTA about 3470 cycles, of which the products take
+// 40 x 65 = 2600 on the tensor cores and their operands' way out of shared memory 2670
+// (128 bytes a cycle); the rest is the turn between the two row tiles.  2048 tokens at
+// 8192 keys of 128 heads (1.2 TFLOP): 790 us with cold caches, 1520 TFLOP/s, 78% of the
+// dense bf16 rate; 725 us back to back.  Three requests of 300 to 2046 tokens of 16 heads
+// (21 GFLOP): 32 us, the 16 key tiles of the longest one's last tokens one after another.
 #include <mutex>
 
 #include "latent_common.cuh"
@@ -113,7 +123,7 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
 
 // A warp's 32 finished rows of P 16-byte pieces on their way out: from the lanes, a row each,
 // into shared memory, and from there in whole rows.  (Stored by the lanes, 16 bytes to 32
-// rows at a time, 8192 keys of 128 heads took 734 us instead of 711.)
+// rows at a time, a row tile's end took 1.5 us instead of 1.0.)
 template <int P>
 __device__ __forceinline__ void ex_stage(uint8_t *stage, int lane, int piece, const float (&y)[8], float inv) {
     *reinterpret_cast<uint4 *>(stage + lane * (16 * P) + ((piece ^ (lane & 7 & (P - 1))) << 4)) =
@@ -695,13 +705,15 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
             done_mask |= bit;
         }
     }
-    // Few token tiles of many keys each leave SMs idle and wait for the longest.  Then the
-    // CTAs of a cluster share a tile's keys: as long as the CTAs were at most one an SM before
-    // they are doubled (a causal chunk's tiles see half of the longest's keys on average), and
-    // each keeps a key tile or more.  2048 tokens of 16 heads: SPLITA; 256 tokens at
-    // 8192 keys: SPLITB.  More CTAs than that pay each one's start and end, 6 us, instead
-    // (300 tokens to 2046 in three requests, 240 CTAs: 33 us whole, 51 us by two), and of
-    // clusters of eight only 15 find a place on the 152 SMs.
+    // Few token tiles of many keys each leave SMs idle and wait for the longest.  Then two or
+    // four CTAs, a cluster, share a tile's keys.  Two where the CTAs were at most one an SM (a
+    // causal chunk's tiles see half of the longest's keys on average, so a second round of
+    // shorter ones still pays: 4096 tokens of 8 heads 40.6 us instead of 57.7, 2048 of 16
+    // heads 29.8 instead of 32.0); four where one round holds them (256 tokens at 8192 keys of
+    // 16 heads: 108 us whole, 59.8 by two, 34.8 by four; 1024 tokens of 16 heads, 64 tiles:
+    // 18.0, 15.4, 22.7).  Each further CTA pays a start and an end of 6 us or so (three requests
+    // of 300 to 2046 tokens, 224 tiles: 32.5 whole, 49.6 by two), and of clusters of eight only
+    // 15 find a place on the 152 SMs (256 at 8192: 43.5).
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
     const int key_tiles = (max_key_len + kExKeys - 1) / kExKeys;

@@ -1,6 +1,6 @@
-// Row pieces of the norm-and-rotation kernels (qk_norm_rope.cu,
-// latent_cache.cu): a row of a head lies across a group of lanes, 8 elements
-// (16 bytes of bf16) per lane.
+// Pieces of the norm-and-rotation kernels (latent_cache.cu; qk_norm_rope.cu, which lays
+// its rows out otherwise, takes the conversions): a row of a head lies across a group of
+// lanes, 8 elements (16 bytes of bf16) per lane.
 //
 //   norm      y_i = x_i * rsqrt(mean(x^2) + eps) * w_i, in fp32
 //   rotation  the first `rot` dims of a row as rot / 2 planes; plane f turns by
