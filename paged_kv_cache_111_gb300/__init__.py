@@ -405,8 +405,12 @@ def _full(what: str, x: Optional[torch.Tensor], dtype, dev: int, shape: tuple, f
     if x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous():
         _refuse(what, x, dtype, dev, form)
     have = x.shape
-    if have != shape and (len(have) != len(shape) or any(b not in (a, -1) for a, b in zip(have, shape))):
-        _refuse(what, x, dtype, dev, form)
+    if have != shape:
+        if len(have) != len(shape):
+            _refuse(what, x, dtype, dev, form)
+        for a, b in zip(have, shape):
+            if a != b and b >= 0:
+                _refuse(what, x, dtype, dev, form)
     return x.data_ptr()
 
 
@@ -453,7 +457,7 @@ def _raw_stream(dev: int, stream) -> int:
 
 def _call(dev: int, name: str, fn, *args) -> None:
     """The C call, with the tensors' device current."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -479,7 +483,7 @@ def _qk_norm_rope(fp8: bool, query_out, kv_cache, query, key, value, q_weight, k
     v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
     table = _full("cos_sin", cos_sin, _F32, dev, (-1, -1), "a contiguous [max_position, rotary_dim]")
     max_position, rot = cos_sin.shape
-    lib = load()
+    lib = _lib or load()
     _call(dev, "pkv_qk_norm_rope_kv_write", lib.pkv_qk_norm_rope_kv_write_fp8 if fp8 else lib.pkv_qk_norm_rope_kv_write,
           qo, qo_step, kv_cache.data_ptr(), nb, H, hkv, d, bs, q, q_step, k, k_step, v, v_step,
           _full("q_weight", q_weight, _BF16, dev, (d,), "[d]"), _full("k_weight", k_weight, _BF16, dev, (d,), "[d]"),
@@ -533,7 +537,7 @@ def latent_kv_write(latent_cache: torch.Tensor, latent: torch.Tensor, key_rope: 
         H = query_rope.shape[1]
         q = (_heads("query_rope_out", query_rope_out, dev, T, H, LATENT_ROPE_DIM, False)
              + _heads("query_rope", query_rope, dev, T, H, LATENT_ROPE_DIM, False))
-    _call(dev, "pkv_latent_kv_write", load().pkv_latent_kv_write, cache, nb, bs, lat, lat_step, kr, kr_step,
+    _call(dev, "pkv_latent_kv_write", (_lib or load()).pkv_latent_kv_write, cache, nb, bs, lat, lat_step, kr, kr_step,
           _full("weight", weight, _BF16, dev, (LATENT_DIM,), f"[{LATENT_DIM}]"), eps,
           _full("cos_sin", cos_sin, _F32, dev, (-1, LATENT_ROPE_DIM),
                 f"a contiguous [max_position, {LATENT_ROPE_DIM}]"), cos_sin.shape[0],
@@ -550,7 +554,7 @@ def latent_gather(out: torch.Tensor, latent_cache: torch.Tensor, block_tables: t
     S = seq_lens.numel()
     if key_start_loc.numel() < S:
         raise ValueError("key_start_loc must have an entry per request")
-    _call(dev, "pkv_latent_gather", load().pkv_latent_gather,
+    _call(dev, "pkv_latent_gather", (_lib or load()).pkv_latent_gather,
           _full("out", out, _BF16, dev, (-1, _ROW), f"a contiguous [rows, {_ROW}]"), out.shape[0], cache, nb, bs,
           _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
           block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
@@ -585,7 +589,7 @@ def latent_paged_attn(out: torch.Tensor, query: torch.Tensor, latent_cache: torc
     q, q_step, _ = _heads("query", query, dev, T, H, _ROW, True)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse("workspace", workspace, None, dev, "contiguous")
-    _call(dev, "pkv_latent_paged_attn", load().pkv_latent_paged_attn,
+    _call(dev, "pkv_latent_paged_attn", (_lib or load()).pkv_latent_paged_attn,
           _full("out", out, _BF16, dev, (T, H, LATENT_DIM), f"a contiguous [T, H, {LATENT_DIM}]"), q, q_step, cache, nb,
           _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
           block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
@@ -607,7 +611,7 @@ def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tens
     K = key_rope.shape[0]
     S = query_start_loc.numel() - 1
     q, q_step, _ = _heads("query", query, dev, T, H, _QK, True)
-    _call(dev, "pkv_latent_attn_expanded", load().pkv_latent_attn_expanded,
+    _call(dev, "pkv_latent_attn_expanded", (_lib or load()).pkv_latent_attn_expanded,
           _full("out", out, _BF16, dev, (T, H, _VALUE), f"a contiguous [T, H, {_VALUE}]"), q, q_step,
           *_heads("key", key, dev, K, H, _NOPE, False), *_tokens("key_rope", key_rope, dev, K, LATENT_ROPE_DIM),
           *_heads("value", value, dev, K, H, _VALUE, False),
