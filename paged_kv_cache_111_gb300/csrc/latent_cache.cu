@@ -16,8 +16,8 @@
 // Both move bytes and compute next to nothing.  The gather is bound by memory (204 k rows of
 // 256 requests, 471 MB: 79.6 us, 5.9 TB/s, 87% of a plain copy's rate).  The write is bound
 // by the latency of its chain (position and slot, table row, sums over the warp) at four waves
-// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 13.4 us, 60% of a copy's rate; CTAs of
-// 128 threads and item numbers in 32 bits took it there from 14.1.
+// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 12.0 us, 67% of a copy's
+// rate (13.7 with the partner dims fetched from other lanes and 64 registers).
 #include "latent_common.cuh"
 #include "norm_rope.cuh"
 
@@ -42,9 +42,43 @@ struct LatentWriteParams {
 
 constexpr int kRopeRows = 16;                      // query heads per warp
 constexpr int kWriteThreads = 128;
+constexpr int kWriteCtas = 10;                     // CTAs an SM: 48 registers (56: 12.3 us, 64: 12.9, 40: 13.3)
+
+// Lane l of eight has planes 4 l .. 4 l + 3 of a row's 64 rotated dims: two pieces of four dims that
+// turn with one another, or of two planes each where a plane's dims are neighbours.  No lane
+// needs another's.
+template <bool INTER> struct RopeLane {
+    static __device__ __forceinline__ int first(int l) { return INTER ? l * 8 : l * 4; }
+    static __device__ __forceinline__ int second(int l) { return INTER ? l * 8 + 4 : kLatRope / 2 + l * 4; }
+    static __device__ __forceinline__ uint4 load(const __nv_bfloat16 *row, int l) {    // (not __ldg: rows may be rotated in place)
+        if constexpr (INTER) return *reinterpret_cast<const uint4 *>(row + first(l));
+        const uint2 a = *reinterpret_cast<const uint2 *>(row + first(l)), b = *reinterpret_cast<const uint2 *>(row + second(l));
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    static __device__ __forceinline__ uint4 turn(const uint4 &v, const float4 &c4, const float4 &s4) {
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+        float x[8], y[8];
+        bf16x8_to_f32(v, x);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int i = INTER ? 2 * f : f, j = INTER ? 2 * f + 1 : f + 4;
+            y[i] = x[i] * c[f] - x[j] * s[f];
+            y[j] = x[j] * c[f] + x[i] * s[f];
+        }
+        return f32_to_bf16x8(y);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *row, int l, const uint4 &v) {
+        if constexpr (INTER) {
+            *reinterpret_cast<uint4 *>(row + first(l)) = v;
+        } else {
+            *reinterpret_cast<uint2 *>(row + first(l)) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2 *>(row + second(l)) = make_uint2(v.z, v.w);
+        }
+    }
+};
 
 template <bool INTER>
-__global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const LatentWriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, kWriteCtas) latent_write_kernel(const LatentWriteParams p) {
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const uint32_t item = blockIdx.x * (kWriteThreads / 32) + (threadIdx.x >> 5);     // below 2^31
@@ -52,25 +86,26 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const Laten
     if (token >= static_cast<uint32_t>(p.num_tokens)) return;                         // whole warps
     const int part = static_cast<int>(item - token * p.warps_per_token);
     const int64_t t = token;
-    const int e0 = (lane & 7) * 8;
+    using Rope = RopeLane<INTER>;
+    const int l = lane & 7;
     const int64_t pos = __ldg(p.positions + t);
     const bool bad_pos = pos < 0 || pos >= p.max_position;
     if (part == 0) {
         const int64_t slot = __ldg(p.slots + t);
         const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + t * p.latent_stride);
         const uint4 raw0 = __ldg(src + lane), raw1 = __ldg(src + 32 + lane);
-        const uint4 rawk = __ldg(reinterpret_cast<const uint4 *>(p.key_rope + t * p.key_stride + e0));
+        const uint4 rawk = Rope::load(p.key_rope + t * p.key_stride, l);
         if (slot < 0) return;                      // padding
         if (bad_pos || slot >= p.num_slots) {
             if (lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
             return;
         }
-        LaneAngles<INTER> ang;
-        ang.load(p.cos_sin + pos * kLatRope, e0, kLatRope);
-        float x[8], y[8], k[8];
+        const float *angles = p.cos_sin + pos * kLatRope + l * 4;
+        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(angles));
+        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(angles + kLatRope / 2));
+        float x[8], y[8];
         bf16x8_to_f32(raw0, x);
         bf16x8_to_f32(raw1, y);
-        bf16x8_to_f32(rawk, k);
         uint4 *dst = p.cache + slot * (kLatRow / 8);
         if (p.weight) {
             float w0[8], w1[8];
@@ -88,34 +123,29 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const Laten
                 y[i] = y[i] * inv * w1[i];
             }
         }
-        rotate8<INTER>(k, ang, e0, kLatRope);      // four copies side by side, one stored
         dst[lane] = f32_to_bf16x8(x);
         dst[32 + lane] = f32_to_bf16x8(y);
-        if (lane < 8) dst[64 + lane] = f32_to_bf16x8(k);
+        const uint4 k = Rope::turn(rawk, c4, s4);  // four copies side by side, one stored
+        if (lane < 8) Rope::store(reinterpret_cast<__nv_bfloat16 *>(dst + kLatent / 8), l, k);
     } else {
         const int h0 = (part - 1) * kRopeRows + (lane >> 3);
         uint4 raw[kRopeRows / 4];
 #pragma unroll
         for (int u = 0; u < kRopeRows / 4; ++u) {
             raw[u] = make_uint4(0, 0, 0, 0);
-            if (h0 + 4 * u < p.heads)              // (not __ldg: q_out may be q)
-                raw[u] = *reinterpret_cast<const uint4 *>(p.q + t * p.q_token + (h0 + 4 * u) * p.q_head + e0);
+            if (h0 + 4 * u < p.heads) raw[u] = Rope::load(p.q + t * p.q_token + (h0 + 4 * u) * p.q_head, l);
         }
         if (bad_pos) {
             if (lane == 0 && __ldg(p.slots + t) >= 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
             return;
         }
-        LaneAngles<INTER> ang;
-        ang.load(p.cos_sin + pos * kLatRope, e0, kLatRope);
+        const float *angles = p.cos_sin + pos * kLatRope + l * 4;
+        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(angles));
+        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(angles + kLatRope / 2));
 #pragma unroll
-        for (int u = 0; u < kRopeRows / 4; ++u) {
-            float x[8];
-            bf16x8_to_f32(raw[u], x);
-            rotate8<INTER>(x, ang, e0, kLatRope);
+        for (int u = 0; u < kRopeRows / 4; ++u)
             if (h0 + 4 * u < p.heads)
-                *reinterpret_cast<uint4 *>(p.q_out + t * p.qo_token + (h0 + 4 * u) * p.qo_head + e0) =
-                    f32_to_bf16x8(x);
-        }
+                Rope::store(p.q_out + t * p.qo_token + (h0 + 4 * u) * p.qo_head, l, Rope::turn(raw[u], c4, s4));
     }
 }
 

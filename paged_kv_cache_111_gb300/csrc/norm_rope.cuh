@@ -1,6 +1,5 @@
-// Pieces of the norm-and-rotation kernels (latent_cache.cu; qk_norm_rope.cu, which lays
-// its rows out otherwise, takes the conversions): a row of a head lies across a group of
-// lanes, 8 elements (16 bytes of bf16) per lane.
+// What the norm-and-rotation kernels (qk_norm_rope.cu, latent_cache.cu) compute, and the
+// conversions they share.
 //
 //   norm      y_i = x_i * rsqrt(mean(x^2) + eps) * w_i, in fp32
 //   rotation  the first `rot` dims of a row as rot / 2 planes; plane f turns by
@@ -32,62 +31,52 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
+// A divisor on the way to E4M3 codes.  The code of a quotient depends on which side of the
+// midpoints between codes it lies; they have at most 5 significant bits, so the low 19 bits of
+// their fp32 form are zero.  x * RN(1 / scale) is less than 2.5 ulps off the rounded quotient
+// (2^-24 of it from either rounding, half an ulp from the quotient's; 5 ulps below the one
+// midpoint that is a power of two), so where it lies more than 8 ulps from every such number
+// its code is the quotient's.  Only the others are divided.  E4M3 write of 2048 tokens of 64/8 heads, 8 of 40
+// rows with codes: 17.4 us, with every element
+// divided 19.5 (the registers that the divisions took cost a CTA an SM too).
+struct E4m3Scale {
+    float scale, inv;
+    int32_t near;             // divide if a product is as near as this: 16, -1 never, 2^19 always
+};
+
+__host__ inline E4m3Scale e4m3_scale(float scale) {
+    E4m3Scale s;
+    s.scale = scale, s.inv = 1.f / scale;
+    int e;
+    const float m = frexpf(scale, &e);
+    // far from the ends of the exponents, what the product loses below them has code 0 anyway;
+    // by a power of two it is exact
+    s.near = e < -100 || e > 100 ? 1 << 19 : (m == 0.5f ? -1 : 16);
+    return s;
+}
+
 // The E4M3 codes nearest to the fp32 quotients x / scale (ties to even, held at +-448).
-__device__ __forceinline__ uint2 f32_to_e4m3x8(const float (&x)[8], float scale) {
+__device__ __forceinline__ uint2 f32_to_e4m3x8(const float (&x)[8], const E4m3Scale &s) {
+    int32_t nearest = 1 << 19;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nearest = min(nearest, (__float_as_int(x[i] * s.inv) + 8) & 0x7FFFF);
+    float q[8];
+    if (nearest <= s.near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], s.scale);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = x[i] * s.inv;
+    }
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float2 lo = make_float2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-        const float2 hi = make_float2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
+        const float2 lo = make_float2(q[4 * i], q[4 * i + 1]);
+        const float2 hi = make_float2(q[4 * i + 2], q[4 * i + 3]);
         w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
                static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16;
     }
     return make_uint2(w[0], w[1]);
-}
-
-// Cosines and sines of one lane's 8 elements, dims e0 .. e0 + 7 (e0 < rot):
-// 8 planes of each, or 4 where a plane's two dims are neighbours.
-template <bool INTER>
-struct LaneAngles {
-    static constexpr int kPlanes = INTER ? 4 : 8;
-    float c[kPlanes], s[kPlanes];
-    __device__ __forceinline__ void load(const float *row, int e0, int rot) {
-        const int half = rot >> 1;
-        const int f0 = INTER ? e0 >> 1 : (e0 < half ? e0 : e0 - half);
-#pragma unroll
-        for (int i = 0; i < kPlanes; i += 4) {
-            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + f0 + i));
-            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + f0 + i));
-            c[i] = c4.x, c[i + 1] = c4.y, c[i + 2] = c4.z, c[i + 3] = c4.w;
-            s[i] = s4.x, s[i + 1] = s4.y, s[i + 2] = s4.z, s[i + 3] = s4.w;
-        }
-    }
-};
-
-// Rotates one lane's 8 elements in place.  Every lane of the warp calls it
-// (split planes exchange their halves by shuffle: the partner dim lies rot / 16
-// lanes away); lanes with e0 >= rot keep their elements.
-template <bool INTER>
-__device__ __forceinline__ void rotate8(float (&x)[8], const LaneAngles<INTER> &a, int e0, int rot) {
-    if constexpr (INTER) {
-        if (e0 < rot) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = x[2 * i], q = x[2 * i + 1];
-                x[2 * i] = p * a.c[i] - q * a.s[i];
-                x[2 * i + 1] = q * a.c[i] + p * a.s[i];
-            }
-        }
-    } else {
-        const int lane = threadIdx.x & 31;
-        const bool first = e0 < (rot >> 1);
-        const int partner = e0 < rot ? (first ? lane + (rot >> 4) : lane - (rot >> 4)) : lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float y = __shfl_sync(0xffffffffu, x[i], partner);
-            if (e0 < rot) x[i] = first ? x[i] * a.c[i] - y * a.s[i] : x[i] * a.c[i] + y * a.s[i];
-        }
-    }
 }
 
 }  // namespace pkv

@@ -19,8 +19,7 @@
 // arithmetic runs on pairs (f32x2).  Whole rows on 16-byte pieces, with the partner
 // dims fetched from other lanes, took four times the instructions: 60 us on 8192
 // tokens of 32/8 heads of 128 (206 MB), against 36 us (5.7 TB/s, 85% of a plain copy's
-// rate).  The E4M3 form, 2048 tokens of 64/8 heads (80 MB): 19.5 us, 61% of the issue
-// slots taken.
+// rate).  The E4M3 form, 2048 tokens of 64/8 heads (80 MB): 17.4 us.
 #include "norm_rope.cuh"
 #include "prefill_common.cuh"
 
@@ -28,6 +27,7 @@ namespace pkv {
 
 constexpr int kRowsUnroll = 4;                   // rows a lane
 constexpr int kQkThreads = 128;                  // (256: 41 us where 128 take 39)
+constexpr int kQkCtas = 9;                       // CTAs an SM: 56 registers (64 and fewer CTAs: 38 us, 48: 37)
 
 struct QkParams {
     __nv_bfloat16 *query_out;
@@ -42,12 +42,13 @@ struct QkParams {
     int64_t num_slots;
     int32_t num_tokens, hq, hkv, rot;
     int32_t q_chunks, kv_chunks, chunks;        // warps per token: of the query, of key or value, in all
-    float eps, k_scale, v_scale;
+    float eps;
+    E4m3Scale k_scale, v_scale;
     int32_t *status;
 };
 
 template <int HD, bool FP8, bool INTER>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_norm_rope_kernel(const QkParams p) {
     pdl_trigger();                            // the attention plan may start (it reads no cache and no query)
     constexpr int kLanes = HD / 8;            // lanes of a row
     constexpr int kGroups = 32 / kLanes;      // rows side by side in a warp
@@ -246,7 +247,7 @@ static int qk_norm_rope(bool fp8, void *query_out, int64_t out_stride, void *kv_
     p.q_chunks = (hq + per_warp - 1) / per_warp;
     p.kv_chunks = (hkv + per_warp - 1) / per_warp;
     p.chunks = p.q_chunks + 2 * p.kv_chunks;
-    p.eps = eps, p.k_scale = k_scale, p.v_scale = v_scale;
+    p.eps = eps, p.k_scale = e4m3_scale(k_scale), p.v_scale = e4m3_scale(v_scale);
     p.status = device_status;
     const int64_t warps = static_cast<int64_t>(num_tokens) * p.chunks;
     const int64_t blocks = (warps + kQkThreads / 32 - 1) / (kQkThreads / 32);

@@ -356,3 +356,41 @@ def test_refused_forms_on_the_gpu():
                    ("query_rope", n["q"][:, :, 128:]), ("cos_sin", n["table"][:, :32]), ("key_rope", n["kr"].t())):
         with pytest.raises(ValueError):
             pkv.latent_kv_write(**dict(ok, **{k: bad}))
+
+
+def test_fp8_codes_beside_the_midpoints():
+    """Codes whose quotients lie on a midpoint between two codes, or an ulp or two beside it, powers of two and ends
+    of the range among the scales: bit for bit those of the rounded fp32 quotient."""
+    g = torch.Generator().manual_seed(31)
+    mid = [(2 * m + 1) * 2.0 ** e for e in range(-10, 5) for m in (0, 1, 4, 7, 8, 11, 13, 15)]
+    scales = [1.0, 0.5, 2.0 ** -40, 2.0 ** 30, 3e-38, 1e-42, 2.9e38, 448.0, 1e-31, 2.0 ** -101, 1.5 * 2.0 ** 99]
+    x0 = (torch.rand(40, generator=g) + 1).to(torch.bfloat16).float()
+    for i, m in enumerate(mid):
+        s = x0[i % 40] / m
+        for _ in range(i % 4):
+            s = torch.nextafter(s, torch.tensor(0.0 if i % 8 < 4 else 1e9))
+        scales.append(s.item())
+    T, h, d = 16, 4, 128
+    dims = torch.arange(T * h * d)
+    table = torch.zeros(1, 16, device="cuda")
+    table[:, :8] = 1
+    at, slots = torch.zeros(T, dtype=torch.int64, device="cuda"), torch.arange(T, device="cuda")
+    for s in scales:
+        s32 = torch.tensor(s, dtype=torch.float32)
+        s = s32.item()
+        x = x0[dims % 40] * 2.0 ** (dims // 40 % 23 - 11)
+        x = torch.where(dims % 3 == 0, (torch.randn(dims.numel(), generator=g) * s32 * 100), x)
+        x[:8] = torch.tensor([0.0, -0.0, float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 1e-38])
+        x = torch.where(dims % 2 == 0, x, -x).to(torch.bfloat16).reshape(T, h, d).cuda()
+        cache = torch.zeros(1, h, 2, 16, d, dtype=torch.uint8, device="cuda")
+        q = torch.zeros(T, h, d, dtype=torch.bfloat16, device="cuda")
+        pkv.qk_norm_rope_kv_write_fp8(q, cache, q, x, x, None, None, 0.0, table, at, slots, s, s)
+        quotient = (x.cpu().float() / s32).clamp(-448, 448)          # fp32, then the nearest code
+        want = quotient.to(torch.float8_e4m3fn).view(torch.uint8).transpose(0, 1)
+        nan = torch.isnan(quotient).transpose(0, 1)
+        # (a turn by no angle: x * 1 - y * 0 is NaN beside an infinity or a NaN, and +0 for -0)
+        plain = torch.isfinite(x.float()).cpu() & (x.float().cpu() != 0)
+        finite = (plain & plain.roll(-8, -1) & plain.roll(8, -1)).transpose(0, 1)
+        got_k, got_v = cache[0, :, 0].cpu(), cache[0, :, 1].cpu()
+        assert torch.equal(torch.where(nan, 0x7F, got_v & torch.where(nan, 0x7F, 0xFF)), torch.where(nan, 0x7F, want)), s
+        assert torch.equal(got_k[finite], want[finite]), s
