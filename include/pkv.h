@@ -525,9 +525,10 @@ int pkv_latent_gather(void *out, int64_t out_rows, const void *latent_cache, int
  *  out               bf16 [num_tokens][num_heads][512], contiguous.  Rows that no
  *                    request owns are left as they were.
  *  query             bf16; token t, head h at query + t*query_token_stride + h*576.
- *  latent_cache      bf16 [num_blocks][16][576]; num_blocks < 2^31.  A key row's values
- *                    must be finite (an infinity or NaN in a row may reach the earlier
- *                    tokens of its own chunk); unwritten slots may hold anything.
+ *  latent_cache      bf16 [num_blocks][16][576]; num_blocks < 2^31.  Unwritten slots may
+ *                    hold anything.  An infinity or NaN in a key row reaches no token
+ *                    that does not see the row; one that sees a NaN is NaN, and what one
+ *                    that sees an infinity gets is not defined.
  *  num_heads         1 .. 1024; num_tokens * num_heads < 2^31.
  *  max_query_len, max_seq_len, block_tables, seq_lens, query_start_loc
  *                    as pkv_paged_attn (a request whose values break them is left
@@ -583,8 +584,10 @@ int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stri
  *                    has fewer keys than queries, is left unwritten.
  *  device_status     optional int32 device word, never cleared by the library:
  *                    PKV_ERR_DEVICE_METADATA for such a request.
- * Values of a request's keys must be finite; what lies between or behind the
- * requests' rows may be anything.  Pointers are 16-byte aligned, strides
+ * What lies between or behind the requests' rows may be anything.  An infinity or
+ * NaN in a key or value row reaches no token that does not see the row; one that
+ * sees a NaN in a key is NaN, and what one that sees another such value gets (NaN
+ * in all its dims, or in those) is not defined.  Pointers are 16-byte aligned, strides
  * multiples of 8.  No workspace.
  */
 int pkv_latent_attn_expanded(void *out, const void *query, int64_t query_token_stride,

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             if (!cur->valid) break;
             const int kv0 = cur->kv0, kv1 = cur->kv1, ntok = cur->ntok, lim0 = cur->lim0, tok0 = cur->tok0;
             const int part = cur->slot;
-            const int rows = ntok * p.hpt;
+            const int rows = ntok * p.hpt, end = lim0 + ntok - 1;
             int lim[2], dst[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -762,6 +762,33 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
             float m_ref[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};
+            // Rows of tile j that some tokens see and others do not, with an infinity or NaN among
+            // their values: zeroed.  (S has been computed from them: the tokens that see one have
+            // weights that are no numbers.)
+            auto clear_odd_rows = [&](int j) {
+                for (int part = 0; part < 2; ++part)          // (landed, as S shows; this thread has to see it)
+                    pf_wait(&bars[kLaKVFull + 2 * (gt % kLaStages) + part], (gt / kLaStages) & 1, status);
+                for (int t = max(lim0 - j * kLaKeys, 0); t < min(kLaKeys, end - j * kLaKeys); ++t) {
+                    const uint32_t a = sKV + (gt % kLaStages) * kLaStage + (lane >> 3) * 1024 + (lane & 7) * 16 + (t & 7) * 128;
+                    const uint32_t at[2] = {a + (t >> 3) * kLaGroupA, a + kLaPartA + (t >> 3) * kLaGroupB};
+                    bool bad = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(at[h])
+                                     : "memory");
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            bad |= (v[e] & 0x7F80u) == 0x7F80u || (v[e] & 0x7F800000u) == 0x7F800000u;
+                    }
+                    if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at[h]), "r"(0u) : "memory");
+                }
+            };
             for (int j = kv0; j < kv1 && ok; ++j, ++gt) {
                 const int sb = gt & 1;
                 ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaSFull + sb], (gt >> 1) & 1, status));
@@ -778,9 +805,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) s[e] *= sl2;
                 if (masked) {
+                    // A score that this row does not see but a later one does: where it is no number,
+                    // an infinity or NaN may lie in the key's row, which must not meet a weight of 0
+                    // (0 x NaN).  `odd` stays 0 as long as every such score is finite.
+                    float odd = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (key0 + (e >> 2) * 8 + (e & 1) >= lim[(e >> 1) & 1]) s[e] = NEG_INF;
+                    for (int e = 0; e < 32; ++e) {
+                        const int key = key0 + (e >> 2) * 8 + (e & 1);
+                        if (key >= lim[(e >> 1) & 1]) {
+                            if (key < end) odd = fmaf(s[e], 0.f, odd);
+                            s[e] = NEG_INF;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, odd != 0.f)) clear_odd_rows(j);
                 }
                 // The reference moves on a row's first visible key, and then only when some
                 // score exceeds it by 2^40: fp32 sums and bf16 weights keep their relative
@@ -856,12 +893,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = rA + 8 * i;
-                    rec->inv[row] = l[i] > 0.f ? 1.f / l[i] : 0.f;
+                    rec->inv[row] = l[i] <= 0.f ? 0.f : 1.f / l[i];       // (NaN stays)
                     rec->dst[row] = dst[i];
                     if (part >= 0) {
                         float *ml = reinterpret_cast<float *>(p.ws + kLaWsMl) +
                                     (static_cast<int64_t>(blockIdx.x) * 2 + part) * 2 * kLaRows;
-                        ml[row] = m_ref[i];
+                        ml[row] = l[i] == l[i] ? m_ref[i] : -NEG_INF;        // (a NaN stays one in the merge)
                         ml[kLaRows + row] = l[i];
                     }
                 }
@@ -1115,7 +1152,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LaParams p, int
             const float mi = ml[part_of(i) * 2 * kLaRows + row];
             L += la_weigh(mi == NEG_INF ? 0.f : fast_exp2(mi - M), ml[part_of(i) * 2 * kLaRows + kLaRows + row]);
         }
-        inv = L > 0.f ? 1.f / L : 0.f;
+        inv = L <= 0.f ? 0.f : 1.f / L;                      // (NaN stays)
         factor[row] = w0 * inv;
         factor[kLaRows + row] = w1 * inv;
     }
@@ -1222,7 +1259,7 @@ __global__ void __launch_bounds__(256) latent_merge_few_kernel(const LaParams p,
                 const float v[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w}, l[4] = {ls[q].x, ls[q].y, ls[q].z, ls[q].w};
                 float y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = l[e] > 0.f ? v[e] / l[e] : 0.f;
+                for (int e = 0; e < 4; ++e) y[e] = l[e] <= 0.f ? 0.f : v[e] / l[e];
                 la_store_rows(p, d, group, r4 + q, m, dim, y);
             }
         }
@@ -1245,12 +1282,12 @@ __global__ void __launch_bounds__(256) latent_merge_few_kernel(const LaParams p,
             for (int i = lane; i < pieces; i += 32) {
                 const float mi = row[part_of(i) * 2 * kLaRows];
                 const float w = mi == NEG_INF ? 0.f : fast_exp2(mi - M);
-                if (w > 0.f) L = fmaf(w, row[part_of(i) * 2 * kLaRows + kLaRows], L);
+                if (w != 0.f) L = fmaf(w, row[part_of(i) * 2 * kLaRows + kLaRows], L);
                 reinterpret_cast<float *>(factor + i)[warp] = w;
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = L <= 0.f ? 0.f : 1.f / L;
             for (int i = lane; i < pieces; i += 32) reinterpret_cast<float *>(factor + i)[warp] *= inv;
         }
         __syncthreads();

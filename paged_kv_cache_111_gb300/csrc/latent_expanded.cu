@@ -29,7 +29,8 @@
 // chunks, where a key is used by many rows.
 //
 // Warp roles (384 threads): warp 0 loads by TMA, warp 1 issues the MMAs, warp 2
-// owns tensor memory, warps 4-7 and 8-11 are the softmax and epilogue of the
+// owns tensor memory, warps 2 and 3 look V over where the causal mask cuts through a
+// key tile, warps 4-7 and 8-11 are the softmax and epilogue of the
 // two row tiles.  V rows past the last visible key are zeroed in shared memory
 // (they belong to other requests, or to nobody).  Every mbarrier wait is bounded.
 //
@@ -71,8 +72,11 @@ enum ExBar {
     kExSFull = 19,       // (+ row tile)
     kExPFull = 21,       // (+ row tile)
     kExODone = 23,       // (+ row tile)
-    kExNumBars = 25
+    kExLoaded = 25,      // V's loads of a tile on the causal diagonal are on their way (+ its number & 1)
+    kExChecked = 27,     // V of that tile looked through (+ its number & 1)
+    kExNumBars = 29
 };
+static_assert(kExNumBars * 8 + 8 + 20 * 4 <= 512, "barriers, tensor-memory address, scan");
 
 struct ExParams {
     __nv_bfloat16 *out;
@@ -159,7 +163,7 @@ __device__ __forceinline__ void ex_join(const uint8_t *smem, int group, int d0, 
         if (f[c] != 0.f)
             L += f[c] * *reinterpret_cast<const float *>(smem + kExOffState + ((c * kPer + group) * 32 + lane) * 8 + 4);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L <= 0.f ? 0.f : 1.f / L;             // (NaN stays)
 #pragma unroll 1
     for (int d = 0; d < kPieces; ++d) {
         float y[8] = {};
@@ -187,6 +191,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kExOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kExNumBars);
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
+    int32_t *odd_key = scan + 18;                                     // first key whose V is no number (on the diagonal)
     const uint32_t sQ = smem_u32(smem + kExOffQ), sRing = smem_u32(smem + kExOffRing);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     // Token tiles (256 tokens of a request) are ranked by the key tiles they see, the
@@ -303,9 +308,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const int n_all = j1 - j0;                          // (the later row tile sees them all)
     const int end = ctx + t0 + rows[0] + rows[1];       // keys the last row sees
     const bool fix = n_all > 0 && j1 == seen_all && end % kExKeys != 0;
+    // first key that the first row does not see, and the first tile (if any) with such keys
+    const int edge = ctx + t0 + 1, diag = edge < end ? max(0, edge / kExKeys - j0) : n_all;
 
+    if (threadIdx.x == 0) *odd_key = INT32_MAX;
     if (threadIdx.x < kExNumBars)
-        mbar_init(&bars[threadIdx.x], threadIdx.x >= kExPFull && threadIdx.x < kExPFull + 2 ? 4 : 1);
+        mbar_init(&bars[threadIdx.x], threadIdx.x >= kExPFull && threadIdx.x < kExPFull + 2 ? 4 : (threadIdx.x >= kExChecked ? 2 : 1));
     if (warp == 2) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -354,6 +362,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
                 issued = s + 1;
             }
+            if (ok && j >= diag && lane == 0) mbar_arrive(&bars[kExLoaded + ((j - diag) & 1)]);
         }
         if (ok && fix) {
             for (int e = 3; e < kExPerTile && ok; ++e) {
@@ -433,7 +442,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
             if (ok && n1) ok = wait(kExQFull + 1, 0) && issue_s(1, 0);
             // tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
             for (int j = 0; j < n_all && ok; ++j) {
-                if (fix && j == n_all - 1) ok = wait(kExFix, 0);
+                if (j >= diag) ok = wait(kExChecked + ((j - diag) & 1), ((j - diag) >> 1) & 1);
+                if (ok && fix && j == n_all - 1) ok = wait(kExFix, 0);
                 if (ok && j < n0) {
                     ok = wait(kExPFull, j & 1);
                     tc_fence_after();
@@ -449,6 +459,55 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp < 4) {
+        // ---------------- V on the diagonal: warp 2 its first half, warp 3 its second ----------------
+        // Keys that some of the rows see and others do not meet weights of 0 in the others, and
+        // 0 x NaN is NaN.  So V's rows with an infinity or NaN are zeroed there, and the rows that
+        // see the first of them are made NaN at the end.  (The load warp's signal comes first: the
+        // slot's barrier is then in the phase waited for, or one further.)
+        const int h = warp - 2;
+        bool ok = true;
+        for (int j = diag; j < n_all && ok; ++j) {
+            const int d = j - diag, s = j * kExPerTile + 3 + h;
+            ok = __all_sync(0xffffffffu, pf_wait(&bars[kExLoaded + (d & 1)], (d >> 1) & 1, status)) &&
+                 __all_sync(0xffffffffu, pf_wait(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1, status));
+            if (!ok) break;
+            const int key0 = (j0 + j) * kExKeys + 64 * h, lo = max(edge - key0, 0), hi = min(end - key0, 64);
+            // 16 bytes of row r a lane, a row 16 lanes
+            const uint32_t base = sRing + (s % kExSlots) * kExChunk + ((lane & 15) >> 3) * 8192 + (lane & 7) * 16;
+            auto largest = [&](int r, uint32_t (&acc)[4]) {     // of |acc| and the piece, NaN if there is one
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                             : "r"(base + r * 128)
+                             : "memory");
+#pragma unroll
+                for (int e = 0; e < 4; ++e) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(acc[e]) : "r"(v[e]));
+            };
+            auto odd = [](const uint32_t (&acc)[4]) {
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    any |= (acc[e] & 0x7F80u) == 0x7F80u || (acc[e] & 0x7F800000u) == 0x7F800000u;
+                return __any_sync(0xffffffffu, any);
+            };
+            uint32_t acc[4] = {};
+#pragma unroll 4
+            for (int r = lo + (lane >> 4); r < hi; r += 2) largest(r, acc);
+            if (odd(acc)) {
+                for (int r = lo; r < hi; ++r) {
+                    uint32_t one[4] = {};
+                    largest(r, one);
+                    if (!odd(one)) continue;
+                    if (lane < 16)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + r * 128), "r"(0u) : "memory");
+                    if (lane == 0) atomicMin(odd_key, key0 + r);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kExChecked + (d & 1)]);
+        }
     } else if (warp >= 4) {
         // ---------------- softmax (a row per thread) and epilogue ----------------
         const int i = (warp - 4) >> 2, quad = warp & 3;
@@ -547,6 +606,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             l += a + b;
         }
         if (ok && n_mine) ok = __all_sync(0xffffffffu, pf_wait(&bars[kExODone + i], (n_mine - 1) & 1, status));
+        if (ok && n_mine && lim > *reinterpret_cast<volatile int32_t *>(odd_key)) l = __int_as_float(0x7fffffff);
         const int64_t stride = static_cast<int64_t>(p.heads) * kExV;
         __nv_bfloat16 *o = p.out + static_cast<int64_t>(req.qs + t0) * stride + head * kExV;
         if (p.split > 1) {
@@ -555,6 +615,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             // every CTA leaves there.
             tc_fence_after();
             if (!ok || !n_mine) m_ref = NEG_INF;
+            else if (l != l) m_ref = -NEG_INF;              // (a NaN stays one in the join)
             const int per = 8 / p.split, w = warp - 4;
             cluster_sync();                             // no CTA's products read shared memory any more
             const uint32_t to = cluster_address(sQ, w / per);
@@ -588,7 +649,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
         } else if (ok && n_mine) {
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l <= 0.f ? 0.f : 1.f / l;         // (NaN stays)
             const int owned = min(32, (i ? rows[1] : rows[0]) - quad * 32);
             uint8_t *stage = smem + kExOffQ + i * kExQ + quad * 8192;      // over Q, which the last S has read
 #pragma unroll 1

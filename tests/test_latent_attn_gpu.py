@@ -298,3 +298,25 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for b, w in zip(bs, want):
         assert torch.equal(b.out, w)
+
+
+@pytest.mark.parametrize("H,q,n", [(16, 70, 150), (1, 64, 64), (5, 100, 1100), (16, 4, 64), (64, 3, 130), (128, 2, 9)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_infinities_and_nan_in_later_tokens_rows(H, q, n, what):
+    """Rows of the chunk's own tokens hold infinities or NaN, in a latent dim or in a rotated one: the tokens before
+    them come out as without, bit for bit; those that see one are no numbers where NaN is seen."""
+    b = Batch(31, [(q, n), (1, 40)], H)
+    want = b.run().clone()
+    b.check()
+    first = n - q + max(1, q // 3)                         # the first key with such a value
+    for i, j in enumerate(range(first, n, 3)):
+        page = b.bt[0, j // 16]
+        b.cache[page, j % 16, (7, 511, 300, 575, 512)[i % 5]] = what
+    b.out.fill_(7.0)
+    b.run()
+    seen = first - (n - q)                                 # query tokens before it
+    assert torch.equal(b.out[:seen], want[:seen])
+    assert torch.equal(b.out[q:], want[q:])
+    if what != what:
+        assert torch.isnan(b.out[seen:q]).all()
+    assert pkv.workspace_status(b.ws) == 0

@@ -298,3 +298,27 @@ def test_a_bad_request_beside_a_shared_one():
     c.run()
     assert int(c.status) != 0
     assert torch.equal(c.out, before)
+
+
+@pytest.mark.parametrize("H,q,n", [(2, 70, 150), (1, 600, 600), (16, 257, 900), (200, 130, 140), (1, 2, 5000), (3, 256, 256)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["value", "key", "rope"])
+def test_infinities_and_nan_in_later_tokens_rows(H, q, n, what, where):
+    """The chunk's own keys or values hold infinities or NaN: the tokens before them come out as without, bit for
+    bit; those that see one are no numbers where NaN is seen."""
+    c = Ragged(31, [(q, n), (1, 40)], H)
+    want = c.run().clone()
+    c.check()
+    first = n - q + max(1, q // 3)                         # the first key with such a value
+    if where == "rope":
+        c.rope[first:n:7, 63] = what
+    else:
+        (c.value if where == "value" else c.key)[first:n:7, :, 77] = what
+    c.out.fill_(7.0)
+    c.run()
+    seen = first - (n - q)                                 # query tokens before it
+    assert torch.equal(c.out[:seen], want[:seen])
+    assert torch.equal(c.out[q:], want[q:])
+    if what != what:
+        assert torch.isnan(c.out[seen:q, :, 77]).all()
+    assert int(c.status) == 0
