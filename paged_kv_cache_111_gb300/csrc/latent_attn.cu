@@ -51,8 +51,8 @@
 // the second products, 72 KiB of loads and 8 of weights, 320 KiB at 128 bytes a cycle: 2560
 // cycles, and 2500 to 2740 are measured.  A row tile costs 6000 cycles beside its key
 // tiles, the merge about 8 us a call.  256 requests of 16 to 4096 keys, 128 heads (330
-// MB, 62.6 GFLOP): 93 us, 3.5 TB/s, 670 TFLOP/s.  Two decodes and a 2046-token chunk of
-// 16 heads (109 GFLOP): 131 us, 830 TFLOP/s.  Bringing Q in in two parts, or into L2 ahead
+// MB, 62.6 GFLOP): 94 us, 3.5 TB/s, 670 TFLOP/s.  Two decodes and a 2046-token chunk of
+// 16 heads (109 GFLOP): 132 us, 820 TFLOP/s.  Bringing Q in in two parts, or into L2 ahead
 // of its item, gained nothing (94 to 96 us).
 #include <mutex>
 #include <type_traits>

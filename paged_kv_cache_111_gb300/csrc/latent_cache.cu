@@ -16,7 +16,7 @@
 // Both move bytes and compute next to nothing.  The gather is bound by memory (204 k rows of
 // 256 requests, 471 MB: 79.6 us, 5.9 TB/s, 87% of a plain copy's rate).  The write is bound
 // by the latency of its chain (position and slot, table row, sums over the warp) at four waves
-// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 12.0 us, 67% of a copy's
+// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 12.3 us, 66% of a copy's
 // rate (13.7 with the partner dims fetched from other lanes and 64 registers).
 #include "latent_common.cuh"
 #include "norm_rope.cuh"

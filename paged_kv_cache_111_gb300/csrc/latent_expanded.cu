@@ -42,7 +42,7 @@
 // (128 bytes a cycle); the rest is the turn between the two row tiles.  2048 tokens at
 // 8192 keys of 128 heads (1.2 TFLOP): 790 us with cold caches, 1520 TFLOP/s, 78% of the
 // dense bf16 rate; 725 us back to back.  Three requests of 300 to 2046 tokens of 16 heads
-// (21 GFLOP): 32 us, the 16 key tiles of the longest one's last tokens one after another.
+// (21 GFLOP): 33.5 us, the 16 key tiles of the longest one's last tokens one after another.
 #include <mutex>
 
 #include "latent_common.cuh"
