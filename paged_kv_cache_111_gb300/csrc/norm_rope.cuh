@@ -36,9 +36,9 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
 // their fp32 form are zero.  x * RN(1 / scale) is less than 2.5 ulps off the rounded quotient
 // (2^-24 of it from either rounding, half an ulp from the quotient's; 5 ulps below the one
 // midpoint that is a power of two), so where it lies more than 8 ulps from every such number
-// its code is the quotient's.  Only the others are divided.  E4M3 write of 2048 tokens of 64/8 heads, 8 of 40
-// rows with codes: 17.4 us, with every element
-// divided 19.5 (the registers that the divisions took cost a CTA an SM too).
+// its code is the quotient's.  Only the others are divided.  2048 tokens of 64/8 heads, one
+// row in five with codes: 17.4 us, with every element divided 19.5 (the registers that the
+// divisions took cost a CTA an SM too).
 struct E4m3Scale {
     float scale, inv;
     int32_t near;             // divide if a product is as near as this: 16, -1 never, 2^19 always
