@@ -74,6 +74,13 @@ constexpr int kLaMaxHeads = 1024;
 constexpr int kLaThreads = 416;
 constexpr int kLaItemSlots = 4;
 constexpr int kLaAhead = 1;                                  // tiles between a page's way into L2 and its load
+// Buffers of the rescale votes, by tile.  A softmax warp that does not rescale at tile g has
+// nobody wait for its look at the votes of g, so they are overwritten only by a tile whose
+// scores that look came before in any order of events: S of tile g + 3 is written to the stage
+// that the second products of g + 1 have released; those wait for every softmax warp's weights
+// of g + 1, and a warp is at g + 1 once it has looked at g.  Two buffers do not hold across items,
+// as an item's first tile looks at no votes; three do, and four are indexed by a mask.
+constexpr int kLaVotes = 4;
 static_assert(kLaAhead * kLaPages <= 32, "one page a lane");
 
 // A stage holds a tile's 64 keys in two parts, each [page][token half][chunk]
@@ -172,7 +179,7 @@ enum LaBar {
     kLaKVEmpty = 23,          // a part read by its last product (+ 2 stage + part)
     kLaNumBars = 35
 };
-static_assert(kLaNumBars * 8 + 24 <= 304, "barriers, tensor-memory address, status, votes");
+static_assert(kLaNumBars * 8 + 8 + 4 * kLaVotes <= 304, "barriers, tensor-memory address, status, votes");
 
 // Request r's share of the line of units.
 struct LaReq {
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kLaOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kLaNumBars);
     int32_t *status = reinterpret_cast<int32_t *>(tmem_slot + 1);       // of this CTA, in shared memory
-    volatile uint8_t *votes = reinterpret_cast<volatile uint8_t *>(tmem_slot + 2);    // [tile & 1][warp]
+    volatile uint8_t *votes = reinterpret_cast<volatile uint8_t *>(tmem_slot + 2);    // [tile % kLaVotes][warp]
     int64_t *scan = reinterpret_cast<int64_t *>(smem + kLaOffAlpha);    // before the roles start only
     volatile LaItem *items = reinterpret_cast<volatile LaItem *>(smem + kLaOffItems);
     const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sOut = smem_u32(smem + kLaOffOut);
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     ok = warp_wait(&bars[kLaFix + st], (fix_par >> st) & 1u, status);
                     fix_par ^= 1u << st;
                 }
-                if (j > 0 && uniform(*reinterpret_cast<volatile const uint32_t *>(votes + 4 * (gt & 1)))) {
+                if (j > 0 && uniform(*reinterpret_cast<volatile const uint32_t *>(votes + 4 * (gt % kLaVotes)))) {
                     if (ok) ok = warp_wait(&bars[kLaRescaled], rescales & 1, status);
                     ++rescales;
                 }
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // between the products of tile g - 1 and those of g.
         auto rescale = [&](int g) -> bool {
             if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaPFull + (g & 1)], (g >> 1) & 1, status))) return false;
-            const uint32_t vote = *reinterpret_cast<volatile const uint32_t *>(votes + 4 * (g & 1));
+            const uint32_t vote = *reinterpret_cast<volatile const uint32_t *>(votes + 4 * (g % kLaVotes));
             if (!vote) return true;
             if (!__all_sync(0xffffffffu, pf_wait(&bars[kLaODone], (g - 1) & 1, status))) return false;
             tc_fence_after();
@@ -872,7 +879,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                     stsm_x4_trans(sW + (c + (m >> 1)) * kLaGroupB + i * 128 + (((2 * quad + (m & 1)) ^ i) << 4),
                                   w[2 * c], w[2 * c + 1], w[2 * c + 2], w[2 * c + 3]);
                 }
-                if (lane == 0) votes[4 * sb + quad] = grow ? 1 : 0;
+                if (lane == 0) votes[4 * (gt % kLaVotes) + quad] = grow ? 1 : 0;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();

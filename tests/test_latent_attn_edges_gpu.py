@@ -1,0 +1,38 @@
+"""The latent attention where its parts meet, against the plain 64-bit form and the bound of test_latent_attn_gpu."""
+
+import pytest
+import torch
+
+import paged_kv_cache_111_gb300 as pkv
+from test_latent_attn_gpu import D, W, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+def rewrite(b, r, rows):
+    """Request r's cached rows replaced (64-bit values of bf16 numbers)."""
+    n = b.reqs[r][1]
+    b.rows[r] = rows
+    at = torch.arange(n)
+    b.cache[b.bt[r, at.cuda() // 16].long(), (at % 16).cuda()] = rows.to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("H,seqs", [(128, 600), (16, 900)])
+def test_scores_that_jump_where_items_meet(H, seqs):
+    """Runs of many short row tiles: the scores of every second key tile jump past the softmax reference's bound, so
+    that rescaling falls into the tiles behind an item's first, again and again, and the same bits come out."""
+    g = torch.Generator().manual_seed(H)
+    b = Batch(41, [(1, int(n)) for n in torch.randint(1, 200, (seqs,), generator=g)], H)
+    for r, (q, n) in enumerate(b.reqs):
+        rows = b.rows[r]
+        rows[:, W:] = 0
+        rows[:, W] = (torch.arange(n) // 64 * 16).double()
+        rewrite(b, r, rows)
+    b.query[:, :, W] = 40.0
+    first = b.run().clone()
+    assert pkv.workspace_status(b.ws) == 0
+    b.check()
+    for _ in range(20):
+        b.out.fill_(7.0)
+        assert torch.equal(b.run(), first)
+    assert pkv.workspace_status(b.ws) == 0
