@@ -536,7 +536,8 @@ int pkv_latent_gather(void *out, int64_t out_rows, const void *latent_cache, int
  *                    reads as zeros (PKV_ERR_DEVICE_INDEX).
  *  workspace         device scratch, 256-byte aligned, of a fixed size (40 MB) whatever
  *                    the batch.  Its first int32 is the device status word: the call
- *                    stores PKV_OK or an error code there.  One workspace serves any
+ *                    stores PKV_OK or an error code there (PKV_OK, and nothing else, if
+ *                    num_seqs == 0).  One workspace serves any
  *                    number of calls in stream order; calls that may overlap (other
  *                    streams, graphs replayed side by side) need one each.
  *  workspace_needed  if not NULL, receives that size; with workspace == NULL or

@@ -1384,7 +1384,15 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (num_blocks > INT32_MAX || static_cast<int64_t>(num_tokens) * num_heads > INT32_MAX) return PKV_ERR_SHAPE;
     if (!(scale > -3.0e38f && scale < 3.0e38f)) return PKV_ERR_SHAPE;
     if (workspace_needed) *workspace_needed = kLaWsBytes;
-    if (num_seqs == 0) return num_tokens ? PKV_ERR_SHAPE : PKV_OK;
+    if (num_seqs == 0) {
+        if (num_tokens) return PKV_ERR_SHAPE;
+        // no request: of the call's results there is the status word alone (without a workspace
+        // this is the size query)
+        if (workspace && workspace_bytes >= static_cast<size_t>(kLaWsBytes) &&
+            cudaMemsetAsync(workspace, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        return PKV_OK;
+    }
     if (max_query_len > max_seq_len || max_seq_len > INT32_MAX - 128) return PKV_ERR_SHAPE;
     if ((static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock > max_blocks_per_seq) return PKV_ERR_SHAPE;
     if (!workspace || workspace_bytes < static_cast<size_t>(kLaWsBytes)) return PKV_ERR_WORKSPACE;
