@@ -584,7 +584,8 @@ int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stri
  *                    host-side bounds of q_r and L_r.  A request that breaks them, or
  *                    has fewer keys than queries, is left unwritten.
  *  device_status     optional int32 device word, never cleared by the library:
- *                    PKV_ERR_DEVICE_METADATA for such a request.
+ *                    PKV_ERR_DEVICE_METADATA for such a request (also where no token can
+ *                    be answered: num_tokens, num_keys or max_query_len of 0).
  * What lies between or behind the requests' rows may be anything.  An infinity or
  * NaN in a key or value row reaches no token that does not see the row; one that
  * sees a NaN in a key is NaN, and what one that sees another such value gets (NaN

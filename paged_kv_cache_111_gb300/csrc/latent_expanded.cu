@@ -677,6 +677,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
 }
 
+// The requests' check alone, where no token can be answered (no rows, no keys, or a bound of no queries).
+__global__ void __launch_bounds__(kExThreads) latent_expanded_check_kernel(const ExParams p) {
+    for (int r = threadIdx.x; r < p.num_seqs; r += kExThreads)
+        if (!ex_request(p, r).ok) set_status(p.status, PKV_ERR_DEVICE_METADATA);
+}
+
 // {dims, heads, tokens} of 16-bit elements: a box is 64 dims of one head of box_rows tokens.
 static int make_rows_map(CUtensorMap *map, const void *base, int dims_in, int64_t heads, int64_t head_stride,
                          int64_t tokens, int64_t token_stride, int box_rows) {
@@ -710,7 +716,20 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     if (num_keys > INT32_MAX - 256 || num_tokens > INT32_MAX - 256) return PKV_ERR_SHAPE;
     if (!(scale > -3.0e38f && scale < 3.0e38f)) return PKV_ERR_SHAPE;
     if (num_seqs == 0) return num_tokens ? PKV_ERR_SHAPE : PKV_OK;
-    if (num_tokens == 0 || num_keys == 0 || max_query_len == 0) return PKV_OK;
+    ExParams p;
+    p.qsl = query_start_loc, p.ksl = key_start_loc;
+    p.num_seqs = num_seqs, p.num_tokens = num_tokens, p.num_keys = num_keys;
+    p.max_query_len = max_query_len, p.max_key_len = max_key_len;
+    p.heads = num_heads;
+    p.status = device_status;
+    if (num_tokens == 0 || num_keys == 0 || max_query_len == 0) {
+        if (!device_status) return PKV_OK;
+        if (!query_start_loc || !key_start_loc) return PKV_ERR_NULL;
+        if ((reinterpret_cast<uintptr_t>(query_start_loc) | reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)
+            return PKV_ERR_ALIGNMENT;
+        latent_expanded_check_kernel<<<1, kExThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
     if (!out || !query || !key || !key_rope || !value || !query_start_loc || !key_start_loc) return PKV_ERR_NULL;
     constexpr int64_t kMost = int64_t(1) << 38;          // of a tensor map's strides, in elements
     if (key_head_stride < kExNope || value_head_stride < kExV || key_head_stride > kMost || value_head_stride > kMost)
@@ -729,12 +748,7 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     if ((reinterpret_cast<uintptr_t>(query_start_loc) | reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)
         return PKV_ERR_ALIGNMENT;
 
-    ExParams p;
     p.out = static_cast<__nv_bfloat16 *>(out);
-    p.qsl = query_start_loc, p.ksl = key_start_loc;
-    p.num_seqs = num_seqs, p.num_tokens = num_tokens, p.num_keys = num_keys;
-    p.max_query_len = max_query_len, p.max_key_len = max_key_len;
-    p.heads = num_heads;
     // the most that sum of ceil(q_r / 256) can be
     const int64_t bound = (num_tokens + static_cast<int64_t>(num_seqs) * (kExTokens - 1)) / kExTokens;
     const int64_t tiles = bound < num_tokens ? bound : num_tokens;
@@ -745,7 +759,6 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     // from memory once instead of once a token tile.
     p.by_head = static_cast<int64_t>(num_keys) * num_heads * (kExNope + kExV) * 2 > (int64_t(64) << 20);
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.status = device_status;
     CUtensorMap qm, km, rm, vm;
     int rc = make_rows_map(&qm, query, kExDim, h, kExDim, num_tokens, query_token_stride, kExRows);
     if (!rc) rc = make_rows_map(&km, key, kExNope, h, key_head_stride, num_keys, key_token_stride, kExKeys);

@@ -33,3 +33,39 @@ def test_a_batch_without_requests_stores_its_status():
     graph.replay()
     assert pkv.workspace_status(b.ws) == 0
     assert torch.equal(b.out, before)
+
+
+def expanded(q, n, T=None, K=None, max_q=None, max_n=None, H=2):
+    """(status, output) of requests of q[r] queries and n[r] keys, in T rows and K keys."""
+    T, K = sum(q) if T is None else T, sum(n) if K is None else K
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full((T, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    starts = [i32(0, *x).cumsum(0).to(torch.int32) for x in (q, n)]
+    pkv.latent_attn_expanded(out, randn(T, H, 192), randn(K, H, 128), randn(K, 64), randn(K, H, 128), *starts,
+                             max(q) if max_q is None else max_q, max(n) if max_n is None else max_n, 0.07,
+                             device_status=status)
+    return int(status), out
+
+
+@pytest.mark.parametrize("S", [1, 3, 500])
+def test_expanded_reports_requests_that_bounds_of_zero_leave_out(S):
+    status, out = expanded([5] * S, [0] * S, max_n=5)      # queries, and no key at all
+    assert status == METADATA and (out == 7.0).all()
+    status, out = expanded([5] * S, [9] * S, max_q=0)      # a bound that no request keeps
+    assert status == METADATA and (out == 7.0).all()
+    status, out = expanded([0] * (S - 1) + [3], [0] * (S - 1) + [4], T=0)      # queries past the batch
+    assert status == METADATA
+    status, out = expanded([0] * S, [0] * (S - 1) + [4], max_n=3)              # a length past its bound
+    assert status == METADATA
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_expanded_with_nothing_to_do_is_no_error(S):
+    assert expanded([0] * S, [0] * S, T=4, max_q=3, max_n=3)[0] == 0
+    assert expanded([0] * S, [6] * S)[0] == 0
+    status, out = expanded([0] * S, [6] * S, T=4)
+    assert status == 0 and (out == 7.0).all()
