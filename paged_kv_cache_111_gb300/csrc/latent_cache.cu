@@ -275,18 +275,21 @@ extern "C" int pkv_latent_gather(void *out, int64_t out_rows, const void *latent
     if (block_size != kBlock) return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 65535) return PKV_ERR_SHAPE;
     if (num_blocks > INT64_MAX / kLatPageBytes) return PKV_ERR_SHAPE;
-    if (num_seqs == 0 || max_seq_len == 0) return PKV_OK;
+    if (num_seqs == 0) return PKV_OK;
+    // a bound of no rows: nothing is copied, and the lengths are looked at for the status alone
+    const bool any = max_seq_len > 0;
+    if (!any && !device_status) return PKV_OK;
     if ((static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock > max_blocks_per_seq) return PKV_ERR_SHAPE;
-    if (!out || !latent_cache || !block_tables || !seq_lens || !key_start_loc) return PKV_ERR_NULL;
+    if (!seq_lens || !key_start_loc || (any && (!out || !latent_cache || !block_tables))) return PKV_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(latent_cache)) & 15u) return PKV_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
          reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)
         return PKV_ERR_ALIGNMENT;
     const int per = kGatherPages * kBlock;
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(max_seq_len) + per - 1) / per),
-                    static_cast<unsigned>(num_seqs));
+    const int64_t most = any ? (static_cast<int64_t>(max_seq_len) + per - 1) / per : 1;
+    const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>(num_seqs));
     latent_gather_kernel<<<grid, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<uint4 *>(out), out_rows, static_cast<const uint4 *>(latent_cache), num_blocks, block_tables,
-        max_blocks_per_seq, seq_lens, key_start_loc, max_seq_len, device_status);
+        any ? max_blocks_per_seq : 0, seq_lens, key_start_loc, max_seq_len, device_status);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

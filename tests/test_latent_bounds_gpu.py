@@ -69,3 +69,27 @@ def test_expanded_with_nothing_to_do_is_no_error(S):
     assert expanded([0] * S, [6] * S)[0] == 0
     status, out = expanded([0] * S, [6] * S, T=4)
     assert status == 0 and (out == 7.0).all()
+
+
+def gather(lens, starts, rows, bound):
+    """(status, output) of the cached rows of requests in `rows` rows."""
+    cache = torch.ones(9, 16, 576, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(len(lens), -(-bound // 16) + 1, dtype=torch.int32, device="cuda")
+    out = torch.full((rows, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.latent_gather(out, cache, table, i32(*lens), i32(*starts), bound, device_status=status)
+    return int(status), out
+
+
+def test_gather_reports_requests_past_a_bound_of_zero():
+    status, out = gather([0, 3], [0, 0], 5, 0)
+    assert status == METADATA and (out == 7.0).all()
+    assert gather([0, 0], [0, 0], 5, 0)[0] == 0
+
+
+def test_gather_with_a_bound_of_zero_needs_the_lengths_alone():
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, cache = torch.empty(0, 576, dtype=torch.bfloat16, device="cuda"), torch.ones(1, 16, 576).bfloat16().cuda()
+    pkv.latent_gather(out, cache, torch.empty(2, 0, dtype=torch.int32, device="cuda"), i32(0, 0), i32(0, 0), 0,
+                      device_status=status)
+    assert int(status) == 0
