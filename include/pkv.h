@@ -493,6 +493,7 @@ int pkv_latent_kv_write(void *latent_cache, int64_t num_blocks, int32_t block_si
  * (pkv_latent_attn_expanded) are a linear map of these rows.
  *
  *  out             bf16 [out_rows][576]; rows no request covers are left as they were.
+ *                  May be NULL if out_rows == 0 (a batch of empty requests).
  *  block_tables    int32 [num_seqs][max_blocks_per_seq].
  *  seq_lens, key_start_loc
  *                  int32 [num_seqs] (key_start_loc may be longer).

@@ -280,7 +280,7 @@ extern "C" int pkv_latent_gather(void *out, int64_t out_rows, const void *latent
     const bool any = max_seq_len > 0;
     if (!any && !device_status) return PKV_OK;
     if ((static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock > max_blocks_per_seq) return PKV_ERR_SHAPE;
-    if (!seq_lens || !key_start_loc || (any && (!out || !latent_cache || !block_tables))) return PKV_ERR_NULL;
+    if (!seq_lens || !key_start_loc || (any && ((!out && out_rows > 0) || !latent_cache || !block_tables))) return PKV_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(latent_cache)) & 15u) return PKV_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
          reinterpret_cast<uintptr_t>(key_start_loc)) & 3u)

@@ -93,3 +93,9 @@ def test_gather_with_a_bound_of_zero_needs_the_lengths_alone():
     pkv.latent_gather(out, cache, torch.empty(2, 0, dtype=torch.int32, device="cuda"), i32(0, 0), i32(0, 0), 0,
                       device_status=status)
     assert int(status) == 0
+
+
+
+def test_gather_into_no_rows():
+    assert gather([0, 0], [0, 0], 0, 40)[0] == 0
+    assert gather([0, 3], [0, 0], 0, 40)[0] == METADATA    # rows outside the output
