@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kGatherThreads) latent_gather_kernel(
     int id[kGatherPages];
 #pragma unroll
     for (int i = 0; i < kGatherPages; ++i) id[i] = page0 + i < max_blocks_per_seq ? __ldg(table + page0 + i) : -1;
-    if (L < 0 || L > max_seq_len || L > static_cast<int64_t>(max_blocks_per_seq) * kBlock || base < 0 ||
-        base + L > out_rows) {
+    if (L < 0 || L > max_seq_len || L > static_cast<int64_t>(max_blocks_per_seq) * kBlock ||
+        (L > 0 && (base < 0 || base + L > out_rows))) {
         if (threadIdx.x == 0 && blockIdx.x == 0) set_status(status, PKV_ERR_DEVICE_METADATA);
         return;
     }

@@ -99,3 +99,10 @@ def test_gather_with_a_bound_of_zero_needs_the_lengths_alone():
 def test_gather_into_no_rows():
     assert gather([0, 0], [0, 0], 0, 40)[0] == 0
     assert gather([0, 3], [0, 0], 0, 40)[0] == METADATA    # rows outside the output
+
+
+
+def test_gather_takes_no_notice_of_where_an_empty_request_would_start():
+    status, out = gather([2, 0, 0], [1, -1, 1000], 4, 40)
+    assert status == 0
+    assert (out[1:3] == 1.0).all() and (out[0] == 7.0).all() and (out[3] == 7.0).all()
