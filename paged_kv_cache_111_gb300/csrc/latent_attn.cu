@@ -368,6 +368,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // query, and the previous use of the workspace
     pdl_wait();
     pdl_trigger();                        // the merge's CTAs may take their places (they wait for this grid)
+    // the call's status word starts afresh here, before any CTA of the merge looks at it: errors
+    // are only ever added to it then, the first one stays
+    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = PKV_OK;
     const bool work = lo < hi;
     // for the merge kernel, {first token, tokens, lanes that it runs across, this lane among them}: the row tile
     // that starts here and ends in another lane, and the one that started in an earlier lane
@@ -1070,7 +1073,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 //    of its first four lanes by rows, and in each over two halves of the pieces
 //    (1000 keys of one request, 16 heads: 15.4 us with one after another, 11.6 us).
 
-// The call's status: the first error of its CTAs.
+// The call's status: the first error of its CTAs (beside one that a CTA of the merge itself adds).
 __device__ __forceinline__ void la_collect_status(const LaParams &p, int ctas) {
     if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= 32) return;
     int32_t s = 0;
@@ -1083,7 +1086,7 @@ __device__ __forceinline__ void la_collect_status(const LaParams &p, int ctas) {
         const int32_t y = __shfl_down_sync(0xffffffffu, s, m);
         s = s ? s : y;
     }
-    if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = s;
+    if (threadIdx.x == 0 && s) set_status(reinterpret_cast<int32_t *>(p.ws), s);
 }
 
 // Four rows (4 r4 ..) of one dim a thread to `out`: neighbouring lanes exchange a

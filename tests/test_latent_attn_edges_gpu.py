@@ -36,3 +36,19 @@ def test_scores_that_jump_where_items_meet(H, seqs):
         b.out.fill_(7.0)
         assert torch.equal(b.run(), first)
     assert pkv.workspace_status(b.ws) == 0
+
+
+@pytest.mark.parametrize("H,seqs", [(16, 3), (128, 200)])  # either form of the merge
+@pytest.mark.parametrize("word", [0, 9, -1, 7])
+def test_the_status_word_starts_afresh(H, seqs, word):
+    b = Batch(7, [(1, 70 + r % 90) for r in range(seqs)], H)
+    table, lens = b.bt.clone(), b.lens.clone()
+    for code in (0, 7, 8):
+        b.ws[:4].view(torch.int32).fill_(word)
+        b.bt.copy_(table), b.lens.copy_(lens)
+        if code == 7:
+            b.bt[seqs - 1, 0] = -1
+        if code == 8:
+            b.lens[0] = 0
+        b.run()
+        assert pkv.workspace_status(b.ws) == code
