@@ -45,7 +45,8 @@
 // warp 2 loads Q (TMA), zeroes the rows past a tile's last visible key
 // (so that what an unwritten slot holds never meets a zero weight) and owns
 // tensor memory; warps 4-7 are the softmax; warps 9-12 write finished tiles out
-// while the softmax is at the next one.  Every wait is bounded.
+// while the softmax is at the next one.  Every wait is bounded; those that last as long as an
+// item go by the tiles loaded meanwhile.
 //
 // What bounds it: shared memory.  A 64-key tile takes 36 x 4 KiB for S, 16 x 6 KiB for
 // the second products, 72 KiB of loads and 8 of weights, 320 KiB at 128 bytes a cycle: 2560
@@ -151,7 +152,7 @@ struct LaItem {
     int32_t slot;             // -1: complete, written to out; else the partial slot of this CTA
     int32_t r;                // request
 };
-static_assert(kLaItemSlots * sizeof(LaItem) <= 160, "item ring");
+static_assert(kLaItemSlots * sizeof(LaItem) + 4 <= 160, "item ring, tiles loaded");
 
 // What the softmax warps leave for the warps that write a finished item out.
 struct LaRows {
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     volatile uint8_t *votes = reinterpret_cast<volatile uint8_t *>(tmem_slot + 2);    // [tile % kLaVotes][warp]
     int64_t *scan = reinterpret_cast<int64_t *>(smem + kLaOffAlpha);    // before the roles start only
     volatile LaItem *items = reinterpret_cast<volatile LaItem *>(smem + kLaOffItems);
+    volatile int32_t *tiles = reinterpret_cast<volatile int32_t *>(smem + kLaOffItems + kLaItemSlots * sizeof(LaItem));
     const uint32_t sQ = smem_u32(smem + kLaOffQ), sKV = smem_u32(smem + kLaOffKV), sOut = smem_u32(smem + kLaOffOut);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     const int my_lane = blockIdx.x / p.groups;               // run
@@ -302,6 +304,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         tma_prefetch_desc(&b_map);
         tma_prefetch_desc(&q_map);
         *status = PKV_OK;
+        *tiles = 0;
     }
     if (warp == 2) {
         tmem_alloc(tmem_slot, kLaTmemCols);
@@ -388,8 +391,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         for (int k = 0; ok; ++k) {
             const int slot = k % kLaItemSlots;
             if (k >= kLaItemSlots)
-                ok = __all_sync(0xffffffffu,
-                                pf_wait(&bars[kLaItemEmpty + slot], (k / kLaItemSlots - 1) & 1, status));
+                ok = warp_wait_tiles(&bars[kLaItemEmpty + slot], (k / kLaItemSlots - 1) & 1, tiles, status);
             if (!ok) break;
             LaItem it{};
             while (left > 0 && !it.valid) {
@@ -522,6 +524,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                     part ? &b_map : &a_map, &bars[kLaKVFull + b], 0, 0, part ? kLaChunksA : 0, 0, id);
                     issued = 2 * gt + part + 1;
                 }
+                if (lane == 0) *tiles = gt + 1;
             }
             win_cur = ahead0, win_next = ahead1;
         }
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
             // the previous item's last S has read its Q (and that tile's keys)
-            if (k > 0) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaQEmpty], (k - 1) & 1, status));
+            if (k > 0) ok = warp_wait_tiles(&bars[kLaQEmpty], (k - 1) & 1, tiles, status);
             if (!ok) break;
             if (valid) {
                 // a box is 64 dims of the group's heads of tpt tokens; tokens past the batch
@@ -932,7 +935,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             if (lane == 0) mbar_arrive(&bars[kLaItemEmpty + slot]);
             if (!valid) break;
             const int rb = k & 1;
-            ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaRowFull + rb], (k >> 1) & 1, status));
+            ok = warp_wait_tiles(&bars[kLaRowFull + rb], (k >> 1) & 1, tiles, status);
             if (ok) ok = __all_sync(0xffffffffu, pf_wait(&bars[kLaOReady], k & 1, status));
             if (!ok) break;
             tc_fence_after();

@@ -38,4 +38,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_
     return ok;
 }
 
+// A converged warp's wait for an event that may be any number of key tiles away (the end of an
+// item, the tiles on the causal diagonal): it gives up once no tile has been loaded for as long as
+// a bounded wait lasts.  Between two looks at `tiles`, which the loading warp counts up, lie at
+// least kWaitLimitNs.  (13.8 M keys at 1.85 us a 128-key tile, or 10 M at 1.25 us a 64-key one,
+// take a CTA longer than that limit.)
+__device__ __forceinline__ bool warp_wait_tiles(uint64_t *bar, uint32_t parity, const volatile int32_t *tiles,
+                                                int32_t *status) {
+    int32_t seen = uniform(*tiles);
+    while (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
+        const int32_t now = uniform(*tiles);
+        if (now == seen) {
+            set_status(status, PKV_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+        seen = now;
+    }
+    return true;
+}
+
 }  // namespace pkv

@@ -32,7 +32,8 @@
 // owns tensor memory, warps 2 and 3 look V over where the causal mask cuts through a
 // key tile, warps 4-7 and 8-11 are the softmax and epilogue of the
 // two row tiles.  V rows past the last visible key are zeroed in shared memory
-// (they belong to other requests, or to nobody).  Every mbarrier wait is bounded.
+// (they belong to other requests, or to nobody).  Every mbarrier wait is bounded; that for the
+// diagonal, which may be all of a long request away, by the key tiles loaded meanwhile.
 //
 // Where token tiles are few, the CTAs of a cluster share a tile's keys and join their
 // sums through distributed shared memory (the rule and its figures: at the launch).
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kExNumBars);
     int32_t *scan = reinterpret_cast<int32_t *>(tmem_slot + 2);       // 12 warps' sums, then {request, tile}
     int32_t *odd_key = scan + 18;                                     // first key whose V is no number (on the diagonal)
+    volatile int32_t *tiles = scan + 19;                              // key tiles loaded
     const uint32_t sQ = smem_u32(smem + kExOffQ), sRing = smem_u32(smem + kExOffRing);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
     // Token tiles (256 tokens of a request) are ranked by the key tiles they see, the
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     // first key that the first row does not see, and the first tile (if any) with such keys
     const int edge = ctx + t0 + 1, diag = edge < end ? max(0, edge / kExKeys - j0) : n_all;
 
-    if (threadIdx.x == 0) *odd_key = INT32_MAX;
+    if (threadIdx.x == 0) *odd_key = INT32_MAX, *tiles = 0;
     if (threadIdx.x < kExNumBars)
         mbar_init(&bars[threadIdx.x], threadIdx.x >= kExPFull && threadIdx.x < kExPFull + 2 ? 4 : (threadIdx.x >= kExChecked ? 2 : 1));
     if (warp == 2) {
@@ -362,6 +364,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
                 issued = s + 1;
             }
+            if (lane == 0) *tiles = j + 1;
             if (ok && j >= diag && lane == 0) mbar_arrive(&bars[kExLoaded + ((j - diag) & 1)]);
         }
         if (ok && fix) {
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
         bool ok = true;
         for (int j = diag; j < n_all && ok; ++j) {
             const int d = j - diag, s = j * kExPerTile + 3 + h;
-            ok = __all_sync(0xffffffffu, pf_wait(&bars[kExLoaded + (d & 1)], (d >> 1) & 1, status)) &&
+            ok = warp_wait_tiles(&bars[kExLoaded + (d & 1)], (d >> 1) & 1, tiles, status) &&
                  __all_sync(0xffffffffu, pf_wait(&bars[kExFull + s % kExSlots], (s / kExSlots) & 1, status));
             if (!ok) break;
             const int key0 = (j0 + j) * kExKeys + 64 * h, lo = max(edge - key0, 0), hi = min(end - key0, 64);
