@@ -483,8 +483,8 @@ def _qk_norm_rope(fp8: bool, query_out, kv_cache, query, key, value, q_weight, k
     v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
     table = _full("cos_sin", cos_sin, _F32, dev, (-1, -1), "a contiguous [max_position, rotary_dim]")
     max_position, rot = cos_sin.shape
-    lib = _lib or load()
-    _call(dev, "pkv_qk_norm_rope_kv_write", lib.pkv_qk_norm_rope_kv_write_fp8 if fp8 else lib.pkv_qk_norm_rope_kv_write,
+    name = "pkv_qk_norm_rope_kv_write_fp8" if fp8 else "pkv_qk_norm_rope_kv_write"
+    _call(dev, name, getattr(_lib or load(), name),
           qo, qo_step, kv_cache.data_ptr(), nb, H, hkv, d, bs, q, q_step, k, k_step, v, v_step,
           _full("q_weight", q_weight, _BF16, dev, (d,), "[d]"), _full("k_weight", k_weight, _BF16, dev, (d,), "[d]"),
           eps, table, max_position, rot, 1 if interleaved else 0,
