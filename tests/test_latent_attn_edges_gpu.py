@@ -52,3 +52,24 @@ def test_the_status_word_starts_afresh(H, seqs, word):
             b.lens[0] = 0
         b.run()
         assert pkv.workspace_status(b.ws) == code
+
+
+@pytest.mark.parametrize("H,short,long", [(128, 63, 40000), (64, 100, 20000), (40, 160, 9000), (128, 30, 3000)])
+def test_one_long_request_among_many_short_ones(H, short, long):
+    """As many row tiles as make the merge one CTA a lane's tile, and among them one of many pieces."""
+    g = torch.Generator().manual_seed(short)
+    reqs = [(1, int(n)) for n in torch.randint(1, 70, (short,), generator=g)]
+    reqs.insert(short // 3, (1, long))
+    b = Batch(51, reqs, H, extra_rows=1)
+    first = b.run().clone()
+    assert pkv.workspace_status(b.ws) == 0
+    b.check()
+    b.ws.random_(0, 256)
+    assert torch.equal(b.run(), first)
+    # a NaN in one of the pieces makes that request's rows NaN, and no other's
+    b.cache[b.bt[short // 3, long // 32].long(), 3, 5] = float("nan")
+    b.out.fill_(7.0)
+    b.run()
+    assert torch.isnan(b.out[short // 3]).all()
+    b.out[short // 3] = first[short // 3]
+    assert torch.equal(b.out, first)
