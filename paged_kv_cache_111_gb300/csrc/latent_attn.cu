@@ -371,9 +371,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // query, and the previous use of the workspace
     pdl_wait();
     pdl_trigger();                        // the merge's CTAs may take their places (they wait for this grid)
-    // the call's status word starts afresh here, before any CTA of the merge looks at it: errors
-    // are only ever added to it then, the first one stays
-    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = PKV_OK;
     const bool work = lo < hi;
     // for the merge kernel, {first token, tokens, lanes that it runs across, this lane among them}: the row tile
     // that starts here and ends in another lane, and the one that started in an earlier lane
@@ -517,14 +514,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                         ok = __all_sync(0xffffffffu,
                                         pf_wait(&bars[kLaKVEmpty + b], (gt / kLaStages - 1) & 1, status));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bars[kLaKVFull + b], part ? kLaPartB : kLaPartA);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars[kLaKVFull + b], part ? kLaPartB : kLaPartA);
+                        *tiles = gt + 1;
+                    }
                     __syncwarp();
                     if (lane < kLaPages)
                         tma_load_5d(smem + kLaOffKV + st * kLaStage + (part ? kLaPartA + lane * kLaPageB : lane * kLaPageA),
                                     part ? &b_map : &a_map, &bars[kLaKVFull + b], 0, 0, part ? kLaChunksA : 0, 0, id);
                     issued = 2 * gt + part + 1;
                 }
-                if (lane == 0) *tiles = gt + 1;
             }
             win_cur = ahead0, win_next = ahead1;
         }
@@ -1057,6 +1056,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         int32_t s = *reinterpret_cast<volatile int32_t *>(status);
         if (s == PKV_OK && any_bad) s = PKV_ERR_DEVICE_METADATA;
         reinterpret_cast<int32_t *>(p.ws + kLaWsStatus)[blockIdx.x] = s;
+        // the call's own word starts afresh, before any CTA of the merge looks at it: those only
+        // add errors to it, and the first one stays
+        if (blockIdx.x == 0) *reinterpret_cast<int32_t *>(p.ws) = PKV_OK;
     }
 }
 

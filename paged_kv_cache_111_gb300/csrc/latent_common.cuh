@@ -39,13 +39,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_
 }
 
 // A converged warp's wait for an event that may be any number of key tiles away (the end of an
-// item, the tiles on the causal diagonal): it gives up once no tile has been loaded for as long as
-// a bounded wait lasts.  Between two looks at `tiles`, which the loading warp counts up, lie at
-// least kWaitLimitNs.  (13.8 M keys at 1.85 us a 128-key tile, or 10 M at 1.25 us a 64-key one,
-// take a CTA longer than that limit.)
+// item, the tiles on the causal diagonal): it gives up once no tile has been loaded between two
+// looks at `tiles`, which the loading warp counts up; a bounded wait lies before each look.
+// (That one is over after 13.8 M keys at 1.85 us a 128-key tile, or 10 M at 1.25 us a 64-key one.)
 __device__ __forceinline__ bool warp_wait_tiles(uint64_t *bar, uint32_t parity, const volatile int32_t *tiles,
                                                 int32_t *status) {
-    int32_t seen = uniform(*tiles);
+    int32_t seen = -1;
     while (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
         const int32_t now = uniform(*tiles);
         if (now == seen) {

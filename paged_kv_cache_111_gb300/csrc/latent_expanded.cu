@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     uint64_t *bar = &bars[kExFull + slot];
                     uint8_t *dst = smem + kExOffRing + slot * kExChunk;
                     mbar_arrive_expect_tx(bar, kExChunk);
+                    *tiles = j + 1;
                     if (e < 2) {
                         tma_load_3d(dst, &k_map, bar, e * 64, head, key0);
                     } else if (e == 2) {
@@ -364,7 +365,6 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
                 issued = s + 1;
             }
-            if (lane == 0) *tiles = j + 1;
             if (ok && j >= diag && lane == 0) mbar_arrive(&bars[kExLoaded + ((j - diag) & 1)]);
         }
         if (ok && fix) {
