@@ -39,11 +39,13 @@
  *  - The attention calls launch their first kernel with programmatic
  *    dependent launch: it may start while the kernel just before it on the
  *    stream (normally pkv_kv_write) is still running, and it reads
- *    seq_lens, query_start_loc and block_tables at once.  Work of any
- *    ordinary kind before the call (copies, memsets, kernels launched
- *    without programmatic dependent launch) is complete by then.  A
- *    caller's own kernel that releases its dependents early
- *    (griddepcontrol.launch_dependents) must write that metadata first.
+ *    seq_lens, query_start_loc, key_start_loc and block_tables at once
+ *    (pkv_latent_attn_expanded may store an error in its device_status
+ *    then, too).  Work of any ordinary kind before the call (copies,
+ *    memsets, kernels launched without programmatic dependent launch) is
+ *    complete by then.  A caller's own kernel that releases its dependents
+ *    early (griddepcontrol.launch_dependents) must write that metadata,
+ *    and clear that status word, first.
  *
  * KV cache layout (this library's own, not the one printed on the pages):
  *     bf16 kv_cache[num_blocks][num_kv_heads][2][16][head_size]
@@ -592,6 +594,10 @@ int pkv_latent_paged_attn(void *out, const void *query, int64_t query_token_stri
  * sees a NaN in a key is NaN, and what one that sees another such value gets (NaN
  * in all its dims, or in those) is not defined.  Pointers are 16-byte aligned, strides
  * multiples of 8.  No workspace.
+ * Like the attention calls above, the kernel may start while the kernel before it
+ * (normally the up-projection that makes key and value) still runs.  It reads
+ * query_start_loc and key_start_loc, and reports requests that break their
+ * bounds, at once; the tensors only when that kernel has ended.
  */
 int pkv_latent_attn_expanded(void *out, const void *query, int64_t query_token_stride,
                              const void *key, int64_t key_token_stride, int64_t key_head_stride,
