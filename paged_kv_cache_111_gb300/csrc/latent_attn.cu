@@ -51,9 +51,9 @@
 // What bounds it: shared memory.  A 64-key tile takes 36 x 4 KiB for S, 16 x 6 KiB for
 // the second products, 72 KiB of loads and 8 of weights, 320 KiB at 128 bytes a cycle: 2560
 // cycles, and 2500 to 2740 are measured.  A row tile costs 6000 cycles beside its key
-// tiles, the merge about 8 us a call.  256 requests of 16 to 4096 keys, 128 heads (330
-// MB, 62.6 GFLOP): 94 us, 3.5 TB/s, 670 TFLOP/s.  Two decodes and a 2046-token chunk of
-// 16 heads (109 GFLOP): 132 us, 820 TFLOP/s.  Bringing Q in in two parts, or into L2 ahead
+// tiles, the merge 10 us a call (of four short requests 3.6).  256 requests of 16 to 4096 keys,
+// 128 heads (330 MB, 62.6 GFLOP): 94 us, 3.5 TB/s, 665 TFLOP/s.  Two decodes and a 2046-token
+// chunk of 16 heads (109 GFLOP): 132.5 us, 820 TFLOP/s.  Bringing Q in in two parts, or into L2 ahead
 // of its item, gained nothing (94 to 96 us).
 #include <mutex>
 #include <type_traits>
@@ -1068,12 +1068,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i.
 // The merge is one trip to memory that the first kernel has just written, and
 // nothing else.  Two kernels, by what a call can hold:
-//  - many row tiles, so most tiles have two pieces and nearly every lane starts
-//    one: latent_merge_kernel, a CTA for 128 dims of a lane's tile, which takes the
-//    two pieces in bulk into shared memory (64 KiB a CTA, three CTAs an SM: twice
+//  - many row tiles, so that of like lengths most have two pieces and nearly every
+//    lane starts one: latent_merge_kernel, a CTA for 128 dims of a lane's tile, which takes
+//    the two pieces in bulk into shared memory (64 KiB a CTA, three CTAs an SM: twice
 //    what registers could have in flight; 256 requests of 128 heads, 40 MB: 15 us by
-//    registers) before it knows whether there is a tile to merge;
-//  - few, so a tile can have many pieces (a long request on an otherwise idle GPU):
+//    registers) before it knows whether there is a tile to merge, and any further pieces one
+//    after another (a request far longer than the others has them, and waits for them);
+//  - few, so that every tile can have many pieces (a long request on an otherwise idle GPU):
 //    latent_merge_few_kernel, which shares a tile of many pieces out over the CTAs
 //    of its first four lanes by rows, and in each over two halves of the pieces
 //    (1000 keys of one request, 16 heads: 15.4 us with one after another, 11.6 us).
@@ -1220,7 +1221,10 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LaParams p, int
     }
 }
 
-constexpr int kLaMany = 8;                    // pieces from which a tile is shared out
+// Pieces from which a tile is shared out: 16 heads, one request of 512 keys (8 pieces): 10.5 us shared
+// out, 11.6 not; 20000 keys (152): 21.8 and 55.9.  From four on (16 requests of 4000 keys, 128 heads, five
+// or six pieces each): 43.6 where eight give 39.6.
+constexpr int kLaMany = 8;
 
 // blockIdx.y: 128 dims x 16 rows; a thread takes one dim of eight rows.
 __global__ void __launch_bounds__(256) latent_merge_few_kernel(const LaParams p, int ctas) {
@@ -1476,8 +1480,12 @@ extern "C" int pkv_latent_paged_attn(void *out, const void *query, int64_t query
     if (launch_pdl(latent_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kLaThreads), kLaSmem,
                    static_cast<cudaStream_t>(stream), am, bm, qm, om, p) != cudaSuccess)
         return PKV_ERR_CUDA;
-    // a tile can have many pieces only where the row tiles are few; and of few rows there
-    // is little to bring in in bulk
+    // All tiles can have many pieces only where they are few; and of few rows there is little to
+    // bring in in bulk.  1000 keys, 128 heads (76 lanes), calls merged few / in bulk: 4 requests 18.1 /
+    // 30.4 us, 8: 21.9 / 24.8, 16: 24.9 / 25.7, 19: 26.4 / 26.6, 24: 28.1 / 27.2, 48: 37.8 / 33.9, 76 and
+    // more within 4%; 64 heads (152 lanes), 30: 27.5 / 28.0, 39: 29.8 / 29.3, 76: 38.7 / 35.4.  256 requests
+    // of 16 rows 66.1 / 71.9, 32: 71.4 / 74.3, 33: 73.7 / 75.8, 40: 74.6 / 74.2, 48: 76.6 / 74.6, 64: 81.1 /
+    // 75.8.
     const bool bulk = most > p.lanes / 4 && p.hpt * p.tpt > 32;
     const dim3 lanes(static_cast<unsigned>(ctas), bulk ? 4 : 16);
     if ((bulk ? launch_pdl(latent_merge_kernel, lanes, dim3(256), 2 * la_merge_bytes(p) + kLaMergeExtra,

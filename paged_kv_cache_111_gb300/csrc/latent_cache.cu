@@ -11,12 +11,14 @@
 //
 // Gather: the cached rows of every request, in order, into one contiguous
 // array (the input of the up-projection to per-head keys and values).  A page
-// is one run of 18432 bytes in both, so this is a copy of runs.
+// is one run of 18432 bytes in both, so this is a copy of runs.  The grid is requests x pages of
+// the longest, so a batch with one request far longer than the others launches mostly CTAs that
+// leave at once.
 //
 // Both move bytes and compute next to nothing.  The gather is bound by memory (204 k rows of
-// 256 requests, 471 MB: 79.6 us, 5.9 TB/s, 87% of a plain copy's rate).  The write is bound
+// 256 requests, 471 MB: 78 us, 6.0 TB/s, 89% of a plain copy's rate).  The write is bound
 // by the latency of its chain (position and slot, table row, sums over the warp) at four waves
-// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 12.3 us, 66% of a copy's
+// of CTAs: 8191 tokens with 16 query heads, 54.7 MB, 12.4 us, 65% of a copy's
 // rate (13.7 with the partner dims fetched from other lanes and 64 registers).
 #include "latent_common.cuh"
 #include "norm_rope.cuh"
@@ -42,7 +44,9 @@ struct LatentWriteParams {
 
 constexpr int kRopeRows = 16;                      // query heads per warp
 constexpr int kWriteThreads = 128;
-constexpr int kWriteCtas = 10;                     // CTAs an SM: 48 registers (56: 12.3 us, 64: 12.9, 40: 13.3)
+// CTAs an SM: ten leave 48 registers and 32 spilled bytes a thread: 12.4 us on 8191 tokens with 16 query
+// heads; nine (56, 4 bytes) 12.6, eight (64, none) 13.0, twelve (40) 13.3.
+constexpr int kWriteCtas = 10;
 
 // Lane l of eight has planes 4 l .. 4 l + 3 of a row's 64 rotated dims: two pieces of four dims that
 // turn with one another, or of two planes each where a plane's dims are neighbours.  No lane

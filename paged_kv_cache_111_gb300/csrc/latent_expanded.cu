@@ -21,8 +21,8 @@
 // five a key tile: K's three 64-dim chunks, then V's two halves of 64 keys.  Each
 // slot is loaded again when the second row tile's product has read it, a key
 // tile's time or so before it is used again.  (K in two whole stages and V in one
-// left V's load, about 1500 cycles, in the way of every tile: 842 us against 782 us
-// on 2048 tokens at 8192 keys of 128 heads.)
+// left V's load, about 1500 cycles, in the way of every tile: 7% of the time of 2048
+// tokens at 8192 keys of 128 heads.)
 //
 // Against the latent-space form this does (128 + 64 + 128) / (576 + 512) = 0.29
 // of the products per visible pair, and reads keys per head: the form for long
@@ -43,7 +43,7 @@
 // (128 bytes a cycle); the rest is the turn between the two row tiles.  2048 tokens at
 // 8192 keys of 128 heads (1.2 TFLOP): 790 us with cold caches, 1520 TFLOP/s, 78% of the
 // dense bf16 rate; 725 us back to back.  Three requests of 300 to 2046 tokens of 16 heads
-// (21 GFLOP): 33.5 us, the 16 key tiles of the longest one's last tokens one after another.
+// (21 GFLOP): 33.4 to 36 us, the 16 key tiles of the longest one's last tokens one after another.
 #include <mutex>
 
 #include "latent_common.cuh"
@@ -759,7 +759,11 @@ extern "C" int pkv_latent_attn_expanded(void *out, const void *query, int64_t qu
     p.tiles = static_cast<int32_t>(tiles);
     // Keys and values of every head at once outgrow L2 (126 MB) long before one head's
     // do: then the token tiles of a head run side by side, and its keys and values come
-    // from memory once instead of once a token tile.
+    // from memory once instead of once a token tile.  All heads of a rank / all ranks of a head:
+    // 2048 tokens at 8192 keys of 128 heads (537 MB of keys and values) 855 / 775 us, 1024 tokens
+    // there 462 / 451; 268 MB, 2048 tokens at 4096 keys of 128 heads 372 / 371, at 8192 of 64 heads 419 /
+    // 429; 134 MB, 16 heads at 16384 keys 218 / 227; 33 MB, 16 heads at 4096 keys 57.7 / 65.7.  So the
+    // bound is on the low side: between it and some 270 MB the order costs up to 8%.
     p.by_head = static_cast<int64_t>(num_keys) * num_heads * (kExNope + kExV) * 2 > (int64_t(64) << 20);
     p.scale_log2 = scale * 1.4426950408889634f;
     CUtensorMap qm, km, rm, vm;

@@ -19,7 +19,7 @@
 // arithmetic runs on pairs (f32x2).  Whole rows on 16-byte pieces, with the partner
 // dims fetched from other lanes, took four times the instructions: 60 us on 8192
 // tokens of 32/8 heads of 128 (206 MB), against 36 us (5.7 TB/s, 85% of a plain copy's
-// rate).  The E4M3 form, 2048 tokens of 64/8 heads (80 MB): 17.4 us.
+// rate).  The E4M3 form, 2048 tokens of 64/8 heads (80 MB): 17.4 us (neighbouring dims), 18.9 (halves).
 #include "norm_rope.cuh"
 #include "prefill_common.cuh"
 
@@ -27,7 +27,11 @@ namespace pkv {
 
 constexpr int kRowsUnroll = 4;                   // rows a lane
 constexpr int kQkThreads = 128;                  // (256: 41 us where 128 take 39)
-constexpr int kQkCtas = 9;                       // CTAs an SM: 56 registers (64 and fewer CTAs: 38 us, 48: 37)
+// CTAs an SM: nine leave 56 registers, with which the E4M3 forms spill (halves: 28 bytes stored and 100
+// loaded a thread, pairs: 12 and 48); they are the fastest all the same.  2048 tokens of 64/8 heads, at
+// nine, eight (64 registers, 4 bytes spilled) and seven (72, none): E4M3 pairs 17.3, 18.2, 18.8 us,
+// halves 18.9, 19.2, 19.9, bf16 17.8, 18.6, 18.6; the 8192-token chunk 36, 38 at eight, 37 at ten.
+constexpr int kQkCtas = 9;
 
 struct QkParams {
     __nv_bfloat16 *query_out;
