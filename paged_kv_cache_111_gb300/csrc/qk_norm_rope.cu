@@ -18,7 +18,7 @@
 // position, slot, then the table row) is issued before any arithmetic; the
 // arithmetic runs on pairs (f32x2).  Whole rows on 16-byte pieces, with the partner
 // dims fetched from other lanes, took four times the instructions: 60 us on 8192
-// tokens of 32/8 heads of 128 (206 MB), against 36 us (5.7 TB/s, 85% of a plain copy's
+// tokens of 32/8 heads of 128 (206 MB), against 36 us (5.7 TB/s, 84% of a plain copy's
 // rate).  The E4M3 form, 2048 tokens of 64/8 heads (80 MB): 17.4 us (neighbouring dims), 18.9 (halves).
 #include "norm_rope.cuh"
 #include "prefill_common.cuh"
