@@ -95,11 +95,9 @@ def test_gather_with_a_bound_of_zero_needs_the_lengths_alone():
     assert int(status) == 0
 
 
-
 def test_gather_into_no_rows():
     assert gather([0, 0], [0, 0], 0, 40)[0] == 0
     assert gather([0, 3], [0, 0], 0, 40)[0] == METADATA    # rows outside the output
-
 
 
 def test_gather_takes_no_notice_of_where_an_empty_request_would_start():
