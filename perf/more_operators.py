@@ -2,13 +2,13 @@
 
 The cache holds a code a value and an fp32 scale for each block of 16 tokens, head and side (K, V).  ``store`` quantises
 a step's keys and values into it and reads the requests back; ``qk-store`` does so behind the norm and rotation of the
-heads; ``attn`` is causal attention over such a cache; ``gather`` reads requests back as bf16; ``copy`` copies blocks with
-their scales.  Lengths are those of the engine steps that the benchmark names: small and large decode batches, and a
+heads; ``attn`` is causal attention over such a cache; ``gather`` reads requests back as bf16; ``copy`` copies blocks
+with their scales.  Lengths are those of the engine steps that the benchmark names: small and large decode batches, and a
 mixed step of decodes and a 2046-token prefill chunk.
 
 Writing.  a = max |x| over the rows of one block, head and side that a step writes, s' = max(a / 127, 2^-60).  A block
-whose first row is written takes the scale s = s', any other s = max(old scale, s'); rows that were there are requantised
-when the scale grows, code = rint(code * old scale / s).  A new code is rint(x / s).  Both quotients are products with
+whose first row is written takes the scale s = s', any other s = max(old scale, s'); rows that were there are
+requantised when the scale grows, code = rint(code * old scale / s).  A new code is rint(x / s).  Both quotients are products with
 r = 1 / s (32 bits) that are rounded once, to the code: x * r, and code * (old scale * r) with 32 bits in the bracket.
 """
 
@@ -325,9 +325,10 @@ def _plain_write(s, key, value):
     r = torch.reciprocal(scale)
     kept = s["cache"][fresh_or_not].float()
     grown = (scale > old) & ~fresh
-    kept = torch.where(grown[..., None, None], (kept.double() * (old * r).double()[..., None, None]).round().float(), kept)
     # (products in 64 bits: they are exact there, and next to a border between codes the last bit decides)
-    codes = torch.where(written[:, None, None, :, None], (new.double() * r.double()[..., None, None]).round().float(), kept)
+    moved, made = (kept.double() * (old * r).double()[..., None, None], new.double() * r.double()[..., None, None])
+    kept = torch.where(grown[..., None, None], moved.round().float(), kept)
+    codes = torch.where(written[:, None, None, :, None], made.round().float(), kept)
     s["cache"][fresh_or_not] = codes.to(torch.int8)
     s["scales"][fresh_or_not] = scale
 
