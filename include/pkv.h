@@ -608,6 +608,116 @@ int pkv_latent_attn_expanded(void *out, const void *query, int64_t query_token_s
                              int32_t max_query_len, int32_t max_key_len,
                              int32_t num_heads, float scale, int32_t *device_status, void *stream);
 
+/*
+ * The int8 cache: pages as the E4M3 cache's, one byte per element, and a scale
+ * for each block, kv head and side, made of the data as it is written,
+ *     int8  kv_cache [num_blocks][num_kv_heads][2][16][head_size]
+ *     float kv_scales[num_blocks][num_kv_heads][2]
+ * (index 0 of the axis of 2 is K, 1 is V).  Code c stands for c * its scale.  There
+ * is nothing to calibrate, and nothing saturates: a value written into a fresh block
+ * is off by at most half a step, the largest magnitude beside it / 254.  Scales are
+ * >= 0; those that the calls below write are 2^-60 at least, or NaN.
+ *
+ * pkv_kv_write_int8 — the cache write.  The rows that a call writes into one
+ * block, for each kv head and side apart, with a the largest magnitude in them:
+ *     s' = max(a * (1/127), 2^-60)
+ *     s  = s' if row 0 of the block is among them (the block starts anew), else
+ *          max(the block's scale, s');   r = 1 / s
+ *     code = rint(x * r) for the new rows; where s grew, rint(code * (old scale * r))
+ *          for the block's other rows.
+ * r, s and old scale * r are fp32; rint, to nearest even, is the one rounding of the
+ * products x * r and code * (..).  Rows requantised g
+ * times are off by at most (g + 1) / 2 of their block's step.  If a value is an
+ * infinity or NaN, s is NaN, and stays NaN until the block starts anew: all 16
+ * rows of that block, head and side read as NaN.
+ *
+ *  kv_cache, kv_scales  16- and 8-byte aligned.  num_blocks < 2^31.
+ *  key, value, strides  as pkv_kv_write.
+ *  slot_mapping         int64 [num_tokens]; negative: padding.  The tokens of one block
+ *                       stand next to each other, as a request's tokens do, in any
+ *                       order; if other tokens (or padding) lie between them, that block's
+ *                       rows and scale are not defined.  Of tokens with one slot the last
+ *                       is written.
+ *  device_status        as pkv_kv_write; tokens of slots past the cache are skipped, as is
+ *                       what follows the 16th token of one block in a row (of which
+ *                       two must have one slot): PKV_ERR_DEVICE_INDEX.
+ */
+int pkv_kv_write_int8(void *kv_cache, float *kv_scales, int64_t num_blocks,
+                      int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                      const void *key, int64_t key_token_stride,
+                      const void *value, int64_t value_token_stride,
+                      const int64_t *slot_mapping, int32_t num_tokens,
+                      int32_t *device_status, void *stream);
+
+/*
+ * pkv_qk_norm_rope_kv_write_int8 — pkv_qk_norm_rope_kv_write into an int8 cache: the
+ * keys' fp32 values (they are not rounded to bf16 on the way) and the values are
+ * quantised as by pkv_kv_write_int8, slot_mapping as there.  A token whose position is
+ * outside the table counts for no scale.
+ */
+int pkv_qk_norm_rope_kv_write_int8(void *query_out, int64_t query_out_token_stride,
+                                   void *kv_cache, float *kv_scales, int64_t num_blocks,
+                                   int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_size, int32_t block_size,
+                                   const void *query, int64_t query_token_stride,
+                                   const void *key, int64_t key_token_stride,
+                                   const void *value, int64_t value_token_stride,
+                                   const void *q_weight, const void *k_weight, float eps,
+                                   const float *cos_sin, int64_t max_position,
+                                   int32_t rotary_dim, int32_t interleaved,
+                                   const int64_t *positions, const int64_t *slot_mapping,
+                                   int32_t num_tokens, int32_t *device_status, void *stream);
+
+/*
+ * pkv_paged_attn_int8 — pkv_paged_attn over an int8 cache, K_j and V_j being code *
+ * scale.  Arguments, workspace and protocol (pkv_paged_attn_combine after it) as
+ * pkv_paged_attn; any scale's sign is allowed.  Codes widen to f16 exactly; the query
+ * enters the products as f16 after a per-row power-of-two scaling (exact for every
+ * element not below 2^-24 of its row's largest), the weights as one f16 each (2^-12
+ * of it); scores, softmax and accumulation are fp32.  Rows behind a request's last
+ * token may hold anything.  A row that sees a key of a block whose scale is NaN is
+ * NaN; one that sees none of its keys does not meet it.
+ */
+int pkv_paged_attn_int8(void *out, const void *query, int64_t query_token_stride,
+                        const void *kv_cache, const float *kv_scales, int64_t num_blocks,
+                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                        const int32_t *seq_lens, const int32_t *query_start_loc,
+                        int32_t num_seqs, int32_t num_tokens,
+                        int32_t max_query_len, int32_t max_seq_len,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                        int32_t block_size, float scale, int32_t num_splits,
+                        void *workspace, size_t workspace_bytes, size_t *workspace_needed,
+                        void *stream);
+
+/*
+ * pkv_kv_gather_int8 — the cached keys and values of every request, in order, as bf16:
+ *     key_out[key_start_loc[r] + j][h][:]   = K of token j of request r (code * scale,
+ *     value_out[key_start_loc[r] + j][h][:] = V                          nearest even)
+ * for j < seq_lens[r]: what attention outside this library, or a cache of another type,
+ * takes.
+ *
+ *  key_out, value_out  bf16 [out_rows][num_kv_heads][head_size], 16-byte aligned; rows no
+ *                      request covers are left as they were.  NULL if out_rows == 0.
+ *  block_tables, seq_lens, key_start_loc, max_seq_len, device_status
+ *                      as pkv_latent_gather (num_seqs at most 65535).
+ */
+int pkv_kv_gather_int8(void *key_out, void *value_out, int64_t out_rows,
+                       const void *kv_cache, const float *kv_scales, int64_t num_blocks,
+                       int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                       const int32_t *seq_lens, const int32_t *key_start_loc,
+                       int32_t num_seqs, int32_t max_seq_len,
+                       int32_t *device_status, void *stream);
+
+/*
+ * pkv_copy_blocks_int8 — pkv_copy_blocks over an int8 cache: the codes and the scales of
+ * every {source, destination} pair's block.
+ */
+int pkv_copy_blocks_int8(void *kv_cache, float *kv_scales, int64_t num_blocks,
+                         int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                         const int64_t *block_mapping, int32_t num_pairs,
+                         int32_t *device_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

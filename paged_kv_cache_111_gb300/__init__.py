@@ -22,6 +22,8 @@ Calls (same names as the C ABI without the ``pkv_`` prefix):
 * ``latent_kv_write`` / ``latent_paged_attn`` / ``latent_gather`` (a cache of one latent row a token, and attention
   over it in the latent space)
 * ``latent_attn_expanded`` (attention over the per-head keys and values that gathered latent rows expand to)
+* ``kv_write_int8`` / ``qk_norm_rope_kv_write_int8`` / ``paged_attn_int8`` / ``kv_gather_int8`` /
+  ``copy_blocks_int8`` (an int8 cache with a scale for each block of 16 tokens, kv head and side)
 
 plus ``paged_attn_workspace_size(...)`` (the C call's size query) and
 ``workspace_status(workspace)`` (reads the device status word).
@@ -45,6 +47,7 @@ __all__ = [
     "kv_write_fp8", "paged_attn_fp8", "paged_attn_shared_prefix_fp8", "workspace_schedule",
     "qk_norm_rope_kv_write", "qk_norm_rope_kv_write_fp8", "LATENT_DIM", "LATENT_ROPE_DIM", "latent_kv_write",
     "latent_gather", "latent_paged_attn", "latent_paged_attn_workspace_size", "latent_attn_expanded",
+    "kv_write_int8", "qk_norm_rope_kv_write_int8", "paged_attn_int8", "kv_gather_int8", "copy_blocks_int8",
 ]
 
 BLOCK_SIZE = 16
@@ -122,6 +125,18 @@ def load():
         lib.pkv_latent_attn_expanded.argtypes = [P, P, i64, P, i64, i64, P, i64, P, i64, i64, P, P, i32, i32, i32, i32,
                                                  i32, i32, f32, P, P]
         lib.pkv_latent_attn_expanded.restype = ctypes.c_int
+        lib.pkv_kv_write_int8.argtypes = [P, P, i64, i32, i32, i32, P, i64, P, i64, P, i32, P, P]
+        lib.pkv_kv_write_int8.restype = ctypes.c_int
+        lib.pkv_qk_norm_rope_kv_write_int8.argtypes = [P, i64, P, P, i64, i32, i32, i32, i32, P, i64, P, i64, P, i64, P,
+                                                       P, f32, P, i64, i32, i32, P, P, i32, P, P]
+        lib.pkv_qk_norm_rope_kv_write_int8.restype = ctypes.c_int
+        lib.pkv_paged_attn_int8.argtypes = [P, P, i64, P, P, i64, P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
+                                            f32, i32, P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), P]
+        lib.pkv_paged_attn_int8.restype = ctypes.c_int
+        lib.pkv_kv_gather_int8.argtypes = [P, P, i64, P, P, i64, i32, i32, i32, P, i32, P, P, i32, i32, P, P]
+        lib.pkv_kv_gather_int8.restype = ctypes.c_int
+        lib.pkv_copy_blocks_int8.argtypes = [P, P, i64, i32, i32, i32, P, i32, P, P]
+        lib.pkv_copy_blocks_int8.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -619,3 +634,108 @@ def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tens
           _full("key_start_loc", key_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"), S, T, K,
           max_query_len, max_key_len, H, scale,
           _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+
+
+# ---- the int8 cache -------------------------------------------------------------------------------------------
+
+def _int8_cache(kv_cache: torch.Tensor, kv_scales: torch.Tensor):
+    """(cache, scales, device, blocks, kv heads, block size, head size) of an int8 cache, the first two as pointers."""
+    dev = kv_cache.get_device()
+    if (dev < 0 or kv_cache.dtype is not torch.int8 or kv_cache.dim() != 5 or not kv_cache.is_contiguous()
+            or kv_cache.shape[2] != 2):
+        _refuse("kv_cache", kv_cache, torch.int8, dev, "a contiguous [NB, Hkv, 2, 16, d]")
+    nb, hkv, _, bs, d = kv_cache.shape
+    scales = _full("kv_scales", kv_scales, _F32, dev, (nb, hkv, 2), "a contiguous [NB, Hkv, 2]")
+    return kv_cache.data_ptr(), scales, dev, nb, hkv, bs, d
+
+
+def kv_write_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                  slot_mapping: torch.Tensor, device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise key/value [T, Hkv, d] (bf16) into kv_cache (int8 [NB, Hkv, 2, 16, d]) and kv_scales (fp32
+    [NB, Hkv, 2]) through slot_mapping [T] (int64), the tokens of a block side by side; the scale of a block that is
+    written from its first row is made anew, any other grows where it has to."""
+    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
+    T = slot_mapping.numel()
+    k, k_step, _ = _heads("key", key, dev, T, hkv, d, True)
+    v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
+    _call(dev, "pkv_kv_write_int8", (_lib or load()).pkv_kv_write_int8, cache, scales, nb, hkv, d, bs, k, k_step, v,
+          v_step, _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+
+
+def qk_norm_rope_kv_write_int8(query_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
+                               query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                               q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], eps: float,
+                               cos_sin: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                               interleaved: bool = False, device_status: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """qk_norm_rope_kv_write into an int8 cache and its scales (see kv_write_int8)."""
+    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
+    if query.dim() != 3:
+        raise ValueError("query must be [T, H, d]")
+    T, H, _ = query.shape
+    qo, qo_step, _ = _heads("query_out", query_out, dev, T, H, d, True)
+    q, q_step, _ = _heads("query", query, dev, T, H, d, True)
+    k, k_step, _ = _heads("key", key, dev, T, hkv, d, True)
+    v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
+    table = _full("cos_sin", cos_sin, _F32, dev, (-1, -1), "a contiguous [max_position, rotary_dim]")
+    max_position, rot = cos_sin.shape
+    _call(dev, "pkv_qk_norm_rope_kv_write_int8", (_lib or load()).pkv_qk_norm_rope_kv_write_int8,
+          qo, qo_step, cache, scales, nb, H, hkv, d, bs, q, q_step, k, k_step, v, v_step,
+          _full("q_weight", q_weight, _BF16, dev, (d,), "[d]"), _full("k_weight", k_weight, _BF16, dev, (d,), "[d]"),
+          eps, table, max_position, rot, 1 if interleaved else 0,
+          _full("positions", positions, _I64, dev, (T,), "a contiguous [T]"),
+          _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+
+
+def paged_attn_int8(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
+                    block_tables: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                    max_query_len: int, max_seq_len: int, scale: float, workspace: torch.Tensor, num_splits: int = 0,
+                    stream=None) -> None:
+    """paged_attn over an int8 cache; the workspace is sized as for paged_attn, and paged_attn_combine follows."""
+    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
+    if query.dim() != 3:
+        raise ValueError("query must be [T, H, d]")
+    T, H, _ = query.shape
+    S = seq_lens.numel()
+    q, q_step, _ = _heads("query", query, dev, T, H, d, True)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("workspace", workspace, None, dev, "contiguous")
+    _call(dev, "pkv_paged_attn_int8", (_lib or load()).pkv_paged_attn_int8,
+          _full("out", out, _BF16, dev, (T, H, d), "a contiguous [T, H, d]"), q, q_step, cache, scales, nb,
+          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
+          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
+          _full("query_start_loc", query_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"), S, T,
+          max_query_len, max_seq_len, H, hkv, d, bs, scale, num_splits, workspace.data_ptr(), workspace.nbytes, None,
+          _raw_stream(dev, stream))
+
+
+def kv_gather_int8(key_out: torch.Tensor, value_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
+                   block_tables: torch.Tensor, seq_lens: torch.Tensor, key_start_loc: torch.Tensor, max_seq_len: int,
+                   device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The cached keys and values of request r into key_out and value_out [key_start_loc[r]:][:seq_lens[r]] (bf16
+    [rows, Hkv, d])."""
+    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
+    S = seq_lens.numel()
+    if key_start_loc.numel() < S:
+        raise ValueError("key_start_loc must have an entry per request")
+    rows = key_out.shape[0]
+    _call(dev, "pkv_kv_gather_int8", (_lib or load()).pkv_kv_gather_int8,
+          _full("key_out", key_out, _BF16, dev, (-1, hkv, d), "a contiguous [rows, Hkv, d]"),
+          _full("value_out", value_out, _BF16, dev, (rows, hkv, d), "a contiguous [rows, Hkv, d]"), rows, cache, scales,
+          nb, hkv, d, bs,
+          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
+          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
+          _full("key_start_loc", key_start_loc, _I32, dev, (-1,), "a contiguous vector"), S, max_seq_len,
+          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+
+
+def copy_blocks_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, block_mapping: torch.Tensor,
+                     device_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Copy-on-write over an int8 cache, codes and scales: block_mapping int64 [num_pairs, 2] of {source, destination}."""
+    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
+    _call(dev, "pkv_copy_blocks_int8", (_lib or load()).pkv_copy_blocks_int8, cache, scales, nb, hkv, d, bs,
+          _full("block_mapping", block_mapping, _I64, dev, (-1, 2), "a contiguous [num_pairs, 2]"),
+          block_mapping.shape[0], _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"),
+          _raw_stream(dev, stream))

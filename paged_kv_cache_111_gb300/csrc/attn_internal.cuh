@@ -12,6 +12,8 @@ constexpr int kPrefillRows = 128;     // rows of one prefill tile (M of the MMA)
 constexpr int kPrefillKeys = 128;     // keys of one prefill KV tile (N of S = Q K^T)
 constexpr int32_t kMagic = 0x504B5633;  // "PKV3"
 
+enum class CacheKind { kBf16, kE4m3, kInt8 };
+
 struct WsHeader {
     int32_t status;          // device status word (first 4 bytes)
     int32_t magic;
@@ -196,6 +198,7 @@ struct AttnParams {
     int64_t num_blocks;
     float scale_log2;         // scale * log2(e)
     float k_scale, v_scale;   // E4M3 cache: stored code * scale is the value (1 for bf16)
+    const float *kv_scales;   // int8 cache: [num_blocks][num_kv_heads][2]
     uint8_t *ws;
     // self_plan = 1: no plan kernel ran; the decode kernel plans the call
     // itself (see decode_self_plan_ok) and writes what the combine reads
@@ -237,6 +240,12 @@ int make_decode_map(CUtensorMap *map, const void *kv_cache, int64_t num_blocks, 
 // dependent launch after the plan).
 int launch_decode_path(const CUtensorMap &map, const AttnParams &ap, int32_t head_size, bool kv8, int grid, int dev,
                        cudaStream_t st);
+
+// The same over an int8 cache (int8_decode.cu); `rows`: the most query rows of a chunk (8, or any more).
+int int8_decode_ctas_per_sm(int32_t head_size, int rows);
+int make_int8_map(CUtensorMap *map, const void *kv_cache, int64_t num_blocks, int32_t num_kv_heads, int32_t head_size);
+int launch_int8_decode_path(const CUtensorMap &map, const AttnParams &ap, int32_t head_size, int rows, int grid, int dev,
+                            cudaStream_t st);
 
 // The one-tile tensor-core kernel over an E4M3 cache (prefill_tc.cu): the
 // shared-prefix (cascade) pass (rows of every request that shares the first

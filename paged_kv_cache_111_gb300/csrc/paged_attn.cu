@@ -574,8 +574,9 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
                            int32_t num_tokens, int32_t max_query_len, int32_t max_seq_len, int32_t num_q_heads,
                            int32_t num_kv_heads, int32_t head_size, int32_t block_size, float scale,
                            int32_t num_splits, int32_t prefix_blocks, void *workspace, size_t workspace_bytes,
-                           size_t *workspace_needed, void *stream, bool kv8 = false, float k_scale = 1.f,
-                           float v_scale = 1.f) {
+                           size_t *workspace_needed, void *stream, CacheKind kind = CacheKind::kBf16,
+                           float k_scale = 1.f, float v_scale = 1.f, const float *kv_scales = nullptr) {
+    const bool kv8 = kind == CacheKind::kE4m3, int8 = kind == CacheKind::kInt8;
     // ---- host-side validation: nothing is enqueued on error ----
     if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_query_len < 0 ||
         max_seq_len < 0 || max_blocks_per_seq < 0 || num_splits < 0 || prefix_blocks < 0)
@@ -594,13 +595,14 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
 
     // long chunks and the shared-prefix pass go to the tensor-core tile kernel
     // (which widens an E4M3 cache's pages to f16 itself)
-    const bool prefill_ok = prefill_supported(num_q_heads, num_kv_heads, head_size);
+    const bool prefill_ok = !int8 && prefill_supported(num_q_heads, num_kv_heads, head_size);
     if (!prefill_ok) prefix_blocks = 0;
     const WsLayout lay = ws_layout(num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
                                    head_size, prefix_blocks);
     if (workspace_needed) *workspace_needed = static_cast<size_t>(lay.total);
     if (num_seqs == 0) return PKV_OK;
     if (!out || !query || !kv_cache || !block_tables || !seq_lens || !query_start_loc) return PKV_ERR_NULL;
+    if (int8 && !kv_scales) return PKV_ERR_NULL;
     if (!workspace || workspace_bytes < static_cast<size_t>(lay.total)) return PKV_ERR_WORKSPACE;
     if (query_token_stride < static_cast<int64_t>(num_q_heads) * head_size) return PKV_ERR_SHAPE;
     if (query_token_stride % 8) return PKV_ERR_ALIGNMENT;
@@ -612,17 +614,23 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
          reinterpret_cast<uintptr_t>(query_start_loc)) & 3u)
         return PKV_ERR_ALIGNMENT;
 
+    if (reinterpret_cast<uintptr_t>(kv_scales) & 7u) return PKV_ERR_ALIGNMENT;
+
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_ERR_CUDA;
 
     CUtensorMap map;
-    int rc = make_decode_map(&map, kv_cache, num_blocks, num_kv_heads, head_size, kv8);
+    int rc = int8 ? make_int8_map(&map, kv_cache, num_blocks, num_kv_heads, head_size)
+                  : make_decode_map(&map, kv_cache, num_blocks, num_kv_heads, head_size, kv8);
     if (rc) return rc;
 
     const int nw = kDecodeWarps;
-    const int per_sm = decode_ctas_per_sm(head_size, kv8);
+    // (int8: query rows of a chunk at most)
+    const int decode_rows = static_cast<int>(
+        std::min<int64_t>(16, static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads)));
+    const int per_sm = int8 ? int8_decode_ctas_per_sm(head_size, decode_rows) : decode_ctas_per_sm(head_size, kv8);
     const int64_t resident = static_cast<int64_t>(sms) * per_sm;
     const int64_t max_items = lay.max_chunks * num_kv_heads;
     int64_t grid = std::max<int64_t>(1, std::min(resident, (max_items + nw - 1) / nw));
@@ -677,6 +685,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     ap.scale_log2 = scale * 1.4426950408889634f;
     ap.k_scale = k_scale;
     ap.v_scale = v_scale;
+    ap.kv_scales = kv_scales;
     ap.ws = static_cast<uint8_t *>(workspace);
     ap.self_plan = self_plan ? 1 : 0;
     ap.num_seqs = num_seqs;
@@ -686,7 +695,8 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     ap.max_seq_len = max_seq_len;
     ap.total_warps = static_cast<int32_t>(chunk_warps);
     ap.lay = lay;
-    rc = launch_decode_path(map, ap, head_size, kv8, static_cast<int>(grid), dev, st);
+    rc = int8 ? launch_int8_decode_path(map, ap, head_size, decode_rows, static_cast<int>(grid), dev, st)
+              : launch_decode_path(map, ap, head_size, kv8, static_cast<int>(grid), dev, st);
     if (rc || (!may_prefill && prefix_blocks == 0)) return rc;
     PrefillParams fp;
     fp.out = ap.out;
@@ -764,8 +774,8 @@ extern "C" int pkv_paged_attn_shared_prefix_fp8(void *out, const void *query, in
     return pkv::paged_attn_impl(out, query, query_token_stride, kv_cache, num_blocks, block_tables,
                                 max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len,
                                 max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale, num_splits,
-                                shared_prefix_blocks, workspace, workspace_bytes, workspace_needed, stream, true,
-                                k_scale, v_scale);
+                                shared_prefix_blocks, workspace, workspace_bytes, workspace_needed, stream,
+                                pkv::CacheKind::kE4m3, k_scale, v_scale);
 }
 
 extern "C" int pkv_paged_attn_combine(void *out, const void *workspace, size_t workspace_bytes, int32_t num_tokens,
@@ -807,5 +817,21 @@ extern "C" int pkv_paged_attn_fp8(void *out, const void *query, int64_t query_to
     return pkv::paged_attn_impl(out, query, query_token_stride, kv_cache, num_blocks, block_tables,
                                 max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len,
                                 max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale, num_splits, 0,
-                                workspace, workspace_bytes, workspace_needed, stream, true, k_scale, v_scale);
+                                workspace, workspace_bytes, workspace_needed, stream, pkv::CacheKind::kE4m3, k_scale,
+                                v_scale);
+}
+
+extern "C" int pkv_paged_attn_int8(void *out, const void *query, int64_t query_token_stride, const void *kv_cache,
+                                   const float *kv_scales, int64_t num_blocks, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                   const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                                   int32_t max_query_len, int32_t max_seq_len, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_size, int32_t block_size, float scale,
+                                   int32_t num_splits, void *workspace, size_t workspace_bytes,
+                                   size_t *workspace_needed, void *stream) {
+    return pkv::paged_attn_impl(out, query, query_token_stride, kv_cache, num_blocks, block_tables,
+                                max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len,
+                                max_seq_len, num_q_heads, num_kv_heads, head_size, block_size, scale, num_splits, 0,
+                                workspace, workspace_bytes, workspace_needed, stream, pkv::CacheKind::kInt8, 1.f, 1.f,
+                                kv_scales);
 }
