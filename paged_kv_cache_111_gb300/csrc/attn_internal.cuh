@@ -258,6 +258,11 @@ int launch_prefix_e4m3(const PrefillParams &p, const void *query, int64_t q_stri
 int launch_prefill_e4m3(const PrefillParams &p, const void *query, int64_t q_stride, const void *kv_cache,
                         int64_t num_blocks, int32_t head_size, int64_t grid, int dev, cudaStream_t stream);
 
+// Chunks over an int8 cache (int8_prefill.cu), any number of query heads a kv head.
+int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_stride, const void *kv_cache,
+                        const float *kv_scales, int64_t num_blocks, int32_t head_size, int64_t grid, int dev,
+                        cudaStream_t stream);
+
 // Is the tensor-core prefill kernel available for this head layout?
 inline bool prefill_supported(int num_q_heads, int num_kv_heads, int head_size) {
     const int G = num_q_heads / num_kv_heads;

@@ -1,0 +1,645 @@
+// Chunks over an int8 cache (int8_common.cuh), on the 5th-generation tensor cores: the computation of int8_decode.cu for
+// requests of many rows (query token, query head of the kv head's group).
+//
+// With codes k_j, v_j and their blocks' scales ks, vs, for a row q scaled by a power of two 2^e into f16:
+//     S_j = <q 2^e, 1152 + k_j>,   e_j = (S_j - 1152 sum q 2^e) (scale 2^-e log2(e) ks) + log2 vs
+//     p'_j = 2^(e_j - m),          out = sum_j p'_j v_j / sum_j p'_j / vs
+// K's codes widen to f16 as 1152 + code (a byte next to 0x64) and stay so: what that adds to S is one number a row, and
+// goes with the block's factor into the constants of the softmax, of which a row has three a block of 16 keys.  V's
+// codes are taken back to themselves.  m is the row's largest e_j, moved only when passed by 2^8, so that p' fits f16
+// whatever the blocks' scales are.
+//
+// Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and share
+// each 128-key tile; a persistent CTA an SM takes items largest first.  Per key tile: 8 pages (one TMA box each, K and V)
+// land raw, two warps widen them into a ring of 16 KiB slots in the layout the products read, S = Q K^T from shared
+// memory (128 x 128 x 16), softmax by four warps a row tile (a row per thread), P as f16 over S in tensor memory,
+// O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
+//
+// Warp roles (384 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2 and 3 widen,
+// warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is bounded.
+#include <mutex>
+#include <type_traits>
+
+#include "int8_common.cuh"
+#include "latent_common.cuh"
+
+namespace pkv {
+
+constexpr int kIpRows = 128;                          // of a row tile
+constexpr int kIpKeys = 128;                          // of a key tile
+constexpr int kIpPages = kIpKeys / kBlock;
+constexpr int kIpThreads = 384;
+constexpr int kIpSlot = 16384;                        // 64 dims of 128 rows, or 128 dims of 64 rows, as f16
+constexpr int kIpRaw = 2;                             // raw key tiles in flight
+constexpr int kIpScaleTiles = 8;                      // key tiles whose blocks' scales are held
+constexpr int kIpReaders = 11;                        // of an item: MMA, two widening and eight softmax warps
+
+template <int HD>
+struct IpCfg {
+    static constexpr int kChunks = HD / 64;           // slots of a K (or V) tile, 64-dim chunks of Q
+    static constexpr int kSlots = HD == 128 ? 6 : 8;
+    static constexpr int kRawBytes = kIpKeys * 2 * HD;
+    static constexpr int kOffQ = 0;                   // [row tile][chunk] 16 KiB
+    static constexpr int kOffRing = kOffQ + 2 * kChunks * kIpSlot;
+    static constexpr int kOffRaw = kOffRing + kSlots * kIpSlot;
+    static constexpr int kOffBar = kOffRaw + kIpRaw * kRawBytes;
+    static constexpr int kOffItems = kOffBar + 512;
+    static constexpr int kOffScales = kOffItems + 256;    // float4 {K's, log2 of V's, 1 / V's, -} [tile & 7][block]
+    static constexpr int kSmem = kOffScales + kIpScaleTiles * kIpPages * 16 + 1024;   // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+enum IpBar {
+    kIpItemFull = 0,     // (+ item & 3)
+    kIpItemEmpty = 4,    // (+ item & 3)
+    kIpRawFull = 8,      // (+ tile & 1)
+    kIpRawEmpty = 10,    // (+ tile & 1)
+    kIpFull = 12,        // (+ slot)
+    kIpEmpty = 20,       // (+ slot)
+    kIpQFull = 28,       // (+ row tile)
+    kIpSFull = 30,       // (+ row tile)
+    kIpPFull = 32,       // (+ row tile)
+    kIpODone = 34,       // (+ row tile)
+    kIpOFree = 36,       // (+ row tile)
+    kIpScFull = 38,      // (+ tile & 7)
+    kIpNumBars = 46
+};
+static_assert(kIpNumBars * 8 + 16 <= 512, "barriers, the tensor-memory address and the tile count");
+
+struct IpItem {
+    int32_t valid, r, g, n[2], L, qs, ctx, rows_total, row0, n_pages, tile;
+};
+static_assert(kItemSlots * sizeof(IpItem) <= 256 && kItemSlots == 4, "the item ring's place");
+
+template <int HD>
+__global__ void __launch_bounds__(kIpThreads, 1)
+    int8_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __nv_bfloat16 *__restrict__ query,
+                        const int64_t q_stride, const float2 *__restrict__ kv_scales, const PrefillParams p) {
+    using Cfg = IpCfg<HD>;
+    constexpr int C = Cfg::kChunks, SLOTS = Cfg::kSlots, PER = 2 * C;     // slots of a key tile: K's, then V's
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kIpNumBars);
+    volatile int32_t *tiles_loaded = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+    volatile IpItem *items = reinterpret_cast<volatile IpItem *>(smem + Cfg::kOffItems);
+    float4 *scales = reinterpret_cast<float4 *>(smem + Cfg::kOffScales);
+    const uint32_t sQ = smem_u32(smem + Cfg::kOffQ), sRing = smem_u32(smem + Cfg::kOffRing);
+    const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
+
+    // As the other chunk kernels: the kernel before this one (decode) writes other rows, and it started when the plan and
+    // the cache write had completed, so the plan's lists are read at once, through L2; the wait on it comes at the end.
+    pdl_trigger();
+    const WsHeader *hdr = reinterpret_cast<const WsHeader *>(p.ws);
+    int32_t *status = reinterpret_cast<int32_t *>(p.ws);
+    const int n_items = ws_ld(&hdr->n_ptiles) * p.num_kv_heads;
+    if (static_cast<int>(blockIdx.x) >= n_items) {    // uniform over the CTA
+        pdl_wait();
+        return;
+    }
+    const int G = p.G;
+    if (threadIdx.x < kIpNumBars) {
+        const int b = threadIdx.x;
+        int count = 1;
+        if (b >= kIpItemEmpty && b < kIpItemEmpty + 4) count = kIpReaders;
+        else if ((b >= kIpRawEmpty && b < kIpRawEmpty + 2) || (b >= kIpFull && b < kIpFull + 8)) count = 2;
+        else if ((b >= kIpQFull && b < kIpQFull + 2) || (b >= kIpPFull && b < kIpPFull + 2) ||
+                 (b >= kIpOFree && b < kIpOFree + 2))
+            count = 4;
+        mbar_init(&bars[b], count);
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&kv_map);
+        *tiles_loaded = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    fence_barrier_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(*tmem_slot);
+
+    if (warp == 0) {
+        // ---------------- items, raw pages, scales ----------------
+        bool ok = true;
+        int item = blockIdx.x, taken = 0, gt = 0;     // gt: key tiles of this CTA so far
+        int *next_item = reinterpret_cast<int *>(p.ws + offsetof(WsHeader, next_ptile_item));
+        for (int k = 0; ok; ++k) {
+            const int slot = k & 3;
+            if (k >= 4) ok = warp_wait(&bars[kIpItemEmpty + slot], (k / 4 - 1) & 1, status);
+            if (!ok) break;
+            IpItem it{};
+            if (item < n_items) {
+                it.valid = 1;
+                it.g = item % p.num_kv_heads;
+                const int4 tile =
+                    ws_ld(reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles)) + item / p.num_kv_heads);
+                it.r = tile.x;
+                it.L = p.seq_lens[it.r];
+                it.qs = p.qsl[it.r];
+                const int qlen = p.qsl[it.r + 1] - it.qs;
+                it.ctx = it.L - qlen;
+                it.rows_total = qlen * G;
+                it.row0 = tile.y * 2 * kIpRows;
+                it.n_pages = (it.L + kBlock - 1) / kBlock;
+                // key tiles that each of the two row tiles sees
+                for (int i = 0; i < 2; ++i) {
+                    const int end = min(it.row0 + (i + 1) * kIpRows, it.rows_total);
+                    it.n[i] = end > it.row0 + i * kIpRows ? (it.ctx + (end - 1) / G + kIpKeys) / kIpKeys : 0;
+                }
+            }
+            if (lane == 0) {
+                volatile int32_t *dst = reinterpret_cast<volatile int32_t *>(items + slot);
+                const int32_t *src = reinterpret_cast<const int32_t *>(&it);
+#pragma unroll
+                for (int e = 0; e < static_cast<int>(sizeof(IpItem) / 4); ++e) dst[e] = src[e];
+                mbar_arrive(&bars[kIpItemFull + slot]);
+            }
+            if (!it.valid) break;
+            ++taken;
+            const int n_kv = max(it.n[0], it.n[1]);
+            const int32_t *bt = p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks_per_seq;
+            // block ids and their scales in windows of 32 pages (4 key tiles), one lane a page, the next window ahead;
+            // pages past the sequence are -1 and load as zeros (outside the tensor map)
+            auto blocks_of = [&](int w) -> int {
+                const int page = w * 32 + lane;
+                const int b = page < it.n_pages ? __ldg(bt + page) : -1;
+                if (page < it.n_pages && (b < 0 || b >= p.num_blocks)) set_status(status, PKV_ERR_DEVICE_INDEX);
+                return b;
+            };
+            auto scales_of = [&](int b) -> float2 {
+                return b >= 0 && b < p.num_blocks ? __ldg(kv_scales + static_cast<int64_t>(b) * p.num_kv_heads + it.g)
+                                                  : make_float2(0.f, 1.f);
+            };
+            int win = blocks_of(0), win_next = blocks_of(1);
+            float2 sc = scales_of(win), sc_next = make_float2(0.f, 1.f);
+            for (int j = 0; j < n_kv && ok; ++j, ++gt) {
+                if (j > 0 && (j & 3) == 0) {
+                    win = win_next, sc = sc_next;
+                    win_next = blocks_of(j / 4 + 1);
+                }
+                if ((j & 3) == 2) sc_next = scales_of(win_next);
+                const int rs = gt & 1;
+                if (gt >= kIpRaw) ok = warp_wait(&bars[kIpRawEmpty + rs], (gt / kIpRaw - 1) & 1, status);
+                if (!ok) break;
+                uint8_t *raw = smem + Cfg::kOffRaw + rs * Cfg::kRawBytes;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars[kIpRawFull + rs], Cfg::kRawBytes);
+                    *tiles_loaded = gt + 1;
+                }
+                __syncwarp();
+                const int at = (j & 3) * kIpPages + (lane & 7);
+                const int b = __shfl_sync(0xffffffffu, win, at);
+                const float ks = __shfl_sync(0xffffffffu, sc.x, at);
+                float vs = __shfl_sync(0xffffffffu, sc.y, at);
+                vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;         // (NaN stays)
+                if (lane < kIpPages) {
+                    tma_load_5d(raw + lane * (2 * kBlock * HD), &kv_map, &bars[kIpRawFull + rs], 0, 0, 0, it.g, b);
+                    scales[(gt & 7) * kIpPages + lane] = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kIpScFull + (gt & 7)]);
+            }
+            int nxt = 0;
+            if (lane == 0) nxt = static_cast<int>(gridDim.x) + atomicAdd(next_item, 1);
+            item = __shfl_sync(0xffffffffu, nxt, 0);
+        }
+        if (!ok)                                      // the copies in flight land before the CTA ends
+            for (int t = max(0, gt - kIpRaw); t < gt; ++t)
+                mbar_wait_bounded(&bars[kIpRawFull + (t & 1)], (t / kIpRaw) & 1);
+        // this CTA's share of the schedule
+        if (lane == 0) reinterpret_cast<int32_t *>(p.ws + kStatsOffset)[blockIdx.x] = taken;
+    } else if (warp == 1) {
+        // ---------------- MMA issue: one elected thread ----------------
+        if (elect_one()) {
+            constexpr uint32_t kIdescS = idesc_f16_f32(kIpRows, kIpKeys, 0, 0);
+            constexpr uint32_t kIdescO = idesc_f16_f32(kIpRows, HD, 0, 1);
+            const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(sRing, 8192, 1024);       // MN-major: 64-dim chunks 8 KiB apart
+            auto wait = [&](int b, uint32_t parity) { return pf_wait(&bars[b], parity, status); };
+            int landed = 0;                           // slots waited for
+            int cnt[2] = {0, 0}, qs[2] = {0, 0};      // key tiles, items of each row tile so far
+            int gt = 0;
+            auto need = [&](int s) {
+                if (s < landed) return true;
+                landed = s + 1;
+                const bool there = wait(kIpFull + s % SLOTS, (s / SLOTS) & 1);
+                tc_fence_after();
+                return there;
+            };
+            auto issue_s = [&](int i, int t, bool frees) {
+                const uint64_t a = dq + i * (C * kIpSlot >> 4);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int s = t * PER + c, slot = s % SLOTS;
+                    if (!need(s)) return false;
+                    const uint64_t b = dk + static_cast<uint32_t>(slot * (kIpSlot >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ss(tmem + 128u * i, a + c * (kIpSlot >> 4) + kk * 2, b + kk * 2, kIdescS,
+                                    (c | kk) ? 1u : 0u);
+                    if (frees) umma_commit(&bars[kIpEmpty + slot]);
+                }
+                umma_commit(&bars[kIpSFull + i]);
+                return true;
+            };
+            auto issue_pv = [&](int i, int t, bool first, bool frees) {
+#pragma unroll
+                for (int h = 0; h < C; ++h) {
+                    const int s = t * PER + C + h, slot = s % SLOTS;
+                    if (!need(s)) return false;
+                    const uint64_t b = dv + static_cast<uint32_t>(slot * (kIpSlot >> 4));
+                    constexpr int kSteps = 8 / C;     // of 16 keys
+#pragma unroll
+                    for (int kk = 0; kk < kSteps; ++kk)
+                        umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * (h * kSteps + kk),
+                                    b + kk * (2048 >> 4), kIdescO, (h | kk) ? 1u : (first ? 0u : 1u));
+                    if (frees) umma_commit(&bars[kIpEmpty + slot]);
+                }
+                umma_commit(&bars[kIpODone + i]);
+                return true;
+            };
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int slot = k & 3;
+                ok = wait(kIpItemFull + slot, (k / 4) & 1);
+                if (!ok) break;
+                const bool valid = items[slot].valid != 0;
+                const int n[2] = {items[slot].n[0], items[slot].n[1]};
+                mbar_arrive(&bars[kIpItemEmpty + slot]);
+                if (!valid) break;
+                const int n_kv = max(n[0], n[1]);
+                const bool two = n[1] > 0;            // the second row tile reads a slot last, where it has rows
+                // (the second sees as many key tiles as the first, or more)
+                ok = wait(kIpQFull, qs[0] & 1) && issue_s(0, gt, !two);
+                if (ok && two) ok = wait(kIpQFull + 1, qs[1] & 1) && issue_s(1, gt, true);
+                // row tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
+                for (int j = 0; j < n_kv && ok; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || j >= n[i]) continue;
+                        const bool frees = i == (two ? 1 : 0);
+                        ok = wait(kIpPFull + i, cnt[i] & 1);
+                        // the item before's O has been read out
+                        if (ok && j == 0 && qs[i] > 0) ok = wait(kIpOFree + i, (qs[i] - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        ok = issue_pv(i, gt + j, j == 0, frees);
+                        ++cnt[i];
+                        if (ok && j + 1 < n[i]) ok = issue_s(i, gt + j + 1, frees);
+                    }
+                }
+                gt += n_kv;
+                ++qs[0];
+                if (two) ++qs[1];
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ---------------- widening: each of the two warps half of every slot ----------------
+        // (both wait for every release of every slot: neither can meet a barrier two phases on)
+        const int half = warp - 2;
+        bool ok = true;
+        int gt = 0;
+        uint32_t src = 0;
+        auto freed = [&](int s) {
+            return s < SLOTS || warp_wait(&bars[kIpEmpty + s % SLOTS], (s / SLOTS - 1) & 1, status);
+        };
+        auto filled = [&](int s) {                     // (the fence: for the tensor cores)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kIpFull + s % SLOTS]);
+        };
+        // rows r0 .. of the raw tile in pieces of 16 dims, P a row, so that eight lanes read 128 bytes side by side;
+        // `at`: the places of 64-dim chunks 0 and 1 of row 0
+        constexpr int P = HD / 16;
+        auto widen = [&](auto is_v, int r0, int rows, uint32_t at0, uint32_t at1) {
+            constexpr bool V = decltype(is_v)::value;
+#pragma unroll 1
+            for (int u0 = 0; u0 < rows * P / 32; u0 += 4) {
+                uint32_t w[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int piece = (u0 + u) * 32 + lane, r = r0 + piece / P, c = piece % P;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                                 : "r"(src + (V ? kBlock * HD : 0) + (r / kBlock) * (2 * kBlock * HD) + (r % kBlock) * HD +
+                                       c * 16));
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int piece = (u0 + u) * 32 + lane, r = r0 + piece / P, c = piece % P;
+                    // lanes of the second 64 dims store their halves the other way round: no two meet in a bank
+                    const bool turn = (c >> 2) & 1;
+                    const uint32_t v[4] = {turn ? w[u][2] : w[u][0], turn ? w[u][3] : w[u][1],
+                                           turn ? w[u][0] : w[u][2], turn ? w[u][1] : w[u][3]};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        int8x4_to_biased_f16(v[e], h[2 * e], h[2 * e + 1]);
+                        if (V) h[2 * e] = unbias_f16(h[2 * e]), h[2 * e + 1] = unbias_f16(h[2 * e + 1]);
+                    }
+                    const uint32_t row = (turn ? at1 : at0) + r * 128;
+                    const int first = ((2 * c + (turn ? 1 : 0)) & 7) ^ (r & 7);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (first << 4)), "r"(h[0]), "r"(h[1]),
+                                 "r"(h[2]), "r"(h[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((first ^ 1) << 4)), "r"(h[4]),
+                                 "r"(h[5]), "r"(h[6]), "r"(h[7])
+                                 : "memory");
+                }
+            }
+        };
+        for (int k = 0; ok; ++k) {
+            const int islot = k & 3;
+            ok = warp_wait(&bars[kIpItemFull + islot], (k / 4) & 1, status);
+            if (!ok) break;
+            const bool valid = items[islot].valid != 0;
+            const int n_kv = max(items[islot].n[0], items[islot].n[1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kIpItemEmpty + islot]);
+            if (!valid) break;
+            for (int j = 0; j < n_kv && ok; ++j, ++gt) {
+                const int rs = gt & 1, s0 = gt * PER;
+                ok = warp_wait(&bars[kIpRawFull + rs], (gt / kIpRaw) & 1, status);
+                src = smem_u32(smem + Cfg::kOffRaw + rs * Cfg::kRawBytes);
+                // K: dims 64 c .. of row r in slot c
+                for (int c = 0; c < C && ok; ++c) ok = freed(s0 + c);
+                if (!ok) break;
+                widen(std::false_type(), 64 * half, 64, sRing + (s0 % SLOTS) * kIpSlot,
+                      sRing + ((s0 + C - 1) % SLOTS) * kIpSlot);
+                for (int c = 0; c < C; ++c) filled(s0 + c);
+                // V: rows 64 h .. in slot h, 64-dim chunks 8 KiB apart (64 dims: one slot)
+                for (int h = 0; h < C && ok; ++h) {
+                    ok = freed(s0 + C + h);
+                    if (!ok) break;
+                    const uint32_t slot = sRing + ((s0 + C + h) % SLOTS) * kIpSlot;
+                    if (C == 2) widen(std::true_type(), 64 * h + 32 * half, 32, slot - h * 8192, slot - h * 8192 + 8192);
+                    else widen(std::true_type(), 64 * half, 64, slot, slot);
+                    filled(s0 + C + h);
+                }
+                // (the raw tile's place is loaded again behind the last of `filled`'s fences)
+                if (ok && lane == 0) mbar_arrive(&bars[kIpRawEmpty + rs]);
+            }
+        }
+    } else {
+        // ---------------- softmax (a row per thread) and epilogue ----------------
+        const int i = (warp - 4) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const float NEG_INF = -__int_as_float(0x7f800000);
+        const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * i;
+        const uint32_t tO = tS + 256u;
+        // the sign of the scale goes into the query, so that the largest score has the largest weight
+        const float sl2 = fabsf(p.scale_log2), flip = p.scale_log2 < 0.f ? -1.f : 1.f;
+        bool ok = true;
+        float factor = 0.f, bias = 0.f;                // of this thread's row: to log2 units, and 1152 sum q times it
+        int tok = 0, hh = 0, lim = INT32_MAX;          // keys [0, lim) visible (a row that is none sees all, for nobody)
+        bool mine = false;
+        // this thread's row of an item: into shared memory as f16, zeros past the request
+        auto load_q = [&](const volatile IpItem *it) {
+            const int rrow = it->row0 + i * kIpRows + row;
+            mine = rrow < it->rows_total;
+            tok = mine ? it->qs + rrow / G : 0;
+            hh = mine ? it->g * G + rrow % G : 0;
+            lim = mine ? it->ctx + rrow / G + 1 : INT32_MAX;
+            const uint4 *qp = reinterpret_cast<const uint4 *>(query + static_cast<int64_t>(tok) * q_stride +
+                                                              static_cast<int64_t>(hh) * HD);
+            uint4 v[HD / 8];
+#pragma unroll
+            for (int c = 0; c < HD / 8; ++c) v[c] = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+            float a = 0.f;
+#pragma unroll
+            for (int c = 0; c < HD / 8; ++c) {
+                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+            }
+            // into [2^14, 2^15): exact but for parts below 2^-24 of the row's largest
+            const int ex = a > 0.f ? min(126, max(-114, 14 - ilogbf(a))) : 0;
+            const float up = __int_as_float((ex + 127) << 23) * flip;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < HD / 8; ++c) {
+                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * up,
+                                                        __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                    const float2 f = __half22float2(h);
+                    sum += f.x + f.y;
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                const uint32_t at = sQ + (i * C + (c >> 3)) * kIpSlot + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+            }
+            factor = sl2 * __int_as_float((127 - ex) << 23);
+            bias = kInt8Bias * sum;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kIpQFull + i]);
+        };
+        int cnt = 0, gt = 0;                           // key tiles of this row tile, and of the CTA, so far
+        ok = warp_wait_tiles(&bars[kIpItemFull], 0, tiles_loaded, status);
+        if (ok && items[0].valid && items[0].n[i]) load_q(items);
+        for (int k = 0; ok && items[k & 3].valid; ++k) {
+            const volatile IpItem *cur = items + (k & 3);
+            const int n = cur->n[i], n_kv = max(cur->n[0], cur->n[1]);
+            const int row_lim = lim;
+            const int64_t dst = mine ? (static_cast<int64_t>(tok) * p.num_q_heads + hh) * HD : -1;
+            float m = NEG_INF, l = 0.f;
+            for (int j = 0; j < n && ok; ++j, ++cnt) {
+                ok = warp_wait(&bars[kIpSFull + i], cnt & 1, status) &&
+                     warp_wait(&bars[kIpScFull + ((gt + j) & 7)], ((gt + j) >> 3) & 1, status);
+                if (!ok) break;
+                tc_fence_after();
+                float s[kIpKeys];
+#pragma unroll
+                for (int c = 0; c < kIpKeys / 32; ++c) tmem_ld32f(tS + 32 * c, s + 32 * c);
+                const float4 *sc = scales + ((gt + j) & 7) * kIpPages;
+                float f[kIpPages], c0[kIpPages], inv[kIpPages];
+#pragma unroll
+                for (int b = 0; b < kIpPages; ++b) {
+                    const float4 v = sc[b];
+                    // (not 0: a masked score times it is -inf)
+                    const float x = factor * v.x;
+                    f[b] = x < 1e-37f ? 1e-37f : x;
+                    c0[b] = fmaf(-bias, f[b], v.y);
+                    inv[b] = v.z;
+                }
+                tmem_ld_wait();
+                const int key0 = j * kIpKeys;
+                const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > row_lim);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kIpKeys; ++c) s[c] = key0 + c < row_lim ? s[c] : NEG_INF;
+                    // a block of which the row sees no key: nothing of its scale counts
+#pragma unroll
+                    for (int b = 0; b < kIpPages; ++b)
+                        if (key0 + b * kBlock >= row_lim) f[b] = 1.f, c0[b] = 0.f, inv[b] = 0.f;
+                }
+                float mx = NEG_INF;
+#pragma unroll
+                for (int b = 0; b < kIpPages; ++b) {
+                    const float *x = s + b * kBlock;
+                    const float a = fmax3(fmaxf(x[0], x[1]), x[2], x[3]), d = fmax3(fmaxf(x[4], x[5]), x[6], x[7]);
+                    const float e = fmax3(fmaxf(x[8], x[9]), x[10], x[11]), g = fmax3(fmaxf(x[12], x[13]), x[14], x[15]);
+                    mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a, d), fmaxf(e, g)), f[b], c0[b]));
+                }
+                // the reference moves on the first visible key, and when it is passed by 2^8 (f16 weights)
+                const bool first = m == NEG_INF;
+                const bool grow = !first && mx > m + 8.f;
+                const float alpha = grow ? fast_exp2(m - mx) : 1.f;
+                if (first || grow) m = mx;
+                if (__any_sync(0xffffffffu, grow)) {
+                    // rare: O rescaled once the previous tile's product has completed
+                    ok = warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < HD / 16; ++c) {
+                        float v[16];
+                        uint32_t w[16];
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                              "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+                              "=f"(v[14]), "=f"(v[15])
+                            : "r"(tO + 16 * c));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * alpha);
+                        tmem_st16(tO + 16 * c, w);
+                    }
+                    l *= alpha;
+                }
+                const float ref = m == NEG_INF ? 0.f : m;
+#pragma unroll
+                for (int c = 0; c < kIpKeys / 32; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int blk = 2 * c + b;
+                        const float cb = c0[blk] - ref;
+                        const uint64_t f2 = f2_pack(f[blk], f[blk]), c2 = f2_pack(cb, cb);
+                        uint64_t sum2 = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int at = blk * kBlock + 2 * e;
+                            float y0, y1;
+                            f2_unpack(f2_fma(f2_pack(s[at], s[at + 1]), f2, c2), y0, y1);
+                            if (masked) {              // (a scale that is no number reaches no key that is not seen)
+                                y0 = key0 + at < row_lim ? y0 : NEG_INF;
+                                y1 = key0 + at + 1 < row_lim ? y1 : NEG_INF;
+                            }
+                            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                            sum2 = e ? f2_add(sum2, f2_pack(p0, p1)) : f2_pack(p0, p1);
+                            w[8 * b + e] = pack_p<true>(p0, p1);
+                        }
+                        float a, d;
+                        f2_unpack(sum2, a, d);
+                        l = fmaf(a + d, inv[blk], l);
+                    }
+                    tmem_st16(tS + 16 * c, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kIpPFull + i]);
+            }
+            gt += n_kv;
+            // the next item's Q right away: every S of this item has completed
+            if (ok) ok = warp_wait_tiles(&bars[kIpItemFull + ((k + 1) & 3)], ((k + 1) / 4) & 1, tiles_loaded, status);
+            if (ok && items[(k + 1) & 3].valid && items[(k + 1) & 3].n[i]) load_q(items + ((k + 1) & 3));
+            if (ok && n) {
+                ok = warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
+                if (ok) {
+                    tc_fence_after();
+                    const float inv = l <= 0.f ? 0.f : 1.f / l;            // (NaN stays)
+                    uint32_t w[HD / 2];
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        float v[32];
+                        tmem_ld32f(tO + 32 * c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[16 * c + e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+                    }
+                    // O is in registers: the next item's first P V may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kIpOFree + i]);
+                    if (dst >= 0) {
+                        uint4 *o = reinterpret_cast<uint4 *>(p.out + dst);
+#pragma unroll
+                        for (int c = 0; c < HD / 8; ++c)
+                            o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kIpItemEmpty + (k & 3)]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    pdl_wait();       // complete only after the kernel launched before this one
+}
+
+// ---- host side --------------------------------------------------------------------
+
+template <int HD>
+static int launch_ip(const PrefillParams &p, const CUtensorMap &map, const void *query, int64_t q_stride,
+                     const float *kv_scales, int64_t grid, int dev, cudaStream_t stream) {
+    static std::mutex mu;
+    static uint64_t done_mask = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+        if (!bit || !(done_mask & bit)) {
+            if (cudaFuncSetAttribute(int8_prefill_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     IpCfg<HD>::kSmem) != cudaSuccess)
+                return PKV_ERR_CUDA;
+            done_mask |= bit;
+        }
+    }
+    return launch_pdl(int8_prefill_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(kIpThreads), IpCfg<HD>::kSmem, stream,
+                      map, static_cast<const __nv_bfloat16 *>(query), q_stride,
+                      reinterpret_cast<const float2 *>(kv_scales), p) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_stride, const void *kv_cache,
+                        const float *kv_scales, int64_t num_blocks, int32_t head_size, int64_t grid, int dev,
+                        cudaStream_t stream) {
+    if (grid <= 0) return PKV_OK;
+    // a box is a page of one kv head, K rows then V rows, as they lie
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    CUtensorMap map;
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(head_size), kBlock, 2, static_cast<cuuint64_t>(p.num_kv_heads),
+                                static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t row = static_cast<cuuint64_t>(head_size);
+    const cuuint64_t strides[4] = {row, row * kBlock, row * kBlock * 2, row * kBlock * 2 * p.num_kv_heads};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(head_size), kBlock, 2, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv_cache), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PKV_ERR_CUDA;
+    return head_size == 64 ? launch_ip<64>(p, map, query, q_stride, kv_scales, grid, dev, stream)
+                           : launch_ip<128>(p, map, query, q_stride, kv_scales, grid, dev, stream);
+}
+
+}  // namespace pkv

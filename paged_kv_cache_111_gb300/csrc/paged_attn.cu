@@ -105,6 +105,7 @@ struct PlanParams {
     int32_t num_splits;       // 0 = auto
     int32_t total_warps;      // warps of the decode grid (for the automatic split size)
     int32_t prefill_ok;       // long requests go to the tensor-core prefill kernel
+    int32_t tile_rows;        // rows of its work items
     int32_t prefix_blocks;    // shared prefix of the tables in blocks (0: no cascade)
     const int32_t *block_tables;
     WsLayout lay;
@@ -114,7 +115,7 @@ struct PlanParams {
 // ---- 1. planning ------------------------------------------------------------------
 
 // Work of request r.  mode 0: rows split along key pages (q_r * G <= 16);
-// mode 1: 16-row tiles on the decode kernel; mode 2: 128-row tiles on the
+// mode 1: 16-row tiles on the decode kernel; mode 2: tile_rows-row tiles on the
 // tensor-core prefill kernel.
 struct ReqPlan {
     int valid;        // metadata consistent
@@ -164,7 +165,7 @@ __device__ ReqPlan plan_request(const PlanParams &p, const int *qsl, const int *
         rp.n_chunks = sg.y;
     } else if (p.prefill_ok && rp.rows > kDecodeTileMaxRows) {
         rp.mode = 2;
-        rp.n_chunks = div_up(rp.rows, kPrefillRows);
+        rp.n_chunks = div_up(rp.rows, p.tile_rows);
     } else {
         rp.mode = 1;
         rp.n_chunks = div_up(rp.rows, 16);
@@ -180,12 +181,12 @@ __device__ __forceinline__ int4 chunk_geometry(const ReqPlan &rp) {
 
 // Mode 0/1: page range of chunk k.  Mode 2: {0, KV tiles} of tile k.  A tile
 // ending before request row `row_end` sees keys 0 .. ctx + last_row / G.
-__device__ __forceinline__ int2 chunk_pages(const int4 &gm, int G, int k) {
+__device__ __forceinline__ int2 chunk_pages(const int4 &gm, int G, int k, int tile_rows) {
     if (gm.x == 0) {
         const int b = gm.y + k * gm.z;
         return make_int2(b, min(gm.w, b + gm.z));
     }
-    const int row_end = gm.x == 1 ? 16 * k + 16 : kPrefillRows * (k + 1);
+    const int row_end = gm.x == 1 ? 16 * k + 16 : tile_rows * (k + 1);
     const int lim = gm.y + (min(gm.z, row_end) - 1) / G + 1;
     if (gm.x == 1) return make_int2(0, div_up(lim, kBlock));
     return make_int2(0, div_up(lim, kPrefillKeys));
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         const int r = owner(c);
         const int4 ri = req[r];
         const int4 gm = geometry(r, ri);
-        const int2 pg = chunk_pages(gm, G, c - ri.z);
+        const int2 pg = chunk_pages(gm, G, c - ri.z, p.tile_rows);
         if (gm.x == 2) agg_inc(pbin_count, min(pg.y, kSizeBins - 1));
         else agg_inc(bin_count, min(pg.y - pg.x, kSizeBins - 1));
     }
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         const bool casc = is_cascade(ri);
         const int4 gm = geometry(r, ri);
         const int k = c - ri.z;
-        const int2 pg = chunk_pages(gm, G, k);
+        const int2 pg = chunk_pages(gm, G, k, p.tile_rows);
         if (gm.x == 2) {
             const int pos = agg_inc(pbin_cursor, min(pg.y, kSizeBins - 1));
             if (pos < p.lay.max_ptiles) ptiles[pos] = make_int4(r, k, pg.y, 0);
@@ -595,7 +596,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
 
     // long chunks and the shared-prefix pass go to the tensor-core tile kernel
     // (which widens an E4M3 cache's pages to f16 itself)
-    const bool prefill_ok = !int8 && prefill_supported(num_q_heads, num_kv_heads, head_size);
+    const bool prefill_ok = int8 || prefill_supported(num_q_heads, num_kv_heads, head_size);
     if (!prefill_ok) prefix_blocks = 0;
     const WsLayout lay = ws_layout(num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
                                    head_size, prefix_blocks);
@@ -660,6 +661,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     pp.num_splits = num_splits;
     pp.total_warps = static_cast<int32_t>(chunk_warps);
     pp.prefill_ok = prefill_ok ? 1 : 0;
+    pp.tile_rows = int8 ? 2 * kPrefillRows : kPrefillRows;
     pp.prefix_blocks = prefix_blocks;
     pp.block_tables = block_tables;
     pp.lay = lay;
@@ -725,6 +727,9 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     }
     if (!may_prefill) return PKV_OK;
     const int64_t items = lay.max_ptiles * num_kv_heads;
+    if (int8)
+        return launch_prefill_int8(fp, query, query_token_stride, kv_cache, kv_scales, num_blocks, head_size,
+                                   std::min(max_ctas, items), dev, st);
     return kv8 ? launch_prefill_e4m3(fp, query, query_token_stride, kv_cache, num_blocks, head_size,
                                      std::min(max_ctas, items), dev, st)
                : launch_prefill_sk(fp, query, query_token_stride, num_tokens, kv_cache, num_blocks, head_size,
