@@ -11,12 +11,12 @@
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and share
 // each 128-key tile; a persistent CTA an SM takes items largest first.  Per key tile: 8 pages (one TMA box each, K and V)
-// land raw, two warps widen them into a ring of 16 KiB slots in the layout the products read, S = Q K^T from shared
+// land raw, four warps widen them into a ring of 16 KiB slots in the layout the products read, S = Q K^T from shared
 // memory (128 x 128 x 16), softmax by four warps a row tile (a row per thread), P as f16 over S in tensor memory,
 // O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
 //
-// Warp roles (384 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2 and 3 widen,
-// warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is bounded.
+// Warp roles (448 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2, 3, 12 and 13 widen
+// (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is bounded.
 #include <mutex>
 #include <type_traits>
 
@@ -28,11 +28,13 @@ namespace pkv {
 constexpr int kIpRows = 128;                          // of a row tile
 constexpr int kIpKeys = 128;                          // of a key tile
 constexpr int kIpPages = kIpKeys / kBlock;
-constexpr int kIpThreads = 384;
+constexpr int kIpSoft = 4;                            // softmax warps of a row tile
+constexpr int kIpWiden = 4;                           // warps that widen
+constexpr int kIpThreads = 32 * (2 + kIpWiden + 2 * kIpSoft);
 constexpr int kIpSlot = 16384;                        // 64 dims of 128 rows, or 128 dims of 64 rows, as f16
 constexpr int kIpRaw = 2;                             // raw key tiles in flight
 constexpr int kIpScaleTiles = 8;                      // key tiles whose blocks' scales are held
-constexpr int kIpReaders = 11;                        // of an item: MMA, two widening and eight softmax warps
+constexpr int kIpReaders = 1 + kIpWiden + 2 * kIpSoft;    // of an item: MMA, widening and softmax warps
 
 template <int HD>
 struct IpCfg {
@@ -64,12 +66,37 @@ enum IpBar {
     kIpScFull = 38,      // (+ tile & 7)
     kIpNumBars = 46
 };
-static_assert(kIpNumBars * 8 + 16 <= 512, "barriers, the tensor-memory address and the tile count");
+static_assert(kIpNumBars * 8 + 8 <= 512, "barriers, the tensor-memory address and the tile count");
 
 struct IpItem {
-    int32_t valid, r, g, n[2], L, qs, ctx, rows_total, row0, n_pages, tile;
+    int32_t valid, r, g, n[2], L, qs, ctx, rows_total, row0, n_pages;
 };
 static_assert(kItemSlots * sizeof(IpItem) <= 256 && kItemSlots == 4, "the item ring's place");
+
+// The bounded waits of this kernel, their loops once in the code: five roles run side by side, and with every wait and
+// loop unrolled in place instruction fetch bounds the kernel.
+__device__ __noinline__ bool ip_wait_long(uint64_t *bar, uint32_t parity, int32_t *status) {
+    return pf_wait(bar, parity, status);
+}
+__device__ __forceinline__ bool ip_wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+    return mbar_try_wait(bar, parity) || ip_wait_long(bar, parity, status);
+}
+__device__ __forceinline__ bool ip_warp_wait(uint64_t *bar, uint32_t parity, int32_t *status) {
+    return __all_sync(0xffffffffu, ip_wait(bar, parity, status));
+}
+__device__ __noinline__ bool ip_warp_wait_tiles(uint64_t *bar, uint32_t parity, const volatile int32_t *tiles,
+                                                int32_t *status) {
+    return warp_wait_tiles(bar, parity, tiles, status);
+}
+
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
+}
 
 template <int HD>
 __global__ void __launch_bounds__(kIpThreads, 1)
@@ -102,10 +129,10 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         const int b = threadIdx.x;
         int count = 1;
         if (b >= kIpItemEmpty && b < kIpItemEmpty + 4) count = kIpReaders;
-        else if ((b >= kIpRawEmpty && b < kIpRawEmpty + 2) || (b >= kIpFull && b < kIpFull + 8)) count = 2;
+        else if ((b >= kIpRawEmpty && b < kIpRawEmpty + 2) || (b >= kIpFull && b < kIpFull + 8)) count = kIpWiden;
         else if ((b >= kIpQFull && b < kIpQFull + 2) || (b >= kIpPFull && b < kIpPFull + 2) ||
                  (b >= kIpOFree && b < kIpOFree + 2))
-            count = 4;
+            count = kIpSoft;
         mbar_init(&bars[b], count);
     }
     if (threadIdx.x == 0) {
@@ -129,7 +156,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         int *next_item = reinterpret_cast<int *>(p.ws + offsetof(WsHeader, next_ptile_item));
         for (int k = 0; ok; ++k) {
             const int slot = k & 3;
-            if (k >= 4) ok = warp_wait(&bars[kIpItemEmpty + slot], (k / 4 - 1) & 1, status);
+            if (k >= 4) ok = ip_warp_wait(&bars[kIpItemEmpty + slot], (k / 4 - 1) & 1, status);
             if (!ok) break;
             IpItem it{};
             if (item < n_items) {
@@ -174,16 +201,17 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 return b >= 0 && b < p.num_blocks ? __ldg(kv_scales + static_cast<int64_t>(b) * p.num_kv_heads + it.g)
                                                   : make_float2(0.f, 1.f);
             };
-            int win = blocks_of(0), win_next = blocks_of(1);
-            float2 sc = scales_of(win), sc_next = make_float2(0.f, 1.f);
+            int win = 0, win_next = blocks_of(0);
+            float2 sc = make_float2(0.f, 1.f), sc_next = scales_of(win_next);
+#pragma unroll 1
             for (int j = 0; j < n_kv && ok; ++j, ++gt) {
-                if (j > 0 && (j & 3) == 0) {
+                if ((j & 3) == 0) {
                     win = win_next, sc = sc_next;
                     win_next = blocks_of(j / 4 + 1);
                 }
                 if ((j & 3) == 2) sc_next = scales_of(win_next);
                 const int rs = gt & 1;
-                if (gt >= kIpRaw) ok = warp_wait(&bars[kIpRawEmpty + rs], (gt / kIpRaw - 1) & 1, status);
+                if (gt >= kIpRaw) ok = ip_warp_wait(&bars[kIpRawEmpty + rs], (gt / kIpRaw - 1) & 1, status);
                 if (!ok) break;
                 uint8_t *raw = smem + Cfg::kOffRaw + rs * Cfg::kRawBytes;
                 if (lane == 0) {
@@ -219,7 +247,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             constexpr uint32_t kIdescO = idesc_f16_f32(kIpRows, HD, 0, 1);
             const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
             const uint64_t dv = smem_desc_sw128(sRing, 8192, 1024);       // MN-major: 64-dim chunks 8 KiB apart
-            auto wait = [&](int b, uint32_t parity) { return pf_wait(&bars[b], parity, status); };
+            auto wait = [&](int b, uint32_t parity) { return ip_wait(&bars[b], parity, status); };
             int landed = 0;                           // slots waited for
             int cnt[2] = {0, 0}, qs[2] = {0, 0};      // key tiles, items of each row tile so far
             int gt = 0;
@@ -255,8 +283,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     constexpr int kSteps = 8 / C;     // of 16 keys
 #pragma unroll
                     for (int kk = 0; kk < kSteps; ++kk)
-                        umma_f16_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * (h * kSteps + kk),
-                                    b + kk * (2048 >> 4), kIdescO, (h | kk) ? 1u : (first ? 0u : 1u));
+                        umma_f16_ts(tmem + 256u + 128u * i,
+                                    tmem + 128u * i + 8u * (h * kSteps + kk), b + kk * (2048 >> 4), kIdescO, (h | kk) ? 1u : (first ? 0u : 1u));
                     if (frees) umma_commit(&bars[kIpEmpty + slot]);
                 }
                 umma_commit(&bars[kIpODone + i]);
@@ -274,22 +302,28 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 const int n_kv = max(n[0], n[1]);
                 const bool two = n[1] > 0;            // the second row tile reads a slot last, where it has rows
                 // (the second sees as many key tiles as the first, or more)
-                ok = wait(kIpQFull, qs[0] & 1) && issue_s(0, gt, !two);
-                if (ok && two) ok = wait(kIpQFull + 1, qs[1] & 1) && issue_s(1, gt, true);
                 // row tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
-                for (int j = 0; j < n_kv && ok; ++j) {
-#pragma unroll
+#pragma unroll 1
+                for (int j = -1; j < n_kv && ok; ++j) {
+#pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
-                        if (!ok || j >= n[i]) continue;
+                        const int mine = i ? n[1] : n[0];
+                        if (!ok || max(j, 0) >= mine) continue;
                         const bool frees = i == (two ? 1 : 0);
-                        ok = wait(kIpPFull + i, cnt[i] & 1);
-                        // the item before's O has been read out
-                        if (ok && j == 0 && qs[i] > 0) ok = wait(kIpOFree + i, (qs[i] - 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        ok = issue_pv(i, gt + j, j == 0, frees);
-                        ++cnt[i];
-                        if (ok && j + 1 < n[i]) ok = issue_s(i, gt + j + 1, frees);
+                        if (j < 0) {
+                            ok = wait(kIpQFull + i, (i ? qs[1] : qs[0]) & 1);
+                        } else {
+                            ok = wait(kIpPFull + i, (i ? cnt[1] : cnt[0]) & 1);
+                            // the item before's O has been read out
+                            if (ok && j == 0 && (i ? qs[1] : qs[0]) > 0)
+                                ok = wait(kIpOFree + i, ((i ? qs[1] : qs[0]) - 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            ok = issue_pv(i, gt + j, j == 0, frees);
+                            if (i) ++cnt[1];
+                            else ++cnt[0];
+                        }
+                        if (ok && j + 1 < mine) ok = issue_s(i, gt + j + 1, frees);
                     }
                 }
                 gt += n_kv;
@@ -298,87 +332,90 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 4) {
-        // ---------------- widening: each of the two warps half of every slot ----------------
-        // (both wait for every release of every slot: neither can meet a barrier two phases on)
-        const int half = warp - 2;
+    } else if (warp < 4 || warp >= 4 + 2 * kIpSoft) {
+        // ---------------- widening: each of the warps its share of every slot ----------------
+        // (all wait for every release of every slot: none can meet a barrier two phases on)
+        const int part = warp < 4 ? warp - 2 : warp - 2 * kIpSoft - 2;
         bool ok = true;
         int gt = 0;
-        uint32_t src = 0;
         auto freed = [&](int s) {
-            return s < SLOTS || warp_wait(&bars[kIpEmpty + s % SLOTS], (s / SLOTS - 1) & 1, status);
+            return s < SLOTS || ip_warp_wait(&bars[kIpEmpty + s % SLOTS], (s / SLOTS - 1) & 1, status);
         };
         auto filled = [&](int s) {                     // (the fence: for the tensor cores)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kIpFull + s % SLOTS]);
         };
-        // rows r0 .. of the raw tile in pieces of 16 dims, P a row, so that eight lanes read 128 bytes side by side;
-        // `at`: the places of 64-dim chunks 0 and 1 of row 0
-        constexpr int P = HD / 16;
-        auto widen = [&](auto is_v, int r0, int rows, uint32_t at0, uint32_t at1) {
+        // A warp widens 8 rows x 64 dims at a time, four lanes a row, 16 dims a lane.  Of eight lanes that access memory
+        // together four have row a and four row a ^ 5 (64 dims: a ^ 1): the raw rows of 128 bytes lie with their 16-byte
+        // pieces permuted by the row (TMA), those of 64 bytes as they are, and the f16 rows with theirs permuted by the
+        // row too, so neither the reads nor the writes meet in a bank.
+        const int c = lane & 3;
+        const int r8 = HD == 128 ? ((lane >> 2) & 1 ? (lane >> 3) ^ 5 : lane >> 3) : lane >> 2;
+        const uint32_t from = r8 * HD + (HD == 128 ? (c ^ r8) << 4 : c << 4);     // (second 64 dims: ^ 64)
+        const uint32_t to = r8 * 128 + (((2 * c) ^ r8) << 4);                     // (its second 8 dims: ^ 16)
+        // groups g0 .. of 8 rows of the raw tile at src (page g / 2), to groups of a slot (dst0; the second 64 dims: dst1)
+        constexpr int B = 4 / C;                       // groups at a time: four 16-byte loads a lane
+        auto widen = [&](auto is_v, int groups, uint32_t src, int g0, uint32_t dst0, uint32_t dst1) {
             constexpr bool V = decltype(is_v)::value;
 #pragma unroll 1
-            for (int u0 = 0; u0 < rows * P / 32; u0 += 4) {
+            for (int n = 0; n < groups; n += B) {
                 uint32_t w[4][4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int piece = (u0 + u) * 32 + lane, r = r0 + piece / P, c = piece % P;
+                    const int g = g0 + n + u / C;
+                    const uint32_t at = src + (g >> 1) * (2 * kBlock * HD) + (g & 1) * 8 * HD + (V ? kBlock * HD : 0) + from;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
-                                 : "r"(src + (V ? kBlock * HD : 0) + (r / kBlock) * (2 * kBlock * HD) + (r % kBlock) * HD +
-                                       c * 16));
+                                 : "r"(at ^ (64u * (u % C))));
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int piece = (u0 + u) * 32 + lane, r = r0 + piece / P, c = piece % P;
-                    // lanes of the second 64 dims store their halves the other way round: no two meet in a bank
-                    const bool turn = (c >> 2) & 1;
-                    const uint32_t v[4] = {turn ? w[u][2] : w[u][0], turn ? w[u][3] : w[u][1],
-                                           turn ? w[u][0] : w[u][2], turn ? w[u][1] : w[u][3]};
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        int8x4_to_biased_f16(v[e], h[2 * e], h[2 * e + 1]);
+                        int8x4_to_biased_f16(w[u][e], h[2 * e], h[2 * e + 1]);
                         if (V) h[2 * e] = unbias_f16(h[2 * e]), h[2 * e + 1] = unbias_f16(h[2 * e + 1]);
                     }
-                    const uint32_t row = (turn ? at1 : at0) + r * 128;
-                    const int first = ((2 * c + (turn ? 1 : 0)) & 7) ^ (r & 7);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (first << 4)), "r"(h[0]), "r"(h[1]),
-                                 "r"(h[2]), "r"(h[3])
+                    const uint32_t row = (u % C ? dst1 : dst0) + (n + u / C) * 1024 + to;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                                 "r"(h[3])
                                  : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((first ^ 1) << 4)), "r"(h[4]),
-                                 "r"(h[5]), "r"(h[6]), "r"(h[7])
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row ^ 16u), "r"(h[4]), "r"(h[5]),
+                                 "r"(h[6]), "r"(h[7])
                                  : "memory");
                 }
             }
         };
+        constexpr int KG = 16 / kIpWiden, VG = 16 / C / kIpWiden;        // groups a warp: of a K tile, of a slot of V
         for (int k = 0; ok; ++k) {
             const int islot = k & 3;
-            ok = warp_wait(&bars[kIpItemFull + islot], (k / 4) & 1, status);
+            ok = ip_warp_wait(&bars[kIpItemFull + islot], (k / 4) & 1, status);
             if (!ok) break;
             const bool valid = items[islot].valid != 0;
             const int n_kv = max(items[islot].n[0], items[islot].n[1]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kIpItemEmpty + islot]);
             if (!valid) break;
+#pragma unroll 1
             for (int j = 0; j < n_kv && ok; ++j, ++gt) {
                 const int rs = gt & 1, s0 = gt * PER;
-                ok = warp_wait(&bars[kIpRawFull + rs], (gt / kIpRaw) & 1, status);
-                src = smem_u32(smem + Cfg::kOffRaw + rs * Cfg::kRawBytes);
+                ok = ip_warp_wait(&bars[kIpRawFull + rs], (gt / kIpRaw) & 1, status);
+                const uint32_t src = smem_u32(smem + Cfg::kOffRaw + rs * Cfg::kRawBytes);
                 // K: dims 64 c .. of row r in slot c
-                for (int c = 0; c < C && ok; ++c) ok = freed(s0 + c);
+#pragma unroll 1
+                for (int s = 0; s < C && ok; ++s) ok = freed(s0 + s);
                 if (!ok) break;
-                widen(std::false_type(), 64 * half, 64, sRing + (s0 % SLOTS) * kIpSlot,
-                      sRing + ((s0 + C - 1) % SLOTS) * kIpSlot);
-                for (int c = 0; c < C; ++c) filled(s0 + c);
+                const uint32_t k0 = sRing + (s0 % SLOTS) * kIpSlot, k1 = sRing + ((s0 + C - 1) % SLOTS) * kIpSlot;
+                widen(std::false_type(), KG, src, part * KG, k0 + part * KG * 1024, k1 + part * KG * 1024);
+                for (int s = 0; s < C; ++s) filled(s0 + s);
                 // V: rows 64 h .. in slot h, 64-dim chunks 8 KiB apart (64 dims: one slot)
-                for (int h = 0; h < C && ok; ++h) {
+#pragma unroll 1
+                for (int h = 0; h < C; ++h) {
                     ok = freed(s0 + C + h);
                     if (!ok) break;
-                    const uint32_t slot = sRing + ((s0 + C + h) % SLOTS) * kIpSlot;
-                    if (C == 2) widen(std::true_type(), 64 * h + 32 * half, 32, slot - h * 8192, slot - h * 8192 + 8192);
-                    else widen(std::true_type(), 64 * half, 64, slot, slot);
+                    const uint32_t slot = sRing + ((s0 + C + h) % SLOTS) * kIpSlot + part * VG * 1024;
+                    widen(std::true_type(), VG, src, 8 * h + part * VG, slot, slot + 8192);
                     filled(s0 + C + h);
                 }
                 // (the raw tile's place is loaded again behind the last of `filled`'s fences)
@@ -387,7 +424,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         }
     } else {
         // ---------------- softmax (a row per thread) and epilogue ----------------
-        const int i = (warp - 4) >> 2, quad = warp & 3;
+        const int i = (warp - 4) / kIpSoft, quad = warp & 3;
         const int row = quad * 32 + lane;
         const float NEG_INF = -__int_as_float(0x7f800000);
         const uint32_t tS = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * i;
@@ -407,13 +444,11 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             lim = mine ? it->ctx + rrow / G + 1 : INT32_MAX;
             const uint4 *qp = reinterpret_cast<const uint4 *>(query + static_cast<int64_t>(tok) * q_stride +
                                                               static_cast<int64_t>(hh) * HD);
-            uint4 v[HD / 8];
-#pragma unroll
-            for (int c = 0; c < HD / 8; ++c) v[c] = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
             float a = 0.f;
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < HD / 8; ++c) {
-                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                const uint4 v = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
@@ -422,9 +457,10 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             const int ex = a > 0.f ? min(126, max(-114, 14 - ilogbf(a))) : 0;
             const float up = __int_as_float((ex + 127) << 23) * flip;
             float sum = 0.f;
-#pragma unroll
+#pragma unroll 4
             for (int c = 0; c < HD / 8; ++c) {
-                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                const uint4 v = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * up,
@@ -444,146 +480,166 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             if (lane == 0) mbar_arrive(&bars[kIpQFull + i]);
         };
         int cnt = 0, gt = 0;                           // key tiles of this row tile, and of the CTA, so far
-        ok = warp_wait_tiles(&bars[kIpItemFull], 0, tiles_loaded, status);
-        if (ok && items[0].valid && items[0].n[i]) load_q(items);
-        for (int k = 0; ok && items[k & 3].valid; ++k) {
+        float m = NEG_INF, l = 0.f;
+        int64_t dst = -1;
+        // (k: the item whose Q is loaded; the epilogue of the item before comes behind that)
+        int n = 0;
+        for (int k = 0;; ++k) {
+            ok = ip_warp_wait_tiles(&bars[kIpItemFull + (k & 3)], (k / 4) & 1, tiles_loaded, status);
+            if (!ok) break;
             const volatile IpItem *cur = items + (k & 3);
-            const int n = cur->n[i], n_kv = max(cur->n[0], cur->n[1]);
-            const int row_lim = lim;
-            const int64_t dst = mine ? (static_cast<int64_t>(tok) * p.num_q_heads + hh) * HD : -1;
-            float m = NEG_INF, l = 0.f;
-            for (int j = 0; j < n && ok; ++j, ++cnt) {
-                ok = warp_wait(&bars[kIpSFull + i], cnt & 1, status) &&
-                     warp_wait(&bars[kIpScFull + ((gt + j) & 7)], ((gt + j) >> 3) & 1, status);
+            const bool valid = cur->valid != 0;
+            const int n_before = n, n_kv = max(cur->n[0], cur->n[1]);
+            const int64_t dst_before = dst;
+            n = valid ? cur->n[i] : 0;
+            // Q right away: every S of the item before has completed
+            if (n) load_q(cur);
+            dst = n && mine ? (static_cast<int64_t>(tok) * p.num_q_heads + hh) * HD : -1;
+            if (n_before) {
+                ok = ip_warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
                 if (!ok) break;
                 tc_fence_after();
-                float s[kIpKeys];
+                const float inv = l <= 0.f ? 0.f : 1.f / l;                // (NaN stays)
+                uint32_t w[HD / 2];
 #pragma unroll
-                for (int c = 0; c < kIpKeys / 32; ++c) tmem_ld32f(tS + 32 * c, s + 32 * c);
-                const float4 *sc = scales + ((gt + j) & 7) * kIpPages;
-                float f[kIpPages], c0[kIpPages], inv[kIpPages];
+                for (int c = 0; c < HD / 32; ++c) {
+                    float v[32];
+                    tmem_ld32f(tO + 32 * c, v);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int b = 0; b < kIpPages; ++b) {
-                    const float4 v = sc[b];
-                    // (not 0: a masked score times it is -inf)
-                    const float x = factor * v.x;
-                    f[b] = x < 1e-37f ? 1e-37f : x;
-                    c0[b] = fmaf(-bias, f[b], v.y);
-                    inv[b] = v.z;
+                    for (int e = 0; e < 16; ++e) w[16 * c + e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
                 }
-                tmem_ld_wait();
-                const int key0 = j * kIpKeys;
-                const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > row_lim);
-                if (masked) {
+                // O is in registers: this item's first P V may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kIpOFree + i]);
+                if (dst_before >= 0) {
+                    uint4 *o = reinterpret_cast<uint4 *>(p.out + dst_before);
 #pragma unroll
-                    for (int c = 0; c < kIpKeys; ++c) s[c] = key0 + c < row_lim ? s[c] : NEG_INF;
-                    // a block of which the row sees no key: nothing of its scale counts
-#pragma unroll
-                    for (int b = 0; b < kIpPages; ++b)
-                        if (key0 + b * kBlock >= row_lim) f[b] = 1.f, c0[b] = 0.f, inv[b] = 0.f;
+                    for (int c = 0; c < HD / 8; ++c) o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                 }
-                float mx = NEG_INF;
-#pragma unroll
-                for (int b = 0; b < kIpPages; ++b) {
-                    const float *x = s + b * kBlock;
-                    const float a = fmax3(fmaxf(x[0], x[1]), x[2], x[3]), d = fmax3(fmaxf(x[4], x[5]), x[6], x[7]);
-                    const float e = fmax3(fmaxf(x[8], x[9]), x[10], x[11]), g = fmax3(fmaxf(x[12], x[13]), x[14], x[15]);
-                    mx = fmaxf(mx, fmaf(fmaxf(fmaxf(a, d), fmaxf(e, g)), f[b], c0[b]));
-                }
-                // the reference moves on the first visible key, and when it is passed by 2^8 (f16 weights)
-                const bool first = m == NEG_INF;
-                const bool grow = !first && mx > m + 8.f;
-                const float alpha = grow ? fast_exp2(m - mx) : 1.f;
-                if (first || grow) m = mx;
-                if (__any_sync(0xffffffffu, grow)) {
-                    // rare: O rescaled once the previous tile's product has completed
-                    ok = warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
-                    if (!ok) break;
-                    tc_fence_after();
+            }
+            __syncwarp();
+            if (valid && lane == 0) mbar_arrive(&bars[kIpItemEmpty + (k & 3)]);    // (what it says is in registers)
+            if (!valid) break;
+            m = NEG_INF, l = 0.f;
 #pragma unroll 1
-                    for (int c = 0; c < HD / 16; ++c) {
-                        float v[16];
-                        uint32_t w[16];
-                        asm volatile(
-                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-                              "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-                              "=f"(v[14]), "=f"(v[15])
-                            : "r"(tO + 16 * c));
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * alpha);
-                        tmem_st16(tO + 16 * c, w);
+            for (int j = 0; j < n; ++j, ++cnt) {
+                ok = ip_warp_wait(&bars[kIpSFull + i], cnt & 1, status) &&
+                     ip_warp_wait(&bars[kIpScFull + ((gt + j) & 7)], ((gt + j) >> 3) & 1, status);
+                if (!ok) break;
+                tc_fence_after();
+                const float4 *sc = scales + ((gt + j) & 7) * kIpPages;
+                const int key0 = j * kIpKeys;
+                const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > lim);
+                // three constants of block b of the tile: what S is times, what is added, what the weights' sum is times
+                auto constants = [&](int b, float &f, float &c0, float &inv) {
+                    const float4 v = sc[b];
+                    f = factor * v.x;
+                    f = f < 1e-37f ? 1e-37f : f;                         // (not 0: a masked score times it is -inf)
+                    c0 = fmaf(-bias, f, v.y);
+                    inv = v.z;
+                    if (masked) {
+                        // a block of which the row sees no key: nothing of its scales counts; one without a scale: the
+                        // keys that it does not see have weight 0 all the same, and the sum is no number
+                        if (key0 + b * kBlock >= lim) f = 1.f, c0 = 0.f, inv = 0.f;
+                        else if (!(fabsf(f) < 3e38f) || !(fabsf(c0) < 3e38f))
+                            f = 1.f, c0 = 0.f, inv = __int_as_float(0x7FC00000);
                     }
-                    l *= alpha;
-                }
-                const float ref = m == NEG_INF ? 0.f : m;
+                };
+                // The weights are taken against the reference that is there.  Where they sum to 2^13 or less none of
+                // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes the
+                // reference.  (Every row has its first visible key in the item's first tile.)
+                bool slow = j == 0;
+                uint32_t w[kIpKeys / 2];               // P, pairs of f16
+                float all, some;                       // the weights' sum, and that of the blocks' times 1 / vs
+                while (true) {
+                    if (slow) {
+                        float mx = NEG_INF;
+#pragma unroll 1
+                        for (int b = 0; b < kIpPages; ++b) {
+                            float x[16], f, c0, inv, y = NEG_INF;
+                            tmem_ld16f(tS + 16 * b, x);
+                            tmem_ld_wait();
+                            constants(b, f, c0, inv);
 #pragma unroll
-                for (int c = 0; c < kIpKeys / 32; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int blk = 2 * c + b;
-                        const float cb = c0[blk] - ref;
-                        const uint64_t f2 = f2_pack(f[blk], f[blk]), c2 = f2_pack(cb, cb);
-                        uint64_t sum2 = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int at = blk * kBlock + 2 * e;
-                            float y0, y1;
-                            f2_unpack(f2_fma(f2_pack(s[at], s[at + 1]), f2, c2), y0, y1);
-                            if (masked) {              // (a scale that is no number reaches no key that is not seen)
-                                y0 = key0 + at < row_lim ? y0 : NEG_INF;
-                                y1 = key0 + at + 1 < row_lim ? y1 : NEG_INF;
-                            }
-                            const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                            sum2 = e ? f2_add(sum2, f2_pack(p0, p1)) : f2_pack(p0, p1);
-                            w[8 * b + e] = pack_p<true>(p0, p1);
+                            for (int e = 0; e < kBlock; ++e) y = fmaxf(y, key0 + b * kBlock + e < lim ? x[e] : NEG_INF);
+                            mx = fmaxf(mx, fmaf(y, f, c0));
                         }
-                        float a, d;
-                        f2_unpack(sum2, a, d);
-                        l = fmaf(a + d, inv[blk], l);
+                        const bool grow = mx > m;      // (m = -inf at first)
+                        const float alpha = grow ? fast_exp2(m - mx) : 1.f;
+                        if (grow) m = mx;
+                        l *= alpha;
+                        if (j > 0) {
+                            // O rescaled once the previous tile's product has completed
+                            ok = ip_warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < HD / 16; ++c) {
+                                float v[16];
+                                uint32_t x[16];
+                                tmem_ld16f(tO + 16 * c, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(v[e] * alpha);
+                                tmem_st16(tO + 16 * c, x);
+                            }
+                        }
                     }
-                    tmem_st16(tS + 16 * c, w);
+                    const float ref = slow && m == NEG_INF ? 0.f : m;
+                    all = some = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kIpKeys / 32; ++c) {
+                        float x[32];
+                        tmem_ld32f(tS + 32 * c, x);
+                        tmem_ld_wait();
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = key0 + 32 * c + e < lim ? x[e] : NEG_INF;
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float f, c0, inv;
+                            constants(2 * c + h, f, c0, inv);
+                            const float cb = c0 - ref;
+                            const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
+                            uint64_t sum2 = 0;
+#pragma unroll
+                            for (int e = 0; e < kBlock / 2; ++e) {
+                                float y0, y1;
+                                f2_unpack(f2_fma(f2_pack(x[16 * h + 2 * e], x[16 * h + 2 * e + 1]), f2, c2), y0, y1);
+                                const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                                sum2 = e ? f2_add(sum2, f2_pack(p0, p1)) : f2_pack(p0, p1);
+                                w[16 * c + 8 * h + e] = pack_p<true>(p0, p1);
+                            }
+                            float a, d;
+                            f2_unpack(sum2, a, d);
+                            a += d;
+                            all += a;
+                            some = fmaf(a, inv, some);
+                        }
+                    }
+                    if (slow) break;
+                    slow = __any_sync(0xffffffffu, !(all <= 8192.f));
+                    if (!slow) break;
+                }
+                if (!ok) break;
+                l += some;
+#pragma unroll
+                for (int c = 0; c < kIpKeys / 64; ++c) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = w[32 * c + e];
+                    tmem_st32(tS + 32 * c, x);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kIpPFull + i]);
             }
+            if (!ok) break;
             gt += n_kv;
-            // the next item's Q right away: every S of this item has completed
-            if (ok) ok = warp_wait_tiles(&bars[kIpItemFull + ((k + 1) & 3)], ((k + 1) / 4) & 1, tiles_loaded, status);
-            if (ok && items[(k + 1) & 3].valid && items[(k + 1) & 3].n[i]) load_q(items + ((k + 1) & 3));
-            if (ok && n) {
-                ok = warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
-                if (ok) {
-                    tc_fence_after();
-                    const float inv = l <= 0.f ? 0.f : 1.f / l;            // (NaN stays)
-                    uint32_t w[HD / 2];
-#pragma unroll
-                    for (int c = 0; c < HD / 32; ++c) {
-                        float v[32];
-                        tmem_ld32f(tO + 32 * c, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[16 * c + e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
-                    }
-                    // O is in registers: the next item's first P V may overwrite it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[kIpOFree + i]);
-                    if (dst >= 0) {
-                        uint4 *o = reinterpret_cast<uint4 *>(p.out + dst);
-#pragma unroll
-                        for (int c = 0; c < HD / 8; ++c)
-                            o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kIpItemEmpty + (k & 3)]);
         }
     }
 
@@ -624,7 +680,7 @@ int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_str
                         const float *kv_scales, int64_t num_blocks, int32_t head_size, int64_t grid, int dev,
                         cudaStream_t stream) {
     if (grid <= 0) return PKV_OK;
-    // a box is a page of one kv head, K rows then V rows, as they lie
+    // a box is a page of one kv head, K rows then V rows; rows of 128 bytes with their 16-byte pieces permuted
     EncodeTiledFn enc = encode_fn();
     if (!enc) return PKV_ERR_CUDA;
     CUtensorMap map;
@@ -635,7 +691,8 @@ int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_str
     const cuuint32_t box[5] = {static_cast<cuuint32_t>(head_size), kBlock, 2, 1, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv_cache), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, head_size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return PKV_ERR_CUDA;
     return head_size == 64 ? launch_ip<64>(p, map, query, q_stride, kv_scales, grid, dev, stream)
