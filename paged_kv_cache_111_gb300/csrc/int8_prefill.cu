@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 const int b = __shfl_sync(0xffffffffu, win, at);
                 const float ks = __shfl_sync(0xffffffffu, sc.x, at);
                 float vs = __shfl_sync(0xffffffffu, sc.y, at);
-                vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;         // (NaN stays)
+                vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;         // (NaN stays, and K's joins it)
+                vs = ks != ks ? ks : vs;
                 if (lane < kIpPages) {
                     tma_load_5d(raw + lane * (2 * kBlock * HD), &kv_map, &bars[kIpRawFull + rs], 0, 0, 0, it.g, b);
                     scales[(gt & 7) * kIpPages + lane] = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
@@ -533,20 +534,32 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 const int key0 = j * kIpKeys;
                 const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > lim);
                 // three constants of block b of the tile: what S is times, what is added, what the weights' sum is times
+                const float least = masked ? 1e-37f : 0.f;               // (not 0 where a score may be -inf)
                 auto constants = [&](int b, float &f, float &c0, float &inv) {
                     const float4 v = sc[b];
-                    f = factor * v.x;
-                    f = f < 1e-37f ? 1e-37f : f;                         // (not 0: a masked score times it is -inf)
+                    f = fmaxf(factor * v.x, least);
                     c0 = fmaf(-bias, f, v.y);
                     inv = v.z;
-                    if (masked) {
-                        // a block of which the row sees no key: nothing of its scales counts; one without a scale: the
-                        // keys that it does not see have weight 0 all the same, and the sum is no number
-                        if (key0 + b * kBlock >= lim) f = 1.f, c0 = 0.f, inv = 0.f;
-                        else if (!(fabsf(f) < 3e38f) || !(fabsf(c0) < 3e38f))
-                            f = 1.f, c0 = 0.f, inv = __int_as_float(0x7FC00000);
-                    }
+                    // (a block without a scale, in a tile of which some rows do not see all: see below)
+                    if (masked && !(fabsf(c0) < 3e38f)) f = 1.f, c0 = inv = 0.f;
                 };
+                if (masked) {
+                    // keys that the row does not see: their scores become -inf where they lie.  Blocks without a scale make
+                    // the sums of the rows that see some of them no number, and have any other for those that do not.
+#pragma unroll 1
+                    for (int b = 0; b < kIpPages; ++b) {
+                        float x[16];
+                        uint32_t y[16];
+                        tmem_ld16f(tS + 16 * b, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < kBlock; ++e)
+                            y[e] = __float_as_uint(key0 + b * kBlock + e < lim ? x[e] : NEG_INF);
+                        tmem_st16(tS + 16 * b, y);
+                        if (key0 + b * kBlock < lim && sc[b].y != sc[b].y) l = sc[b].y;
+                    }
+                    tmem_st_wait();
+                }
                 // The weights are taken against the reference that is there.  Where they sum to 2^13 or less none of
                 // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes the
                 // reference.  (Every row has its first visible key in the item's first tile.)
@@ -563,7 +576,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                             tmem_ld_wait();
                             constants(b, f, c0, inv);
 #pragma unroll
-                            for (int e = 0; e < kBlock; ++e) y = fmaxf(y, key0 + b * kBlock + e < lim ? x[e] : NEG_INF);
+                            for (int e = 0; e < kBlock; ++e) y = fmaxf(y, x[e]);
                             mx = fmaxf(mx, fmaf(y, f, c0));
                         }
                         const bool grow = mx > m;      // (m = -inf at first)
@@ -594,30 +607,39 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                         float x[32];
                         tmem_ld32f(tS + 32 * c, x);
                         tmem_ld_wait();
-                        if (masked) {
+                        // (in three sweeps, each of them independent of itself: products, exponentials, sums and pairs)
+                        uint64_t y[16];
+                        float inv[2];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = key0 + 32 * c + e < lim ? x[e] : NEG_INF;
+                        for (int h = 0; h < 2; ++h) {
+                            float f, c0;
+                            constants(2 * c + h, f, c0, inv[h]);
+                            const float cb = c0 - ref;
+                            const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
+#pragma unroll
+                            for (int e = 8 * h; e < 8 * h + 8; ++e) y[e] = f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), f2, c2);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float y0, y1;
+                            f2_unpack(y[e], y0, y1);
+                            x[2 * e] = fast_exp2(y0), x[2 * e + 1] = fast_exp2(y1);
+                        }
+                        uint64_t sum[4];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t p2 = f2_pack(x[2 * e], x[2 * e + 1]);
+                            const int q = 2 * (e >> 3) + (e & 1);
+                            sum[q] = (e & 7) < 2 ? p2 : f2_add(sum[q], p2);
+                            w[16 * c + e] = pack_p<true>(x[2 * e], x[2 * e + 1]);
                         }
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float f, c0, inv;
-                            constants(2 * c + h, f, c0, inv);
-                            const float cb = c0 - ref;
-                            const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
-                            uint64_t sum2 = 0;
-#pragma unroll
-                            for (int e = 0; e < kBlock / 2; ++e) {
-                                float y0, y1;
-                                f2_unpack(f2_fma(f2_pack(x[16 * h + 2 * e], x[16 * h + 2 * e + 1]), f2, c2), y0, y1);
-                                const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                                sum2 = e ? f2_add(sum2, f2_pack(p0, p1)) : f2_pack(p0, p1);
-                                w[16 * c + 8 * h + e] = pack_p<true>(p0, p1);
-                            }
                             float a, d;
-                            f2_unpack(sum2, a, d);
+                            f2_unpack(f2_add(sum[2 * h], sum[2 * h + 1]), a, d);
                             a += d;
                             all += a;
-                            some = fmaf(a, inv, some);
+                            some = fmaf(a, inv[h], some);
                         }
                     }
                     if (slow) break;
