@@ -670,8 +670,9 @@ int pkv_qk_norm_rope_kv_write_int8(void *query_out, int64_t query_out_token_stri
 
 /*
  * pkv_paged_attn_int8 — pkv_paged_attn over an int8 cache, K_j and V_j being code *
- * scale.  Arguments, workspace and protocol (pkv_paged_attn_combine after it) as
- * pkv_paged_attn; any scale's sign is allowed.  Codes widen to f16 exactly; the query
+ * scale.  Arguments and protocol (pkv_paged_attn_combine after it) as pkv_paged_attn;
+ * any scale's sign is allowed.  The workspace is pkv_paged_attn's, and up to 41 MB more
+ * where max_query_len times the query heads of a kv head passes 64 (the size query says).  Codes widen to f16 exactly; the query
  * enters the products as f16 after a per-row power-of-two scaling (exact for every
  * element not below 2^-24 of its row's largest), the weights as one f16 each (2^-12
  * of it); scores, softmax and accumulation are fp32.  Rows behind a request's last

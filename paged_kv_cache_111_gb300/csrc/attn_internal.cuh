@@ -31,6 +31,8 @@ struct WsHeader {
     int32_t next_prefix_item;   // shared-prefix pass: the same
     int32_t n_split_tokens;     // tokens whose rows the combine merges
     int32_t epoch;              // decode kernel that plans itself: bumped once the header is written
+    int32_t split_items;        // chunks over an int8 cache: entries of the list of cut items (SplitItem)
+    int32_t unused;
     int64_t off_req;         // int4 [num_seqs]: {splits (0: refused), partial row base, first chunk, chunks}
     int64_t off_stoks;       // int4 [num_tokens]: split tokens {token, partial row of q head 0, splits, 0}
     int64_t off_chunks;      // int4 [max_chunks]: {request, split or tile, page begin, page end}
@@ -43,6 +45,7 @@ struct WsHeader {
     int64_t max_crows;
     int64_t max_prow;
     int64_t prow_used;
+    int64_t off_split;       // SplitLayout's base
 };
 static_assert(sizeof(WsHeader) <= 256, "header must fit its 256-byte slot");
 
@@ -57,6 +60,29 @@ struct WsLayout {
     int64_t max_chunks, max_ptiles, max_crows, max_prow;
     int32_t prefix_parts;     // splits of the shared prefix (0: no cascade)
 };
+
+// Chunks over an int8 cache (int8_prefill.cu), where work items are fewer than CTAs: the CTAs share them out in equal runs,
+// so that an item is cut along its keys.  Its pieces' sums lie behind the layout above, two places a CTA (what its run
+// begins with, and what it ends with): {reference, sum} of each row, and rows x head_size fp32 unnormalised sums, four dims
+// of each row side by side.  The CTA of an item's first piece notes it down, and the combine joins the pieces.
+constexpr int kSplitCtas = 152;            // CTAs at most
+constexpr int kSplitRows = 256;            // rows of an item
+struct SplitItem {
+    int32_t qs, rows_total, row0, h0;      // first query token, rows of the request, the item's first, its first query head
+    int32_t place, cta, pieces, G;         // the first piece's place (-1: no item) and CTA; query heads a kv head
+};
+struct SplitLayout {
+    int64_t off_items, off_state, off_sums, total;
+};
+__host__ __device__ inline SplitLayout split_layout(int64_t base, int64_t head_size) {
+    SplitLayout s;
+    s.off_items = base;
+    s.off_state = s.off_items + kSplitCtas * static_cast<int64_t>(sizeof(SplitItem));      // (multiples of 256)
+    s.off_sums = s.off_state + 2 * kSplitCtas * kSplitRows * 8;
+    s.total = s.off_sums + 2 * kSplitCtas * kSplitRows * head_size * 4;
+    return s;
+}
+static_assert(kSplitCtas * sizeof(SplitItem) % 256 == 0, "aligned regions");
 
 // ---- splitting decode rows along their keys (the plan kernel, and the decode
 // kernel when it plans a call itself, take the same decisions) ----
@@ -120,6 +146,7 @@ struct PrefillParams {
     int32_t lo_tiles;         // leading KV tiles whose P always enters P V as a bf16 pair
     float k_scale, v_scale;   // E4M3 cache: stored code * scale is the value
     uint8_t *ws;
+    SplitLayout split;        // int8 cache
 };
 
 // Log-sum-exp merge of one split row by one warp: the row's n partial

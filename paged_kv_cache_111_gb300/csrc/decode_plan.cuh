@@ -312,6 +312,7 @@ __device__ void decode_self_plan_publish(const AttnParams &p, const int *scr, co
         hdr->next_ptile_item = 0;
         hdr->next_prefix_item = 0;
         hdr->n_split_tokens = fits ? sh.tot.z : 0;
+        hdr->split_items = 0;
         hdr->off_req = p.lay.off_req;
         hdr->off_stoks = p.lay.off_stoks;
         hdr->off_chunks = p.lay.off_chunks;

@@ -6,14 +6,17 @@
 //     p'_j = 2^(e_j - m),          out = sum_j p'_j v_j / sum_j p'_j / vs
 // K's codes widen to f16 as 1152 + code (a byte next to 0x64) and stay so: what that adds to S is one number a row, and
 // goes with the block's factor into the constants of the softmax, of which a row has three a block of 16 keys.  V's
-// codes are taken back to themselves.  m is the row's largest e_j, moved only when passed by 2^8, so that p' fits f16
-// whatever the blocks' scales are.
+// codes are taken back to themselves.  m is the row's largest e_j so far, looked for again only where the weights of a tile
+// sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and share
-// each 128-key tile; a persistent CTA an SM takes items largest first.  Per key tile: 8 pages (one TMA box each, K and V)
-// land raw, four warps widen them into a ring of 16 KiB slots in the layout the products read, S = Q K^T from shared
-// memory (128 x 128 x 16), softmax by four warps a row tile (a row per thread), P as f16 over S in tensor memory,
-// O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
+// each 128-key tile; a persistent CTA an SM takes items largest first.  Where there are fewer items than CTAs their key
+// tiles are one line that is cut into an equal run for each CTA; the combine that follows joins the pieces' sums, which are
+// left in the workspace.
+//
+// Per key tile: 8 pages (one TMA box each, K and V) land raw, four warps widen them into a ring of 16 KiB slots in the
+// layout the products read, S = Q K^T from shared memory (128 x 128 x 16), softmax by four warps a row tile (a row per
+// thread), P as f16 over S in tensor memory, O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
 //
 // Warp roles (448 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2, 3, 12 and 13 widen
 // (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is bounded.
@@ -70,6 +73,8 @@ static_assert(kIpNumBars * 8 + 8 <= 512, "barriers, the tensor-memory address an
 
 struct IpItem {
     int32_t valid, r, g, n[2], L, qs, ctx, rows_total, row0, n_pages;
+    int32_t first;       // first key tile; n: key tiles from there on that each of the two row tiles sees
+    int32_t place;       // where the piece's sums go, -1: the item is whole
 };
 static_assert(kItemSlots * sizeof(IpItem) <= 256 && kItemSlots == 4, "the item ring's place");
 
@@ -98,6 +103,10 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
+// In the line that is cut, an item counts for as many units as it has key tiles and kIpOver more (Q, epilogue, and what a
+// piece more costs); a CTA gets kIpLeast units at least.
+constexpr int kIpOver = 3, kIpLeast = 6;
+
 template <int HD>
 __global__ void __launch_bounds__(kIpThreads, 1)
     int8_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __nv_bfloat16 *__restrict__ query,
@@ -119,10 +128,28 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     pdl_trigger();
     const WsHeader *hdr = reinterpret_cast<const WsHeader *>(p.ws);
     int32_t *status = reinterpret_cast<int32_t *>(p.ws);
-    const int n_items = ws_ld(&hdr->n_ptiles) * p.num_kv_heads;
-    if (static_cast<int>(blockIdx.x) >= n_items) {    // uniform over the CTA
+    const int n_tiles = ws_ld(&hdr->n_ptiles);
+    const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));     // {request, tile, key tiles, -}
+    const int n_items = n_tiles * p.num_kv_heads;
+    // fewer items than CTAs: the units of all items, and the CTAs that share them
+    const bool runs = n_items < static_cast<int>(gridDim.x);
+    int64_t all = 0;
+    int ctas = gridDim.x;
+    if (runs) {                                       // (a few hundred tiles at most)
+        for (int t = lane; t < n_tiles; t += 32) all += ws_ld(ptiles + t).z + kIpOver;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        all *= p.num_kv_heads;
+        ctas = static_cast<int>(min(static_cast<int64_t>(ctas), max(static_cast<int64_t>(1), all / kIpLeast)));
+    }
+    if (static_cast<int>(blockIdx.x) >= (runs ? (n_items ? ctas : 0) : n_items)) {     // uniform over the CTA
         pdl_wait();
         return;
+    }
+    SplitItem *cut = reinterpret_cast<SplitItem *>(p.ws + p.split.off_items) + blockIdx.x;
+    if (runs && threadIdx.x == 0) {
+        cut->place = -1;
+        if (blockIdx.x == 0) const_cast<WsHeader *>(hdr)->split_items = ctas;
     }
     const int G = p.G;
     if (threadIdx.x < kIpNumBars) {
@@ -152,31 +179,67 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     if (warp == 0) {
         // ---------------- items, raw pages, scales ----------------
         bool ok = true;
-        int item = blockIdx.x, taken = 0, gt = 0;     // gt: key tiles of this CTA so far
+        int taken = 0, gt = 0;                        // items, and key tiles of this CTA so far
+        int item = blockIdx.x;                        // whole items: the next one
         int *next_item = reinterpret_cast<int *>(p.ws + offsetof(WsHeader, next_ptile_item));
+        int tile = 0;                                 // runs: a tile, where its units begin, the next unit, and the end
+        int64_t at = 0, u = all * blockIdx.x / ctas;
+        const int64_t u0 = u, u1 = all * (blockIdx.x + 1) / ctas;
         for (int k = 0; ok; ++k) {
             const int slot = k & 3;
             if (k >= 4) ok = ip_warp_wait(&bars[kIpItemEmpty + slot], (k / 4 - 1) & 1, status);
             if (!ok) break;
             IpItem it{};
-            if (item < n_items) {
+            int n_kv = 0, last = 0;
+            int4 pt = make_int4(0, 0, 0, 0);
+            it.place = -1;
+            if (!runs) {
+                if (item < n_items) {
+                    pt = ws_ld(ptiles + item / p.num_kv_heads);
+                    it.g = item % p.num_kv_heads;
+                    n_kv = pt.z;
+                }
+            } else {
+                while (u < u1 && n_kv <= 0) {         // (a run may begin with an item's end that has no key tiles)
+                    pt = ws_ld(ptiles + tile);
+                    const int units = pt.z + kIpOver;
+                    const int64_t next = at + static_cast<int64_t>(units) * p.num_kv_heads;
+                    if (u >= next) {
+                        at = next, ++tile;
+                        continue;
+                    }
+                    it.g = static_cast<int>((u - at) / units);
+                    const int64_t begin = at + static_cast<int64_t>(it.g) * units;          // of this item
+                    const int o0 = static_cast<int>(u - begin);
+                    const int o1 = static_cast<int>(min(u1 - begin, static_cast<int64_t>(units)));
+                    it.first = max(0, o0 - kIpOver);
+                    n_kv = max(0, o1 - kIpOver) - it.first;
+                    if (n_kv > 0 && n_kv < pt.z) {
+                        it.place = 2 * static_cast<int>(blockIdx.x) + (u == u0 ? 0 : 1);
+                        // the run that its last key tile is in
+                        last = static_cast<int>(((begin + units) * ctas - 1) / all);
+                    }
+                    u = begin + o1;
+                }
+            }
+            if (n_kv > 0) {
                 it.valid = 1;
-                it.g = item % p.num_kv_heads;
-                const int4 tile =
-                    ws_ld(reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles)) + item / p.num_kv_heads);
-                it.r = tile.x;
+                it.r = pt.x;
                 it.L = p.seq_lens[it.r];
                 it.qs = p.qsl[it.r];
                 const int qlen = p.qsl[it.r + 1] - it.qs;
                 it.ctx = it.L - qlen;
                 it.rows_total = qlen * G;
-                it.row0 = tile.y * 2 * kIpRows;
+                it.row0 = pt.y * 2 * kIpRows;
                 it.n_pages = (it.L + kBlock - 1) / kBlock;
-                // key tiles that each of the two row tiles sees
                 for (int i = 0; i < 2; ++i) {
                     const int end = min(it.row0 + (i + 1) * kIpRows, it.rows_total);
-                    it.n[i] = end > it.row0 + i * kIpRows ? (it.ctx + (end - 1) / G + kIpKeys) / kIpKeys : 0;
+                    const int seen = end > it.row0 + i * kIpRows ? (it.ctx + (end - 1) / G + kIpKeys) / kIpKeys : 0;
+                    it.n[i] = max(0, min(seen - it.first, n_kv));
                 }
+                if (it.place >= 0 && it.first == 0 && lane == 0)
+                    *cut = SplitItem{it.qs, it.rows_total, it.row0, it.g * G, it.place, static_cast<int>(blockIdx.x),
+                                     last - static_cast<int>(blockIdx.x) + 1, G};
             }
             if (lane == 0) {
                 volatile int32_t *dst = reinterpret_cast<volatile int32_t *>(items + slot);
@@ -187,12 +250,11 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             }
             if (!it.valid) break;
             ++taken;
-            const int n_kv = max(it.n[0], it.n[1]);
             const int32_t *bt = p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks_per_seq;
             // block ids and their scales in windows of 32 pages (4 key tiles), one lane a page, the next window ahead;
             // pages past the sequence are -1 and load as zeros (outside the tensor map)
             auto blocks_of = [&](int w) -> int {
-                const int page = w * 32 + lane;
+                const int page = it.first * kIpPages + w * 32 + lane;
                 const int b = page < it.n_pages ? __ldg(bt + page) : -1;
                 if (page < it.n_pages && (b < 0 || b >= p.num_blocks)) set_status(status, PKV_ERR_DEVICE_INDEX);
                 return b;
@@ -232,9 +294,11 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kIpScFull + (gt & 7)]);
             }
-            int nxt = 0;
-            if (lane == 0) nxt = static_cast<int>(gridDim.x) + atomicAdd(next_item, 1);
-            item = __shfl_sync(0xffffffffu, nxt, 0);
+            if (!runs) {
+                int nxt = 0;
+                if (lane == 0) nxt = static_cast<int>(gridDim.x) + atomicAdd(next_item, 1);
+                item = __shfl_sync(0xffffffffu, nxt, 0);
+            }
         }
         if (!ok)                                      // the copies in flight land before the CTA ends
             for (int t = max(0, gt - kIpRaw); t < gt; ++t)
@@ -301,8 +365,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 mbar_arrive(&bars[kIpItemEmpty + slot]);
                 if (!valid) break;
                 const int n_kv = max(n[0], n[1]);
-                const bool two = n[1] > 0;            // the second row tile reads a slot last, where it has rows
-                // (the second sees as many key tiles as the first, or more)
+                const bool two = n[1] > 0;            // the second row tile reads a slot last, where it sees keys
+                // (it sees as many key tiles as the first, or more, where it has rows)
                 // row tile i's P V of key tile j, then its S of j + 1 (over the P that was just read)
 #pragma unroll 1
                 for (int j = -1; j < n_kv && ok; ++j) {
@@ -328,7 +392,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     }
                 }
                 gt += n_kv;
-                ++qs[0];
+                if (n[0]) ++qs[0];
                 if (two) ++qs[1];
             }
         }
@@ -434,92 +498,120 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         const float sl2 = fabsf(p.scale_log2), flip = p.scale_log2 < 0.f ? -1.f : 1.f;
         bool ok = true;
         float factor = 0.f, bias = 0.f;                // of this thread's row: to log2 units, and 1152 sum q times it
-        int tok = 0, hh = 0, lim = INT32_MAX;          // keys [0, lim) visible (a row that is none sees all, for nobody)
-        bool mine = false;
+        int lim = INT32_MAX;                           // keys [0, lim) visible (a row that is none sees all, for nobody)
+        int64_t dst = -1;                              // where its output goes
         // this thread's row of an item: into shared memory as f16, zeros past the request
-        auto load_q = [&](const volatile IpItem *it) {
-            const int rrow = it->row0 + i * kIpRows + row;
-            mine = rrow < it->rows_total;
-            tok = mine ? it->qs + rrow / G : 0;
-            hh = mine ? it->g * G + rrow % G : 0;
-            lim = mine ? it->ctx + rrow / G + 1 : INT32_MAX;
-            const uint4 *qp = reinterpret_cast<const uint4 *>(query + static_cast<int64_t>(tok) * q_stride +
-                                                              static_cast<int64_t>(hh) * HD);
-            float a = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < HD / 8; ++c) {
-                const uint4 v = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        auto take_row = [&](const volatile IpItem *it) {
+            const int rrow = it->row0 + i * kIpRows + row, tok = rrow / G, hh = it->g * G + (rrow - tok * G);
+            const bool mine = rrow < it->rows_total;
+            lim = mine ? it->ctx + tok + 1 : INT32_MAX;
+            dst = mine ? (static_cast<int64_t>(it->qs + tok) * p.num_q_heads + hh) * HD : -1;
+            const uint4 *qp = reinterpret_cast<const uint4 *>(query + (it->qs + tok) * q_stride + static_cast<int64_t>(hh) * HD);
+            uint4 v[HD / 8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-            }
+            for (int c = 0; c < HD / 8; ++c) v[c] = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+            uint32_t a = 0;                            // the largest |q|, of the halves of the words
+#pragma unroll
+            for (int c = 0; c < HD / 8; ++c)
+                a = __vmaxu2(a, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
+            a = max(a & 0xFFFF0000u, a << 16);
             // into [2^14, 2^15): exact but for parts below 2^-24 of the row's largest
-            const int ex = a > 0.f ? min(126, max(-114, 14 - ilogbf(a))) : 0;
+            const int ex = a ? min(126, max(-114, 141 - static_cast<int>(a >> 23))) : 0;
             const float up = __int_as_float((ex + 127) << 23) * flip;
-            float sum = 0.f;
-#pragma unroll 4
+            const uint64_t up2 = f2_pack(up, up);
+            uint64_t sum2 = 0;
+#pragma unroll
             for (int c = 0; c < HD / 8; ++c) {
-                const uint4 v = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const __half2 h = __floats2half2_rn(__uint_as_float(w[e] << 16) * up,
-                                                        __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                    const float2 f = __half22float2(h);
-                    sum += f.x + f.y;
-                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                    const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), up2);
+                    float x0, x1;
+                    f2_unpack(x2, x0, x1);
+                    w[e] = pack_p<true>(x0, x1);
+                    sum2 = f2_add(sum2, x2);
                 }
                 const uint32_t at = sQ + (i * C + (c >> 3)) * kIpSlot + row * 128 + (((c & 7) ^ (row & 7)) << 4);
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                              : "memory");
             }
+            float s0, s1;
+            f2_unpack(sum2, s0, s1);
             factor = sl2 * __int_as_float((127 - ex) << 23);
-            bias = kInt8Bias * sum;
+            bias = kInt8Bias * (s0 + s1);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kIpQFull + i]);
         };
         int cnt = 0, gt = 0;                           // key tiles of this row tile, and of the CTA, so far
         float m = NEG_INF, l = 0.f;
-        int64_t dst = -1;
+        int place = -1, n = 0;
+        // A piece of an item: {reference, sum} and the sums as they are, into the workspace.
+        auto leave_piece = [&](int tiles) {
+            // (a row tile that sees none of these keys has no part; a sum that is no number counts in any join)
+            *(reinterpret_cast<float2 *>(p.ws + p.split.off_state) + static_cast<int64_t>(place) * kSplitRows + i * kIpRows + row) =
+                make_float2(tiles ? (l != l && m == NEG_INF ? 0.f : m) : NEG_INF, l);
+            if (!tiles) return true;
+            if (!ip_warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status)) return false;
+            tc_fence_after();
+            float4 *sums = reinterpret_cast<float4 *>(p.ws + p.split.off_sums) +
+                           static_cast<int64_t>(place) * (HD / 4) * kSplitRows + i * kIpRows + row;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                float v[32];
+                tmem_ld32f(tO + 32 * c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sums[(8 * c + e) * kSplitRows] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kIpOFree + i]);
+            return true;
+        };
         // (k: the item whose Q is loaded; the epilogue of the item before comes behind that)
-        int n = 0;
         for (int k = 0;; ++k) {
             ok = ip_warp_wait_tiles(&bars[kIpItemFull + (k & 3)], (k / 4) & 1, tiles_loaded, status);
             if (!ok) break;
             const volatile IpItem *cur = items + (k & 3);
             const bool valid = cur->valid != 0;
-            const int n_before = n, n_kv = max(cur->n[0], cur->n[1]);
+            const int n_before = n, n_kv = max(cur->n[0], cur->n[1]), place_before = place;
             const int64_t dst_before = dst;
             n = valid ? cur->n[i] : 0;
+            const int first = cur->first;
             // Q right away: every S of the item before has completed
-            if (n) load_q(cur);
-            dst = n && mine ? (static_cast<int64_t>(tok) * p.num_q_heads + hh) * HD : -1;
-            if (n_before) {
+            if (n) take_row(cur);
+            if (place_before >= 0) {
+                ok = leave_piece(n_before);
+                if (!ok) break;
+            } else if (n_before) {
                 ok = ip_warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status);
                 if (!ok) break;
                 tc_fence_after();
                 const float inv = l <= 0.f ? 0.f : 1.f / l;                // (NaN stays)
-                uint32_t w[HD / 2];
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < HD / 32; ++c) {
                     float v[32];
                     tmem_ld32f(tO + 32 * c, v);
                     tmem_ld_wait();
+                    if (dst_before >= 0) {
+                        uint4 *o = reinterpret_cast<uint4 *>(p.out + dst_before) + 4 * c;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[16 * c + e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = make_uint4(pack_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                              pack_bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                              pack_bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                              pack_bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    }
                 }
-                // O is in registers: this item's first P V may overwrite it
+                // O is read: this item's first P V may overwrite it
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kIpOFree + i]);
-                if (dst_before >= 0) {
-                    uint4 *o = reinterpret_cast<uint4 *>(p.out + dst_before);
-#pragma unroll
-                    for (int c = 0; c < HD / 8; ++c) o[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-                }
             }
+            place = valid ? cur->place : -1;
             __syncwarp();
             if (valid && lane == 0) mbar_arrive(&bars[kIpItemEmpty + (k & 3)]);    // (what it says is in registers)
             if (!valid) break;
@@ -531,7 +623,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const float4 *sc = scales + ((gt + j) & 7) * kIpPages;
-                const int key0 = j * kIpKeys;
+                const int key0 = (first + j) * kIpKeys;
                 const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > lim);
                 // three constants of block b of the tile: what S is times, what is added, what the weights' sum is times
                 const float least = masked ? 1e-37f : 0.f;               // (not 0 where a score may be -inf)
@@ -547,22 +639,22 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     // keys that the row does not see: their scores become -inf where they lie.  Blocks without a scale make
                     // the sums of the rows that see some of them no number, and have any other for those that do not.
 #pragma unroll 1
-                    for (int b = 0; b < kIpPages; ++b) {
-                        float x[16];
-                        uint32_t y[16];
-                        tmem_ld16f(tS + 16 * b, x);
+                    for (int c = 0; c < kIpKeys / 32; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(tS + 32 * c, x);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < kBlock; ++e)
-                            y[e] = __float_as_uint(key0 + b * kBlock + e < lim ? x[e] : NEG_INF);
-                        tmem_st16(tS + 16 * b, y);
-                        if (key0 + b * kBlock < lim && sc[b].y != sc[b].y) l = sc[b].y;
+                        for (int e = 0; e < 32; ++e) x[e] = key0 + 32 * c + e < lim ? x[e] : 0xFF800000u;
+                        tmem_st32(tS + 32 * c, x);
+#pragma unroll
+                        for (int b = 2 * c; b < 2 * c + 2; ++b)
+                            if (key0 + b * kBlock < lim && sc[b].y != sc[b].y) l = sc[b].y;
                     }
                     tmem_st_wait();
                 }
                 // The weights are taken against the reference that is there.  Where they sum to 2^13 or less none of
                 // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes the
-                // reference.  (Every row has its first visible key in the item's first tile.)
+                // reference.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
                 bool slow = j == 0;
                 uint32_t w[kIpKeys / 2];               // P, pairs of f16
                 float all, some;                       // the weights' sum, and that of the blocks' times 1 / vs
@@ -570,14 +662,20 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     if (slow) {
                         float mx = NEG_INF;
 #pragma unroll 1
-                        for (int b = 0; b < kIpPages; ++b) {
-                            float x[16], f, c0, inv, y = NEG_INF;
-                            tmem_ld16f(tS + 16 * b, x);
+                        for (int b = 0; b < kIpPages; b += 2) {
+                            float x[32];
+                            tmem_ld32f(tS + 16 * b, x);
                             tmem_ld_wait();
-                            constants(b, f, c0, inv);
 #pragma unroll
-                            for (int e = 0; e < kBlock; ++e) y = fmaxf(y, x[e]);
-                            mx = fmaxf(mx, fmaf(y, f, c0));
+                            for (int h = 0; h < 2; ++h) {
+                                float f, c0, inv, *y = x + 16 * h;
+                                constants(b + h, f, c0, inv);
+#pragma unroll
+                                for (int e = 8; e > 0; e >>= 1)
+#pragma unroll
+                                    for (int d = 0; d < e; ++d) y[d] = fmaxf(y[d], y[d + e]);
+                                mx = fmaxf(mx, fmaf(y[0], f, c0));
+                            }
                         }
                         const bool grow = mx > m;      // (m = -inf at first)
                         const float alpha = grow ? fast_exp2(m - mx) : 1.f;

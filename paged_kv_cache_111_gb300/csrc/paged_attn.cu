@@ -520,6 +520,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         hdr->off_req = p.lay.off_req;
         hdr->off_stoks = p.lay.off_stoks;
         hdr->n_split_tokens = fits ? totals.w : 0;
+        hdr->split_items = 0;
+        hdr->off_split = p.lay.total;
         hdr->off_chunks = p.lay.off_chunks;
         hdr->off_ptiles = p.lay.off_ptiles;
         hdr->off_part_lse = p.lay.off_part_lse;
@@ -540,14 +542,67 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
 
 // ---- 3. combine -------------------------------------------------------------------------
 
+// The pieces of items that were cut along their keys (SplitItem), joined:
+//     out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+// A warp takes 32 rows (one a lane) x 8 dims of an item, two pieces at a time, as an online sum.
 template <int HD>
-__global__ void __launch_bounds__(256) combine_kernel(__nv_bfloat16 *out, const uint8_t *ws, int32_t num_tokens,
+__device__ __forceinline__ void join_split_items(__nv_bfloat16 *out, const uint8_t *ws, int n, int64_t base,
+                                                 int32_t num_q_heads, int warp, int warps) {
+    constexpr int kPer = kSplitRows / 32 * (HD / 8);
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const SplitLayout lay = split_layout(base, HD);
+    const int lane = threadIdx.x & 31;
+    const float2 *state = reinterpret_cast<const float2 *>(ws + lay.off_state);
+    const float4 *sums = reinterpret_cast<const float4 *>(ws + lay.off_sums);
+#pragma unroll 1
+    for (int u = warp; u < n * kPer; u += warps) {
+        const int4 *e = reinterpret_cast<const int4 *>(ws + lay.off_items) + 2 * (u / kPer);
+        const int4 what = __ldcg(e), where = __ldcg(e + 1);
+        if (where.x < 0) continue;
+        const int part = u % kPer, d0 = part % (HD / 8), row = part / (HD / 8) * 32 + lane, rrow = what.z + row;
+        float M = NEG_INF, L = 0.f, acc[8] = {};
+#pragma unroll 1
+        for (int k0 = 0; k0 < where.z; k0 += 2) {
+            float2 s[2];
+            float4 v[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int64_t place = k0 + k == 0 ? where.x : 2 * (where.y + min(k0 + k, where.z - 1));
+                s[k] = __ldcg(state + place * kSplitRows + row);
+                if (k0 + k >= where.z) s[k].x = NEG_INF;
+#pragma unroll
+                for (int d = 0; d < 2; ++d) v[k][d] = __ldcg(sums + (place * (HD / 4) + 2 * d0 + d) * kSplitRows + row);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (s[k].x == NEG_INF) continue;                   // (a piece of which the row sees no key)
+                const float top = fmaxf(M, s[k].x), keep = fast_exp2(M - top), f = fast_exp2(s[k].x - top);
+                M = top;
+                L = fmaf(f, s[k].y, keep * L);
+                const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+                for (int d = 0; d < 8; ++d) acc[d] = fmaf(f, x[d], keep * acc[d]);
+            }
+        }
+        if (rrow >= what.y) continue;
+        const float inv = L <= 0.f ? 0.f : 1.f / L;                // (NaN stays)
+        const int tok = rrow / where.w;
+        *reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(what.x + tok) * num_q_heads + what.w + rrow - tok * where.w) * HD +
+                                   8 * d0) =
+            make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                       pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(256, 4) combine_kernel(__nv_bfloat16 *out, const uint8_t *ws, int32_t num_tokens,
                                                       int32_t num_q_heads) {
     pdl_wait();       // every partial of the attention kernels is written
     const WsHeader *hdr = reinterpret_cast<const WsHeader *>(ws);
     // every header field this kernel uses, loaded at once (one round trip)
     const int magic = hdr->magic, h_tokens = hdr->num_tokens, h_heads = hdr->num_q_heads, h_hd = hdr->head_size;
-    const int n_split = hdr->n_split_tokens;
+    const int n_split = hdr->n_split_tokens, split_items = hdr->split_items;
+    const int64_t off_split = hdr->off_split;
     const int64_t off_stoks = hdr->off_stoks, off_lse = hdr->off_part_lse, off_o = hdr->off_part_o;
     if ((magic != kMagic) | (h_tokens != num_tokens) | (h_heads != num_q_heads) | (h_hd != HD)) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
@@ -567,6 +622,9 @@ __global__ void __launch_bounds__(256) combine_kernel(__nv_bfloat16 *out, const 
         merge_split_row<HD>(part_o, part_lse, st.y + static_cast<int64_t>(h) * st.z, st.z,
                             out + (static_cast<int64_t>(st.x) * num_q_heads + h) * HD, lane);
     }
+    if (split_items)
+        join_split_items<HD>(out, ws, split_items, off_split, num_q_heads, static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5),
+                             static_cast<int>(gridDim.x) * 8);
 }
 
 static int paged_attn_impl(void *out, const void *query, int64_t query_token_stride, const void *kv_cache,
@@ -600,11 +658,16 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     if (!prefill_ok) prefix_blocks = 0;
     const WsLayout lay = ws_layout(num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
                                    head_size, prefix_blocks);
-    if (workspace_needed) *workspace_needed = static_cast<size_t>(lay.total);
+    // (chunks over an int8 cache: room for the pieces of work items that are cut along their keys)
+    const bool may_prefill =
+        prefill_ok && static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads) > kDecodeTileMaxRows;
+    const SplitLayout split = split_layout(lay.total, head_size);
+    const int64_t needed = int8 && may_prefill ? split.total : lay.total;
+    if (workspace_needed) *workspace_needed = static_cast<size_t>(needed);
     if (num_seqs == 0) return PKV_OK;
     if (!out || !query || !kv_cache || !block_tables || !seq_lens || !query_start_loc) return PKV_ERR_NULL;
     if (int8 && !kv_scales) return PKV_ERR_NULL;
-    if (!workspace || workspace_bytes < static_cast<size_t>(lay.total)) return PKV_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < static_cast<size_t>(needed)) return PKV_ERR_WORKSPACE;
     if (query_token_stride < static_cast<int64_t>(num_q_heads) * head_size) return PKV_ERR_SHAPE;
     if (query_token_stride % 8) return PKV_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(query) |
@@ -636,7 +699,6 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     const int64_t max_items = lay.max_chunks * num_kv_heads;
     int64_t grid = std::max<int64_t>(1, std::min(resident, (max_items + nw - 1) / nw));
     const int G = num_q_heads / num_kv_heads;
-    const bool may_prefill = prefill_ok && static_cast<int64_t>(max_query_len) * G > kDecodeTileMaxRows;
     // a small decode-only batch is planned by the decode kernel itself: its
     // last CTA writes the header, the others (still one wave) take the chunks
     const int64_t sp_ctas = std::max<int64_t>(1, std::min(resident - 1, (max_items + nw - 1) / nw));
@@ -661,7 +723,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     pp.num_splits = num_splits;
     pp.total_warps = static_cast<int32_t>(chunk_warps);
     pp.prefill_ok = prefill_ok ? 1 : 0;
-    pp.tile_rows = int8 ? 2 * kPrefillRows : kPrefillRows;
+    pp.tile_rows = int8 ? kSplitRows : kPrefillRows;
     pp.prefix_blocks = prefix_blocks;
     pp.block_tables = block_tables;
     pp.lay = lay;
@@ -715,6 +777,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     fp.k_scale = k_scale;
     fp.v_scale = v_scale;
     fp.ws = ap.ws;
+    fp.split = split;
     // persistent kernels: one CTA per SM at most, and no more than their items
     const int64_t max_ctas = std::min(sms, kStatsCtas);
     if (prefix_blocks > 0) {
@@ -729,7 +792,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     const int64_t items = lay.max_ptiles * num_kv_heads;
     if (int8)
         return launch_prefill_int8(fp, query, query_token_stride, kv_cache, kv_scales, num_blocks, head_size,
-                                   std::min(max_ctas, items), dev, st);
+                                   std::min<int64_t>(max_ctas, kSplitCtas), dev, st);
     return kv8 ? launch_prefill_e4m3(fp, query, query_token_stride, kv_cache, num_blocks, head_size,
                                      std::min(max_ctas, items), dev, st)
                : launch_prefill_sk(fp, query, query_token_stride, num_tokens, kv_cache, num_blocks, head_size,

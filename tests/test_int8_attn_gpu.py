@@ -92,6 +92,38 @@ def test_chunks(hq, hkv, d, reqs):
     check(s, run(s))
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(40, 40, 128), (80, 40, 64), (60, 60, 128)])
+@pytest.mark.parametrize("reqs", [[(700, 800), (300, 300)], [(129, 129), (256, 1000), (257, 300), (1, 77)]])
+def test_more_work_items_than_ctas(hq, hkv, d, reqs):
+    s = batch(reqs, hq, hkv, d, seed=6)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("q", [17, 65, 128, 129, 256, 300])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (5, 1), (2, 2)])
+def test_a_few_work_items_of_many_keys(q, hq, hkv):
+    """Items cut along their keys, down to a few key tiles a piece, and cuts on the causal diagonal."""
+    for n in (q, q + 1, q + 500, q + 1900, 9000):
+        s = batch([(q, n)], hq, hkv, 128, seed=n)
+        check(s, run(s), str(n))
+    s = batch([(q, 5000), (1, 300), (q + 40, q + 40), (q + 3, 700)], hq, hkv, 64, seed=q)
+    check(s, run(s))
+
+
+def test_cut_items_with_blocks_without_a_scale():
+    s = batch([(200, 6000)], 4, 2, 64, seed=4)
+    want, bound = ref.attention(s["query"], s["cache"], s["scales"], s["tables"], s["lens"], s["qsl"], s["scale"])
+    for page in (3, 200, 370):                          # in pieces that all rows see; one that the last rows see
+        scales = s["scales"].clone()
+        s["scales"][s["tables"][0, page].long(), 1] = float("nan")
+        out = run(s)
+        sees = torch.arange(5800, 6000, device="cuda") >= page * BLOCK
+        assert torch.isnan(out[sees][:, 2:].float()).all()
+        ref.check(out[:, :2], want[:, :2], bound[:, :2])
+        ref.check(out[~sees], want[~sees], bound[~sees])
+        s["scales"] = scales
+
+
 @pytest.mark.parametrize("num_splits", [1, 2, 3, 7, 32])
 @pytest.mark.parametrize("d", [64, 128])
 def test_splits(num_splits, d):
