@@ -333,11 +333,12 @@ def paged_attn_shared_prefix_fp8(out: torch.Tensor, query: torch.Tensor, kv_cach
 
 def paged_attn_combine(out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Log-sum-exp merge of the rows pkv_paged_attn split; out as given to paged_attn."""
-    _need_cuda(out, workspace)
+    dev = out.get_device()
+    if dev < 0 or workspace.get_device() < 0:
+        raise ValueError("paged KV-cache calls take CUDA tensors only")
     T, H, d = out.shape
-    rc = load().pkv_paged_attn_combine(_ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       T, H, d, _stream(out, stream))
-    _check(rc, "pkv_paged_attn_combine")
+    _call(dev, "pkv_paged_attn_combine", (_lib or load()).pkv_paged_attn_combine, out.data_ptr(), workspace.data_ptr(),
+          workspace.nbytes, T, H, d, _raw_stream(dev, stream))
 
 
 def workspace_status(workspace: torch.Tensor) -> int:
