@@ -332,10 +332,12 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
         const int h = h0 + hh;
         const int64_t unit = unit_of(h);
         const float old = fresh ? 0.f : p.scales[unit];
+        const __nv_bfloat16 *rows = row_of(h, t - kBlock);
+        const int64_t step = side_of(h) ? p.v_stride : p.k_stride;
         uint4 raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            raw[u] = at[u] >= 0 ? load(row_of(h, t - kBlock + at[u])) : make_uint4(0, 0, 0, 0);
+            raw[u] = at[u] >= 0 ? load(rows + at[u] * step) : make_uint4(0, 0, 0, 0);
         uint64_t x[U][4];                                     // (FORM 0: made twice, for fewer registers)
         uint32_t m = 0;
 #pragma unroll
