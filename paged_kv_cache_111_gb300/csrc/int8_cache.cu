@@ -388,8 +388,10 @@ template <int HD>
 __global__ void __launch_bounds__(kGatherThreads) int8_gather_kernel(const Int8GatherParams p) {
     constexpr int kLanes = HD / 8, kGroups = 32 / kLanes, U = kBlock / kGroups;
     const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = __ldg(p.seq_lens + r);
-    const int64_t row0 = __ldg(p.starts + r);
+    // a write of this cache may be the kernel before (so no load here is one of memory that never changes, __ldg's)
+    pdl_wait();
+    const int L = p.seq_lens[r];
+    const int64_t row0 = p.starts[r];
     const int page0 = blockIdx.x * p.per;
     if (L < 0 || L > p.max_seq_len || row0 < 0 || row0 + L > p.rows) {
         if (L != 0 && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, PKV_ERR_DEVICE_METADATA);
@@ -400,21 +402,21 @@ __global__ void __launch_bounds__(kGatherThreads) int8_gather_kernel(const Int8G
     const int l = lane % kLanes, g = lane / kLanes;
     for (int unit = warp; unit < pages * p.hkv; unit += kGatherThreads / 32) {
         const int page = unit / p.hkv, h = unit - page * p.hkv;
-        const int b = __ldg(p.block_tables + static_cast<int64_t>(r) * p.width + page0 + page);
+        const int b = p.block_tables[static_cast<int64_t>(r) * p.width + page0 + page];
         if (b < 0 || b >= p.num_blocks) {
             if (h == 0 && lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
             continue;
         }
         const int64_t at = static_cast<int64_t>(b) * p.hkv + h;
         const int8_t *src = p.cache + at * 2 * kBlock * HD + g * HD + l * 8;
-        const float2 s = __ldg(reinterpret_cast<const float2 *>(p.scales) + at);
+        const float2 s = reinterpret_cast<const float2 *>(p.scales)[at];
         const int first = (page0 + page) * kBlock;
         uint2 c[2][U];
 #pragma unroll
         for (int side = 0; side < 2; ++side)
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                c[side][u] = __ldg(reinterpret_cast<const uint2 *>(src + (side * kBlock + u * kGroups) * HD));
+                c[side][u] = *reinterpret_cast<const uint2 *>(src + (side * kBlock + u * kGroups) * HD);
         const int64_t dst = ((row0 + first + g) * p.hkv + h) * HD + l * 8;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
@@ -627,11 +629,10 @@ extern "C" int pkv_kv_gather_int8(void *key_out, void *value_out, int64_t out_ro
     // one (four requests of up to 128 tokens: 2.5 us, two pages 3.3).
     p.per = pages * num_seqs > 2048 ? 2 : 1;
     const dim3 grid(static_cast<unsigned>(pages ? (pages + p.per - 1) / p.per : 1), static_cast<unsigned>(num_seqs));
-    if (head_size == 128)
-        int8_gather_kernel<128><<<grid, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    else
-        int8_gather_kernel<64><<<grid, kGatherThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch_pdl(head_size == 128 ? int8_gather_kernel<128> : int8_gather_kernel<64>, grid, dim3(kGatherThreads), 0,
+                      static_cast<cudaStream_t>(stream), p) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
 }
 
 extern "C" int pkv_copy_blocks_int8(void *kv_cache, float *kv_scales, int64_t num_blocks, int32_t num_kv_heads,

@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
         const int32_t *bt = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq + pb;
         // windows of 32 pages: lane l holds page (window + l)'s block, and the scales of that block as {the score
         // factor's part, log2 and reciprocal of V's}; the next window's come while this one is at work
-        auto blocks_of = [&](int first) { return first + lane < npages ? __ldg(bt + first + lane) : -1; };
+        auto blocks_of = [&](int first) { return first + lane < npages ? bt[first + lane] : -1; };
         auto scales_of = [&](int blk) {
             float2 s = make_float2(0.f, 0.f);
             if (blk >= 0 && blk < p.num_blocks)
-                s = __ldg(reinterpret_cast<const float2 *>(p.kv_scales) + static_cast<int64_t>(blk) * p.num_kv_heads + g);
+                s = reinterpret_cast<const float2 *>(p.kv_scales)[static_cast<int64_t>(blk) * p.num_kv_heads + g];
             return s;
         };
         int wbase = 0;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                                       static_cast<int64_t>(g * p.G + hh) * HD + t4 * (HD / 4);
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; kk += 2) {
-                const uint4 v = R < rows ? __ldg(reinterpret_cast<const uint4 *>(qp + 4 * kk)) : make_uint4(0, 0, 0, 0);
+                const uint4 v = R < rows ? *reinterpret_cast<const uint4 *>(qp + 4 * kk) : make_uint4(0, 0, 0, 0);
                 qf[nt][kk][0] = v.x, qf[nt][kk][1] = v.y, qf[nt][kk + 1][0] = v.z, qf[nt][kk + 1][1] = v.w;
             }
             float a = 0.f;

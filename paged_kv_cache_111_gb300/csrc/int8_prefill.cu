@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             // pages past the sequence are -1 and load as zeros (outside the tensor map)
             auto blocks_of = [&](int w) -> int {
                 const int page = it.first * kIpPages + w * 32 + lane;
-                const int b = page < it.n_pages ? __ldg(bt + page) : -1;
+                const int b = page < it.n_pages ? bt[page] : -1;
                 if (page < it.n_pages && (b < 0 || b >= p.num_blocks)) set_status(status, PKV_ERR_DEVICE_INDEX);
                 return b;
             };
             auto scales_of = [&](int b) -> float2 {
-                return b >= 0 && b < p.num_blocks ? __ldg(kv_scales + static_cast<int64_t>(b) * p.num_kv_heads + it.g)
+                return b >= 0 && b < p.num_blocks ? kv_scales[static_cast<int64_t>(b) * p.num_kv_heads + it.g]
                                                   : make_float2(0.f, 1.f);
             };
             int win = 0, win_next = blocks_of(0);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             const uint4 *qp = reinterpret_cast<const uint4 *>(query + (it->qs + tok) * q_stride + static_cast<int64_t>(hh) * HD);
             uint4 v[HD / 8];
 #pragma unroll
-            for (int c = 0; c < HD / 8; ++c) v[c] = mine ? __ldg(qp + c) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < HD / 8; ++c) v[c] = mine ? qp[c] : make_uint4(0, 0, 0, 0);
             uint32_t a = 0;                            // the largest |q|, of the halves of the words
 #pragma unroll
             for (int c = 0; c < HD / 8; ++c)
