@@ -5,8 +5,9 @@
 //     a = max |x| over them,  s' = max(a / 127, 2^-60)
 //     s = s' where the block's first row is among them, else max(the block's scale, s')
 //     code = rint(x / s);  rows that were there, where s grew: code = rint(code * old / s)
-// (quotients as products with the fp32 number r = 1 / s, rounded once: x r, and code (old r) with old r in fp32).  A new code is off by at most half a step s,
-// one that saw g growths by at most (g + 1) / 2 steps.  If an x is no number, s is NaN.
+// (quotients as products with the fp32 number r = 1 / s, rounded once: x r, and code (old r) with old r in fp32).  A
+// new code is off by at most half a step s, one that saw g growths by at most (g + 1) / 2 steps.  If an x is no number,
+// s is NaN.
 //
 // The tokens of a block stand side by side in a call (a stretch, at most 16), and every one of its warps finds its
 // ends from the slots around its own token.  A stretch of n tokens is n warps' work: with n = 1 (decode) a warp
@@ -29,7 +30,6 @@ struct Int8WriteParams {
     int64_t k_stride, v_stride;               // elements between tokens, as the others
     const int64_t *slots;
     int32_t num_tokens, hkv;
-    int32_t heads;                            // a warp's
     int32_t q_chunks, kv_chunks, chunks;      // warps per token: query, one side (plain: both), all
     int32_t *status;
     // norm and rotation
@@ -125,7 +125,7 @@ __device__ __forceinline__ void int8_requantise(int8_t *page, uint32_t written, 
 }
 
 // FORM 0: keys and values as they are; 1: norm and rotation, planes of halves; 2: of neighbouring dims.  UA: rows a lane
-// takes at a time where it takes rows of one token.
+// takes of one token.
 template <int HD, int FORM, int UA>
 __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kernel(const Int8WriteParams p) {
     pdl_trigger();                            // the attention plan may start (it reads no cache and no query)
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
     constexpr int kLanes = HD / 8;            // lanes of a row
     constexpr int kGroups = 32 / kLanes;      // rows side by side in a warp
     constexpr int U = kBlock / kGroups;       // rows of a block a lane
-    constexpr int A = UA * kGroups;           // rows of one token a warp takes at a time
+    constexpr int kHeads = UA * kGroups;      // heads a warp
     __shared__ int8_t s_row[kI8Warps][kBlock];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t item = blockIdx.x * kI8Warps + warp;                            // below 2^31
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
     const int kind = FORM == 0 ? 2 : (chunk < p.q_chunks ? 0 : (chunk < p.q_chunks + p.kv_chunks ? 1 : 2));
     chunk -= FORM == 0 || kind == 0 ? 0 : (kind == 1 ? p.q_chunks : p.q_chunks + p.kv_chunks);
     const int heads = FORM == 0 ? 2 * p.hkv : (kind == 0 ? p.hq : p.hkv);
-    const int h0 = chunk * p.heads, cnt = min(p.heads, heads - h0);
+    const int h0 = chunk * kHeads, cnt = min(kHeads, heads - h0);
 
     // this lane's two pieces of four dims: turned together, or neighbours
     const bool turns = FORM != 0 && kind < 2 && l * 8 < p.rot;
@@ -180,37 +180,33 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
 
     if (FORM != 0 && kind == 0) {
         const int64_t slot = __ldg(p.slots + t), pos = __ldg(p.positions + t);
-        for (int i0 = 0; i0 < cnt; i0 += A) {
-            uint4 raw[UA];
+        uint4 raw[UA];
 #pragma unroll
-            for (int u = 0; u < UA; ++u) {
-                const int i = i0 + u * kGroups + g;
-                raw[u] = i < cnt ? load(p.query + t * p.q_stride + static_cast<int64_t>(h0 + i) * HD) : make_uint4(0, 0, 0, 0);
-            }
-            if (i0 == 0) {
-                if (pos < 0 || pos >= p.max_position) {
-                    if (slot >= 0 && lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
-                    return;
-                }
-                if (turns) angles(pos);
-            }
+        for (int u = 0; u < UA; ++u) {
+            const int i = u * kGroups + g;
+            raw[u] = i < cnt ? load(p.query + t * p.q_stride + static_cast<int64_t>(h0 + i) * HD) : make_uint4(0, 0, 0, 0);
+        }
+        if (pos < 0 || pos >= p.max_position) {
+            if (slot >= 0 && lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
+            return;
+        }
+        if (turns) angles(pos);
 #pragma unroll
-            for (int u = 0; u < UA; ++u) {
-                const int i = i0 + u * kGroups + g;
-                uint64_t x[4];
-                finish(raw[u], x);
-                if (i >= cnt) continue;
-                float f[8];
+        for (int u = 0; u < UA; ++u) {
+            const int i = u * kGroups + g;
+            uint64_t x[4];
+            finish(raw[u], x);
+            if (i >= cnt) continue;
+            float f[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f2_unpack(x[e], f[2 * e], f[2 * e + 1]);
-                const uint4 v = f32_to_bf16x8(f);
-                __nv_bfloat16 *out = p.query_out + t * p.out_stride + static_cast<int64_t>(h0 + i) * HD;
-                if (whole) {
-                    *reinterpret_cast<uint4 *>(out + da) = v;
-                } else {
-                    *reinterpret_cast<uint2 *>(out + da) = make_uint2(v.x, v.y);
-                    *reinterpret_cast<uint2 *>(out + db) = make_uint2(v.z, v.w);
-                }
+            for (int e = 0; e < 4; ++e) f2_unpack(x[e], f[2 * e], f[2 * e + 1]);
+            const uint4 v = f32_to_bf16x8(f);
+            __nv_bfloat16 *out = p.query_out + t * p.out_stride + static_cast<int64_t>(h0 + i) * HD;
+            if (whole) {
+                *reinterpret_cast<uint4 *>(out + da) = v;
+            } else {
+                *reinterpret_cast<uint2 *>(out + da) = make_uint2(v.x, v.y);
+                *reinterpret_cast<uint2 *>(out + db) = make_uint2(v.z, v.w);
             }
         }
         return;
@@ -284,38 +280,36 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
         // one row of each of the heads: row u * kGroups + g is head h0 + it
         const int off = static_cast<int>(slot & (kBlock - 1));
         if (turns) angles(pos);
-        for (int i0 = 0; i0 < cnt; i0 += A) {
-            uint4 raw[UA];
-            float old[UA];
+        uint4 raw[UA];
+        float old[UA];
 #pragma unroll
-            for (int u = 0; u < UA; ++u) {
-                const int i = i0 + u * kGroups + g;
-                raw[u] = i < cnt ? load(row_of(h0 + i, t)) : make_uint4(0, 0, 0, 0);
-                old[u] = i < cnt && !fresh ? p.scales[unit_of(h0 + i)] : 0.f;
+        for (int u = 0; u < UA; ++u) {
+            const int i = u * kGroups + g;
+            raw[u] = i < cnt ? load(row_of(h0 + i, t)) : make_uint4(0, 0, 0, 0);
+            old[u] = i < cnt && !fresh ? p.scales[unit_of(h0 + i)] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < UA; ++u) {
+            const int i = u * kGroups + g;
+            uint64_t x[4];
+            finish(raw[u], x);
+            uint32_t m = largest_bits(x);
+#pragma unroll
+            for (int k = kLanes / 2; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+            const float s = int8_scale(m, old[u], fresh), r = __frcp_rn(s);
+            if (i < cnt) {
+                const int64_t unit = unit_of(h0 + i);
+                store(p.cache + (unit * kBlock + off) * HD, x, r);
+                if (l == 0 && !(s == old[u])) p.scales[unit] = s;
             }
-#pragma unroll
-            for (int u = 0; u < UA; ++u) {
-                const int i = i0 + u * kGroups + g;
-                uint64_t x[4];
-                finish(raw[u], x);
-                uint32_t m = largest_bits(x);
-#pragma unroll
-                for (int k = kLanes / 2; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
-                const float s = int8_scale(m, old[u], fresh), r = __frcp_rn(s);
-                if (i < cnt) {
-                    const int64_t unit = unit_of(h0 + i);
-                    store(p.cache + (unit * kBlock + off) * HD, x, r);
-                    if (l == 0 && !(s == old[u])) p.scales[unit] = s;
-                }
-                // the older rows of the heads whose scale grew, one head after the other
-                const float ratio = __fmul_rn(old[u], r);
-                uint32_t grown = __ballot_sync(0xffffffffu, l == 0 && i < cnt && !fresh && s > old[u]);
-                while (grown) {
-                    const int from = __ffs(static_cast<int>(grown)) - 1;
-                    grown &= grown - 1;
-                    int8_requantise<HD>(p.cache + unit_of(h0 + i0 + u * kGroups + from / kLanes) * kBlock * HD, written,
-                                        __shfl_sync(0xffffffffu, ratio, from), lane);
-                }
+            // the older rows of the heads whose scale grew, one head after the other
+            const float ratio = __fmul_rn(old[u], r);
+            uint32_t grown = __ballot_sync(0xffffffffu, l == 0 && i < cnt && !fresh && s > old[u]);
+            while (grown) {
+                const int from = __ffs(static_cast<int>(grown)) - 1;
+                grown &= grown - 1;
+                int8_requantise<HD>(p.cache + unit_of(h0 + u * kGroups + from / kLanes) * kBlock * HD, written,
+                                    __shfl_sync(0xffffffffu, ratio, from), lane);
             }
         }
         return;
@@ -487,7 +481,6 @@ static int int8_write(Int8WriteParams &p, int form, int32_t head_size, void *str
     // 32/8 heads: 23 us, with two rows a lane 29).
     const int few = 2 * (32 / (head_size / 8));
     auto spread = [&](int heads) {
-        p.heads = heads;
         p.q_chunks = form ? (p.hq + heads - 1) / heads : 0;
         p.kv_chunks = form ? (p.hkv + heads - 1) / heads : 0;
         p.chunks = form ? p.q_chunks + 2 * p.kv_chunks : (2 * p.hkv + heads - 1) / heads;
@@ -508,7 +501,8 @@ static int int8_write(Int8WriteParams &p, int form, int32_t head_size, void *str
                                     : (form == 1 ? int8_write_kernel<64, 1, 2> : int8_write_kernel<64, 2, 2>))
                        : (form == 0 ? int8_write_kernel<64, 0, 4>
                                     : (form == 1 ? int8_write_kernel<64, 1, 4> : int8_write_kernel<64, 2, 4>));
-    kernel<<<static_cast<unsigned>((warps + kI8Warps - 1) / kI8Warps), kI8Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    kernel<<<static_cast<unsigned>((warps + kI8Warps - 1) / kI8Warps), kI8Threads, 0, static_cast<cudaStream_t>(stream)>>>(
+        p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -62,6 +62,8 @@ PLACES = {
     "chunk in a block": [(37, 131)],
     "mixed": [(20, 1), (33, 1), (7, 77), (0, 3)],
     "odd": [(1, 15), (2, 31), (11, 5), (4, 9)],
+    # so many that a warp takes more heads than in the others
+    "many": [(p % 40, 1) for p in range(1500)] + [(5, 700), (0, 333), (47, 1), (30, 3)],
 }
 
 
@@ -242,6 +244,12 @@ def test_norm_rope_write(hq, hkv, d, rot, inter, place, normed):
     assert (got_c[:, :, 0] != c[:, :, 0]).mean() < 1e-3
 
 
+@pytest.mark.parametrize("hq,hkv,d,rot,inter", [(8, 8, 64, 64, False), (6, 2, 128, 128, False), (17, 17, 128, 64, True),
+                                                (20, 4, 64, 16, True)])
+def test_norm_rope_write_of_many_tokens(hq, hkv, d, rot, inter):
+    test_norm_rope_write(hq, hkv, d, rot, inter, "many", True)
+
+
 def test_norm_rope_in_place_padding_and_positions():
     hq = hkv = 2
     d = rot = 64
@@ -347,3 +355,39 @@ def test_copy(hkv, d):
     pkv.copy_blocks_int8(cache, scales, torch.tensor([(2, 30), (-1, 3), (4, 10)], device="cuda"), device_status=word)
     want_c[10], want_s[10] = want_c[4].clone(), want_s[4].clone()
     assert torch.equal(cache, want_c) and torch.equal(scales, want_s) and word.item() == 7
+
+
+# ---- one after the other, with nothing waited for between ---------------------------------------------------------
+
+@pytest.mark.parametrize("hkv,d,tokens", [(8, 128, 1), (3, 64, 1), (8, 128, 5), (40, 128, 1)])
+def test_writes_and_read_backs_in_a_row(hkv, d, tokens):
+    # each read-back sees the codes and scales of the write before it, while the scales of neighbouring heads (one
+    # stretch of memory) grow under other warps
+    steps, S = 32, 64
+    blocks = S * -(-steps * tokens // BLOCK)
+    order = torch.randperm(blocks, generator=torch.Generator().manual_seed(3)).reshape(S, -1)
+    cache, scales = ref.new_cache(blocks, hkv, d)
+    dc, ds = cache.cuda(), scales.cuda()
+    table = order.int().cuda()
+    data, slots, lens = [], [], []
+    for i in range(steps):
+        at = torch.arange(i * tokens, (i + 1) * tokens)
+        slots.append((order[:, at // BLOCK] * BLOCK + at % BLOCK).flatten())
+        data.append([heads(S * tokens, hkv, d, 2 * i + k, std=1.5 ** i) for k in range(2)])
+        lens.append((i + 1) * tokens)
+    on = [(k.cuda(), v.cuda(), s.cuda(), torch.full((S,), n, dtype=torch.int32, device="cuda"),
+           torch.arange(0, S * n, n, dtype=torch.int32, device="cuda")) for (k, v), s, n in zip(data, slots, lens)]
+    outs = [[torch.empty(S * n, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for n in lens]
+    torch.cuda.synchronize()
+    for (k, v, s, n, start), out in zip(on, outs):
+        pkv.kv_write_int8(dc, ds, k, v, s)
+        pkv.kv_gather_int8(*out, dc, ds, table, n, start, int(out[0].shape[0] // S))
+    torch.cuda.synchronize()
+    c, sc = cache.numpy().copy(), scales.numpy().copy()
+    for i, ((k, v), s, n) in enumerate(zip(data, slots, lens)):
+        ref.write(c, sc, k.float().numpy(), v.float().numpy(), s.numpy())
+        if i % 5 and i != steps - 1:
+            continue
+        for r in range(0, S, 7):
+            for got, want in zip(outs[i], ref.rows_of(torch.from_numpy(c), torch.from_numpy(sc), order[r], n)):
+                assert torch.equal(got[r * n:(r + 1) * n].cpu(), want.float().bfloat16()), (i, r)
