@@ -61,14 +61,16 @@ struct WsLayout {
     int32_t prefix_parts;     // splits of the shared prefix (0: no cascade)
 };
 
-// Chunks over an int8 cache (int8_prefill.cu), where work items are fewer than CTAs: the CTAs share them out in equal runs,
-// so that an item is cut along its keys.  Its pieces' sums lie behind the layout above, two places a CTA (what its run
-// begins with, and what it ends with): {reference, sum} of each row, and rows x head_size fp32 unnormalised sums, four dims
-// of each row side by side.  The CTA of an item's first piece notes it down, and the combine joins the pieces.
+// Chunks over an int8 cache (int8_prefill.cu), where work items are fewer than CTAs: the CTAs share them out in equal
+// runs, so that an item is cut along its keys.  Its pieces' sums lie behind the layout above, two places a CTA (what
+// its run begins with, and what it ends with): {reference, sum} of each row, and rows x head_size fp32 unnormalised
+// sums, four dims of each row side by side.  The CTA of an item's first piece notes it down, and the combine joins the
+// pieces.
 constexpr int kSplitCtas = 152;            // CTAs at most
 constexpr int kSplitRows = 256;            // rows of an item
 struct SplitItem {
-    int32_t qs, rows_total, row0, h0;      // first query token, rows of the request, the item's first, its first query head
+    // first query token, rows of the request, the item's first, its first query head
+    int32_t qs, rows_total, row0, h0;
     int32_t place, cta, pieces, G;         // the first piece's place (-1: no item) and CTA; query heads a kv head
 };
 struct SplitLayout {

@@ -124,8 +124,8 @@ __device__ __forceinline__ void int8_requantise(int8_t *page, uint32_t written, 
     }
 }
 
-// FORM 0: keys and values as they are; 1: norm and rotation, planes of halves; 2: of neighbouring dims.  UA: rows a lane
-// takes of one token.
+// FORM 0: keys and values as they are; 1: norm and rotation, planes of halves; 2: of neighbouring dims.  UA: rows a
+// lane takes of one token.
 template <int HD, int FORM, int UA>
 __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kernel(const Int8WriteParams p) {
     pdl_trigger();                            // the attention plan may start (it reads no cache and no query)
@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
 #pragma unroll
         for (int u = 0; u < UA; ++u) {
             const int i = u * kGroups + g;
-            raw[u] = i < cnt ? load(p.query + t * p.q_stride + static_cast<int64_t>(h0 + i) * HD) : make_uint4(0, 0, 0, 0);
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (i < cnt) raw[u] = load(p.query + t * p.q_stride + static_cast<int64_t>(h0 + i) * HD);
         }
         if (pos < 0 || pos >= p.max_position) {
             if (slot >= 0 && lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
     const int n = min(kBlock, __ffs(static_cast<int>(~(same >> start))) - 1);
     const int j = kBlock - start;
     const bool in = lane >= start && lane < start + n;
-    const int off0 = static_cast<int>(slot & (kBlock - 1)) - j;            // of the first token, where offsets ascend by one
+    const int off0 = static_cast<int>(slot & (kBlock - 1)) - j;   // of the first token, where offsets ascend by one
     uint32_t written;                                         // rows of the block
     const bool plain = !__any_sync(0xffffffffu, in && (slot_l != slot + (lane - kBlock) || !known_l));
     if (plain) {
@@ -501,8 +502,8 @@ static int int8_write(Int8WriteParams &p, int form, int32_t head_size, void *str
                                     : (form == 1 ? int8_write_kernel<64, 1, 2> : int8_write_kernel<64, 2, 2>))
                        : (form == 0 ? int8_write_kernel<64, 0, 4>
                                     : (form == 1 ? int8_write_kernel<64, 1, 4> : int8_write_kernel<64, 2, 4>));
-    kernel<<<static_cast<unsigned>((warps + kI8Warps - 1) / kI8Warps), kI8Threads, 0, static_cast<cudaStream_t>(stream)>>>(
-        p);
+    const unsigned ctas = static_cast<unsigned>((warps + kI8Warps - 1) / kI8Warps);
+    kernel<<<ctas, kI8Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -623,10 +624,9 @@ extern "C" int pkv_kv_gather_int8(void *key_out, void *value_out, int64_t out_ro
     // one (four requests of up to 128 tokens: 2.5 us, two pages 3.3).
     p.per = pages * num_seqs > 2048 ? 2 : 1;
     const dim3 grid(static_cast<unsigned>(pages ? (pages + p.per - 1) / p.per : 1), static_cast<unsigned>(num_seqs));
-    return launch_pdl(head_size == 128 ? int8_gather_kernel<128> : int8_gather_kernel<64>, grid, dim3(kGatherThreads), 0,
-                      static_cast<cudaStream_t>(stream), p) == cudaSuccess
-               ? PKV_OK
-               : PKV_ERR_CUDA;
+    const cudaError_t e = launch_pdl(head_size == 128 ? int8_gather_kernel<128> : int8_gather_kernel<64>, grid,
+                                     dim3(kGatherThreads), 0, static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 extern "C" int pkv_copy_blocks_int8(void *kv_cache, float *kv_scales, int64_t num_blocks, int32_t num_kv_heads,
@@ -643,7 +643,7 @@ extern "C" int pkv_copy_blocks_int8(void *kv_cache, float *kv_scales, int64_t nu
     const int64_t ctas = static_cast<int64_t>(num_pairs) * pieces;
     if (ctas > INT32_MAX) return PKV_ERR_SHAPE;
     int8_copy_kernel<<<static_cast<unsigned>(ctas), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<uint4 *>(kv_cache), reinterpret_cast<float2 *>(kv_scales), num_blocks, num_kv_heads, vectors, pieces,
-        block_mapping, device_status);
+        static_cast<uint4 *>(kv_cache), reinterpret_cast<float2 *>(kv_scales), num_blocks, num_kv_heads, vectors,
+        pieces, block_mapping, device_status);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

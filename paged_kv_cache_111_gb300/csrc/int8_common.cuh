@@ -25,7 +25,8 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     return d;
 }
 
-// Four codes -> two pairs of fp32.  A byte u = code + 128 in the low bits of the fp32 number 2^23 gives 2^23 + u exactly.
+// Four codes -> two pairs of fp32.  A byte u = code + 128 in the low bits of the fp32 number 2^23 gives 2^23 + u
+// exactly.
 __device__ __forceinline__ void int8x4_to_f32(uint32_t w, uint64_t &p01, uint64_t &p23) {
     const uint32_t u = w ^ 0x80808080u;
     const uint64_t bias = f2_pack(-8388736.f, -8388736.f);
@@ -35,7 +36,8 @@ __device__ __forceinline__ void int8x4_to_f32(uint32_t w, uint64_t &p01, uint64_
                  bias);
 }
 
-// Four codes -> f16 numbers 1152 + code (a byte u = code + 128 in the low bits of the f16 number 1024 gives 1024 + u exactly).
+// Four codes -> f16 numbers 1152 + code (a byte u = code + 128 in the low bits of the f16 number 1024 gives 1024 + u
+// exactly).
 constexpr float kInt8Bias = 1152.f;
 __device__ __forceinline__ void int8x4_to_biased_f16(uint32_t w, uint32_t &h01, uint32_t &h23) {
     const uint32_t u = w ^ 0x80808080u;

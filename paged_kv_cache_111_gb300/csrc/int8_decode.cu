@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
         const int item = (round & 1) ? round * W + (W - 1 - wid) : round * W + wid;   // snake order
         if (item >= n_items) continue;
         const SelfChunk sc = (round & 1) ? self_chunks[1] : self_chunks[0];
-        const int4 ch = p.self_plan ? make_int4(sc.r, sc.k, sc.pb, sc.pb + sc.npages) : __ldcg(chunks + item / p.num_kv_heads);
+        const int4 ch = p.self_plan ? make_int4(sc.r, sc.k, sc.pb, sc.pb + sc.npages)
+                                    : __ldcg(chunks + item / p.num_kv_heads);
         const int g = item % p.num_kv_heads;
         const int r = ch.x;
         const int pb = ch.z;
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
         for (int k = 0; k < issued; ++k) issue(k, __shfl_sync(0xffffffffu, win, k));
         float2 scale_win = scales_of(win), scale_next = make_float2(0.f, 0.f);
 
-        // the query rows this lane holds dims of: g4, and g4 + 8.  Lane column t4 takes dims t4 HD/4 .. of a row, four a
-        // k-step, so that its part of a key is whole words of the page (the order of a product's terms is free)
+        // the query rows this lane holds dims of: g4, and g4 + 8.  Lane column t4 takes dims t4 HD/4 .. of a row, four
+        // a k-step, so that its part of a key is whole words of the page (the order of a product's terms is free)
         uint32_t qf[NT][KSTEPS][2];
         float bias[NT], factor[NT];               // of row g4 (+ 8): -1152 sum q, and what brings S to log2 units
 #pragma unroll
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint32_t w = qf[nt][kk][e];
-                    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+                    const __half2 h =
+                        __floats2half2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
                     const float2 f = __half22float2(h);
                     sum += f.x + f.y;
                     qf[nt][kk][e] = *reinterpret_cast<const uint32_t *>(&h);
@@ -374,9 +376,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-                const uint32_t lo = prmt(vw[0][i >> 1], vw[1][i >> 1], sel), hi = prmt(vw[2][i >> 1], vw[3][i >> 1], sel);
-                const uint32_t a[4] = {unbias_f16(prmt(lo, 0x64646464u, 0x4140)), unbias_f16(prmt(lo, 0x64646464u, 0x4342)),
-                                       unbias_f16(prmt(hi, 0x64646464u, 0x4140)), unbias_f16(prmt(hi, 0x64646464u, 0x4342))};
+                const uint32_t lo = prmt(vw[0][i >> 1], vw[1][i >> 1], sel);
+                const uint32_t hi = prmt(vw[2][i >> 1], vw[3][i >> 1], sel);
+                const uint32_t top = 0x64646464u;
+                const uint32_t a[4] = {unbias_f16(prmt(lo, top, 0x4140)), unbias_f16(prmt(lo, top, 0x4342)),
+                                       unbias_f16(prmt(hi, top, 0x4140)), unbias_f16(prmt(hi, top, 0x4342))};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], a, pb0[nt], pb1[nt]);
             }
@@ -410,7 +414,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                     uint32_t w[MT];
 #pragma unroll
                     for (int v = 0; v < MT; ++v) w[v] = pack_bf16x2(o[nt][v][e] * inv, o[nt][v][e + 2] * inv);
-                    __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(qs + i) * p.num_q_heads + h) * HD + g4 * (HD / 8);
+                    __nv_bfloat16 *dst =
+                        p.out + (static_cast<int64_t>(qs + i) * p.num_q_heads + h) * HD + g4 * (HD / 8);
 #pragma unroll
                     for (int v = 0; v < MT; v += 4)
                         *reinterpret_cast<uint4 *>(dst + 2 * v) = make_uint4(w[v], w[v + 1], w[v + 2], w[v + 3]);

@@ -1,25 +1,26 @@
-// Chunks over an int8 cache (int8_common.cuh), on the 5th-generation tensor cores: the computation of int8_decode.cu for
-// requests of many rows (query token, query head of the kv head's group).
+// Chunks over an int8 cache (int8_common.cuh), on the 5th-generation tensor cores: the computation of int8_decode.cu
+// for requests of many rows (query token, query head of the kv head's group).
 //
 // With codes k_j, v_j and their blocks' scales ks, vs, for a row q scaled by a power of two 2^e into f16:
 //     S_j = <q 2^e, 1152 + k_j>,   e_j = (S_j - 1152 sum q 2^e) (scale 2^-e log2(e) ks) + log2 vs
 //     p'_j = 2^(e_j - m),          out = sum_j p'_j v_j / sum_j p'_j / vs
 // K's codes widen to f16 as 1152 + code (a byte next to 0x64) and stay so: what that adds to S is one number a row, and
 // goes with the block's factor into the constants of the softmax, of which a row has three a block of 16 keys.  V's
-// codes are taken back to themselves.  m is the row's largest e_j so far, looked for again only where the weights of a tile
-// sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
+// codes are taken back to themselves.  m is the row's largest e_j so far, looked for again only where the weights of a
+// tile sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
 //
-// Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and share
-// each 128-key tile; a persistent CTA an SM takes items largest first.  Where there are fewer items than CTAs their key
-// tiles are one line that is cut into an equal run for each CTA; the combine that follows joins the pieces' sums, which are
-// left in the workspace.
+// Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and
+// share each 128-key tile; a persistent CTA an SM takes items largest first.  Where there are fewer items than CTAs
+// their key tiles are one line that is cut into an equal run for each CTA; the combine that follows joins the pieces'
+// sums, which are left in the workspace.
 //
 // Per key tile: 8 pages (one TMA box each, K and V) land raw, four warps widen them into a ring of 16 KiB slots in the
 // layout the products read, S = Q K^T from shared memory (128 x 128 x 16), softmax by four warps a row tile (a row per
 // thread), P as f16 over S in tensor memory, O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
 //
-// Warp roles (448 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2, 3, 12 and 13 widen
-// (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is bounded.
+// Warp roles (448 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2, 3, 12 and 13
+// widen (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is
+// bounded.
 #include <mutex>
 #include <type_traits>
 
@@ -103,8 +104,8 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
-// In the line that is cut, an item counts for as many units as it has key tiles and kIpOver more (Q, epilogue, and what a
-// piece more costs); a CTA gets kIpLeast units at least.
+// In the line that is cut, an item counts for as many units as it has key tiles and kIpOver more (Q, epilogue, and what
+// a piece more costs); a CTA gets kIpLeast units at least.
 constexpr int kIpOver = 3, kIpLeast = 6;
 
 template <int HD>
@@ -123,13 +124,14 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     const uint32_t sQ = smem_u32(smem + Cfg::kOffQ), sRing = smem_u32(smem + Cfg::kOffRing);
     const int warp = uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
 
-    // As the other chunk kernels: the kernel before this one (decode) writes other rows, and it started when the plan and
-    // the cache write had completed, so the plan's lists are read at once, through L2; the wait on it comes at the end.
+    // As the other chunk kernels: the kernel before this one (decode) writes other rows, and it started when the plan
+    // and the cache write had completed, so the plan's lists are read at once, through L2; the wait on it comes at the
+    // end.
     pdl_trigger();
     const WsHeader *hdr = reinterpret_cast<const WsHeader *>(p.ws);
     int32_t *status = reinterpret_cast<int32_t *>(p.ws);
     const int n_tiles = ws_ld(&hdr->n_ptiles);
-    const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));     // {request, tile, key tiles, -}
+    const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));   // {request, tile, key tiles, -}
     const int n_items = n_tiles * p.num_kv_heads;
     // fewer items than CTAs: the units of all items, and the CTAs that share them
     const bool runs = n_items < static_cast<int>(gridDim.x);
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < kSteps; ++kk)
                         umma_f16_ts(tmem + 256u + 128u * i,
-                                    tmem + 128u * i + 8u * (h * kSteps + kk), b + kk * (2048 >> 4), kIdescO, (h | kk) ? 1u : (first ? 0u : 1u));
+                                    tmem + 128u * i + 8u * (h * kSteps + kk), b + kk * (2048 >> 4), kIdescO,
+                                    (h | kk) ? 1u : (first ? 0u : 1u));
                     if (frees) umma_commit(&bars[kIpEmpty + slot]);
                 }
                 umma_commit(&bars[kIpODone + i]);
@@ -411,15 +414,16 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kIpFull + s % SLOTS]);
         };
-        // A warp widens 8 rows x 64 dims at a time, four lanes a row, 16 dims a lane.  Of eight lanes that access memory
-        // together four have row a and four row a ^ 5 (64 dims: a ^ 1): the raw rows of 128 bytes lie with their 16-byte
-        // pieces permuted by the row (TMA), those of 64 bytes as they are, and the f16 rows with theirs permuted by the
-        // row too, so neither the reads nor the writes meet in a bank.
+        // A warp widens 8 rows x 64 dims at a time, four lanes a row, 16 dims a lane.  Of eight lanes that access
+        // memory together four have row a and four row a ^ 5 (64 dims: a ^ 1): the raw rows of 128 bytes lie with their
+        // 16-byte pieces permuted by the row (TMA), those of 64 bytes as they are, and the f16 rows with theirs
+        // permuted by the row too, so neither the reads nor the writes meet in a bank.
         const int c = lane & 3;
         const int r8 = HD == 128 ? ((lane >> 2) & 1 ? (lane >> 3) ^ 5 : lane >> 3) : lane >> 2;
         const uint32_t from = r8 * HD + (HD == 128 ? (c ^ r8) << 4 : c << 4);     // (second 64 dims: ^ 64)
         const uint32_t to = r8 * 128 + (((2 * c) ^ r8) << 4);                     // (its second 8 dims: ^ 16)
-        // groups g0 .. of 8 rows of the raw tile at src (page g / 2), to groups of a slot (dst0; the second 64 dims: dst1)
+        // groups g0 .. of 8 rows of the raw tile at src (page g / 2), to groups of a slot (dst0; the second 64 dims:
+        // dst1)
         constexpr int B = 4 / C;                       // groups at a time: four 16-byte loads a lane
         auto widen = [&](auto is_v, int groups, uint32_t src, int g0, uint32_t dst0, uint32_t dst1) {
             constexpr bool V = decltype(is_v)::value;
@@ -429,7 +433,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int g = g0 + n + u / C;
-                    const uint32_t at = src + (g >> 1) * (2 * kBlock * HD) + (g & 1) * 8 * HD + (V ? kBlock * HD : 0) + from;
+                    const uint32_t at =
+                        src + (g >> 1) * (2 * kBlock * HD) + (g & 1) * 8 * HD + (V ? kBlock * HD : 0) + from;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
                                  : "r"(at ^ (64u * (u % C))));
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         const float sl2 = fabsf(p.scale_log2), flip = p.scale_log2 < 0.f ? -1.f : 1.f;
         bool ok = true;
         float factor = 0.f, bias = 0.f;                // of this thread's row: to log2 units, and 1152 sum q times it
-        int lim = INT32_MAX;                           // keys [0, lim) visible (a row that is none sees all, for nobody)
+        int lim = INT32_MAX;                      // keys [0, lim) visible (a row that is none sees all, for nobody)
         int64_t dst = -1;                              // where its output goes
         // this thread's row of an item: into shared memory as f16, zeros past the request
         auto take_row = [&](const volatile IpItem *it) {
@@ -506,7 +511,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             const bool mine = rrow < it->rows_total;
             lim = mine ? it->ctx + tok + 1 : INT32_MAX;
             dst = mine ? (static_cast<int64_t>(it->qs + tok) * p.num_q_heads + hh) * HD : -1;
-            const uint4 *qp = reinterpret_cast<const uint4 *>(query + (it->qs + tok) * q_stride + static_cast<int64_t>(hh) * HD);
+            const uint4 *qp =
+                reinterpret_cast<const uint4 *>(query + (it->qs + tok) * q_stride + static_cast<int64_t>(hh) * HD);
             uint4 v[HD / 8];
 #pragma unroll
             for (int c = 0; c < HD / 8; ++c) v[c] = mine ? qp[c] : make_uint4(0, 0, 0, 0);
@@ -526,7 +532,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), up2);
+                    const uint64_t x2 =
+                        f2_mul(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), up2);
                     float x0, x1;
                     f2_unpack(x2, x0, x1);
                     w[e] = pack_p<true>(x0, x1);
@@ -550,7 +557,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         // A piece of an item: {reference, sum} and the sums as they are, into the workspace.
         auto leave_piece = [&](int tiles) {
             // (a row tile that sees none of these keys has no part; a sum that is no number counts in any join)
-            *(reinterpret_cast<float2 *>(p.ws + p.split.off_state) + static_cast<int64_t>(place) * kSplitRows + i * kIpRows + row) =
+            *(reinterpret_cast<float2 *>(p.ws + p.split.off_state) + static_cast<int64_t>(place) * kSplitRows +
+              i * kIpRows + row) =
                 make_float2(tiles ? (l != l && m == NEG_INF ? 0.f : m) : NEG_INF, l);
             if (!tiles) return true;
             if (!ip_warp_wait(&bars[kIpODone + i], (cnt - 1) & 1, status)) return false;
@@ -625,7 +633,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                 const float4 *sc = scales + ((gt + j) & 7) * kIpPages;
                 const int key0 = (first + j) * kIpKeys;
                 const bool masked = __any_sync(0xffffffffu, key0 + kIpKeys > lim);
-                // three constants of block b of the tile: what S is times, what is added, what the weights' sum is times
+                // three constants of block b of the tile: what S is times, what is added, what the weights' sum is
+                // times
                 const float least = masked ? 1e-37f : 0.f;               // (not 0 where a score may be -inf)
                 auto constants = [&](int b, float &f, float &c0, float &inv) {
                     const float4 v = sc[b];
@@ -636,8 +645,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     if (masked && !(fabsf(c0) < 3e38f)) f = 1.f, c0 = inv = 0.f;
                 };
                 if (masked) {
-                    // keys that the row does not see: their scores become -inf where they lie.  Blocks without a scale make
-                    // the sums of the rows that see some of them no number, and have any other for those that do not.
+                    // keys that the row does not see: their scores become -inf where they lie.  Blocks without a scale
+                    // make the sums of the rows that see some of them no number, and have any other for those that do
+                    // not.
 #pragma unroll 1
                     for (int c = 0; c < kIpKeys / 32; ++c) {
                         uint32_t x[32];
@@ -653,8 +663,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     tmem_st_wait();
                 }
                 // The weights are taken against the reference that is there.  Where they sum to 2^13 or less none of
-                // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes the
-                // reference.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
+                // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes
+                // the reference.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
                 bool slow = j == 0;
                 uint32_t w[kIpKeys / 2];               // P, pairs of f16
                 float all, some;                       // the weights' sum, and that of the blocks' times 1 / vs
@@ -715,7 +725,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                             const float cb = c0 - ref;
                             const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
 #pragma unroll
-                            for (int e = 8 * h; e < 8 * h + 8; ++e) y[e] = f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), f2, c2);
+                            for (int e = 8 * h; e < 8 * h + 8; ++e)
+                                y[e] = f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), f2, c2);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {

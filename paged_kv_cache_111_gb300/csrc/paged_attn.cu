@@ -579,7 +579,8 @@ __device__ __forceinline__ void join_split_items(__nv_bfloat16 *out, const uint8
                 const float top = fmaxf(M, s[k].x), keep = fast_exp2(M - top), f = fast_exp2(s[k].x - top);
                 M = top;
                 L = fmaf(f, s[k].y, keep * L);
-                const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+                const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                    v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
                 for (int d = 0; d < 8; ++d) acc[d] = fmaf(f, x[d], keep * acc[d]);
             }
@@ -587,8 +588,8 @@ __device__ __forceinline__ void join_split_items(__nv_bfloat16 *out, const uint8
         if (rrow >= what.y) continue;
         const float inv = L <= 0.f ? 0.f : 1.f / L;                // (NaN stays)
         const int tok = rrow / where.w;
-        *reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(what.x + tok) * num_q_heads + what.w + rrow - tok * where.w) * HD +
-                                   8 * d0) =
+        const int64_t to = static_cast<int64_t>(what.x + tok) * num_q_heads + what.w + rrow - tok * where.w;
+        *reinterpret_cast<uint4 *>(out + to * HD + 8 * d0) =
             make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                        pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
     }
@@ -623,8 +624,8 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(__nv_bfloat16 *out, con
                             out + (static_cast<int64_t>(st.x) * num_q_heads + h) * HD, lane);
     }
     if (split_items)
-        join_split_items<HD>(out, ws, split_items, off_split, num_q_heads, static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5),
-                             static_cast<int>(gridDim.x) * 8);
+        join_split_items<HD>(out, ws, split_items, off_split, num_q_heads,
+                             static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), static_cast<int>(gridDim.x) * 8);
 }
 
 static int paged_attn_impl(void *out, const void *query, int64_t query_token_stride, const void *kv_cache,
