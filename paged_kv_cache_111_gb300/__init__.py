@@ -640,15 +640,19 @@ def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tens
 
 # ---- the int8 cache -------------------------------------------------------------------------------------------
 
-def _int8_cache(kv_cache: torch.Tensor, kv_scales: torch.Tensor):
-    """(cache, scales, device, blocks, kv heads, block size, head size) of an int8 cache, the first two as pointers."""
-    dev = kv_cache.get_device()
-    if (dev < 0 or kv_cache.dtype is not torch.int8 or kv_cache.dim() != 5 or not kv_cache.is_contiguous()
-            or kv_cache.shape[2] != 2):
-        _refuse("kv_cache", kv_cache, torch.int8, dev, "a contiguous [NB, Hkv, 2, 16, d]")
-    nb, hkv, _, bs, d = kv_cache.shape
-    scales = _full("kv_scales", kv_scales, _F32, dev, (nb, hkv, 2), "a contiguous [NB, Hkv, 2]")
-    return kv_cache.data_ptr(), scales, dev, nb, hkv, bs, d
+_int8_module = None
+
+
+def _int8():
+    """The module that marshals the int8 calls (csrc/int8_calls.c): the same checks, made in C."""
+    global _int8_module
+    if _int8_module is None:
+        load()
+        from . import _int8_calls
+        _int8_calls.bind(torch.int8, _BF16, _F32, _I32, _I64, _refuse, PagedKVError, torch._C._cuda_getDevice,
+                         torch.cuda.device, torch._C._cuda_getCurrentRawStream)
+        _int8_module = _int8_calls
+    return _int8_module
 
 
 def kv_write_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -656,13 +660,7 @@ def kv_write_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, key: torch.Te
     """Quantise key/value [T, Hkv, d] (bf16) into kv_cache (int8 [NB, Hkv, 2, 16, d]) and kv_scales (fp32
     [NB, Hkv, 2]) through slot_mapping [T] (int64), the tokens of a block side by side; the scale of a block that is
     written from its first row is made anew, any other grows where it has to."""
-    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
-    T = slot_mapping.numel()
-    k, k_step, _ = _heads("key", key, dev, T, hkv, d, True)
-    v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
-    _call(dev, "pkv_kv_write_int8", (_lib or load()).pkv_kv_write_int8, cache, scales, nb, hkv, d, bs, k, k_step, v,
-          v_step, _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T,
-          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+    (_int8_module or _int8()).kv_write(kv_cache, kv_scales, key, value, slot_mapping, device_status, stream)
 
 
 def qk_norm_rope_kv_write_int8(query_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -672,23 +670,9 @@ def qk_norm_rope_kv_write_int8(query_out: torch.Tensor, kv_cache: torch.Tensor, 
                                interleaved: bool = False, device_status: Optional[torch.Tensor] = None,
                                stream=None) -> None:
     """qk_norm_rope_kv_write into an int8 cache and its scales (see kv_write_int8)."""
-    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
-    if query.dim() != 3:
-        raise ValueError("query must be [T, H, d]")
-    T, H, _ = query.shape
-    qo, qo_step, _ = _heads("query_out", query_out, dev, T, H, d, True)
-    q, q_step, _ = _heads("query", query, dev, T, H, d, True)
-    k, k_step, _ = _heads("key", key, dev, T, hkv, d, True)
-    v, v_step, _ = _heads("value", value, dev, T, hkv, d, True)
-    table = _full("cos_sin", cos_sin, _F32, dev, (-1, -1), "a contiguous [max_position, rotary_dim]")
-    max_position, rot = cos_sin.shape
-    _call(dev, "pkv_qk_norm_rope_kv_write_int8", (_lib or load()).pkv_qk_norm_rope_kv_write_int8,
-          qo, qo_step, cache, scales, nb, H, hkv, d, bs, q, q_step, k, k_step, v, v_step,
-          _full("q_weight", q_weight, _BF16, dev, (d,), "[d]"), _full("k_weight", k_weight, _BF16, dev, (d,), "[d]"),
-          eps, table, max_position, rot, 1 if interleaved else 0,
-          _full("positions", positions, _I64, dev, (T,), "a contiguous [T]"),
-          _full("slot_mapping", slot_mapping, _I64, dev, (T,), "a contiguous [T]"), T,
-          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+    (_int8_module or _int8()).qk_norm_rope_kv_write(
+        query_out, kv_cache, kv_scales, query, key, value, q_weight, k_weight, eps, cos_sin, positions, slot_mapping,
+        interleaved, device_status, stream)
 
 
 def paged_attn_int8(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -696,21 +680,8 @@ def paged_attn_int8(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tens
                     max_query_len: int, max_seq_len: int, scale: float, workspace: torch.Tensor, num_splits: int = 0,
                     stream=None) -> None:
     """paged_attn over an int8 cache; the workspace is sized as for paged_attn, and paged_attn_combine follows."""
-    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
-    if query.dim() != 3:
-        raise ValueError("query must be [T, H, d]")
-    T, H, _ = query.shape
-    S = seq_lens.numel()
-    q, q_step, _ = _heads("query", query, dev, T, H, d, True)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _refuse("workspace", workspace, None, dev, "contiguous")
-    _call(dev, "pkv_paged_attn_int8", (_lib or load()).pkv_paged_attn_int8,
-          _full("out", out, _BF16, dev, (T, H, d), "a contiguous [T, H, d]"), q, q_step, cache, scales, nb,
-          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
-          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
-          _full("query_start_loc", query_start_loc, _I32, dev, (S + 1,), "a contiguous [num_seqs + 1]"), S, T,
-          max_query_len, max_seq_len, H, hkv, d, bs, scale, num_splits, workspace.data_ptr(), workspace.nbytes, None,
-          _raw_stream(dev, stream))
+    (_int8_module or _int8()).paged_attn(out, query, kv_cache, kv_scales, block_tables, seq_lens, query_start_loc,
+                                         max_query_len, max_seq_len, scale, workspace, num_splits, stream)
 
 
 def kv_gather_int8(key_out: torch.Tensor, value_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -718,26 +689,11 @@ def kv_gather_int8(key_out: torch.Tensor, value_out: torch.Tensor, kv_cache: tor
                    device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """The cached keys and values of request r into key_out and value_out [key_start_loc[r]:][:seq_lens[r]] (bf16
     [rows, Hkv, d])."""
-    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
-    S = seq_lens.numel()
-    if key_start_loc.numel() < S:
-        raise ValueError("key_start_loc must have an entry per request")
-    rows = key_out.shape[0]
-    _call(dev, "pkv_kv_gather_int8", (_lib or load()).pkv_kv_gather_int8,
-          _full("key_out", key_out, _BF16, dev, (-1, hkv, d), "a contiguous [rows, Hkv, d]"),
-          _full("value_out", value_out, _BF16, dev, (rows, hkv, d), "a contiguous [rows, Hkv, d]"), rows, cache, scales,
-          nb, hkv, d, bs,
-          _full("block_tables", block_tables, _I32, dev, (S, -1), "a contiguous [num_seqs, max_blocks]"),
-          block_tables.shape[1], _full("seq_lens", seq_lens, _I32, dev, (S,), "a contiguous [num_seqs]"),
-          _full("key_start_loc", key_start_loc, _I32, dev, (-1,), "a contiguous vector"), S, max_seq_len,
-          _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"), _raw_stream(dev, stream))
+    (_int8_module or _int8()).kv_gather(key_out, value_out, kv_cache, kv_scales, block_tables, seq_lens, key_start_loc,
+                                        max_seq_len, device_status, stream)
 
 
 def copy_blocks_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, block_mapping: torch.Tensor,
                      device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Copy-on-write over an int8 cache, codes and scales: block_mapping int64 [num_pairs, 2] of {source, destination}."""
-    cache, scales, dev, nb, hkv, bs, d = _int8_cache(kv_cache, kv_scales)
-    _call(dev, "pkv_copy_blocks_int8", (_lib or load()).pkv_copy_blocks_int8, cache, scales, nb, hkv, d, bs,
-          _full("block_mapping", block_mapping, _I64, dev, (-1, 2), "a contiguous [num_pairs, 2]"),
-          block_mapping.shape[0], _full("device_status", device_status, _I32, dev, (-1,), "a contiguous vector"),
-          _raw_stream(dev, stream))
+    (_int8_module or _int8()).copy_blocks(kv_cache, kv_scales, block_mapping, device_status, stream)

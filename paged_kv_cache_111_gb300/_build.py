@@ -1,8 +1,10 @@
 """Build libpagedkv.so in-tree with nvcc for sm_103a (no CMake, no torch extension).
 
 Each .cu file under csrc/ is compiled in parallel to an object file, then all
-are linked into one shared library beside this file.  The build is skipped
-when the library is newer than every source and header.
+are linked into one shared library beside this file.  The Python module that
+marshals the int8 calls (csrc/int8_calls.c, no torch headers) is compiled with
+the host's C compiler and linked to it.  The build is skipped when both are
+newer than every source and header.
 """
 
 from __future__ import annotations
@@ -12,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from typing import List
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpagedkv.so")
+CALLS = os.path.join(PKG, "_int8_calls.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,13 +43,13 @@ def sources() -> List[str]:
 
 def _inputs() -> List[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -72,6 +76,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"linking libpagedkv.so failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    res = subprocess.run([os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC",
+                          "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+                          os.path.join(CSRC, "int8_calls.c"), "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
+                          "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compiling int8_calls.c failed:\n{res.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 
