@@ -672,12 +672,12 @@ int pkv_qk_norm_rope_kv_write_int8(void *query_out, int64_t query_out_token_stri
  * pkv_paged_attn_int8 — pkv_paged_attn over an int8 cache, K_j and V_j being code *
  * scale.  Arguments and protocol (pkv_paged_attn_combine after it) as pkv_paged_attn;
  * any scale's sign is allowed.  The workspace is pkv_paged_attn's, and up to 41 MB more
- * where max_query_len times the query heads of a kv head passes 64 (the size query says).  Codes widen to f16 exactly; the query
- * enters the products as f16 after a per-row power-of-two scaling (exact for every
- * element not below 2^-24 of its row's largest), the weights as one f16 each (2^-12
- * of it); scores, softmax and accumulation are fp32.  Rows behind a request's last
- * token may hold anything.  A row that sees a key of a block whose scale is NaN is
- * NaN; one that sees none of its keys does not meet it.
+ * where max_query_len times the query heads of a kv head passes 64 (the size query says).
+ * Codes widen to f16 exactly; the query enters the products as f16 after a per-row
+ * power-of-two scaling (exact for every element not below 2^-24 of its row's largest),
+ * the weights as one f16 each (2^-12 of it); scores, softmax and accumulation are fp32.
+ * Rows behind a request's last token may hold anything.  A row that sees a key of a
+ * block whose scale is NaN is NaN; one that sees none of its keys does not meet it.
  */
 int pkv_paged_attn_int8(void *out, const void *query, int64_t query_token_stride,
                         const void *kv_cache, const float *kv_scales, int64_t num_blocks,
@@ -712,7 +712,8 @@ int pkv_kv_gather_int8(void *key_out, void *value_out, int64_t out_rows,
 
 /*
  * pkv_copy_blocks_int8 — pkv_copy_blocks over an int8 cache: the codes and the scales of
- * every {source, destination} pair's block.
+ * every {source, destination} pair's block.  A block that is the destination of two pairs
+ * has no defined result.
  */
 int pkv_copy_blocks_int8(void *kv_cache, float *kv_scales, int64_t num_blocks,
                          int32_t num_kv_heads, int32_t head_size, int32_t block_size,

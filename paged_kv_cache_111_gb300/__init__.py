@@ -68,6 +68,21 @@ class PagedKVError(RuntimeError):
         self.code = code
 
 
+_module = None
+
+
+def _calls():
+    """The module that marshals the int8 calls and the combine (csrc/py_calls.c)."""
+    global _module
+    if _module is None:
+        load()
+        from . import _py_calls
+        _py_calls.bind(torch.int8, _BF16, _F32, _I32, _I64, _refuse, PagedKVError, torch._C._cuda_getDevice,
+                       torch.cuda.device, torch._C._cuda_getCurrentRawStream)
+        _module = _py_calls
+    return _module
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -333,12 +348,7 @@ def paged_attn_shared_prefix_fp8(out: torch.Tensor, query: torch.Tensor, kv_cach
 
 def paged_attn_combine(out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Log-sum-exp merge of the rows pkv_paged_attn split; out as given to paged_attn."""
-    dev = out.get_device()
-    if dev < 0 or workspace.get_device() < 0:
-        raise ValueError("paged KV-cache calls take CUDA tensors only")
-    T, H, d = out.shape
-    _call(dev, "pkv_paged_attn_combine", (_lib or load()).pkv_paged_attn_combine, out.data_ptr(), workspace.data_ptr(),
-          workspace.nbytes, T, H, d, _raw_stream(dev, stream))
+    (_module or _calls()).combine(out, workspace, stream)
 
 
 def workspace_status(workspace: torch.Tensor) -> int:
@@ -640,27 +650,12 @@ def latent_attn_expanded(out: torch.Tensor, query: torch.Tensor, key: torch.Tens
 
 # ---- the int8 cache -------------------------------------------------------------------------------------------
 
-_int8_module = None
-
-
-def _int8():
-    """The module that marshals the int8 calls (csrc/int8_calls.c): the same checks, made in C."""
-    global _int8_module
-    if _int8_module is None:
-        load()
-        from . import _int8_calls
-        _int8_calls.bind(torch.int8, _BF16, _F32, _I32, _I64, _refuse, PagedKVError, torch._C._cuda_getDevice,
-                         torch.cuda.device, torch._C._cuda_getCurrentRawStream)
-        _int8_module = _int8_calls
-    return _int8_module
-
-
 def kv_write_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
                   slot_mapping: torch.Tensor, device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise key/value [T, Hkv, d] (bf16) into kv_cache (int8 [NB, Hkv, 2, 16, d]) and kv_scales (fp32
     [NB, Hkv, 2]) through slot_mapping [T] (int64), the tokens of a block side by side; the scale of a block that is
     written from its first row is made anew, any other grows where it has to."""
-    (_int8_module or _int8()).kv_write(kv_cache, kv_scales, key, value, slot_mapping, device_status, stream)
+    (_module or _calls()).kv_write(kv_cache, kv_scales, key, value, slot_mapping, device_status, stream)
 
 
 def qk_norm_rope_kv_write_int8(query_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -670,7 +665,7 @@ def qk_norm_rope_kv_write_int8(query_out: torch.Tensor, kv_cache: torch.Tensor, 
                                interleaved: bool = False, device_status: Optional[torch.Tensor] = None,
                                stream=None) -> None:
     """qk_norm_rope_kv_write into an int8 cache and its scales (see kv_write_int8)."""
-    (_int8_module or _int8()).qk_norm_rope_kv_write(
+    (_module or _calls()).qk_norm_rope_kv_write(
         query_out, kv_cache, kv_scales, query, key, value, q_weight, k_weight, eps, cos_sin, positions, slot_mapping,
         interleaved, device_status, stream)
 
@@ -680,8 +675,8 @@ def paged_attn_int8(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tens
                     max_query_len: int, max_seq_len: int, scale: float, workspace: torch.Tensor, num_splits: int = 0,
                     stream=None) -> None:
     """paged_attn over an int8 cache; the workspace is sized as for paged_attn, and paged_attn_combine follows."""
-    (_int8_module or _int8()).paged_attn(out, query, kv_cache, kv_scales, block_tables, seq_lens, query_start_loc,
-                                         max_query_len, max_seq_len, scale, workspace, num_splits, stream)
+    (_module or _calls()).paged_attn(out, query, kv_cache, kv_scales, block_tables, seq_lens, query_start_loc,
+                                     max_query_len, max_seq_len, scale, workspace, num_splits, stream)
 
 
 def kv_gather_int8(key_out: torch.Tensor, value_out: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,
@@ -689,11 +684,11 @@ def kv_gather_int8(key_out: torch.Tensor, value_out: torch.Tensor, kv_cache: tor
                    device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """The cached keys and values of request r into key_out and value_out [key_start_loc[r]:][:seq_lens[r]] (bf16
     [rows, Hkv, d])."""
-    (_int8_module or _int8()).kv_gather(key_out, value_out, kv_cache, kv_scales, block_tables, seq_lens, key_start_loc,
-                                        max_seq_len, device_status, stream)
+    (_module or _calls()).kv_gather(key_out, value_out, kv_cache, kv_scales, block_tables, seq_lens, key_start_loc,
+                                    max_seq_len, device_status, stream)
 
 
 def copy_blocks_int8(kv_cache: torch.Tensor, kv_scales: torch.Tensor, block_mapping: torch.Tensor,
                      device_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Copy-on-write over an int8 cache, codes and scales: block_mapping int64 [num_pairs, 2] of {source, destination}."""
-    (_int8_module or _int8()).copy_blocks(kv_cache, kv_scales, block_mapping, device_status, stream)
+    (_module or _calls()).copy_blocks(kv_cache, kv_scales, block_mapping, device_status, stream)

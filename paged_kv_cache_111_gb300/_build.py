@@ -2,7 +2,7 @@
 
 Each .cu file under csrc/ is compiled in parallel to an object file, then all
 are linked into one shared library beside this file.  The Python module that
-marshals the int8 calls (csrc/int8_calls.c, no torch headers) is compiled with
+marshals the int8 calls (csrc/py_calls.c, no torch headers) is compiled with
 the host's C compiler and linked to it.  The build is skipped when both are
 newer than every source and header.
 """
@@ -22,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpagedkv.so")
-CALLS = os.path.join(PKG, "_int8_calls.so")
+CALLS = os.path.join(PKG, "_py_calls.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -79,10 +79,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     tmp = CALLS + f".tmp{os.getpid()}"
     res = subprocess.run([os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC",
                           "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-                          os.path.join(CSRC, "int8_calls.c"), "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
+                          os.path.join(CSRC, "py_calls.c"), "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
                           "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"compiling int8_calls.c failed:\n{res.stderr}")
+        raise RuntimeError(f"compiling py_calls.c failed:\n{res.stderr}")
     os.replace(tmp, CALLS)
     return LIB
 

@@ -1,8 +1,9 @@
-/* The int8 cache's calls from Python (module _int8_calls, linked to libpagedkv.so): each reads its tensors' properties
- * through their Python methods, refuses what does not do (with the binding's own messages), and makes the C call.
+/* The int8 cache's calls and the combine from Python (module _py_calls, linked to libpagedkv.so): each reads its
+ * tensors' properties through their Python methods, refuses what does not do (with the binding's own messages), and
+ * makes the C call.
  *
- * These calls stand in a decode step of a few microseconds of GPU time.  Marshalled in Python (ctypes) they take 5.6 to
- * 11.5 us of host time each, of which the launch is 2; here 3.4 to 6.6.  Every call reads its tensors anew.
+ * These calls stand in a decode step of a few microseconds of GPU time.  Marshalled in Python (ctypes) they take 3.4 to
+ * 11.5 us of host time each, of which the launch is 2; here 2.7 to 6.6.  Every call reads its tensors anew.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -137,6 +138,14 @@ static int heads(const char *what, PyObject *x, long dev, int64_t T, int64_t H, 
     }
     *step = T > 1 ? strides[0] : H * width;
     return pointer(t);
+}
+
+static int bytes_of(PyObject *x, int64_t *out) {
+    PyObject *v = PyObject_GetAttr(x, s_nbytes);
+    if (!v) return -1;
+    const int rc = get_int(v, out);
+    Py_DECREF(v);
+    return rc;
 }
 
 typedef struct {
@@ -289,8 +298,8 @@ static PyObject *qk_norm_rope_kv_write(PyObject *self, PyObject *const *a, Py_ss
         stream_of(a[14], c.dev, &stream))
         return NULL;
     CALL(pkv_qk_norm_rope_kv_write_int8, c.dev, qo.ptr, qo_step, c.cache, c.scales, c.blocks, H, c.heads, c.width,
-         c.tokens, q.ptr, q_step, k.ptr, k_step, v.ptr, v_step, wq.ptr, wk.ptr, (float)eps, table.ptr, table.size[0], rot, inter,
-         positions.ptr, slots.ptr, T, status.ptr, stream);
+         c.tokens, q.ptr, q_step, k.ptr, k_step, v.ptr, v_step, wq.ptr, wk.ptr, (float)eps, table.ptr, table.size[0],
+         rot, inter, positions.ptr, slots.ptr, T, status.ptr, stream);
 }
 
 /* out, query, kv_cache, kv_scales, block_tables, seq_lens, query_start_loc, max_query_len, max_seq_len, scale,
@@ -323,12 +332,8 @@ static PyObject *paged_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         refuse("workspace", a[10], NULL, c.dev, "contiguous");
         return NULL;
     }
-    PyObject *size = PyObject_GetAttr(a[10], s_nbytes);
-    if (!size) return NULL;
-    const int bad = get_int(size, &bytes);
-    Py_DECREF(size);
-    if (bad || pointer(&ws) || int32_arg(a[7], &max_q) || int32_arg(a[8], &max_n) || int32_arg(a[11], &splits) ||
-        stream_of(a[12], c.dev, &stream))
+    if (bytes_of(a[10], &bytes) || pointer(&ws) || int32_arg(a[7], &max_q) || int32_arg(a[8], &max_n) ||
+        int32_arg(a[11], &splits) || stream_of(a[12], c.dev, &stream))
         return NULL;
     CALL(pkv_paged_attn_int8, c.dev, out.ptr, q.ptr, q_step, c.cache, c.scales, c.blocks, tables.ptr, width, lens.ptr,
          starts.ptr, S, T, max_q, max_n, H, c.heads, c.width, c.tokens, (float)scale, splits, ws.ptr,
@@ -379,6 +384,27 @@ static PyObject *copy_blocks(PyObject *self, PyObject *const *a, Py_ssize_t n) {
          status.ptr, stream);
 }
 
+/* out, workspace, stream */
+static PyObject *combine(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor out, ws;
+    int64_t bytes;
+    int32_t size[3];
+    void *stream;
+    if (arity(n, 3) || look(a[0], &out) || look(a[1], &ws)) return NULL;
+    if (out.dev < 0 || ws.dev < 0) {
+        PyErr_SetString(PyExc_ValueError, "paged KV-cache calls take CUDA tensors only");
+        return NULL;
+    }
+    if (out.dims != 3) {
+        PyErr_SetString(PyExc_ValueError, "out must be [T, H, d]");
+        return NULL;
+    }
+    for (int i = 0; i < 3; ++i)
+        if (int32_of(out.size[i], size + i)) return NULL;
+    if (bytes_of(a[1], &bytes) || pointer(&out) || pointer(&ws) || stream_of(a[2], out.dev, &stream)) return NULL;
+    CALL(pkv_paged_attn_combine, out.dev, out.ptr, ws.ptr, (size_t)bytes, size[0], size[1], size[2], stream);
+}
+
 /* torch's int8, bfloat16, float32, int32 and int64; the binding's refusal and error; torch's current device, device
  * guard and current stream */
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -393,12 +419,12 @@ static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {METHOD(bind),       METHOD(kv_write),    METHOD(qk_norm_rope_kv_write),
-                                METHOD(paged_attn), METHOD(kv_gather),   METHOD(copy_blocks),
-                                {NULL, NULL, 0, NULL}};
-static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_int8_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
+static PyMethodDef methods[] = {METHOD(bind),       METHOD(kv_write),  METHOD(qk_norm_rope_kv_write),
+                                METHOD(paged_attn), METHOD(kv_gather), METHOD(copy_blocks),
+                                METHOD(combine),    {NULL, NULL, 0, NULL}};
+static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_py_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
-PyMODINIT_FUNC PyInit__int8_calls(void) {
+PyMODINIT_FUNC PyInit__py_calls(void) {
     PyObject **to[] = {&s_shape, &s_dtype, &s_get_device, &s_is_contiguous, &s_data_ptr,
                        &s_stride, &s_nbytes, &s_cuda_stream, &s_enter, &s_exit};
     static const char *const names[] = {"shape", "dtype", "get_device", "is_contiguous", "data_ptr",
