@@ -675,7 +675,7 @@ int pkv_qk_norm_rope_kv_write_int8(void *query_out, int64_t query_out_token_stri
  * where max_query_len times the query heads of a kv head passes 64 (the size query says).
  * Codes widen to f16 exactly; the query enters the products as f16 after a per-row
  * power-of-two scaling (exact for every element not below 2^-24 of its row's largest),
- * the weights as one f16 each (2^-12 of it); scores, softmax and accumulation are fp32.
+ * the weights as one f16 each (2^-11 of it); scores, softmax and accumulation are fp32.
  * Rows behind a request's last token may hold anything.  A row that sees a key of a
  * block whose scale is NaN is NaN; one that sees none of its keys does not meet it.
  */
