@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
 
     const int W = (p.self_plan ? gridDim.x - 1 : gridDim.x) * NW;
     const int wid = blockIdx.x * NW + warp;
-    uint32_t seq = 0;                             // pages consumed so far by this warp (ring position)
+    uint32_t st = 0, par = 0;                     // this warp's next ring stage, and its barrier's phase there
     const int g4 = lane >> 2, t4 = lane & 3;
     const float NEG_INF = -__int_as_float(0x7f800000);
     // the sign of the scale goes into the query, so that the largest score has the largest weight
@@ -137,14 +137,18 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
         const int pb = ch.z;
         const int npages = ch.w - ch.z;
         const int32_t *bt = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq + pb;
-        // windows of 32 pages: lane l holds page (window + l)'s block, and the scales of that block as {the score
-        // factor's part, log2 and reciprocal of V's}; the next window's come while this one is at work
+        // windows of 32 pages: lane l holds page (window + l)'s block, and of that block's scales K's, and log2 of V's;
+        // the next window's come while this one is at work
         auto blocks_of = [&](int first) { return first + lane < npages ? bt[first + lane] : -1; };
         auto scales_of = [&](int blk) {
             float2 s = make_float2(0.f, 0.f);
             if (blk >= 0 && blk < p.num_blocks)
                 s = reinterpret_cast<const float2 *>(p.kv_scales)[static_cast<int64_t>(blk) * p.num_kv_heads + g];
             return s;
+        };
+        float ks_win, lv_win;
+        auto scales_in = [&](float2 s) {
+            ks_win = s.x, lv_win = __log2f(s.y < kInt8LeastScale ? kInt8LeastScale : s.y);      // (NaN stays)
         };
         int wbase = 0;
         int win = blocks_of(0), win_next = blocks_of(32);
@@ -160,17 +164,24 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
         const int n_split = split_mode ? info.x : 1;
         const int rows = min(16, rows_total - 16 * tile);
 
-        auto issue = [&](int k, int blk) {        // page k of this chunk -> its ring stage
+        auto issue = [&](uint32_t stage, int blk) {               // a page of this chunk -> its ring stage
             if (lane == 0) {
                 if (blk < 0 || blk >= p.num_blocks) report(PKV_ERR_DEVICE_INDEX);   // (read as zeros)
-                const uint32_t st = (seq + k) % DEPTH;
-                mbar_arrive_expect_tx(&bars[st], Cfg::kStage);
-                tma_load_5d(ring + st * Cfg::kStage, &kv_map, &bars[st], 0, 0, 0, g, blk);
+                mbar_arrive_expect_tx(&bars[stage], Cfg::kStage);
+                tma_load_5d(ring + stage * Cfg::kStage, &kv_map, &bars[stage], 0, 0, 0, g, blk);
             }
         };
         int issued = min(DEPTH, npages);
-        for (int k = 0; k < issued; ++k) issue(k, __shfl_sync(0xffffffffu, win, k));
-        float2 scale_win = scales_of(win), scale_next = make_float2(0.f, 0.f);
+        for (int k = 0; k < issued; ++k)
+            issue(st + k < DEPTH ? st + k : st + k - DEPTH, __shfl_sync(0xffffffffu, win, k));
+        const float2 scale_first = scales_of(win);
+        float2 scale_next = make_float2(0.f, 0.f);
+        // query token and head of the group of the tile's row R
+        auto place_of = [&](int R) {
+            const int row = 16 * tile + R;
+            if (qlen == 1) return make_int2(0, row);
+            return make_int2(row / p.G, row % p.G);
+        };
 
         // the query rows this lane holds dims of: g4, and g4 + 8.  Lane column t4 takes dims t4 HD/4 .. of a row, four
         // a k-step, so that its part of a key is whole words of the page (the order of a product's terms is free)
@@ -179,9 +190,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int R = g4 + 8 * nt;
-            const int i = (16 * tile + R) / p.G, hh = (16 * tile + R) % p.G;
-            const __nv_bfloat16 *qp = p.query + static_cast<int64_t>(qs + i) * p.q_stride +
-                                      static_cast<int64_t>(g * p.G + hh) * HD + t4 * (HD / 4);
+            const int2 at = place_of(R);
+            const __nv_bfloat16 *qp = p.query + static_cast<int64_t>(qs + at.x) * p.q_stride +
+                                      static_cast<int64_t>(g * p.G + at.y) * HD + t4 * (HD / 4);
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; kk += 2) {
                 const uint4 v = R < rows ? *reinterpret_cast<const uint4 *>(qp + 4 * kk) : make_uint4(0, 0, 0, 0);
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                 S0[nt][e] = __shfl_sync(0xffffffffu, bias[nt], 4 * R);
                 sf[nt][e] = __shfl_sync(0xffffffffu, factor[nt], 4 * R);
                 m[nt][e] = NEG_INF, l[nt][e] = 0.f;
-                lim[nt][e] = R + 8 * nt < rows ? ctx + (16 * tile + R + 8 * nt) / p.G + 1 : INT32_MAX;
+                lim[nt][e] = R + 8 * nt < rows ? ctx + place_of(R + 8 * nt).x + 1 : INT32_MAX;
                 lim_least = min(lim_least, lim[nt][e]);
             }
         lim_least = __reduce_min_sync(0xffffffffu, lim_least);
@@ -240,9 +251,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
             for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
         int failed_at = -1;
 
+        scales_in(scale_first);
+
         for (int k = 0; k < npages; ++k) {
-            const uint32_t st = (seq + k) % DEPTH;
-            const uint32_t par = ((seq + k) / DEPTH) & 1u;
             const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], par));
             if (!ok) {
                 failed_at = k;
@@ -282,20 +293,21 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
             __syncwarp();
             if (k - wbase == 32) {
                 wbase += 32;
-                win = win_next, scale_win = scale_next;
+                win = win_next;
+                scales_in(scale_next);
                 win_next = blocks_of(wbase + 32);
             }
             if (k - wbase == 16) scale_next = scales_of(win_next);
             const int nk = k + DEPTH;
             if (nk < npages) {
                 const int at = nk - wbase;
-                issue(nk, __shfl_sync(0xffffffffu, at < 32 ? win : win_next, at & 31));
+                issue(st, __shfl_sync(0xffffffffu, at < 32 ? win : win_next, at & 31));
                 ++issued;
             }
-            const float ks = __shfl_sync(0xffffffffu, scale_win.x, k - wbase);
-            float vs = __shfl_sync(0xffffffffu, scale_win.y, k - wbase);
-            vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;          // (NaN stays)
-            const float lv = __log2f(vs), vr = __frcp_rn(vs);
+            if (++st == DEPTH) st = 0, par ^= 1u;
+            const float ks = __shfl_sync(0xffffffffu, ks_win, k - wbase);
+            const float lv = __shfl_sync(0xffffffffu, lv_win, k - wbase);
+            const float vr = fast_exp2(-lv);      // (1 / vs with lv's own rounding, which so falls out of the weights)
             const int j0 = (pb + k) * kBlock;     // first key of this page
             const bool masked = j0 + kBlock > lim_least;               // (uniform over the warp)
 
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                     const float inv = masked && j0 >= lim[nt][e] ? 0.f : vr;
                     l[nt][e] = fmaf(pr[e] + pr[e + 2], inv, l[nt][e]);
                 }
-                // one f16 a weight: 2^-12 of it at most, several times below the output's bf16
+                // one f16 a weight: off by 2^-11 of it at most, an eighth of the output's rounding to bf16
                 pb0[nt] = movmatrix(pack_f16x2(pr[0], pr[1]));
                 pb1[nt] = movmatrix(pack_f16x2(pr[2], pr[3]));
             }
@@ -390,12 +402,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
             report(PKV_ERR_DEVICE_TIMEOUT);
             // let copies already in flight land before the CTA's memory is released
             for (int k = failed_at; k < issued; ++k) {
-                const uint32_t st = (seq + k) % DEPTH;
-                mbar_wait_bounded(&bars[st], ((seq + k) / DEPTH) & 1u);
+                mbar_wait_bounded(&bars[st], par);
+                if (++st == DEPTH) st = 0, par ^= 1u;
             }
             return;
         }
-        seq += npages;
 
         const float LN2 = 0.69314718055994531f;
 #pragma unroll
@@ -409,7 +420,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (R >= rows) continue;
                 const float inv = sum <= 0.f ? 0.f : 1.f / sum;         // (NaN stays)
-                const int i = (16 * tile + R) / p.G, h = g * p.G + (16 * tile + R) % p.G;
+                const int2 at = place_of(R);
+                const int i = at.x, h = g * p.G + at.y;
                 if (n_split <= 1) {
                     uint32_t w[MT];
 #pragma unroll
