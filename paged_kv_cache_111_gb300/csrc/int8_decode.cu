@@ -21,21 +21,28 @@
 
 namespace pkv {
 
-// Columns of the products: rows of a chunk at most.  Warps a CTA, ring stages a warp, CTAs an SM.
+// Columns of the products: rows of a chunk at most.  Warps a CTA, ring stages a warp, CTAs an SM.  Two stages a warp: 64
+// to 96 KB in flight an SM are more than memory's rate times its latency, and what shared memory leaves is L1 (256
+// requests of 40 heads of 128: 347 us, with three stages 361, with three and a CTA more, of 128 registers that spill,
+// 382; 64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.7 us, with six stages 20.2).  Sixteen columns of 128 dims
+// spill at 168 registers; two CTAs without spills are faster in large batches (512 requests of 64/4 heads: 167 us, three
+// 191) and slower in small ones (64: 44 us, three 32).
 template <int HD, int ROWS> struct Int8Tiling;
-template <> struct Int8Tiling<64, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 6, CTAS_PER_SM = 4; };
-template <> struct Int8Tiling<128, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 3, CTAS_PER_SM = 4; };
-template <> struct Int8Tiling<64, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 6, CTAS_PER_SM = 4; };
-template <> struct Int8Tiling<128, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 4, CTAS_PER_SM = 3; };
+template <> struct Int8Tiling<64, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 4; };
+template <> struct Int8Tiling<128, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
+template <> struct Int8Tiling<64, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
+template <> struct Int8Tiling<128, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
 
 template <int HD, int ROWS>
 struct Int8DecodeCfg {
     using T = Int8Tiling<HD, ROWS>;
     static constexpr int kStage = 2 * kBlock * HD;           // a raw page of one kv head
     static constexpr int kWarpBytes = T::DEPTH * kStage;
-    static constexpr int kSmem = T::NW * kWarpBytes + T::NW * T::DEPTH * 8 + 1024;
+    // (before the rings are used, a plan lies where they are)
+    static constexpr int kPlanBytes = ((8 * kSelfPlanSeqs + 1) * 4 + 15) & ~15;
+    static constexpr int kOffBar = T::NW * kWarpBytes > kPlanBytes ? T::NW * kWarpBytes : kPlanBytes;
+    static constexpr int kSmem = kOffBar + T::NW * T::DEPTH * 8 + 1024;
     static_assert((kSmem + 1024) * T::CTAS_PER_SM <= 228 * 1024, "the tiling's CTAs fit one SM's shared memory");
-    static_assert(T::NW * kWarpBytes >= (8 * kSelfPlanSeqs + 1) * 4, "a plan fits the rings' memory");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -71,7 +78,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * Cfg::kWarpBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * Cfg::kWarpBytes) + warp * DEPTH;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar) + warp * DEPTH;
     const uint32_t ring_u32 = smem_u32(ring);
     if (lane < DEPTH) mbar_init(&bars[lane], 1);
     if (threadIdx.x == 0) tma_prefetch_desc(&kv_map);
