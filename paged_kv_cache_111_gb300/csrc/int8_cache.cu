@@ -15,10 +15,10 @@
 // heads j, j + n, ... of them, all n rows of each, so that a scale is made where all of its rows are.  So a chunk and a
 // decode step both put every warp to work, without a plan and without atomics.
 //
-// What bounds it: of few tokens a chain of three trips to memory (slots, rows, the store; 64 tokens of 8 heads of 128, GPU
-// time with their read-back: 5.9 us); of many, some 600 instructions a warp and 16 rows (issue 50%, 8331 tokens: 15 us,
-// 3.4 TB/s).  Behind norm and rotation a lane's fp32 rows wait for their scale in registers (128; 2046 tokens of 32/8
-// heads: 18 us); made a second time from the bf16 rows instead they leave room for more warps, and take 19.
+// What bounds it: of few tokens a chain of three trips to memory (slots, rows, the store; 64 tokens of 8 heads of 128,
+// GPU time with their read-back: 5.9 us); of many, some 600 instructions a warp and 16 rows (issue 50%, 8331 tokens: 15
+// us, 3.4 TB/s).  Behind norm and rotation a lane's fp32 rows wait for their scale in registers (128; 2046 tokens of
+// 32/8 heads: 18 us); made a second time from the bf16 rows instead they leave room for more warps, and take 19.
 //
 // Reading back moves whole pages, 99% of a copy's rate where there are many; so do the copies.
 #include "int8_common.cuh"

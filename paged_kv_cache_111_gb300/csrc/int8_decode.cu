@@ -25,12 +25,12 @@
 
 namespace pkv {
 
-// Columns of the products: rows of a chunk at most.  Warps a CTA, ring stages a warp, CTAs an SM.  Two stages a warp: 64
-// to 96 KB in flight an SM are more than memory's rate times its latency, and what shared memory leaves is L1 (256
+// Columns of the products: rows of a chunk at most.  Warps a CTA, ring stages a warp, CTAs an SM.  Two stages a warp:
+// 64 to 96 KB in flight an SM are more than memory's rate times its latency, and what shared memory leaves is L1 (256
 // requests of 40 heads of 128: 347 us, with three stages 361, with three and a CTA more, of 128 registers that spill,
 // 382; 64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.7 us, with six stages 20.2).  Sixteen columns of 128 dims
-// spill at 168 registers; two CTAs without spills are faster in large batches (512 requests of 64/4 heads: 167 us, three
-// 191) and slower in small ones (64: 44 us, three 32).
+// spill at 168 registers; two CTAs without spills are faster in large batches (512 requests of 64/4 heads: 167 us,
+// three 191) and slower in small ones (64: 44 us, three 32).
 template <int HD, int ROWS> struct Int8Tiling;
 template <> struct Int8Tiling<64, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 4; };
 template <> struct Int8Tiling<128, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
@@ -77,6 +77,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
     constexpr int MT = HD / 16;                   // 16-dim tiles of O^T
     constexpr int NT = ROWS / 8;                  // 8-row tiles of the columns
     constexpr int VW = HD / 32;                   // words of a V row a lane
+    // V's words are read when the scores are done (fewer registers at a time: 256 requests of 40 heads 345 -> 343 us, 512
+    // of 64/4 heads 191 -> 186), of 64 dims at once (256 requests of 32 heads: 256 us, 260 so)
+    constexpr bool kLateV = HD == 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
@@ -286,39 +289,44 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
                                  : "r"(page + row * HD + c * 16));
                 }
             }
+            auto load_v = [&]() {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int row = kBlock + 2 * t4 + (n & 1) + 8 * (n >> 1);
-                if constexpr (HD == 128) {
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(vw[n][0]), "=r"(vw[n][1]), "=r"(vw[n][2]), "=r"(vw[n][3])
-                                 : "r"(page + row * HD + ((g4 ^ (row & 7)) << 4)));
-                } else {
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(vw[n][0]), "=r"(vw[n][1])
-                                 : "r"(page + row * HD + (((g4 >> 1) ^ ((row >> 1) & 3)) << 4) + (g4 & 1) * 8));
+                for (int n = 0; n < 4; ++n) {
+                    const int row = kBlock + 2 * t4 + (n & 1) + 8 * (n >> 1);
+                    if constexpr (HD == 128) {
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(vw[n][0]), "=r"(vw[n][1]), "=r"(vw[n][2]), "=r"(vw[n][3])
+                                     : "r"(page + row * HD + ((g4 ^ (row & 7)) << 4)));
+                    } else {
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                     : "=r"(vw[n][0]), "=r"(vw[n][1])
+                                     : "r"(page + row * HD + (((g4 >> 1) ^ ((row >> 1) & 3)) << 4) + (g4 & 1) * 8));
+                    }
                 }
+            };
+            auto release = [&]() {
+                // the page is in registers: its stage goes back to the copy engine
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (k - wbase == 32) {
+                    wbase += 32;
+                    win = win_next;
+                    scales_in(scale_next);
+                    win_next = blocks_of(wbase + 32);
+                }
+                if (k - wbase == 16) scale_next = scales_of(win_next);
+                const int nk = k + DEPTH;
+                if (nk < npages) {
+                    const int at = nk - wbase;
+                    issue(st, __shfl_sync(0xffffffffu, at < 32 ? win : win_next, at & 31));
+                    ++issued;
+                }
+                if (++st == DEPTH) st = 0, par ^= 1u;
+            };
+            if (!kLateV) {
+                load_v();
+                release();
             }
-            // the page is in registers: its stage goes back to the copy engine
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (k - wbase == 32) {
-                wbase += 32;
-                win = win_next;
-                scales_in(scale_next);
-                win_next = blocks_of(wbase + 32);
-            }
-            if (k - wbase == 16) scale_next = scales_of(win_next);
-            const int nk = k + DEPTH;
-            if (nk < npages) {
-                const int at = nk - wbase;
-                issue(st, __shfl_sync(0xffffffffu, at < 32 ? win : win_next, at & 31));
-                ++issued;
-            }
-            if (++st == DEPTH) st = 0, par ^= 1u;
-            const float ks = __shfl_sync(0xffffffffu, ks_win, k - wbase);
-            const float lv = __shfl_sync(0xffffffffu, lv_win, k - wbase);
-            const float vr = fast_exp2(-lv);      // (1 / vs with lv's own rounding, which so falls out of the weights)
             const int j0 = (pb + k) * kBlock;     // first key of this page
             const bool masked = j0 + kBlock > lim_least;               // (uniform over the warp)
 
@@ -334,6 +342,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt], a, qf[nt][kk][0], qf[nt][kk][1]);
             }
+            if (kLateV) {
+                load_v();
+                release();
+            }
+            const float ks = __shfl_sync(0xffffffffu, ks_win, k - wbase);
+            const float lv = __shfl_sync(0xffffffffu, lv_win, k - wbase);
+            const float vr = fast_exp2(-lv);      // (1 / vs with lv's own rounding, which so falls out of the weights)
 
             // s + log2 vs above the row's reference
             float x[NT][4];

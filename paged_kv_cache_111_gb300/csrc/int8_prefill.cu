@@ -22,11 +22,11 @@
 // widen (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is
 // bounded.
 //
-// What bounds it: the chain of a row tile.  2046 tokens at 8190 keys of 32/8 heads of 128 take 262 us, 4400 cycles a pair
-// of tiles where the products take 2080 (the tensor pipe is at 40%, issue at 44%): a softmax warp gets an instruction out
-// every 4 to 5 cycles, and tensor memory has no room for a third score tile.  Tried and slower: two threads a row, halves
-// of 64 keys, an MMA warp a row tile, a pass for each row's largest score (367 us with loops unrolled: instruction fetch).
-// 256 tokens at 6400 keys: 65 us, with items left whole 121.
+// What bounds it: the chain of a row tile.  2046 tokens at 8190 keys of 32/8 heads of 128 take 262 us, 4400 cycles a
+// pair of tiles where the products take 2080 (the tensor pipe is at 40%, issue at 44%): a softmax warp gets an
+// instruction out every 4 to 5 cycles, and tensor memory has no room for a third score tile.  Tried and slower: two
+// threads a row, halves of 64 keys, an MMA warp a row tile, a pass for each row's largest score (367 us with loops
+// unrolled: instruction fetch). 256 tokens at 6400 keys: 65 us, with items left whole 121.
 #include <mutex>
 #include <type_traits>
 
@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     const WsHeader *hdr = reinterpret_cast<const WsHeader *>(p.ws);
     int32_t *status = reinterpret_cast<int32_t *>(p.ws);
     const int n_tiles = ws_ld(&hdr->n_ptiles);
-    const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));   // {request, tile, key tiles, -}
+    // {request, tile, key tiles, -}
+    const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));
     const int n_items = n_tiles * p.num_kv_heads;
     // fewer items than CTAs: the units of all items, and the CTAs that share them
     const bool runs = n_items < static_cast<int>(gridDim.x);
@@ -546,7 +547,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     sum2 = f2_add(sum2, x2);
                 }
                 const uint32_t at = sQ + (i * C + (c >> 3)) * kIpSlot + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                             :
+                             : "r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                              : "memory");
             }
             float s0, s1;
@@ -806,11 +809,10 @@ static int launch_ip(const PrefillParams &p, const CUtensorMap &map, const void 
             done_mask |= bit;
         }
     }
-    return launch_pdl(int8_prefill_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(kIpThreads), IpCfg<HD>::kSmem, stream,
-                      map, static_cast<const __nv_bfloat16 *>(query), q_stride,
-                      reinterpret_cast<const float2 *>(kv_scales), p) == cudaSuccess
-               ? PKV_OK
-               : PKV_ERR_CUDA;
+    const cudaError_t e = launch_pdl(int8_prefill_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(kIpThreads),
+                                     IpCfg<HD>::kSmem, stream, map, static_cast<const __nv_bfloat16 *>(query), q_stride,
+                                     reinterpret_cast<const float2 *>(kv_scales), p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_stride, const void *kv_cache,
