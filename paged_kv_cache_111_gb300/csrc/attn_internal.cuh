@@ -61,8 +61,8 @@ struct WsLayout {
     int32_t prefix_parts;     // splits of the shared prefix (0: no cascade)
 };
 
-// Chunks over an int8 cache (int8_prefill.cu), where work items are fewer than CTAs: the CTAs share them out in equal
-// runs, so that an item is cut along its keys.  Its pieces' sums lie behind the layout above, two places a CTA (what
+// Chunks over an int8 cache (int8_prefill.cu), where whole work items would leave CTAs idle: the CTAs share them out in
+// equal runs, so that an item is cut along its keys.  Its pieces' sums lie behind the layout above, two places a CTA (what
 // its run begins with, and what it ends with): {reference, sum} of each row, and rows x head_size fp32 unnormalised
 // sums, four dims of each row side by side.  The CTA of an item's first piece notes it down, and the combine joins the
 // pieces.

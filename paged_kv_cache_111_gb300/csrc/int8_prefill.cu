@@ -10,9 +10,9 @@
 // tile sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and
-// share each 128-key tile; a persistent CTA an SM takes items largest first.  Where there are fewer items than CTAs
-// their key tiles are one line that is cut into an equal run for each CTA; the combine that follows joins the pieces'
-// sums, which are left in the workspace.
+// share each 128-key tile; a persistent CTA an SM takes items largest first.  Where that would leave CTAs idle for longer
+// than a join takes, the items' key tiles are one line that is cut into an equal run for each CTA; the combine that
+// follows joins the pieces' sums, which are left in the workspace.
 //
 // Per key tile: 8 pages (one TMA box each, K and V) land raw, four warps widen them into a ring of 16 KiB slots in the
 // layout the products read, S = Q K^T from shared memory (128 x 128 x 16), softmax by four warps a row tile (a row per
@@ -111,8 +111,8 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
 }
 
 // In the line that is cut, an item counts for as many units as it has key tiles and kIpOver more (Q, epilogue, and what
-// a piece more costs); a CTA gets kIpLeast units at least.
-constexpr int kIpOver = 3, kIpLeast = 6;
+// a piece more costs); a CTA gets kIpLeast units at least.  The cut and the join cost about kIpJoin units more.
+constexpr int kIpOver = 3, kIpLeast = 6, kIpJoin = 13;
 
 template <int HD>
 __global__ void __launch_bounds__(kIpThreads, 1)
@@ -140,18 +140,24 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     // {request, tile, key tiles, -}
     const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));
     const int n_items = n_tiles * p.num_kv_heads;
-    // fewer items than CTAs: the units of all items, and the CTAs that share them
-    const bool runs = n_items < static_cast<int>(gridDim.x);
+    // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items' units?
+    // 32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 169 and 240 us, 2046 (256) 255 and 265,
+    // 2432 (304) 309 and 278; 1280 behind none 66 and 47.  From four rounds on whole items.
+    bool runs = n_items <= 3 * static_cast<int>(gridDim.x);
     int64_t all = 0;
     int ctas = gridDim.x;
-    if (runs) {                                       // (a few hundred tiles at most)
+    if (runs && n_items) {                            // (some hundred tiles at most)
         for (int t = lane; t < n_tiles; t += 32) all += ws_ld(ptiles + t).z + kIpOver;
+        const int64_t largest = ws_ld(ptiles).z + kIpOver;
 #pragma unroll
         for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const int64_t rounds = (n_items + ctas - 1) / ctas;
         all *= p.num_kv_heads;
+        runs = all / ctas + kIpJoin < max(largest, rounds * all / n_items);
         ctas = static_cast<int>(min(static_cast<int64_t>(ctas), max(static_cast<int64_t>(1), all / kIpLeast)));
     }
-    if (static_cast<int>(blockIdx.x) >= (runs ? (n_items ? ctas : 0) : n_items)) {     // uniform over the CTA
+    if (!runs) ctas = gridDim.x;
+    if (static_cast<int>(blockIdx.x) >= (runs && n_items ? ctas : n_items)) {     // uniform over the CTA
         pdl_wait();
         return;
     }
@@ -194,6 +200,24 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         int tile = 0;                                 // runs: a tile, where its units begin, the next unit, and the end
         int64_t at = 0, u = all * blockIdx.x / ctas;
         const int64_t u0 = u, u1 = all * (blockIdx.x + 1) / ctas;
+        while (runs) {                                // the tile that this run begins in
+            const int units = tile + lane < n_tiles ? ws_ld(ptiles + tile + lane).z + kIpOver : 0;
+            int64_t sum = static_cast<int64_t>(units) * p.num_kv_heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t before = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += before;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, at + sum > u0);
+            if (past) {
+                const int f = __ffs(static_cast<int>(past)) - 1;
+                at += __shfl_sync(0xffffffffu, sum - static_cast<int64_t>(units) * p.num_kv_heads, f);
+                tile += f;
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, sum, 31);
+            tile += 32;
+        }
         for (int k = 0; ok; ++k) {
             const int slot = k & 3;
             if (k >= 4) ok = ip_warp_wait(&bars[kIpItemEmpty + slot], (k / 4 - 1) & 1, status);

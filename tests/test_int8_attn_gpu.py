@@ -110,6 +110,17 @@ def test_a_few_work_items_of_many_keys(q, hq, hkv):
     check(s, run(s))
 
 
+@pytest.mark.parametrize("hq,hkv,d,reqs", [
+    (40, 40, 128, [(1100, 6000)]),                            # 200 items, some of them in three runs
+    (40, 40, 64, [(900, 5000), (300, 300), (1, 40)]),
+    (16, 1, 64, [(2700, 4000)]),                              # 169 tiles of one kv head
+    (8, 1, 128, [(2046, 3500), (700, 6000), (1, 50)]),
+    (4, 2, 128, [(5000, 5200)] + [(1, 77)] * 3)])
+def test_equal_runs_of_more_items_than_ctas(hq, hkv, d, reqs):
+    s = batch(reqs, hq, hkv, d, seed=7)
+    check(s, run(s))
+
+
 def test_cut_items_with_blocks_without_a_scale():
     s = batch([(200, 6000)], 4, 2, 64, seed=4)
     want, bound = ref.attention(s["query"], s["cache"], s["scales"], s["tables"], s["lens"], s["qsl"], s["scale"])
