@@ -42,19 +42,19 @@ constexpr int kIpSoft = 4;                            // softmax warps of a row 
 constexpr int kIpWiden = 4;                           // warps that widen
 constexpr int kIpThreads = 32 * (2 + kIpWiden + 2 * kIpSoft);
 constexpr int kIpSlot = 16384;                        // 64 dims of 128 rows, or 128 dims of 64 rows, as f16
-constexpr int kIpRaw = 2;                             // raw key tiles in flight
+constexpr int kIpSlots = 8;
 constexpr int kIpScaleTiles = 8;                      // key tiles whose blocks' scales are held
 constexpr int kIpReaders = 1 + kIpWiden + 2 * kIpSoft;    // of an item: MMA, widening and softmax warps
 
 template <int HD>
 struct IpCfg {
     static constexpr int kChunks = HD / 64;           // slots of a K (or V) tile, 64-dim chunks of Q
-    static constexpr int kSlots = HD == 128 ? 6 : 8;
-    static constexpr int kRawBytes = kIpKeys * 2 * HD;
+    static constexpr int kRaw = HD == 128 ? 2 : 4;    // raw K or V tiles in flight
+    static constexpr int kRawBytes = kIpKeys * HD;
     static constexpr int kOffQ = 0;                   // [row tile][chunk] 16 KiB
     static constexpr int kOffRing = kOffQ + 2 * kChunks * kIpSlot;
-    static constexpr int kOffRaw = kOffRing + kSlots * kIpSlot;
-    static constexpr int kOffBar = kOffRaw + kIpRaw * kRawBytes;
+    static constexpr int kOffRaw = kOffRing + kIpSlots * kIpSlot;
+    static constexpr int kOffBar = kOffRaw + kRaw * kRawBytes;
     static constexpr int kOffItems = kOffBar + 512;
     static constexpr int kOffScales = kOffItems + 256;    // float4 {K's, log2 of V's, 1 / V's, -} [tile & 7][block]
     static constexpr int kSmem = kOffScales + kIpScaleTiles * kIpPages * 16 + 1024;   // + alignment slack
@@ -64,17 +64,17 @@ struct IpCfg {
 enum IpBar {
     kIpItemFull = 0,     // (+ item & 3)
     kIpItemEmpty = 4,    // (+ item & 3)
-    kIpRawFull = 8,      // (+ tile & 1)
-    kIpRawEmpty = 10,    // (+ tile & 1)
-    kIpFull = 12,        // (+ slot)
-    kIpEmpty = 20,       // (+ slot)
-    kIpQFull = 28,       // (+ row tile)
-    kIpSFull = 30,       // (+ row tile)
-    kIpPFull = 32,       // (+ row tile)
-    kIpODone = 34,       // (+ row tile)
-    kIpOFree = 36,       // (+ row tile)
-    kIpScFull = 38,      // (+ tile & 7)
-    kIpNumBars = 46
+    kIpRawFull = 8,      // (+ place of the raw K or V tile)
+    kIpRawEmpty = 12,    // (+ place)
+    kIpFull = 16,        // (+ slot)
+    kIpEmpty = 24,       // (+ slot)
+    kIpQFull = 32,       // (+ row tile)
+    kIpSFull = 34,       // (+ row tile)
+    kIpPFull = 36,       // (+ row tile)
+    kIpODone = 38,       // (+ row tile)
+    kIpOFree = 40,       // (+ row tile)
+    kIpScFull = 42,      // (+ tile & 7)
+    kIpNumBars = 50
 };
 static_assert(kIpNumBars * 8 + 8 <= 512, "barriers, the tensor-memory address and the tile count");
 
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     int8_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __nv_bfloat16 *__restrict__ query,
                         const int64_t q_stride, const float2 *__restrict__ kv_scales, const PrefillParams p) {
     using Cfg = IpCfg<HD>;
-    constexpr int C = Cfg::kChunks, SLOTS = Cfg::kSlots, PER = 2 * C;     // slots of a key tile: K's, then V's
+    constexpr int C = Cfg::kChunks, SLOTS = kIpSlots, RAW = Cfg::kRaw, PER = 2 * C;     // slots of a key tile: K's, then V's
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         const int b = threadIdx.x;
         int count = 1;
         if (b >= kIpItemEmpty && b < kIpItemEmpty + 4) count = kIpReaders;
-        else if ((b >= kIpRawEmpty && b < kIpRawEmpty + 2) || (b >= kIpFull && b < kIpFull + 8)) count = kIpWiden;
+        else if ((b >= kIpRawEmpty && b < kIpRawEmpty + 4) || (b >= kIpFull && b < kIpFull + 8)) count = kIpWiden;
         else if ((b >= kIpQFull && b < kIpQFull + 2) || (b >= kIpPFull && b < kIpPFull + 2) ||
                  (b >= kIpOFree && b < kIpOFree + 2))
             count = kIpSoft;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     if (warp == 0) {
         // ---------------- items, raw pages, scales ----------------
         bool ok = true;
-        int taken = 0, gt = 0;                        // items, and key tiles of this CTA so far
+        int taken = 0, gt = 0, loads = 0;             // items, key tiles, and K and V tiles of this CTA so far
         int item = blockIdx.x;                        // whole items: the next one
         int *next_item = reinterpret_cast<int *>(p.ws + offsetof(WsHeader, next_ptile_item));
         int tile = 0;                                 // runs: a tile, where its units begin, the next unit, and the end
@@ -305,27 +305,32 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     win_next = blocks_of(j / 4 + 1);
                 }
                 if ((j & 3) == 2) sc_next = scales_of(win_next);
-                const int rs = gt & 1;
-                if (gt >= kIpRaw) ok = ip_warp_wait(&bars[kIpRawEmpty + rs], (gt / kIpRaw - 1) & 1, status);
-                if (!ok) break;
-                uint8_t *raw = smem + Cfg::kOffRaw + rs * Cfg::kRawBytes;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars[kIpRawFull + rs], Cfg::kRawBytes);
-                    *tiles_loaded = gt + 1;
-                }
-                __syncwarp();
                 const int at = (j & 3) * kIpPages + (lane & 7);
                 const int b = __shfl_sync(0xffffffffu, win, at);
-                const float ks = __shfl_sync(0xffffffffu, sc.x, at);
-                float vs = __shfl_sync(0xffffffffu, sc.y, at);
-                vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;         // (NaN stays, and K's joins it)
-                vs = ks != ks ? ks : vs;
-                if (lane < kIpPages) {
-                    tma_load_5d(raw + lane * (2 * kBlock * HD), &kv_map, &bars[kIpRawFull + rs], 0, 0, 0, it.g, b);
-                    scales[(gt & 7) * kIpPages + lane] = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    const int rs = loads % RAW;
+                    if (loads >= RAW) ok = ip_warp_wait(&bars[kIpRawEmpty + rs], (loads / RAW - 1) & 1, status);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars[kIpRawFull + rs], Cfg::kRawBytes);
+                        *tiles_loaded = gt + 1;
+                    }
+                    __syncwarp();
+                    if (lane < kIpPages)
+                        tma_load_5d(smem + Cfg::kOffRaw + rs * Cfg::kRawBytes + lane * (kBlock * HD), &kv_map,
+                                    &bars[kIpRawFull + rs], 0, 0, side, it.g, b);
+                    ++loads;
+                    if (side) continue;
+                    const float ks = __shfl_sync(0xffffffffu, sc.x, at);
+                    float vs = __shfl_sync(0xffffffffu, sc.y, at);
+                    vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;     // (NaN stays, and K's joins it)
+                    vs = ks != ks ? ks : vs;
+                    if (lane < kIpPages)
+                        scales[(gt & 7) * kIpPages + lane] = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kIpScFull + (gt & 7)]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kIpScFull + (gt & 7)]);
             }
             if (!runs) {
                 int nxt = 0;
@@ -334,8 +339,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             }
         }
         if (!ok)                                      // the copies in flight land before the CTA ends
-            for (int t = max(0, gt - kIpRaw); t < gt; ++t)
-                mbar_wait_bounded(&bars[kIpRawFull + (t & 1)], (t / kIpRaw) & 1);
+            for (int t = max(0, loads - RAW); t < loads; ++t)
+                mbar_wait_bounded(&bars[kIpRawFull + t % RAW], (t / RAW) & 1);
         // this CTA's share of the schedule
         if (lane == 0) reinterpret_cast<int32_t *>(p.ws + kStatsOffset)[blockIdx.x] = taken;
     } else if (warp == 1) {
@@ -453,8 +458,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
         const int r8 = HD == 128 ? ((lane >> 2) & 1 ? (lane >> 3) ^ 5 : lane >> 3) : lane >> 2;
         const uint32_t from = r8 * HD + (HD == 128 ? (c ^ r8) << 4 : c << 4);     // (second 64 dims: ^ 64)
         const uint32_t to = r8 * 128 + (((2 * c) ^ r8) << 4);                     // (its second 8 dims: ^ 16)
-        // groups g0 .. of 8 rows of the raw tile at src (page g / 2), to groups of a slot (dst0; the second 64 dims:
-        // dst1)
+        // groups g0 .. of 8 rows of the raw tile at src, to groups of a slot (dst0; the second 64 dims: dst1)
         constexpr int B = 4 / C;                       // groups at a time: four 16-byte loads a lane
         auto widen = [&](auto is_v, int groups, uint32_t src, int g0, uint32_t dst0, uint32_t dst1) {
             constexpr bool V = decltype(is_v)::value;
@@ -464,8 +468,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int g = g0 + n + u / C;
-                    const uint32_t at =
-                        src + (g >> 1) * (2 * kBlock * HD) + (g & 1) * 8 * HD + (V ? kBlock * HD : 0) + from;
+                    const uint32_t at = src + g * 8 * HD + from;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
                                  : "r"(at ^ (64u * (u % C))));
@@ -500,27 +503,30 @@ __global__ void __launch_bounds__(kIpThreads, 1)
             if (!valid) break;
 #pragma unroll 1
             for (int j = 0; j < n_kv && ok; ++j, ++gt) {
-                const int rs = gt & 1, s0 = gt * PER;
-                ok = ip_warp_wait(&bars[kIpRawFull + rs], (gt / kIpRaw) & 1, status);
-                const uint32_t src = smem_u32(smem + Cfg::kOffRaw + rs * Cfg::kRawBytes);
+                const int s0 = gt * PER, rk = 2 * gt % RAW, rv = rk + 1;
+                const uint32_t raw = smem_u32(smem + Cfg::kOffRaw);
+                ok = ip_warp_wait(&bars[kIpRawFull + rk], (2 * gt / RAW) & 1, status);
                 // K: dims 64 c .. of row r in slot c
 #pragma unroll 1
                 for (int s = 0; s < C && ok; ++s) ok = freed(s0 + s);
                 if (!ok) break;
                 const uint32_t k0 = sRing + (s0 % SLOTS) * kIpSlot, k1 = sRing + ((s0 + C - 1) % SLOTS) * kIpSlot;
-                widen(std::false_type(), KG, src, part * KG, k0 + part * KG * 1024, k1 + part * KG * 1024);
+                widen(std::false_type(), KG, raw + rk * Cfg::kRawBytes, part * KG, k0 + part * KG * 1024,
+                      k1 + part * KG * 1024);
                 for (int s = 0; s < C; ++s) filled(s0 + s);
+                // (the raw tile's place is loaded again behind the last of `filled`'s fences)
+                if (lane == 0) mbar_arrive(&bars[kIpRawEmpty + rk]);
+                ok = ip_warp_wait(&bars[kIpRawFull + rv], (2 * gt / RAW) & 1, status);
                 // V: rows 64 h .. in slot h, 64-dim chunks 8 KiB apart (64 dims: one slot)
 #pragma unroll 1
-                for (int h = 0; h < C; ++h) {
+                for (int h = 0; h < C && ok; ++h) {
                     ok = freed(s0 + C + h);
                     if (!ok) break;
                     const uint32_t slot = sRing + ((s0 + C + h) % SLOTS) * kIpSlot + part * VG * 1024;
-                    widen(std::true_type(), VG, src, 8 * h + part * VG, slot, slot + 8192);
+                    widen(std::true_type(), VG, raw + rv * Cfg::kRawBytes, 8 * h + part * VG, slot, slot + 8192);
                     filled(s0 + C + h);
                 }
-                // (the raw tile's place is loaded again behind the last of `filled`'s fences)
-                if (ok && lane == 0) mbar_arrive(&bars[kIpRawEmpty + rs]);
+                if (ok && lane == 0) mbar_arrive(&bars[kIpRawEmpty + rv]);
             }
         }
     } else {
@@ -843,7 +849,7 @@ int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_str
                         const float *kv_scales, int64_t num_blocks, int32_t head_size, int64_t grid, int dev,
                         cudaStream_t stream) {
     if (grid <= 0) return PKV_OK;
-    // a box is a page of one kv head, K rows then V rows; rows of 128 bytes with their 16-byte pieces permuted
+    // a box is a page of one kv head, its K or V rows; rows of 128 bytes with their 16-byte pieces permuted
     EncodeTiledFn enc = encode_fn();
     if (!enc) return PKV_ERR_CUDA;
     CUtensorMap map;
@@ -851,7 +857,7 @@ int launch_prefill_int8(const PrefillParams &p, const void *query, int64_t q_str
                                 static_cast<cuuint64_t>(num_blocks)};
     const cuuint64_t row = static_cast<cuuint64_t>(head_size);
     const cuuint64_t strides[4] = {row, row * kBlock, row * kBlock * 2, row * kBlock * 2 * p.num_kv_heads};
-    const cuuint32_t box[5] = {static_cast<cuuint32_t>(head_size), kBlock, 2, 1, 1};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(head_size), kBlock, 1, 1, 1};
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv_cache), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, head_size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
