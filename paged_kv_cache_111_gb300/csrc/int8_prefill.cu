@@ -10,23 +10,24 @@
 // tile sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and
-// share each 128-key tile; a persistent CTA an SM takes items largest first.  Where that would leave CTAs idle for longer
-// than a join takes, the items' key tiles are one line that is cut into an equal run for each CTA; the combine that
-// follows joins the pieces' sums, which are left in the workspace.
+// share each 128-key tile; a persistent CTA an SM takes items largest first.  Where that would leave CTAs idle for
+// longer than a join takes, the items' key tiles are one line that is cut into an equal run for each CTA; the combine
+// that follows joins the pieces' sums, which are left in the workspace.
 //
-// Per key tile: 8 pages (one TMA box each, K and V) land raw, four warps widen them into a ring of 16 KiB slots in the
-// layout the products read, S = Q K^T from shared memory (128 x 128 x 16), softmax by four warps a row tile (a row per
-// thread), P as f16 over S in tensor memory, O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
+// Per key tile: 8 pages (a TMA box each for K and for V) land raw, four warps widen them into a ring of 16 KiB slots in
+// the layout the products read, S = Q K^T from shared memory (128 x 128 x 16), softmax by four warps a row tile (a row
+// per thread), P as f16 over S in tensor memory, O += P V.  Tensor memory: S of both tiles, O of both (512 columns).
 //
 // Warp roles (448 threads): warp 0 items, loads and the pages' scales, warp 1 issues the MMAs, warps 2, 3, 12 and 13
 // widen (one on each scheduler), warps 4-7 and 8-11 are the softmax and epilogue of the two row tiles.  Every wait is
 // bounded.
 //
-// What bounds it: the chain of a row tile.  2046 tokens at 8190 keys of 32/8 heads of 128 take 262 us, 4400 cycles a
-// pair of tiles where the products take 2080 (the tensor pipe is at 40%, issue at 44%): a softmax warp gets an
-// instruction out every 4 to 5 cycles, and tensor memory has no room for a third score tile.  Tried and slower: two
-// threads a row, halves of 64 keys, an MMA warp a row tile, a pass for each row's largest score (367 us with loops
-// unrolled: instruction fetch). 256 tokens at 6400 keys: 65 us, with items left whole 121.
+// What bounds it: the softmax warps, three warps a scheduler with the widening one.  2432 tokens behind 6144 keys of
+// 32/8 heads of 128 (two rounds of items) take 274 us, 4300 cycles a pair of tiles where the products take 2080, and
+// 2046 tokens 253 (the tensor pipe is at 40%, issue at 44%).  Tried and slower: two threads a row, halves of 64 keys (P
+// V early, or the next S early: the other half's S while P V runs hides what the softmax waits for, and reads Q twice),
+// an MMA warp a row tile, a pass for each row's largest score (367 us with loops unrolled: instruction fetch).  256
+// tokens at 6400 keys: 65 us, with items left whole 121.
 #include <mutex>
 #include <type_traits>
 
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     int8_prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __nv_bfloat16 *__restrict__ query,
                         const int64_t q_stride, const float2 *__restrict__ kv_scales, const PrefillParams p) {
     using Cfg = IpCfg<HD>;
-    constexpr int C = Cfg::kChunks, SLOTS = kIpSlots, RAW = Cfg::kRaw, PER = 2 * C;     // slots of a key tile: K's, then V's
+    constexpr int C = Cfg::kChunks, SLOTS = kIpSlots, RAW = Cfg::kRaw;
+    constexpr int PER = 2 * C;                            // slots of a key tile: K's, then V's
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
@@ -140,9 +142,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     // {request, tile, key tiles, -}
     const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));
     const int n_items = n_tiles * p.num_kv_heads;
-    // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items' units?
-    // 32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 169 and 240 us, 2046 (256) 255 and 265,
-    // 2432 (304) 309 and 278; 1280 behind none 66 and 47.  From four rounds on whole items.
+    // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items'
+    // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 169 and 240 us, 2046 (256)
+    // 255 and 265, 2432 (304) 309 and 278; 1280 behind none 66 and 47.  From four rounds on whole items.
     bool runs = n_items <= 3 * static_cast<int>(gridDim.x);
     int64_t all = 0;
     int ctas = gridDim.x;
