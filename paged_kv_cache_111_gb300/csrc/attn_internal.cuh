@@ -271,7 +271,7 @@ int launch_decode_path(const CUtensorMap &map, const AttnParams &ap, int32_t hea
                        cudaStream_t st);
 
 // The same over an int8 cache (int8_decode.cu); `rows`: the most query rows of a chunk (8, or any more).
-int int8_decode_ctas_per_sm(int32_t head_size, int rows);
+int int8_decode_ctas_per_sm(int32_t head_size, int rows, bool self_plan);
 int make_int8_map(CUtensorMap *map, const void *kv_cache, int64_t num_blocks, int32_t num_kv_heads, int32_t head_size);
 int launch_int8_decode_path(const CUtensorMap &map, const AttnParams &ap, int32_t head_size, int rows, int grid, int dev,
                             cudaStream_t st);

@@ -25,28 +25,29 @@
 
 namespace pkv {
 
-// Columns of the products: rows of a chunk at most.  Warps a CTA, ring stages a warp, CTAs an SM.  Two stages a warp:
-// 64 to 96 KB in flight an SM are more than memory's rate times its latency, and what shared memory leaves is L1 (256
-// requests of 40 heads of 128: 347 us, with three stages 361, with three and a CTA more, of 128 registers that spill,
-// 382; 64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.7 us, with six stages 20.2).  Sixteen columns of 128 dims
-// spill at 168 registers; two CTAs without spills are faster in large batches (512 requests of 64/4 heads: 167 us,
-// three 191) and slower in small ones (64: 44 us, three 32).
-template <int HD, int ROWS> struct Int8Tiling;
-template <> struct Int8Tiling<64, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 4; };
-template <> struct Int8Tiling<128, 8> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
-template <> struct Int8Tiling<64, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
-template <> struct Int8Tiling<128, 16> { static constexpr int NW = kDecodeWarps, DEPTH = 2, CTAS_PER_SM = 3; };
+// ROWS: columns of the products, rows of a chunk at most.  Two ring stages a warp: 64 to 96 KB in flight an SM are more
+// than memory's rate times its latency, and what shared memory leaves is L1 (256 requests of 40 heads of 128: 347 us,
+// with three stages 361, with three and a CTA more, of 128 registers that spill, 382; 64 requests of 512 to 2048 keys,
+// 32/4 heads of 64: 17.7 us, with six stages 20.2).
+constexpr int kInt8Depth = 2;
 
-template <int HD, int ROWS>
+// CTAs an SM.  Sixteen columns of 128 dims spill at the 168 registers of three; a large batch, which the decode kernel
+// does not plan itself, is faster with two (512 requests of 64/4 heads: 167 us, three 186), a small one slower (64: 44
+// us, three 32).
+constexpr int int8_ctas(int head_size, bool wide, bool self_plan) {
+    if (head_size == 64) return wide ? 3 : 4;
+    return wide && !self_plan ? 2 : 3;
+}
+
+template <int HD, int ROWS, int CTAS>
 struct Int8DecodeCfg {
-    using T = Int8Tiling<HD, ROWS>;
     static constexpr int kStage = 2 * kBlock * HD;           // a raw page of one kv head
-    static constexpr int kWarpBytes = T::DEPTH * kStage;
+    static constexpr int kWarpBytes = kInt8Depth * kStage;
     // (before the rings are used, a plan lies where they are)
     static constexpr int kPlanBytes = ((8 * kSelfPlanSeqs + 1) * 4 + 15) & ~15;
-    static constexpr int kOffBar = T::NW * kWarpBytes > kPlanBytes ? T::NW * kWarpBytes : kPlanBytes;
-    static constexpr int kSmem = kOffBar + T::NW * T::DEPTH * 8 + 1024;
-    static_assert((kSmem + 1024) * T::CTAS_PER_SM <= 228 * 1024, "the tiling's CTAs fit one SM's shared memory");
+    static constexpr int kOffBar = kDecodeWarps * kWarpBytes > kPlanBytes ? kDecodeWarps * kWarpBytes : kPlanBytes;
+    static constexpr int kSmem = kOffBar + kDecodeWarps * kInt8Depth * 8 + 1024;
+    static_assert((kSmem + 1024) * CTAS <= 228 * 1024, "the tiling's CTAs fit one SM's shared memory");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -68,17 +69,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int HD, int ROWS>
-__global__ void __launch_bounds__(kDecodeWarps * 32, Int8Tiling<HD, ROWS>::CTAS_PER_SM)
+template <int HD, int ROWS, int CTAS>
+__global__ void __launch_bounds__(kDecodeWarps * 32, CTAS)
     int8_decode_kernel(const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
-    using Cfg = Int8DecodeCfg<HD, ROWS>;
-    constexpr int NW = Cfg::T::NW, DEPTH = Cfg::T::DEPTH;
+    using Cfg = Int8DecodeCfg<HD, ROWS, CTAS>;
+    constexpr int NW = kDecodeWarps, DEPTH = kInt8Depth;
     constexpr int KSTEPS = HD / 16;               // of S^T = K Q^T
     constexpr int MT = HD / 16;                   // 16-dim tiles of O^T
     constexpr int NT = ROWS / 8;                  // 8-row tiles of the columns
     constexpr int VW = HD / 32;                   // words of a V row a lane
-    // V's words are read when the scores are done (fewer registers at a time: 256 requests of 40 heads 345 -> 343 us, 512
-    // of 64/4 heads 191 -> 186), of 64 dims at once (256 requests of 32 heads: 256 us, 260 so)
+    // V's words are read when the scores are done (fewer registers at a time: 256 requests of 40 heads 345 -> 343 us,
+    // 512 of 64/4 heads 191 -> 186), of 64 dims at once (256 requests of 32 heads: 256 us, 260 so)
     constexpr bool kLateV = HD == 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -493,27 +494,26 @@ int make_int8_map(CUtensorMap *map, const void *kv_cache, int64_t num_blocks, in
                : PKV_ERR_CUDA;
 }
 
-int int8_decode_ctas_per_sm(int32_t head_size, int rows) {
-    if (rows <= 8) return head_size == 64 ? Int8Tiling<64, 8>::CTAS_PER_SM : Int8Tiling<128, 8>::CTAS_PER_SM;
-    return head_size == 64 ? Int8Tiling<64, 16>::CTAS_PER_SM : Int8Tiling<128, 16>::CTAS_PER_SM;
+int int8_decode_ctas_per_sm(int32_t head_size, int rows, bool self_plan) {
+    return int8_ctas(head_size, rows > 8, self_plan);
 }
 
-template <int HD, int ROWS>
+template <int HD, int ROWS, int CTAS>
 static int launch_int8_decode(const CUtensorMap &map, const AttnParams &p, int grid, int dev, cudaStream_t stream) {
-    using Cfg = Int8DecodeCfg<HD, ROWS>;
+    using Cfg = Int8DecodeCfg<HD, ROWS, CTAS>;
     static std::mutex mu;
     static uint64_t done_mask = 0;                // devices whose shared-memory limit is already raised
     {
         std::lock_guard<std::mutex> lock(mu);
         const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
         if (!bit || !(done_mask & bit)) {
-            if (cudaFuncSetAttribute(int8_decode_kernel<HD, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            if (cudaFuncSetAttribute(int8_decode_kernel<HD, ROWS, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Cfg::kSmem) != cudaSuccess)
                 return PKV_ERR_CUDA;
             done_mask |= bit;
         }
     }
-    return launch_pdl(int8_decode_kernel<HD, ROWS>, dim3(grid), dim3(kDecodeWarps * 32), Cfg::kSmem, stream, map, p) ==
+    return launch_pdl(int8_decode_kernel<HD, ROWS, CTAS>, dim3(grid), dim3(kDecodeWarps * 32), Cfg::kSmem, stream, map, p) ==
                    cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
@@ -521,11 +521,12 @@ static int launch_int8_decode(const CUtensorMap &map, const AttnParams &p, int g
 
 int launch_int8_decode_path(const CUtensorMap &map, const AttnParams &p, int32_t head_size, int rows, int grid, int dev,
                             cudaStream_t st) {
-    if (rows <= 8)
-        return head_size == 64 ? launch_int8_decode<64, 8>(map, p, grid, dev, st)
-                               : launch_int8_decode<128, 8>(map, p, grid, dev, st);
-    return head_size == 64 ? launch_int8_decode<64, 16>(map, p, grid, dev, st)
-                           : launch_int8_decode<128, 16>(map, p, grid, dev, st);
+    if (head_size == 64)
+        return rows <= 8 ? launch_int8_decode<64, 8, int8_ctas(64, false, false)>(map, p, grid, dev, st)
+                         : launch_int8_decode<64, 16, int8_ctas(64, true, false)>(map, p, grid, dev, st);
+    if (rows <= 8) return launch_int8_decode<128, 8, int8_ctas(128, false, false)>(map, p, grid, dev, st);
+    return p.self_plan ? launch_int8_decode<128, 16, int8_ctas(128, true, true)>(map, p, grid, dev, st)
+                       : launch_int8_decode<128, 16, int8_ctas(128, true, false)>(map, p, grid, dev, st);
 }
 
 }  // namespace pkv

@@ -695,17 +695,19 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     // (int8: query rows of a chunk at most)
     const int decode_rows = static_cast<int>(
         std::min<int64_t>(16, static_cast<int64_t>(max_query_len) * (num_q_heads / num_kv_heads)));
-    const int per_sm = int8 ? int8_decode_ctas_per_sm(head_size, decode_rows) : decode_ctas_per_sm(head_size, kv8);
-    const int64_t resident = static_cast<int64_t>(sms) * per_sm;
+    auto resident_of = [&](bool self_plan) {
+        return static_cast<int64_t>(sms) * (int8 ? int8_decode_ctas_per_sm(head_size, decode_rows, self_plan)
+                                                 : decode_ctas_per_sm(head_size, kv8));
+    };
     const int64_t max_items = lay.max_chunks * num_kv_heads;
-    int64_t grid = std::max<int64_t>(1, std::min(resident, (max_items + nw - 1) / nw));
     const int G = num_q_heads / num_kv_heads;
     // a small decode-only batch is planned by the decode kernel itself: its
     // last CTA writes the header, the others (still one wave) take the chunks
-    const int64_t sp_ctas = std::max<int64_t>(1, std::min(resident - 1, (max_items + nw - 1) / nw));
-    const bool self_plan = !may_prefill && resident >= 2 &&
+    const int64_t sp_ctas = std::max<int64_t>(1, std::min(resident_of(true) - 1, (max_items + nw - 1) / nw));
+    const bool self_plan = !may_prefill && resident_of(true) >= 2 &&
                            decode_self_plan_ok(num_seqs, max_query_len, max_seq_len, G, num_kv_heads, num_splits,
                                                prefix_blocks, sp_ctas * nw);
+    int64_t grid = std::max<int64_t>(1, std::min(resident_of(false), (max_items + nw - 1) / nw));
     if (self_plan) grid = sp_ctas + 1;
     const int64_t chunk_warps = (self_plan ? sp_ctas : grid) * nw;
 

@@ -142,6 +142,14 @@ def test_splits(num_splits, d):
     check(s, run(s, num_splits=num_splits), str(num_splits))
 
 
+@pytest.mark.parametrize("num_splits", [0, 1, 5])
+@pytest.mark.parametrize("reqs", [[(1, 300), (1, 17)], [(2, 900), (1, 33), (2, 2)]])
+def test_sixteen_rows_of_128_dims(num_splits, reqs):
+    """Planned by the decode kernel itself (no splits given), and by the plan."""
+    s = batch(reqs, 16 // reqs[0][0], 1, 128, seed=14)
+    check(s, run(s, num_splits=num_splits))
+
+
 def test_many_requests():
     g = torch.Generator().manual_seed(0)
     for S in (33, 65, 300, 1100):
@@ -328,6 +336,41 @@ def test_a_step_in_a_graph(reqs):
         fused.copy_(torch.randn(fused.shape, generator=g) * (k + 1))
         graph.replay()
         look(f"replay {k}")
+
+
+def test_graphs_of_several_steps_with_one_workspace():
+    """Decodes, whole chunks, and chunks cut along their keys, replayed in turn with nothing waited for between."""
+    steps = [batch([(1, 64), (1, 300), (1, 17)], 8, 2, 128, seed=11), batch([(150, 300), (1, 40)], 8, 2, 128, seed=12),
+             batch([(40, 6000), (1, 5)], 8, 2, 128, seed=13)]
+    ws = torch.empty(max(pkv.paged_attn_workspace_size(len(s["lens"]), s["query"].shape[0], s["max_q"], s["max_n"], 8, 2,
+                                                       128) for s in steps), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for s in steps:
+        lens, qsl = (torch.tensor(s[k], dtype=torch.int32, device="cuda") for k in ("lens", "qsl"))
+        out = torch.empty_like(s["query"])
+        s["keep"] = lens, qsl
+
+        def step():
+            pkv.paged_attn_int8(out, s["query"], s["cache"], s["scales"], s["tables"], lens, qsl, s["max_q"], s["max_n"],
+                                s["scale"], ws)
+            pkv.paged_attn_combine(out, ws)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        graphs.append(graph)
+        outs.append(out)
+    for order in ((0, 1, 2), (2, 0, 2, 1, 0), (1, 1, 2, 2, 0)):
+        for out in outs:
+            out.fill_(float("nan"))
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        assert pkv.workspace_status(ws) == 0
+        for s, out in zip(steps, outs):
+            check(s, out, str(order))
 
 
 def test_far_blocks():
