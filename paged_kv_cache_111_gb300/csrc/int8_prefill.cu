@@ -111,6 +111,15 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
+// What the loads before left in flight is there, this among it.
+__device__ __forceinline__ void ip_ld_wait(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
+
 // In the line that is cut, an item counts for as many units as it has key tiles and kIpOver more (Q, epilogue, and what
 // a piece more costs); a CTA gets kIpLeast units at least.  The cut and the join cost about kIpJoin units more.
 constexpr int kIpOver = 3, kIpLeast = 6, kIpJoin = 13;
@@ -751,46 +760,39 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     }
                     const float ref = slow && m == NEG_INF ? 0.f : m;
                     all = some = 0.f;
+                    float x[2][16];
+                    tmem_ld16f(tS, x[0]);
 #pragma unroll
-                    for (int c = 0; c < kIpKeys / 32; ++c) {
-                        float x[32];
-                        tmem_ld32f(tS + 32 * c, x);
-                        tmem_ld_wait();
+                    for (int b = 0; b < kIpPages; ++b) {
+                        float (&z)[16] = x[b & 1];
+                        ip_ld_wait(z);
+                        if (b + 1 < kIpPages) tmem_ld16f(tS + 16 * (b + 1), x[(b + 1) & 1]);
+                        float f, c0, inv;
+                        constants(b, f, c0, inv);
+                        const float cb = c0 - ref;
+                        const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
                         // (in three sweeps, each of them independent of itself: products, exponentials, sums and pairs)
-                        uint64_t y[16];
-                        float inv[2];
+                        uint64_t y[8];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float f, c0;
-                            constants(2 * c + h, f, c0, inv[h]);
-                            const float cb = c0 - ref;
-                            const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(cb, cb);
+                        for (int e = 0; e < 8; ++e) y[e] = f2_fma(f2_pack(z[2 * e], z[2 * e + 1]), f2, c2);
 #pragma unroll
-                            for (int e = 8 * h; e < 8 * h + 8; ++e)
-                                y[e] = f2_fma(f2_pack(x[2 * e], x[2 * e + 1]), f2, c2);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < 8; ++e) {
                             float y0, y1;
                             f2_unpack(y[e], y0, y1);
-                            x[2 * e] = fast_exp2(y0), x[2 * e + 1] = fast_exp2(y1);
+                            z[2 * e] = fast_exp2(y0), z[2 * e + 1] = fast_exp2(y1);
                         }
-                        uint64_t sum[4];
+                        uint64_t sum[2];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t p2 = f2_pack(x[2 * e], x[2 * e + 1]);
-                            const int q = 2 * (e >> 3) + (e & 1);
-                            sum[q] = (e & 7) < 2 ? p2 : f2_add(sum[q], p2);
-                            w[16 * c + e] = pack_p<true>(x[2 * e], x[2 * e + 1]);
+                        for (int e = 0; e < 8; ++e) {
+                            const uint64_t p2 = f2_pack(z[2 * e], z[2 * e + 1]);
+                            sum[e & 1] = e < 2 ? p2 : f2_add(sum[e & 1], p2);
+                            w[8 * b + e] = pack_p<true>(z[2 * e], z[2 * e + 1]);
                         }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float a, d;
-                            f2_unpack(f2_add(sum[2 * h], sum[2 * h + 1]), a, d);
-                            a += d;
-                            all += a;
-                            some = fmaf(a, inv[h], some);
-                        }
+                        float s0, s1;
+                        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+                        s0 += s1;
+                        all += s0;
+                        some = fmaf(s0, inv, some);
                     }
                     if (slow) break;
                     slow = __any_sync(0xffffffffu, !(all <= 8192.f));
