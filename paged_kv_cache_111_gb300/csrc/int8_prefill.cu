@@ -23,11 +23,11 @@
 // bounded.
 //
 // What bounds it: the softmax warps, three warps a scheduler with the widening one.  2432 tokens behind 6144 keys of
-// 32/8 heads of 128 (two rounds of whole items) take 274 us, 4300 cycles a pair of tiles where the products take 2080;
-// 2046 tokens 249, in runs (the tensor pipe and issue at 45%).  Tried and slower: two threads a row, halves of 64 keys
-// (P V early, or the next S early: the other half's S while P V runs hides what the softmax waits for, and reads Q
+// 32/8 heads of 128 (two rounds of whole items) take 263 us, 4100 cycles a pair of tiles where the products take 2080;
+// 2046 tokens 239, in runs (the tensor pipe at 48%, issue at 47%).  Tried and slower: two threads a row, halves of 64
+// keys (P V early, or the next S early: the other half's S while P V runs hides what the softmax waits for, and reads Q
 // twice), an MMA warp a row tile, a pass for each row's largest score (367 us with loops unrolled: instruction fetch).
-// 256 tokens at 6400 keys: 65 us, with items left whole 121.
+// 256 tokens at 6400 keys: 62 us, with items left whole 121 before.
 #include <mutex>
 #include <type_traits>
 
