@@ -27,7 +27,7 @@
 // 2046 tokens 239, in runs (the tensor pipe at 48%, issue at 47%).  Tried and slower: two threads a row, halves of 64
 // keys (P V early, or the next S early: the other half's S while P V runs hides what the softmax waits for, and reads Q
 // twice), an MMA warp a row tile, a pass for each row's largest score (367 us with loops unrolled: instruction fetch).
-// 256 tokens at 6400 keys: 62 us, with items left whole 121 before.
+// 256 tokens at 6400 keys: 63 us, with items left whole 119.
 #include <mutex>
 #include <type_traits>
 
@@ -114,8 +114,8 @@ __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&r)[16]) {
 // What the loads before left in flight is there, this among it.
 __device__ __forceinline__ void ip_ld_wait(float (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
-                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                  :
                  : "memory");
 }
@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));
     const int n_items = n_tiles * p.num_kv_heads;
     // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items'
-    // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 169 and 240 us, 2046 (256)
-    // 255 and 265, 2432 (304) 309 and 278; 1280 behind none 66 and 47.  From four rounds on whole items.
+    // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 161 and 229 us, 2046 (256) 241
+    // and 252, 2432 (304) 283 and 264; 1280 behind none 58 and 45.  From four rounds on whole items.
     bool runs = n_items <= 3 * static_cast<int>(gridDim.x);
     int64_t all = 0;
     int ctas = gridDim.x;
