@@ -67,6 +67,7 @@ struct WsLayout {
 // sums, four dims of each row side by side.  The CTA of an item's first piece notes it down, and the combine joins the
 // pieces.
 constexpr int kSplitCtas = 152;            // CTAs at most
+constexpr int kSplitItems = 3 * kSplitCtas;    // work items at most: with more, all of them stay whole
 constexpr int kSplitRows = 256;            // rows of an item
 struct SplitItem {
     // first query token, rows of the request, the item's first, its first query head

@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items'
     // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 161 and 229 us, 2046 (256) 241
     // and 252, 2432 (304) 283 and 264; 1280 behind none 58 and 45.  From four rounds on whole items.
-    bool runs = n_items <= 3 * static_cast<int>(gridDim.x);
+    // The plan lists tiles of one size by their index, as far as runs are taken: which items are cut, and where, and so
+    // the order of their sums, is the same in every call.
+    bool runs = n_items <= min(kSplitItems, 3 * static_cast<int>(gridDim.x));
     int64_t all = 0;
     int ctas = gridDim.x;
     if (runs && n_items) {                            // (some hundred tiles at most)

@@ -106,6 +106,7 @@ struct PlanParams {
     int32_t total_warps;      // warps of the decode grid (for the automatic split size)
     int32_t prefill_ok;       // long requests go to the tensor-core prefill kernel
     int32_t tile_rows;        // rows of its work items
+    int32_t ordered_tiles;    // up to so many of its tiles, those of one size are listed by their index
     int32_t prefix_blocks;    // shared prefix of the tables in blocks (0: no cascade)
     const int32_t *block_tables;
     WsLayout lay;
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
     __shared__ int s_len[kPlanStagedSeqs];
     __shared__ int4 s_req[kPlanStagedSeqs];
     __shared__ int4 s_geom[kPlanStagedSeqs];   // chunk geometry per request (staged batches)
+    __shared__ int s_tile[kSplitItems];        // the chunk at each place of the tile list, where its order counts
 
     WsHeader *hdr = reinterpret_cast<WsHeader *>(p.ws);
     int4 *req_ws = reinterpret_cast<int4 *>(p.ws + p.lay.off_req);
@@ -489,7 +491,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         if (!fits) bad = 1;
     }
 
-    // pass 4: emit every chunk at its sorted position
+    // pass 4: emit every chunk at its sorted position.  (Chunks of one size bin in whatever order the atomics give,
+    // which no result depends on but where tiles may be cut along their keys: see below.)
+    const int n_tiles = bin_total[1];
+    const bool ordered = n_tiles > 0 && n_tiles <= p.ordered_tiles;
     for (int c = tid; c < n_emit; c += nthr) {
         const int r = owner(c);
         const int4 ri = req[r];
@@ -499,11 +504,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p) {
         const int2 pg = chunk_pages(gm, G, k, p.tile_rows);
         if (gm.x == 2) {
             const int pos = agg_inc(pbin_cursor, min(pg.y, kSizeBins - 1));
-            if (pos < p.lay.max_ptiles) ptiles[pos] = make_int4(r, k, pg.y, 0);
+            if (ordered) s_tile[pos] = c;
+            else if (pos < p.lay.max_ptiles) ptiles[pos] = make_int4(r, k, pg.y, 0);
         } else {
             // chunk {request, split index (cascade: after the prefix ranges), pages}
             const int pos = agg_inc(bin_cursor, min(pg.y - pg.x, kSizeBins - 1));
             if (pos < p.lay.max_chunks) chunks[pos] = make_int4(r, k + (casc ? p.lay.prefix_parts : 0), pg.x, pg.y);
+        }
+    }
+    if (ordered) {
+        // a tile's place among those of its bin, which now end at the bin's cursor
+        __syncthreads();
+        for (int t = tid; t < n_tiles; t += nthr) {
+            const int c = s_tile[t], r = owner(c), k = c - req[r].z;
+            const int tiles = chunk_pages(geometry(r, req[r]), G, k, p.tile_rows).y, bin = min(tiles, kSizeBins - 1);
+            const int end = pbin_cursor[bin], begin = end - pbin_count[bin];
+            int pos = begin;
+            for (int u = begin; u < end; ++u) pos += s_tile[u] < c ? 1 : 0;
+            if (pos < p.lay.max_ptiles) ptiles[pos] = make_int4(r, k, tiles, 0);
         }
     }
     if (staged)
@@ -727,6 +745,7 @@ static int paged_attn_impl(void *out, const void *query, int64_t query_token_str
     pp.total_warps = static_cast<int32_t>(chunk_warps);
     pp.prefill_ok = prefill_ok ? 1 : 0;
     pp.tile_rows = int8 ? kSplitRows : kPrefillRows;
+    pp.ordered_tiles = int8 ? kSplitItems / num_kv_heads : 0;
     pp.prefix_blocks = prefix_blocks;
     pp.block_tables = block_tables;
     pp.lay = lay;
