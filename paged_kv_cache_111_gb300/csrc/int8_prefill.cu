@@ -337,8 +337,10 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     if (side) continue;
                     const float ks = __shfl_sync(0xffffffffu, sc.x, at);
                     float vs = __shfl_sync(0xffffffffu, sc.y, at);
-                    vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;     // (NaN stays, and K's joins it)
-                    vs = ks != ks ? ks : vs;
+                    vs = vs < kInt8LeastScale ? kInt8LeastScale : vs;
+                    // a block without a scale, of either side: NaN here (an infinity is none)
+                    if (!(ks < __int_as_float(0x7f800000) && vs < __int_as_float(0x7f800000)))
+                        vs = __int_as_float(0x7fc00000);
                     if (lane < kIpPages)
                         scales[(gt & 7) * kIpPages + lane] = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
                     __syncwarp();
@@ -693,8 +695,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     f = fmaxf(factor * v.x, least);
                     c0 = fmaf(-bias, f, v.y);
                     inv = v.z;
-                    // (a block without a scale, in a tile of which some rows do not see all: see below)
-                    if (masked && !(fabsf(c0) < 3e38f)) f = 1.f, c0 = inv = 0.f;
+                    // (a block without a scale, in a tile of which some rows do not see all: see below.  Not a query that
+                    // is no number: its row becomes NaN by its own bias)
+                    if (masked && v.y != v.y) f = 1.f, c0 = inv = 0.f;
                 };
                 if (masked) {
                     // keys that the row does not see: their scores become -inf where they lie.  Blocks without a scale
