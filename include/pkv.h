@@ -674,8 +674,17 @@ int pkv_qk_norm_rope_kv_write_int8(void *query_out, int64_t query_out_token_stri
  * any scale's sign is allowed.  The workspace is pkv_paged_attn's, and up to 41 MB more
  * where max_query_len times the query heads of a kv head passes 64 (the size query says).
  * Codes widen to f16 exactly; the query enters the products as f16 after a per-row
- * power-of-two scaling (exact for every element not below 2^-24 of its row's largest),
- * the weights as one f16 each (2^-11 of it); scores, softmax and accumulation are fp32.
+ * power-of-two scaling (exact for every element not below 2^-24 of its row's largest);
+ * scores, softmax and accumulation are fp32.  Errors beside the output's rounding:
+ *   - a weight p_j times its V scale is one f16: off by 2^-11 of it, and by 2^-28 of the
+ *     row's largest such product at most (2^-32 where max_query_len times the query heads
+ *     of a kv head is at most 64), which counts for a tail of weights below 2^-17 of it;
+ *   - a score carries 1152 times the sum of its query row until that is taken off in
+ *     fp32: it is off by some 2^-23 (at most 2^-20) of 1152 sum |q| ks |scale|.  Rounding
+ *     the keys to codes moves it by ks |q|_2 |scale| / sqrt(12) (root mean square), some
+ *     200 times as much or more.
+ * The V scales of one request lie within 2^100 of each other (else the keys of the
+ * smallest may drop out of the weights' sum).  The same call gives the same bits.
  * Rows behind a request's last token may hold anything.  A row that sees a key of a
  * block whose scale is NaN is NaN; one that sees none of its keys does not meet it.
  */

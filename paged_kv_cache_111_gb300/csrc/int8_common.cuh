@@ -51,6 +51,16 @@ __device__ __forceinline__ uint32_t unbias_f16(uint32_t h) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Attention's weights p' = 2^(e - m) enter P V as one f16 each, so a weight below 2^-14, a subnormal, is off by 2^-25
+// absolute.  The reference m lies a lift below a row's largest e (or further): f16 has the room, and what counts is
+// 2^-(25 + lift) of the largest weight, for long tails beside a key that takes most of the sum.  In the decode kernel a
+// weight may grow by 2^8 before the reference moves, as without the lift.  In the chunk kernel, which looks for a row's
+// largest e only where a tile's 128 weights sum to more than f16 holds, a higher lift has it look more often: 2046 tokens
+// at 8190 keys of 32/8 heads 282 us with scores four times as far apart as normal data's and a lift of 3 (without one,
+// and a bound of 2^13, 283), 290 with 4, 302 with 6; on normal data 238 with any.
+constexpr float kInt8DecodeLift = 7.f, kInt8DecodeMost = 15.f;      // 2^15 fits f16
+constexpr float kInt8ChunkLift = 3.f, kInt8ChunkMost = 6e4f;        // a sum that no weight in it passes f16 with
+
 // rint(x r) of two pairs as four codes.  |x r| is below 128, so that in 1.5 * 2^23 + x r, rounded once, the low byte is
 // the code.  (A product rounded by itself would have to be kept from the addition: f32x2 products and sums are fused.)
 __device__ __forceinline__ uint32_t f32_to_int8x4(uint64_t x01, uint64_t x23, uint64_t r2) {

@@ -8,8 +8,8 @@
 // next to 0x64 is 1152 + code.  K is left like that, and S starts at -1152 sum q; V has the 1152 taken off (left in, it
 // would be most of O).  The query row is scaled by a power of two into f16.
 //
-// vs goes into the weights, p'_j = 2^(s_j + log2 vs - m), as far as m, a row's largest s_j + log2 vs (it moves only
-// when passed by 2^8): whatever the blocks' scales are, p' fits f16 where it counts.  The sum is that of p' / vs.
+// vs goes into the weights, p'_j = 2^(s_j + log2 vs - m), with m 7 below a row's largest s_j + log2 vs (it moves only
+// when passed by 2^15): whatever the blocks' scales are, p' fits f16 where it counts.  The sum is that of p' / vs.
 //
 // A lane has the same 16 (8) dims of four keys of V as its part of V^T and 32 (16) dims of two keys as its part of K:
 // whole words of a raw page, which TMA lays out so that no two lanes meet in a bank; P^T goes from the products'
@@ -361,12 +361,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, CTAS)
                     for (int e = 0; e < 4; ++e) {
                         x[nt][e] = fmaf(s[nt][e], sf[nt][e & 1] * ks, lv - m[nt][e & 1]);
                         if (masked) x[nt][e] = j0 + g4 + 8 * (e >> 1) < lim[nt][e & 1] ? x[nt][e] : NEG_INF;
-                        passed |= x[nt][e] > 8.f;
+                        passed |= x[nt][e] > kInt8DecodeMost;
                     }
                 return passed;
             };
             if (__any_sync(0xffffffffu, above())) {
-                // the first key that a row sees, or one that passes its reference by 2^8: the largest is the reference
+                // the first key that a row sees, or one that passes its reference by 2^15: the reference moves to 7 below
+                // the largest
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -381,9 +382,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, CTAS)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        if (mx > m[nt][e] + 8.f) {              // (the same in the lanes of a row)
-                            const float alpha = fast_exp2(m[nt][e] - mx);      // 0 when m = -inf
-                            m[nt][e] = mx;
+                        if (mx > m[nt][e] + kInt8DecodeMost) {              // (the same in the lanes of a row)
+                            const float alpha = fast_exp2(m[nt][e] - (mx - kInt8DecodeLift));      // 0 when m = -inf
+                            m[nt][e] = mx - kInt8DecodeLift;
                             l[nt][e] *= alpha;
 #pragma unroll
                             for (int i = 0; i < MT; ++i) o[nt][i][e] *= alpha, o[nt][i][e + 2] *= alpha;
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, CTAS)
                     const float inv = masked && j0 >= lim[nt][e] ? 0.f : vr;
                     l[nt][e] = fmaf(pr[e] + pr[e + 2], inv, l[nt][e]);
                 }
-                // one f16 a weight: off by 2^-11 of it at most, an eighth of the output's rounding to bf16
+                // one f16 a weight: off by 2^-11 of it (an eighth of the output's rounding to bf16) and 2^-32 of the
+                // row's largest at most
                 pb0[nt] = movmatrix(pack_f16x2(pr[0], pr[1]));
                 pb1[nt] = movmatrix(pack_f16x2(pr[2], pr[3]));
             }

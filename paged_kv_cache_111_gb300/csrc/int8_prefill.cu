@@ -6,8 +6,9 @@
 //     p'_j = 2^(e_j - m),          out = sum_j p'_j v_j / sum_j p'_j / vs
 // K's codes widen to f16 as 1152 + code (a byte next to 0x64) and stay so: what that adds to S is one number a row, and
 // goes with the block's factor into the constants of the softmax, of which a row has three a block of 16 keys.  V's
-// codes are taken back to themselves.  m is the row's largest e_j so far, looked for again only where the weights of a
-// tile sum to more than 2^13, so that p' fits f16 whatever the blocks' scales are.
+// codes are taken back to themselves.  m is 3 below the row's largest e_j so far, which is looked for again only where the
+// weights of a tile sum to more than 6e4, so that p' fits f16 whatever the blocks' scales are, and a long tail of small
+// ones is no more than 2^-28 of the largest off each.
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and
 // share each 128-key tile; a persistent CTA an SM takes items largest first.  Where that would leave CTAs idle for
@@ -717,9 +718,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     }
                     tmem_st_wait();
                 }
-                // The weights are taken against the reference that is there.  Where they sum to 2^13 or less none of
-                // them is past f16, and the row's largest score need not be looked for; where they do not, it becomes
-                // the reference.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
+                // The weights are taken against the reference that is there.  Where they sum to 6e4 or less none of
+                // them is past f16, and the row's largest score need not be looked for; where they do not, the reference
+                // moves to 3 below it.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
                 bool slow = j == 0;
                 uint32_t w[kIpKeys / 2];               // P, pairs of f16
                 float all, some;                       // the weights' sum, and that of the blocks' times 1 / vs
@@ -742,6 +743,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                                 mx = fmaxf(mx, fmaf(y[0], f, c0));
                             }
                         }
+                        mx -= kInt8ChunkLift;
                         const bool grow = mx > m;      // (m = -inf at first)
                         const float alpha = grow ? fast_exp2(m - mx) : 1.f;
                         if (grow) m = mx;
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                         some = fmaf(s0, inv, some);
                     }
                     if (slow) break;
-                    slow = __any_sync(0xffffffffu, !(all <= 8192.f));
+                    slow = __any_sync(0xffffffffu, !(all <= kInt8ChunkMost));
                     if (!slow) break;
                 }
                 if (!ok) break;

@@ -52,6 +52,42 @@ def test_rows_that_do_not_see_a_block_of_an_infinite_scale(side, reqs):
     ref.check(out[blind], want[blind], bound[blind])
 
 
+# The kernels' references: a row's largest weight (times its V scale) is 2^7 (decode) or 2^3 (chunks) or more of the unit
+# that a weight's f16 has, so a subnormal weight is off by 2^-25 / 2^7, 2^-25 / 2^3 of the largest at most.
+SUBNORMAL_DECODE, SUBNORMAL_CHUNK = 2.0 ** -32, 2.0 ** -28
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("reqs,num_splits", [([(1, 579)], 1), ([(1, 579), (3, 2000)], 0), ([(200, 779)], 0),
+                                             ([(40, 6000)], 0)])
+def test_a_key_that_takes_nearly_all_of_the_weight(reqs, num_splits, d):
+    """The first key has a value of zero and the others a weight of 5.45 * 2^-24 of its own each, with values of one
+    sign: an f16 against that weight would be off by 9%, and all of them the same way."""
+    s = batch(reqs, 8, 2, d, seed=22)
+    lift = -math.log(5.45 * 2.0 ** -24)
+    s["scales"].fill_(1 / 36)
+    s["scale"] = lift * 36 / (127 * d)
+    s["query"].fill_(1.0)
+    g = torch.Generator().manual_seed(3)
+    shape = s["cache"][:, :, 1].shape
+    s["cache"][:, :, 0] = 0
+    s["cache"][:, :, 1] = torch.randint(64, 128, shape, generator=g, dtype=torch.int8).cuda()
+    first = s["tables"][:, 0].long()
+    s["cache"][first, :, 0, 0] = 127
+    s["cache"][first, :, 1, 0] = 0
+    out = run(s, num_splits=num_splits)
+    want, _ = ref.attention(s["query"], s["cache"], s["scales"], s["tables"], s["lens"], s["qsl"], s["scale"])
+    # per row, all of `want` positive: f16 of the weights, subnormal weights, the scores' errors (int8_ref.attention's
+    # bound of them: the largest term of S is 1152 sum q, 1152 / 127 times the largest score), the output's bf16
+    rows = torch.tensor([q for q, _ in reqs], device="cuda")
+    keys = torch.tensor([n for _, n in reqs], device="cuda").repeat_interleave(rows)
+    slip = 2 * 16 * 2 * ref.FP32_STEP * (1152 / 127 * lift) + 2.0 ** -18
+    least = SUBNORMAL_DECODE if s["max_q"] * 4 <= 64 else SUBNORMAL_CHUNK
+    top = (127 * least * keys.double() / 36)[:, None, None]                   # (the largest weight is below one)
+    e = (ref.F16_HALF_STEP + slip) * want + top
+    ref.check(out, want, ref.BF16_HALF_STEP * want + (1 + ref.BF16_HALF_STEP) * e)
+
+
 @pytest.mark.parametrize("reqs,hq,hkv", [([(1, 2000)] * 300 + [(300, 9000)] * 5, 32, 1),
                                          ([(1, 30)] * 1100 + [(33, 9000)] * 40, 8, 1),
                                          ([(64, 40000), (64, 40000), (64, 36000)] * 3, 8, 2)])
