@@ -98,3 +98,40 @@ def test_the_same_again_and_again(reqs, hq, hkv):
     check(s, one)
     for k in range(100):
         assert torch.equal(run(s), one), k
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 1), (24, 1), (64, 1), (65, 1), (128, 1), (300, 1), (256, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_query_heads_a_kv_head(hq, hkv, d):
+    """One token is two or more tiles of 16 rows up to 64 heads a kv head, and a chunk's work item beyond."""
+    for reqs in ([(1, 1)], [(1, 17), (1, 300), (1, 128)], [(1, 9000)], [(2, 40), (1, 500)], [(3, 9000), (1, 5)]):
+        s = batch(reqs, hq, hkv, d, seed=hq)
+        check(s, run(s), str(reqs))
+
+
+@pytest.mark.parametrize("q,n", [(1, 131072), (16, 131072), (40, 100003)])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (128, 1, 64)])
+def test_few_work_items_of_very_many_keys(q, n, hq, hkv, d):
+    s = batch([(q, n)], hq, hkv, d, seed=24)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("reqs", [[(1, 900)] * 20, [(200, 6000), (1, 40)], [(2046, 2100)]])
+def test_two_calls_at_once(reqs):
+    """On two streams, each with a workspace of its own and the cache in common."""
+    s = batch(reqs, 8, 2, 128, seed=26)
+    one = run(s)
+    T, hq, d = s["query"].shape
+    lens, qsl = (torch.tensor(s[k], dtype=torch.int32, device="cuda") for k in ("lens", "qsl"))
+    n = pkv.paged_attn_workspace_size(len(reqs), T, s["max_q"], s["max_n"], hq, 2, d)
+    sides = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.zeros_like(one)) for _ in "ab"]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for stream, ws, out in sides:
+            pkv.paged_attn_int8(out, s["query"], s["cache"], s["scales"], s["tables"], lens, qsl, s["max_q"], s["max_n"],
+                                s["scale"], ws, stream=stream)
+            pkv.paged_attn_combine(out, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, ws, out in sides:
+        assert pkv.workspace_status(ws) == 0
+        assert torch.equal(out, one)
