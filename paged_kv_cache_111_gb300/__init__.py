@@ -32,6 +32,7 @@ plus ``paged_attn_workspace_size(...)`` (the C call's size query) and
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 from typing import Optional
@@ -76,6 +77,10 @@ def _calls():
     global _module
     if _module is None:
         load()
+        if not os.path.exists(_build.CALLS):
+            raise RuntimeError(f"{_build.CALLS} is missing: build it first, with this Python's headers "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        importlib.invalidate_caches()
         from . import _py_calls
         _py_calls.bind(torch.int8, _BF16, _F32, _I32, _I64, _refuse, PagedKVError, torch._C._cuda_getDevice,
                        torch.cuda.device, torch._C._cuda_getCurrentRawStream)
@@ -348,6 +353,13 @@ def paged_attn_shared_prefix_fp8(out: torch.Tensor, query: torch.Tensor, kv_cach
 
 def paged_attn_combine(out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Log-sum-exp merge of the rows pkv_paged_attn split; out as given to paged_attn."""
+    if _module is None and not os.path.exists(_build.CALLS):      # (built without Python's headers)
+        _need_cuda(out, workspace)
+        T, H, d = out.shape
+        with torch.cuda.device(out.device):
+            rc = load().pkv_paged_attn_combine(_ptr(out), _ptr(workspace), workspace.nbytes, T, H, d, _stream(out, stream))
+        _check(rc, "pkv_paged_attn_combine")
+        return
     (_module or _calls()).combine(out, workspace, stream)
 
 

@@ -135,3 +135,20 @@ def test_two_calls_at_once(reqs):
     for _, ws, out in sides:
         assert pkv.workspace_status(ws) == 0
         assert torch.equal(out, one)
+
+
+def test_the_combine_without_the_module(monkeypatch, tmp_path):
+    """As built without Python's headers: attention over the other caches still has its combine."""
+    from paged_kv_cache_111_gb300 import _build
+    s = batch([(1, 900), (3, 400), (70, 90)], 8, 2, 64, seed=27)
+    one = run(s)
+    combine = pkv.paged_attn_combine
+
+    def without(*args, **kw):
+        with monkeypatch.context() as m:
+            m.setattr(pkv, "_module", None)
+            m.setattr(_build, "CALLS", str(tmp_path / "none.so"))
+            combine(*args, **kw)
+
+    monkeypatch.setattr(pkv, "paged_attn_combine", without)
+    assert torch.equal(run(s), one)
