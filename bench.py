@@ -311,7 +311,7 @@ def run_gpu(args, rank: int, world: int) -> dict:
                                                                step.max_seq_len, H, step.num_kv_heads, d, K)
     else:
         ws_bytes = pkv.paged_attn_workspace_size(step.num_seqs, T, step.max_query_len, step.max_seq_len, H,
-                                                 step.num_kv_heads, d)
+                                                 step.num_kv_heads, d, int8=False)
     ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev)
     out = torch.empty(T, H, d, dtype=torch.bfloat16, device=dev)
     stream = torch.cuda.current_stream(dev)

@@ -209,16 +209,20 @@ def copy_blocks(kv_cache: torch.Tensor, block_mapping: torch.Tensor, device_stat
 
 
 def paged_attn_workspace_size(num_seqs: int, num_tokens: int, max_query_len: int, max_seq_len: int,
-                              num_q_heads: int, num_kv_heads: int, head_size: int) -> int:
-    """Bytes of workspace that paged_attn, paged_attn_fp8 and paged_attn_int8 need for these sizes (no GPU work): that of
-    the last, which for chunks is up to 41 MB more than the others'."""
+                              num_q_heads: int, num_kv_heads: int, head_size: int, int8: bool = True) -> int:
+    """Bytes of workspace that paged_attn, paged_attn_fp8 and paged_attn_int8 need for these sizes (no GPU work).  With
+    int8=False what the first two need: where max_query_len times the query heads of a kv head passes 64, that is 20 MB
+    (head size 64) or 40 MB (128) less."""
     need = ctypes.c_size_t(0)
     max_blocks = (max_seq_len + BLOCK_SIZE - 1) // BLOCK_SIZE
-    rc = load().pkv_paged_attn_int8(None, None, num_q_heads * head_size, None, None, 1, None, max_blocks, None, None,
-                                    num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
-                                    head_size, BLOCK_SIZE, 1.0, 0, None, 0, ctypes.byref(need), None)
+    tables = (max_blocks, None, None, num_seqs, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
+              head_size, BLOCK_SIZE, 1.0, 0, None, 0, ctypes.byref(need), None)
+    if int8:
+        rc = load().pkv_paged_attn_int8(None, None, num_q_heads * head_size, None, None, 1, None, *tables)
+    else:
+        rc = load().pkv_paged_attn(None, None, num_q_heads * head_size, None, 1, None, *tables)
     if rc not in (0, 1, 5):
-        _check(rc, "pkv_paged_attn_int8 (size query)")
+        _check(rc, f"pkv_paged_attn{'_int8' if int8 else ''} (size query)")
     return int(need.value)
 
 
