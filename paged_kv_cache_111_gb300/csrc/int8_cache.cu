@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kI8Threads, FORM == 0 ? 7 : 4) int8_write_kern
         if (lane == 0) set_status(p.status, PKV_ERR_DEVICE_INDEX);
         return;
     }
-    const int start = 32 - __clz(~same & 0xFFFFu);            // 0 .. 16; the 32 lanes hold all of the first 16
+    const int start = 32 - __clz(~same & 0xFFFFu);            // 1 .. 16; the 32 lanes hold all of the first 16
     const int n = min(kBlock, __ffs(static_cast<int>(~(same >> start))) - 1);
     const int j = kBlock - start;
     const bool in = lane >= start && lane < start + n;
@@ -484,9 +484,12 @@ static int check_cache(int64_t num_blocks, int32_t num_kv_heads, int32_t head_si
 static bool misaligned(const void *a, unsigned bytes) { return (reinterpret_cast<uintptr_t>(a) & (bytes - 1)) != 0; }
 
 static int int8_write(Int8WriteParams &p, int form, int32_t head_size, void *stream) {
-    // Heads a warp: 16, or two rows a lane where that would put fewer than 16 warps on each of the 152 SMs (writing and
-    // reading back 64 tokens of 8 heads of 128: 6.4 us, with 16 heads 8.7; queries, keys and values of 2046 tokens of
-    // 32/8 heads: 23 us, with two rows a lane 29).
+    // Heads a warp: 16, or two rows a lane where that would put fewer than 16 warps on each of the 152 SMs.  GPU time,
+    // two rows a lane against 16 heads: keys and values of 8 heads of 128, one prompt of 100 tokens 2.3 us against 4.3,
+    // 600 3.0 against 3.1, 1000 3.5 against 3.4, 2000 4.9 against 4.4, 4000 7.5 against 5.4, of 600 decodes 2.8 against
+    // 4.1; queries, keys and values of 32/8 heads, 100 tokens 4.9 against 6.3, 300 6.2 against 5.1, 600 8.1 against
+    // 5.7, 1000 11.2 against 8.5, 2046 24.0 against 18.7.  So the two meet at some 1000 warps of 16 heads (prompts;
+    // decodes later).
     const int few = 2 * (32 / (head_size / 8));
     auto spread = [&](int heads) {
         p.q_chunks = form ? (p.hq + heads - 1) / heads : 0;
@@ -627,8 +630,11 @@ extern "C" int pkv_kv_gather_int8(void *key_out, void *value_out, int64_t out_ro
     p.status = device_status;
     // (one CTA a request where none may have rows: the lengths are looked at all the same)
     const int64_t pages = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
-    // Pages a CTA: two where there are enough of them (256 requests of up to 4096 tokens: 188 us, one page 193), else
-    // one (four requests of up to 128 tokens: 2.5 us, two pages 3.3).
+    // Pages a CTA: two where there are enough of them, else one.  One page against two: 8 heads of 128, four requests
+    // of up to 128 tokens 2.5 us against 3.3, 8 requests of 2048 tokens 17.6 against 19.4, 16 (the bound) 32.2 against
+    // 33.1, 32 61.7 against 62.8, 256 of up to 4096 193 against 188; 2 heads, 8 requests 6.0 against 5.2, 16 12.3
+    // against 10.6, 32 20.2 against 18.0; 1 head, 16 requests 8.3 against 6.0, 32 15.7 against 12.6 (fewer units than
+    // warps in one page).
     p.per = pages * num_seqs > 2048 ? 2 : 1;
     const dim3 grid(static_cast<unsigned>(pages ? (pages + p.per - 1) / p.per : 1), static_cast<unsigned>(num_seqs));
     const cudaError_t e = launch_pdl(head_size == 128 ? int8_gather_kernel<128> : int8_gather_kernel<64>, grid,

@@ -55,9 +55,9 @@ __device__ __forceinline__ uint32_t unbias_f16(uint32_t h) {
 // absolute.  The reference m lies a lift below a row's largest e (or further): f16 has the room, and what counts is
 // 2^-(25 + lift) of the largest weight, for long tails beside a key that takes most of the sum.  In the decode kernel a
 // weight may grow by 2^8 before the reference moves, as without the lift.  In the chunk kernel, which looks for a row's
-// largest e only where a tile's 128 weights sum to more than f16 holds, a higher lift has it look more often: 2046 tokens
-// at 8190 keys of 32/8 heads 282 us with scores four times as far apart as normal data's and a lift of 3 (without one,
-// and a bound of 2^13, 283), 290 with 4, 302 with 6; on normal data 238 with any.
+// largest e only where a tile's 128 weights sum to more than f16 holds, a higher lift has it look more often: 2046
+// tokens at 8190 keys of 32/8 heads 282 us with scores four times as far apart as normal data's and a lift of 3
+// (without one, and a bound of 2^13, 283), 290 with 4, 302 with 6; on normal data 238 with any.
 constexpr float kInt8DecodeLift = 7.f, kInt8DecodeMost = 15.f;      // 2^15 fits f16
 constexpr float kInt8ChunkLift = 3.f, kInt8ChunkMost = 6e4f;        // a sum that no weight in it passes f16 with
 

@@ -25,10 +25,11 @@
 
 namespace pkv {
 
-// ROWS: columns of the products, rows of a chunk at most.  Two ring stages a warp: 64 to 96 KB in flight an SM are more
-// than memory's rate times its latency, and what shared memory leaves is L1 (256 requests of 40 heads of 128: 347 us,
-// with three stages 361, with three and a CTA more, of 128 registers that spill, 382; 64 requests of 512 to 2048 keys,
-// 32/4 heads of 64: 17.7 us, with six stages 20.2).
+// ROWS: columns of the products, rows of a chunk at most.  Two ring stages a warp: 48 KB (16 columns of 64 dims) to 96
+// KB in flight an SM are more than an SM's share of memory's rate times its latency, some 35 KB, and what shared memory
+// leaves is L1 (256 requests of 40 heads of 128: 347 us, with three stages 361, with three and a CTA more, of 128
+// registers that spill, 382; 64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.7 us, with six stages 20.2; 256
+// requests of 64/4 heads of 64: 68.9 us, with three stages 69.4).
 constexpr int kInt8Depth = 2;
 
 // CTAs an SM.  Sixteen columns of 128 dims spill at the 168 registers of three; a large batch, which the decode kernel
@@ -366,8 +367,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, CTAS)
                 return passed;
             };
             if (__any_sync(0xffffffffu, above())) {
-                // the first key that a row sees, or one that passes its reference by 2^15: the reference moves to 7 below
-                // the largest
+                // the first key that a row sees, or one that passes its reference by 2^15: the reference moves to 7
+                // below the largest
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -6,9 +6,9 @@
 //     p'_j = 2^(e_j - m),          out = sum_j p'_j v_j / sum_j p'_j / vs
 // K's codes widen to f16 as 1152 + code (a byte next to 0x64) and stay so: what that adds to S is one number a row, and
 // goes with the block's factor into the constants of the softmax, of which a row has three a block of 16 keys.  V's
-// codes are taken back to themselves.  m is 3 below the row's largest e_j so far, which is looked for again only where the
-// weights of a tile sum to more than 6e4, so that p' fits f16 whatever the blocks' scales are, and a long tail of small
-// ones is no more than 2^-28 of the largest off each.
+// codes are taken back to themselves.  m is 3 below the row's largest e_j so far, which is looked for again only where
+// the weights of a tile sum to more than 6e4, so that p' fits f16 whatever the blocks' scales are, and a long tail of
+// small ones is no more than 2^-28 of the largest off each.
 //
 // Work item: 256 rows of one request for one kv head, as two 128-row tiles that take turns on the tensor cores and
 // share each 128-key tile; a persistent CTA an SM takes items largest first.  Where that would leave CTAs idle for
@@ -153,10 +153,12 @@ __global__ void __launch_bounds__(kIpThreads, 1)
     const int4 *ptiles = reinterpret_cast<const int4 *>(p.ws + ws_ld(&hdr->off_ptiles));
     const int n_items = n_tiles * p.num_kv_heads;
     // Whole items to each CTA (rounds of an item's mean, and the largest item at least), or equal runs of all items'
-    // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 1280 tokens (160 items) 161 and 229 us, 2046 (256) 241
-    // and 252, 2432 (304) 283 and 264; 1280 behind none 58 and 45.  From four rounds on whole items.
-    // The plan lists tiles of one size by their index, as far as runs are taken: which items are cut, and where, and so
-    // the order of their sums, is the same in every call.
+    // units?  32/8 heads of 128 behind 6144 keys, runs and whole: 256 tokens (32 items) 63 and 120 us, 1280 (160) 159
+    // and 229, 2046 (256) 239 and 252, 2432 (304) 283 and 263; 1280 behind none 59 and 46.  Of 64 dims (a piece's sums
+    // are half as large): 256 tokens 51 and 103, 1280 130 and 193, 2046 198 and 214, 2432 231 and 224; behind none 44
+    // and 37, behind 2000 keys 1000 tokens 61 and 60.  From four rounds on whole items.  The plan lists tiles of one
+    // size by their index, as far as runs are taken: which items are cut, and where, and so the order of their sums, is
+    // the same in every call.
     bool runs = n_items <= min(kSplitItems, 3 * static_cast<int>(gridDim.x));
     int64_t all = 0;
     int ctas = gridDim.x;
@@ -696,8 +698,8 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     f = fmaxf(factor * v.x, least);
                     c0 = fmaf(-bias, f, v.y);
                     inv = v.z;
-                    // (a block without a scale, in a tile of which some rows do not see all: see below.  Not a query that
-                    // is no number: its row becomes NaN by its own bias)
+                    // (a block without a scale, in a tile of which some rows do not see all: see below.  A query that is
+                    // no number makes its own row NaN, by its bias)
                     if (masked && v.y != v.y) f = 1.f, c0 = inv = 0.f;
                 };
                 if (masked) {
@@ -719,8 +721,9 @@ __global__ void __launch_bounds__(kIpThreads, 1)
                     tmem_st_wait();
                 }
                 // The weights are taken against the reference that is there.  Where they sum to 6e4 or less none of
-                // them is past f16, and the row's largest score need not be looked for; where they do not, the reference
-                // moves to 3 below it.  (Where there is none, m = -inf, they sum to an infinity or to no number.)
+                // them is past f16, and the row's largest score need not be looked for; where they do not, the
+                // reference moves to 3 below it.  (Where there is none, m = -inf, they sum to an infinity or to no
+                // number.)
                 bool slow = j == 0;
                 uint32_t w[kIpKeys / 2];               // P, pairs of f16
                 float all, some;                       // the weights' sum, and that of the blocks' times 1 / vs

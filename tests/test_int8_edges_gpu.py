@@ -20,7 +20,8 @@ def built():
 
 
 @pytest.mark.parametrize("value", [-math.inf, math.inf, math.nan])
-@pytest.mark.parametrize("reqs", [[(1, 100), (1, 16)], [(3, 40), (2, 2)], [(70, 70), (1, 30)], [(200, 333)], [(40, 6000)]])
+@pytest.mark.parametrize("reqs", [[(1, 100), (1, 16)], [(3, 40), (2, 2)], [(70, 70), (1, 30)], [(200, 333)],
+                                  [(40, 6000)]])
 @pytest.mark.parametrize("scale", [0.1, -0.1])
 def test_queries_that_are_no_numbers(value, reqs, scale):
     """Such a row is NaN, wherever the mask cuts it; the others are as if it were not there."""
@@ -52,8 +53,8 @@ def test_rows_that_do_not_see_a_block_of_an_infinite_scale(side, reqs):
     ref.check(out[blind], want[blind], bound[blind])
 
 
-# The kernels' references: a row's largest weight (times its V scale) is 2^7 (decode) or 2^3 (chunks) or more of the unit
-# that a weight's f16 has, so a subnormal weight is off by 2^-25 / 2^7, 2^-25 / 2^3 of the largest at most.
+# The kernels' references: a row's largest weight (times its V scale) is 2^7 (decode) or 2^3 (chunks) or more of the
+# unit that a weight's f16 has, so a subnormal weight is off by 2^-25 / 2^7, 2^-25 / 2^3 of the largest at most.
 SUBNORMAL_DECODE, SUBNORMAL_CHUNK = 2.0 ** -32, 2.0 ** -28
 
 
@@ -124,12 +125,13 @@ def test_two_calls_at_once(reqs):
     T, hq, d = s["query"].shape
     lens, qsl = (torch.tensor(s[k], dtype=torch.int32, device="cuda") for k in ("lens", "qsl"))
     n = pkv.paged_attn_workspace_size(len(reqs), T, s["max_q"], s["max_n"], hq, 2, d)
-    sides = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.zeros_like(one)) for _ in "ab"]
+    sides = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.zeros_like(one))
+             for _ in range(2)]
     torch.cuda.synchronize()
     for _ in range(5):
         for stream, ws, out in sides:
-            pkv.paged_attn_int8(out, s["query"], s["cache"], s["scales"], s["tables"], lens, qsl, s["max_q"], s["max_n"],
-                                s["scale"], ws, stream=stream)
+            pkv.paged_attn_int8(out, s["query"], s["cache"], s["scales"], s["tables"], lens, qsl, s["max_q"],
+                                s["max_n"], s["scale"], ws, stream=stream)
             pkv.paged_attn_combine(out, ws, stream=stream)
     torch.cuda.synchronize()
     for _, ws, out in sides:

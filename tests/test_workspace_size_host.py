@@ -22,9 +22,9 @@ def needed(fn, before, S, T, max_q, max_n, hq, hkv, d, floats):
     return need.value
 
 
-@pytest.mark.parametrize("sizes", [(4, 4, 1, 300, 32, 8, 128), (4, 64, 16, 300, 32, 8, 128), (4, 68, 17, 300, 32, 8, 128),
-                                   (3, 2050, 2046, 8190, 32, 8, 128), (2, 100, 99, 400, 8, 8, 64), (1, 1, 1, 17, 65, 1, 64),
-                                   (0, 0, 0, 0, 4, 2, 64)])
+@pytest.mark.parametrize("sizes", [
+    (4, 4, 1, 300, 32, 8, 128), (4, 64, 16, 300, 32, 8, 128), (4, 68, 17, 300, 32, 8, 128),
+    (3, 2050, 2046, 8190, 32, 8, 128), (2, 100, 99, 400, 8, 8, 64), (1, 1, 1, 17, 65, 1, 64), (0, 0, 0, 0, 4, 2, 64)])
 def test_each_cache_pays_for_what_its_call_needs(lib, sizes):
     hq, hkv, d = sizes[4:]
     step = hq * d
