@@ -613,12 +613,13 @@ __device__ __forceinline__ void join_split_items(__nv_bfloat16 *out, const uint8
     }
 }
 
-// No stack frame: what only the join reads is loaded there, and the registers are not held to four CTAs an SM.  (Held to
-// 64 registers the merge of split rows spilled 4 to 12 bytes, and every launch that has local memory takes 0.2 us more:
-// attention and combine of 4 requests of 8 heads 8.04 us, so 7.85; 32 requests of 64/8 heads of 128 59.0 and 58.4.)
+// No stack frame in the 64 registers that four CTAs an SM have: what only the join reads is loaded there, and rows count
+// in 32 bits.  (Where the merge of split rows spilled 4 to 12 bytes, every launch took 0.2 us more, as one with local
+// memory does: attention and combine of 4 requests of 8 heads 8.04 us, so 7.85; 32 requests of 64/8 heads of 128 59.0 and
+// 58.4.)
 template <int HD>
-__global__ void __launch_bounds__(256) combine_kernel(__nv_bfloat16 *out, const uint8_t *ws, int32_t num_tokens,
-                                                      int32_t num_q_heads) {
+__global__ void __launch_bounds__(256, 4) combine_kernel(__nv_bfloat16 *out, const uint8_t *ws, int32_t num_tokens,
+                                                         int32_t num_q_heads) {
     pdl_wait();       // every partial of the attention kernels is written
     const WsHeader *hdr = reinterpret_cast<const WsHeader *>(ws);
     // every header field this kernel uses, loaded at once (one round trip)
@@ -635,11 +636,11 @@ __global__ void __launch_bounds__(256) combine_kernel(__nv_bfloat16 *out, const 
     const float *part_o = reinterpret_cast<const float *>(ws + off_o);
     const int lane = threadIdx.x & 31;
     // one warp per row (split token, q head), grid-strided over the rows
-    const int64_t n_rows = static_cast<int64_t>(n_split) * num_q_heads;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < n_rows;
-         row += static_cast<int64_t>(gridDim.x) * 8) {
-        const int4 st = __ldg(stoks + row / num_q_heads);   // {token, partial row of q head 0, splits, 0}
-        const int h = static_cast<int>(row % num_q_heads);
+    // (32 bits: see the host side)
+    const uint32_t heads = static_cast<uint32_t>(num_q_heads), n_rows = static_cast<uint32_t>(n_split) * heads;
+    for (uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < n_rows; row += gridDim.x * 8) {
+        const int4 st = __ldg(stoks + row / heads);         // {token, partial row of q head 0, splits, 0}
+        const int h = static_cast<int>(row % heads);
         merge_split_row<HD>(part_o, part_lse, st.y + static_cast<int64_t>(h) * st.z, st.z,
                             out + (static_cast<int64_t>(st.x) * num_q_heads + h) * HD, lane);
     }
@@ -883,6 +884,8 @@ extern "C" int pkv_paged_attn_combine(void *out, const void *workspace, size_t w
     // the rows to merge are known on the device only: a grid of at most 8
     // CTAs per SM strides over them
     const int64_t rows = static_cast<int64_t>(num_tokens) * num_q_heads;
+    // the kernel counts rows in 32 bits, a stride past the last (an output of so many rows has 2^39 bytes)
+    if (rows > UINT32_MAX - (1 << 16)) return PKV_ERR_SHAPE;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -4,6 +4,7 @@ import os
 import re
 import subprocess
 
+import paged_kv_cache_111_gb300 as pkv
 from paged_kv_cache_111_gb300 import _build
 
 
@@ -15,3 +16,9 @@ def test_the_combine_has_no_stack_frame(tmp_path):
     frames = dict(re.findall(r"Function properties for (\S*combine_kernel\S*)\n\s*(\d+) bytes stack frame", res.stderr))
     assert len(frames) == 2, res.stderr
     assert set(frames.values()) == {"0"}, frames
+
+
+def test_more_rows_than_the_combine_counts_are_refused():
+    _build.build()
+    combine = pkv.load().pkv_paged_attn_combine
+    assert combine(0x10000, 0x20000, 1 << 20, (1 << 31) - 1, 1 << 10, 64, None) == 2       # PKV_ERR_SHAPE
