@@ -15,9 +15,9 @@
 // whole words of a raw page, which TMA lays out so that no two lanes meet in a bank; P^T goes from the products'
 // result to their operand through movmatrix.  No value is staged in shared memory a second time.
 //
-// What bounds it: memory in large batches (256 requests of up to 4096 keys, 40 heads of 128, with plan and combine: 347
+// What bounds it: memory in large batches (256 requests of up to 4096 keys, 40 heads of 128, with plan and combine: 346
 // us, 98% of a copy's rate); in small ones the chain of plan, tables, first pages and partial rows, and some 300
-// instructions a page (64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.7 us, 4.5 of them the combine).
+// instructions a page (64 requests of 512 to 2048 keys, 32/4 heads of 64: 17.4 us, 4.9 of them the combine).
 #include <mutex>
 
 #include "decode_plan.cuh"
